@@ -1,7 +1,9 @@
 /*
  * pk.h -- packed-sequence RoPE attention on one GB300 (sm_103a): the forward pass (pk_attend
  * and its typed forms, pk_attend_noalloc, pk_attend_mixed), its backward pass
- * (pk_attend_backward), the tile schedule (pk_schedule) and the standalone rotation (pk_rope).
+ * (pk_attend_backward), the tile schedule (pk_schedule) and the standalone rotation (pk_rope);
+ * and what an encoder needs around it on the same token rows: the projection (pk_linear), dropout
+ * (pk_dropout) and the cross entropy over a vocabulary (pk_cross_entropy), with their gradients.
  *
  * The operation (hanzo-kernel 0.2.42 packed.rs, module doc and fn attend / fn attend_ref):
  * attention over packed variable-length sequences straight from a packed QKV projection,
@@ -89,11 +91,13 @@ enum pk_status {
     PK_ERR_UNSUPPORTED = 4,  /* the current device is not sm_103 (GB300) */
     PK_ERR_BAD_CU = 5,       /* device: cu[0] != 0, cu decreasing, or cu[S] != T */
     PK_ERR_TIMEOUT = 6,      /* device: a pipeline wait exceeded its bound; results invalid */
-    PK_ERR_NOMEM = 7,        /* workspace allocation failed */
+    PK_ERR_NOMEM = 7,        /* workspace allocation failed; token-row operators: the workspace
+                                given is smaller than the call's *_workspace answer */
     PK_ERR_INTERNAL = 8,     /* device: schedule exceeded its capacity (a library bug) */
     PK_ERR_TOO_LARGE = 9,    /* pk_attend_noalloc: T above PK_NOALLOC_MAX_T */
-    PK_ERR_CAPTURE = 10      /* the stream is being captured and its workspace would have to
+    PK_ERR_CAPTURE = 10,     /* the stream is being captured and its workspace would have to
                                 be allocated or grown: make one uncaptured call first */
+    PK_ERR_BAD_LABEL = 11    /* device: pk_cross_entropy: a label at or past V */
 };
 
 enum pk_dtype { PK_F32 = 0, PK_BF16 = 1, PK_F16 = 2 };
@@ -331,6 +335,101 @@ int pk_attend_mixed_ops(int op_dtype, const float *qkv, const float *cos, const 
 int pk_rope(int dtype, const void *x, void *y, const void *cos, const void *sin, int64_t P,
             const uint32_t *cu, int S, int64_t T, int H, int dims, int traditional, int inverse,
             int *status, struct CUstream_st *stream);
+
+/*
+ * Token-row operators: what stands around the attention in an encoder, on the rows of the same
+ * packed batch -- the projection with its epilogue, dropout, and the cross entropy over a
+ * vocabulary, each with its gradient.
+ *
+ * Conventions of these entry points:
+ *   - Matrices are row-major in one element type (`dtype`, enum pk_dtype). `ld*` arguments are
+ *     row strides in elements (>= the row's length); matrices without one are dense. Pointers
+ *     are aligned to the element; matrices whose base and row stride are multiples of 16 bytes
+ *     are read where they lie, others (and fp32 operands of a product, which become three bf16
+ *     planes each) through a copy in the workspace.
+ *   - Products run on the tensor cores with fp32 accumulation; sums, activations and exponentials
+ *     are fp32, with one rounding to the element type at the end. fp32 operands: six products of
+ *     bf16 planes (24 significant bits); a non-finite fp32 operand gives non-finite results, not
+ *     always of the same kind.
+ *   - `workspace`: caller-owned scratch of at least the bytes the entry point's *_workspace
+ *     function gives for the same arguments (0: may be NULL), 256-byte aligned, used only by
+ *     the call's own launches: two calls that may run at the same time (other streams, two
+ *     captured graphs) need two workspaces. Nothing is kept in it between calls.
+ *   - `status`: optional device int (NULL: none), set to PK_OK in stream order and then to the first
+ *     error that the device finds (PK_ERR_TIMEOUT, PK_ERR_BAD_LABEL). With NULL such errors go to a
+ *     word of the device that pk_last_status of any of its streams reads.
+ *   - T (rows) <= PK_ROWS_MAX_T, other sizes <= PK_ROWS_MAX_DIM. T = 0 is a valid call: gradients of
+ *     weights are set to zero, nothing else is written.
+ *   - Results do not depend on timing: no sum's order does. Nothing is allocated. A call can be
+ *     captured in a graph once one of these operators has run on the device.
+ *   - Outputs overlap no input, except where an entry point says so.
+ */
+#define PK_ROWS_MAX_T 1073741824LL
+#define PK_ROWS_MAX_DIM 1048576
+
+enum pk_act {
+    PK_ACT_NONE = 0,
+    PK_ACT_RELU = 1,
+    PK_ACT_GELU = 2,         /* z Phi(z), Phi the normal distribution function (erf form) */
+    PK_ACT_SILU = 3          /* z / (1 + exp(-z)) */
+};
+
+/*
+ * Projection: y = r + drop(act(x W^T + b)).
+ *   x [T, K] (ldx), w [N, K], bias [N] or NULL, residual [T, N] (ldr) or NULL, y [T, N] (ldy),
+ *   pre [T, N] or NULL: z = x W^T + b, which pk_linear_backward needs when act is not PK_ACT_NONE.
+ *   p, seed, offset: dropout of act(z) before the residual, as pk_dropout (p = 0: none).
+ *   y may be residual itself (ldy = ldr).
+ */
+int pk_linear(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, const void *residual, int64_t ldr,
+              int act, double p, uint64_t seed, uint64_t offset, int64_t T, int N, int K, void *y, int64_t ldy, void *pre,
+              void *workspace, int64_t workspace_bytes, int *status, struct CUstream_st *stream);
+int pk_linear_workspace(int dtype, const void *x, int64_t ldx, const void *w, int64_t T, int N, int K, int64_t *bytes);
+
+/*
+ * Its gradients: dz = act'(pre) drop(dy);  dx = dz W,  dw = dz^T x,  db = column sums of dz (the
+ * residual's gradient is dy). pre: the forward's, in the element type (may be NULL for
+ * PK_ACT_NONE); p, seed, offset as in the forward. dx [T, K], dw [N, K], db [N]: each may be NULL.
+ * dz is rounded to the element type before the products (db sums it unrounded).
+ */
+int pk_linear_backward(int dtype, const void *x, int64_t ldx, const void *w, const void *dy, int64_t lddy, const void *pre,
+                       int act, double p, uint64_t seed, uint64_t offset, int64_t T, int N, int K, void *dx, void *dw,
+                       void *db, void *workspace, int64_t workspace_bytes, int *status, struct CUstream_st *stream);
+int pk_linear_backward_workspace(int dtype, const void *x, int64_t ldx, const void *w, const void *dy, int64_t lddy, int act,
+                                 double p, int need_dx, int need_dw, int need_db, int64_t T, int N, int K, int64_t *bytes);
+
+/*
+ * Dropout: y = r + x keep / (1 - p), 0 <= p < 1 taken to the nearest multiple of 2^-16. keep(t, n)
+ * depends on seed, offset, t and n alone (Philox4x32-10 of Salmon, Moraes, Dror and Shaw, SC 2011:
+ * key seed, counter (n / 8, t, offset), element n the (n mod 8)th 16 bits of the four words, low
+ * half first, kept when they are at least p 65536). The gradient is the same call on dy
+ * with residual NULL. x [T, N] (ldx), residual [T, N] (ldr) or NULL, y [T, N] (ldy); y may be x
+ * (ldy = ldx) or residual (ldy = ldr) itself.
+ */
+int pk_dropout(int dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr, double p, uint64_t seed,
+               uint64_t offset, int64_t T, int N, void *y, int64_t ldy, struct CUstream_st *stream);
+
+/*
+ * Softmax cross entropy of logits z = x W^T + b that are never stored:
+ *   lse[t] = ln sum_v exp z[t, v],  loss[t] = lse[t] - z[t, labels[t]].
+ *   x [T, D] (ldx), w [V, D], bias [V] or NULL, labels [T] int64; loss, lse [T] float32.
+ * A negative label marks a row without one: loss and lse 0, no work. A label >= V: loss NaN, lse 0,
+ * PK_ERR_BAD_LABEL, no gradient.
+ */
+int pk_cross_entropy(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, const int64_t *labels, int64_t T,
+                     int D, int V, float *loss, float *lse, void *workspace, int64_t workspace_bytes, int *status,
+                     struct CUstream_st *stream);
+/*
+ * The gradient of sum_t dloss[t] loss[t] for the forward's lse: dz = dloss (exp(z - lse) - onehot),
+ * dx = dz W [T, D], dw = dz^T x [V, D], db = column sums of dz [V]; each may be NULL. dz is
+ * rounded to the element type before the products and the sums.
+ */
+int pk_cross_entropy_backward(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, const int64_t *labels,
+                              const float *lse, const float *dloss, int64_t T, int D, int V, void *dx, void *dw, void *db,
+                              void *workspace, int64_t workspace_bytes, int *status, struct CUstream_st *stream);
+/* backward: 0 or 1; need_db: whether the backward call has db. */
+int pk_cross_entropy_workspace(int dtype, const void *x, int64_t ldx, const void *w, int backward, int need_db, int64_t T,
+                               int D, int V, int64_t *bytes);
 
 /* Text of a status code (static storage). */
 const char *pk_status_string(int status);

@@ -9,6 +9,11 @@ The entry points mirror include/pk.h:
     pk_attend(qkv, cos, sin, cu, S, T, H, window, scale, out, lse, stream)   (raw pointers)
     schedule(cu, T, window)      -> tile records [NT, 8]
     last_status(stream=None)     -> int
+
+and, on the token rows of the same packed batch:
+    linear(x, w, bias, residual, act, p, seed, offset)          linear_backward(x, w, dy, pre, act, p, seed, offset)
+    dropout(x, p, seed, offset, residual)                       dropout_backward(dy, p, seed, offset)
+    cross_entropy(x, w, labels, bias) -> loss, lse              cross_entropy_backward(x, w, labels, lse, dloss, bias)
 """
 
 from __future__ import annotations
@@ -23,8 +28,9 @@ PK_F32, PK_BF16, PK_F16 = 0, 1, 2
 STATUS = {
     0: "PK_OK", 1: "PK_ERR_ARG", 2: "PK_ERR_ALIGN", 3: "PK_ERR_CUDA", 4: "PK_ERR_UNSUPPORTED",
     5: "PK_ERR_BAD_CU", 6: "PK_ERR_TIMEOUT", 7: "PK_ERR_NOMEM", 8: "PK_ERR_INTERNAL",
-    9: "PK_ERR_TOO_LARGE", 10: "PK_ERR_CAPTURE",
+    9: "PK_ERR_TOO_LARGE", 10: "PK_ERR_CAPTURE", 11: "PK_ERR_BAD_LABEL",
 }
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NOALLOC_MAX_T = 1048576
 
 # names declared in include/pk.h
@@ -32,7 +38,9 @@ EXPORTS = ("pk_attend", "pk_attend_bf16", "pk_attend_f16", "pk_attend_f32", "pk_
            "pk_schedule", "pk_schedule_capacity", "pk_last_status", "pk_status_string",
            "pk_version", "pk_release", "pk_profile_start", "pk_profile_stop", "pk_attend_noalloc", "pk_rope", "pk_attend_mixed",
            "pk_attend_backward", "pk_attend_tuned", "pk_tune_pick", "pk_tune_key", "pk_tune_clear",
-           "pk_forward_kernel", "pk_kernel_name", "pk_attend_mixed_ops")
+           "pk_forward_kernel", "pk_kernel_name", "pk_attend_mixed_ops",
+           "pk_linear", "pk_linear_workspace", "pk_linear_backward", "pk_linear_backward_workspace", "pk_dropout",
+           "pk_cross_entropy", "pk_cross_entropy_backward", "pk_cross_entropy_workspace")
 KERNELS = {0: "band", 1: "f32", 2: "tc", 3: "q4", 4: "tc_single", 5: "split"}
 
 _lib = None
@@ -100,6 +108,20 @@ def load(path: str | None = None):
     dp = ctypes.POINTER(ctypes.c_double)
     L.pk_profile_stop.argtypes = [dp, dp, ctypes.POINTER(i32)]
     L.pk_profile_stop.restype = i32
+    u64, f64, pi64 = ctypes.c_uint64, ctypes.c_double, ctypes.POINTER(i64)
+    tail = [vp, i64, vp, vp]  # workspace, its bytes, status, stream
+    for name, args in {
+        "pk_linear": [i32, vp, i64, vp, vp, vp, i64, i32, f64, u64, u64, i64, i32, i32, vp, i64, vp] + tail,
+        "pk_linear_workspace": [i32, vp, i64, vp, i64, i32, i32, pi64],
+        "pk_linear_backward": [i32, vp, i64, vp, vp, i64, vp, i32, f64, u64, u64, i64, i32, i32, vp, vp, vp] + tail,
+        "pk_linear_backward_workspace": [i32, vp, i64, vp, vp, i64, i32, f64, i32, i32, i32, i64, i32, i32, pi64],
+        "pk_dropout": [i32, vp, i64, vp, i64, f64, u64, u64, i64, i32, vp, i64, vp],
+        "pk_cross_entropy": [i32, vp, i64, vp, vp, vp, i64, i32, i32, vp, vp] + tail,
+        "pk_cross_entropy_backward": [i32, vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp] + tail,
+        "pk_cross_entropy_workspace": [i32, vp, i64, vp, i32, i32, i64, i32, i32, pi64],
+    }.items():
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = i32
     _lib = L
     return L
 
@@ -422,6 +444,283 @@ def _rope(qkv, cos, sin, cu, S, T, H, dims, traditional, inverse, out, status, s
                  status.data_ptr() if status is not None else None, _stream_handle(stream))
     _check(rc, "pk_rope")
     return out
+
+
+# ------------------------------------------------------------------------------------------
+# token-row operators (the projection, dropout, the vocabulary cross entropy)
+
+
+class _OnDevice:
+    """The context of a token-row call: the tensors' device current and, when the caller names a stream, that stream
+    current, so that outputs and workspace are allocated for the stream that uses them (a workspace may then be freed as
+    soon as the call returns: its memory is handed out again in the order of that stream), and the given tensors are
+    held back from reuse until the stream is past them."""
+
+    __slots__ = ("dev", "stream", "entered", "tensors")
+
+    def __init__(self, dev, stream, tensors):
+        self.dev, self.stream, self.entered, self.tensors = dev, stream, (), tensors
+
+    def __enter__(self):
+        torch = _torch()
+        if self.stream is None and torch.cuda.current_device() == self.dev.index:
+            return torch.cuda.current_stream().cuda_stream
+        on = [torch.cuda.device(self.dev)]
+        on[0].__enter__()
+        self.entered = on
+        if self.stream is not None:
+            st = self.stream
+            if not hasattr(st, "cuda_stream"):
+                st = torch.cuda.ExternalStream(int(st), device=self.dev) if int(st) else torch.cuda.default_stream(self.dev)
+            if st != torch.cuda.current_stream():
+                for t in self.tensors:
+                    if t is not None:
+                        t.record_stream(st)
+            on.append(torch.cuda.stream(st))
+            on[1].__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.entered):
+            c.__exit__(*exc)
+        return False
+
+
+def _rows(t, cols, what, dtype=None, dev=None, rows=None):
+    """The row stride of a [T, cols] CUDA matrix whose rows are contiguous (strided rows allowed, none overlapping)."""
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{what} must be [{'T' if rows is None else rows}, {'K' if cols is None else cols}], "
+                         f"not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+    n, (s0, s1) = t.shape[1], t.stride()
+    if n > 1 and s1 != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    if t.shape[0] <= 1:
+        return max(n, 1)
+    if s0 < n:
+        raise ValueError(f"{what} must not have overlapping rows")
+    return s0
+
+
+def _vector(t, n, what, dtype, dev):
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous [{n}] {dtype} CUDA tensor, not {tuple(t.shape)} {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+
+
+def _dense(t, rows, cols, what, dtype, dev):
+    if _rows(t, cols, what, dtype, dev, rows) != max(cols, 1) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _act_code(act):
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, not {act!r}")
+    return ACTS[act]
+
+
+def _drop_check(p, seed, offset):
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"p must be in [0, 1), not {p}")
+    if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
+        raise ValueError("seed and offset must be unsigned 64-bit numbers")
+
+
+def _workspace(name, device, *args):
+    """(tensor or None, its address, its bytes) of the workspace that `name` asks for."""
+    n = ctypes.c_int64(0)
+    _check(getattr(load(), name)(*args, ctypes.byref(n)), name)
+    if n.value == 0:
+        return None, None, 0
+    t = _torch().empty(n.value, dtype=_torch().uint8, device=device)
+    return t, t.data_ptr(), n.value
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _disjoint(out, what, *inputs):
+    """An output that the caller gives must not share memory with what the call reads while it writes it."""
+    a, b = out.data_ptr(), out.data_ptr() + _extent(out)
+    for t in inputs:
+        if t is not None and t.data_ptr() < b and a < t.data_ptr() + _extent(t):
+            raise ValueError(f"{what} overlaps an input")
+
+
+def _extent(t):
+    if t.numel() == 0:
+        return 0
+    return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _same_place(a, b):
+    return b is not None and a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
+
+
+def linear(x, w, bias=None, residual=None, act: str = "none", p: float = 0.0, seed: int = 0, offset: int = 0, out=None,
+           return_pre: bool = False, status=None, stream=None):
+    """y [T, N] = residual + dropout(act(x w^T + bias)) for x [T, K] and w [N, K] (float32, bfloat16 or float16, everything
+    of one type); act "none", "relu", "gelu" or "silu"; dropout of probability p with the bits of (seed, offset), as
+    `dropout`. x, residual and out may have strided rows; out may be residual itself. return_pre: also the
+    pre-activation x w^T + bias [T, N], which linear_backward needs when act is not "none". `status`: optional int32
+    device tensor of one element (otherwise last_status tells of device-detected errors)."""
+    torch = _torch()
+    dt, dev = x.dtype, x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, K = x.shape
+    N = w.shape[0] if w.dim() == 2 else 0
+    _dense(w, N, K, "w", dt, dev)
+    if N < 1 or K < 1:
+        raise ValueError("x and w must have at least one column, w at least one row")
+    if bias is not None:
+        _vector(bias, N, "bias", dt, dev)
+    ldr = _rows(residual, N, "residual", dt, dev, T) if residual is not None else N
+    a = _act_code(act)
+    _drop_check(p, seed, offset)
+    _check_stream(stream, dev)
+    if status is not None:
+        _vector(status, 1, "status", torch.int32, dev)
+    ldy = N
+    if out is not None:
+        ldy = _rows(out, N, "out", dt, dev, T)
+        _disjoint(out, "out", x, w, bias, None if _same_place(out, residual) else residual)
+    with _OnDevice(dev, stream, (x, w, bias, residual, out, status)) as st:
+        if out is None:
+            out = torch.empty((T, N), dtype=dt, device=dev)
+        pre = torch.empty((T, N), dtype=dt, device=dev) if return_pre else None
+        ws, wp, wb = _workspace("pk_linear_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), T, N, K)
+        _check(_lib.pk_linear(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), _ptr(residual), ldr, a, p, seed, offset, T,
+                              N, K, out.data_ptr(), ldy, _ptr(pre), wp, wb, _ptr(status), st), "pk_linear")
+    return (out, pre) if return_pre else out
+
+
+def linear_backward(x, w, dy, pre=None, act: str = "none", p: float = 0.0, seed: int = 0, offset: int = 0,
+                    need_dx: bool = True, need_dw: bool = True, need_db: bool = True, status=None, stream=None):
+    """(dx [T, K], dw [N, K], db [N]) of `linear` for the gradient dy [T, N] of its output, each None where not needed;
+    pre is the forward's pre-activation (not needed for act "none"), act, p, seed and offset the forward's. The gradient
+    of the residual is dy."""
+    torch = _torch()
+    dt, dev = x.dtype, x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, K = x.shape
+    N = w.shape[0] if w.dim() == 2 else 0
+    _dense(w, N, K, "w", dt, dev)
+    if N < 1 or K < 1:
+        raise ValueError("x and w must have at least one column, w at least one row")
+    lddy = _rows(dy, N, "dy", dt, dev, T)
+    a = _act_code(act)
+    if a and pre is None:
+        raise ValueError(f"act {act!r} needs the forward's pre-activation")
+    if pre is not None:
+        _dense(pre, T, N, "pre", dt, dev)
+    _drop_check(p, seed, offset)
+    _check_stream(stream, dev)
+    if status is not None:
+        _vector(status, 1, "status", torch.int32, dev)
+    with _OnDevice(dev, stream, (x, w, dy, pre, status)) as st:
+        dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
+        dw = torch.empty((N, K), dtype=dt, device=dev) if need_dw else None
+        db = torch.empty(N, dtype=dt, device=dev) if need_db else None
+        ws, wp, wb = _workspace("pk_linear_backward_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), dy.data_ptr(), lddy,
+                                a, p, bool(need_dx), bool(need_dw), bool(need_db), T, N, K)
+        _check(_lib.pk_linear_backward(code, x.data_ptr(), ldx, w.data_ptr(), dy.data_ptr(), lddy, _ptr(pre), a, p, seed,
+                                       offset, T, N, K, _ptr(dx), _ptr(dw), _ptr(db), wp, wb, _ptr(status), st),
+               "pk_linear_backward")
+    return dx, dw, db
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, residual=None, out=None, stream=None):
+    """y [T, N] = residual + x keep / (1 - p): each element of x [T, N] kept with probability 1 - p (p to the nearest
+    multiple of 2^-16) by bits that depend on (seed, offset, row, column) alone, so nothing is stored for the backward
+    pass. One (seed, offset) for each use: the same pair draws the same mask. out may be x or residual itself."""
+    torch = _torch()
+    dt, dev = x.dtype, x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, N = x.shape
+    if N < 1:
+        raise ValueError("x must have at least one column")
+    ldr = _rows(residual, N, "residual", dt, dev, T) if residual is not None else N
+    _drop_check(p, seed, offset)
+    _check_stream(stream, dev)
+    ldy = N
+    if out is not None:
+        ldy = _rows(out, N, "out", dt, dev, T)
+        _disjoint(out, "out", None if _same_place(out, x) else x, None if _same_place(out, residual) else residual)
+    with _OnDevice(dev, stream, (x, residual, out)) as st:
+        if out is None:
+            out = torch.empty((T, N), dtype=dt, device=dev)
+        _check(load().pk_dropout(code, x.data_ptr(), ldx, _ptr(residual), ldr, p, seed, offset, T, N, out.data_ptr(), ldy, st),
+               "pk_dropout")
+    return out
+
+
+def dropout_backward(dy, p: float, seed: int, offset: int = 0, out=None, stream=None):
+    """The gradient of `dropout` with respect to x: dy keep / (1 - p), with the forward's p, seed and offset."""
+    return dropout(dy, p, seed, offset, out=out, stream=stream)
+
+
+def _xent_inputs(x, w, labels, bias, status, stream):
+    torch = _torch()
+    dt, dev = x.dtype, x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, D = x.shape
+    V = w.shape[0] if w.dim() == 2 else 0
+    _dense(w, V, D, "w", dt, dev)
+    if V < 1 or D < 1:
+        raise ValueError("x and w must have at least one column, w at least one row")
+    _vector(labels, T, "labels", torch.int64, dev)
+    if bias is not None:
+        _vector(bias, V, "bias", dt, dev)
+    if status is not None:
+        _vector(status, 1, "status", torch.int32, dev)
+    _check_stream(stream, dev)
+    return code, dt, dev, ldx, T, D, V
+
+
+def cross_entropy(x, w, labels, bias=None, status=None, stream=None):
+    """(loss [T], lse [T]), float32: the softmax cross entropy of the logits x w^T + bias, x [T, D], w [V, D], against
+    int64 labels [T], without storing the logits. A negative label leaves its row out (loss 0, no work); a label >= V
+    gives a loss of NaN and PK_ERR_BAD_LABEL (in `status`, an int32 device tensor of one element, or last_status)."""
+    torch = _torch()
+    code, dt, dev, ldx, T, D, V = _xent_inputs(x, w, labels, bias, status, stream)
+    with _OnDevice(dev, stream, (x, w, labels, bias, status)) as st:
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        ws, wp, wb = _workspace("pk_cross_entropy_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), 0, 0, T, D, V)
+        _check(_lib.pk_cross_entropy(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), labels.data_ptr(), T, D, V,
+                                     loss.data_ptr(), lse.data_ptr(), wp, wb, _ptr(status), st), "pk_cross_entropy")
+    return loss, lse
+
+
+def cross_entropy_backward(x, w, labels, lse, dloss, bias=None, need_dx: bool = True, need_dw: bool = True, status=None,
+                           stream=None):
+    """(dx [T, D], dw [V, D], db [V] or None without a bias): the gradient of sum(dloss * loss) of `cross_entropy` for its
+    lse [T]; dloss [T] float32 (1 / count for a mean). Rows without a label get a zero dx."""
+    torch = _torch()
+    code, dt, dev, ldx, T, D, V = _xent_inputs(x, w, labels, bias, status, stream)
+    _vector(lse, T, "lse", torch.float32, dev)
+    _vector(dloss, T, "dloss", torch.float32, dev)
+    with _OnDevice(dev, stream, (x, w, labels, lse, dloss, bias, status)) as st:
+        dx = torch.empty((T, D), dtype=dt, device=dev) if need_dx else None
+        dw = torch.empty((V, D), dtype=dt, device=dev) if need_dw else None
+        db = torch.empty(V, dtype=dt, device=dev) if bias is not None else None
+        ws, wp, wb = _workspace("pk_cross_entropy_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), 1, bias is not None,
+                                T, D, V)
+        _check(_lib.pk_cross_entropy_backward(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), labels.data_ptr(),
+                                              lse.data_ptr(), dloss.data_ptr(), T, D, V, _ptr(dx), _ptr(dw), _ptr(db), wp, wb,
+                                              _ptr(status), st), "pk_cross_entropy_backward")
+    return dx, dw, db
 
 
 def schedule(cu, T: int, window: int, stream=None):

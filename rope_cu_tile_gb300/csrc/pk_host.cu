@@ -161,6 +161,15 @@ int tensor_kernel_choice() {
 
 }  // namespace
 
+unsigned long long wait_limit_ns() {
+  std::lock_guard<std::mutex> lock(g_mu);
+  return timeout_ns();
+}
+
+namespace rows {
+int take_status(int dev);  // the token-row operators' status word of a device (pk_rows.cu)
+}
+
 int select_forward_kernel(int dtype, int window) {
   if (window >= 1 && window <= kBandMaxW) return kKernelBand;
   if (dtype == PK_F32) {
@@ -719,13 +728,14 @@ int pk_last_status(struct CUstream_st* stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PK_ERR_CUDA;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return PK_ERR_CUDA;
+  const int row_st = rows::take_status(dev);
   auto it = g_ws.find(std::make_pair(dev, static_cast<cudaStream_t>(stream)));
-  if (it == g_ws.end() || !it->second.base) return PK_OK;
+  if (it == g_ws.end() || !it->second.base) return row_st;
   int st = 0, zero = 0;
   if (cudaMemcpy(&st, &it->second.ctl->status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess ||
       cudaMemcpy(&it->second.ctl->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
     return PK_ERR_CUDA;
-  return st;
+  return st != PK_OK ? st : row_st;
 }
 
 int pk_profile_start(int n) {
@@ -788,10 +798,11 @@ const char* pk_status_string(int status) {
     case PK_ERR_UNSUPPORTED: return "device is not sm_103 (GB300)";
     case PK_ERR_BAD_CU: return "cu malformed (cu[0] != 0, decreasing, or cu[S] != T), or a position past the tables";
     case PK_ERR_TIMEOUT: return "a device wait exceeded its bound; results invalid";
-    case PK_ERR_NOMEM: return "workspace allocation failed";
+    case PK_ERR_NOMEM: return "workspace allocation failed, or the workspace given is too small";
     case PK_ERR_INTERNAL: return "schedule capacity exceeded (library bug)";
     case PK_ERR_TOO_LARGE: return "T exceeds PK_NOALLOC_MAX_T, the static scratch capacity of pk_attend_noalloc";
     case PK_ERR_CAPTURE: return "stream capture would have to allocate the workspace: make one uncaptured call first";
+    case PK_ERR_BAD_LABEL: return "a label past the vocabulary";
     default: return "unknown status";
   }
 }

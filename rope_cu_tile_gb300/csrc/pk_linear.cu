@@ -1,0 +1,319 @@
+// pk_linear.cu -- the projection of token rows and its gradients (pk_linear, pk_linear_backward in include/pk.h).
+//
+//     z = x W^T + b,   y = r + drop(act(z))          x [T, K], W [N, K], b [N], r and y [T, N]
+//     dz = act'(z) drop(dy),  dx = dz W,  dW = dz^T x,  db = sum over rows of dz,  dr = dy
+//
+// The products run on the tensor cores (pk_gemm.cuh); the forward's bias, activation, dropout and residual are its
+// epilogue, so z and the mask are never stored unless the caller asks for z. The backward makes dz once (pk_dz_kernel: it
+// is an operand of both products, so it has to exist in memory in the operand's type) and sums its columns on the way.
+#include <cstring>
+
+#include "pk_rows.cuh"
+
+namespace pk {
+
+namespace {
+
+using namespace rows;
+
+// ------------------------------------------------------------------------------------
+// dz and its column sums
+
+constexpr int kDzThreads = 256;
+constexpr int kDzRows = 128;  // rows of a block: 16 a thread, then a fixed-order sum over the block's eight row lanes
+
+struct DzArgs {
+  const void* dy;
+  const void* pre;
+  int64_t lddy, ldpre;
+  int64_t T;
+  int N;
+  int act;
+  DropArgs drop;
+  uint16_t* dz;  // [T, ldz] operand (three planes for fp32), or null
+  int64_t ldz, plane;
+  float* part;  // [blocks of rows, ldz] column sums, or null
+  int dy_vec, pre_vec;
+};
+
+// A warp takes 256 columns of a row (8 a lane: one draw of the generator); a block eight rows at a time.
+// Bound by bytes: dy and z read, dz written.
+template <int DT>
+__global__ void __launch_bounds__(kDzThreads) pk_dz_kernel(const __grid_constant__ DzArgs a) {
+  __shared__ float sums[8][256];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.y * 256 + lane * 8;
+  const int n = a.N - c;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kDzRows;
+  griddep_wait();
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (c < a.ldz) {
+    for (int64_t r = r0 + w; r < r0 + kDzRows && r < a.T; r += 8) {
+      float v[8], z[8];
+      if (a.dy_vec && n >= 8)
+        load8<DT>(a.dy, r * a.lddy + c, v);
+      else
+        load8_any<DT>(a.dy, r * a.lddy + c, n, v);
+      if (a.drop.cut) drop8(v, static_cast<uint32_t>(r), c / 8, a.drop);
+      if (a.act != PK_ACT_NONE) {
+        if (a.pre_vec && n >= 8)
+          load8<DT>(a.pre, r * a.ldpre + c, z);
+        else
+          load8_any<DT>(a.pre, r * a.ldpre + c, n, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= act_slope(a.act, z[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= n) v[j] = 0.0f;  // the operand's padding
+        sum[j] += v[j];
+      }
+      if (a.dz) {
+        if constexpr (DT == PK_F32) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              h[j] = Elem<true>::pack(v[2 * j], v[2 * j + 1]);
+              const float2 b = Elem<true>::unpack(h[j]);
+              v[2 * j] -= b.x;
+              v[2 * j + 1] -= b.y;
+            }
+            *reinterpret_cast<uint4*>(a.dz + k * a.plane + r * a.ldz + c) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+          store8<DT>(a.dz, r * a.ldz + c, v);
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[w][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int col = blockIdx.y * 256 + threadIdx.x;
+  if (col < a.ldz) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += sums[i][threadIdx.x];
+    a.part[static_cast<int64_t>(blockIdx.x) * a.ldz + col] = v;
+  }
+}
+
+cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
+  a.dy_vec = rows16(a.dy, a.lddy, elem_bytes(dtype));
+  a.pre_vec = a.pre && rows16(a.pre, a.ldpre, elem_bytes(dtype));
+  Launch l(1, kDzThreads, stream);
+  l.cfg.gridDim = dim3(static_cast<unsigned int>((a.T + kDzRows - 1) / kDzRows), static_cast<unsigned int>((a.ldz + 255) / 256));
+  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F32>, a);
+  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_BF16>, a);
+  return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F16>, a);
+}
+
+// ------------------------------------------------------------------------------------
+// plans: the scratch of a call, laid out the same way when its size is asked for and when it is used
+
+struct Fwd {
+  gemm::Shape shape;
+  void *x, *w;
+  float* partial;
+  int64_t bytes;
+};
+Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T, int N, int K, int sms, void* ws) {
+  Fwd f;
+  Carver c(ws);
+  f.x = in_place(dtype, x, ldx) ? nullptr : c.take(copy_bytes(dtype, T, K));
+  f.w = in_place(dtype, w, K) ? nullptr : c.take(copy_bytes(dtype, N, K));
+  f.shape = gemm::pick_shape(T, N, K, dtype == PK_F32 ? gemm::kTerms32 : 1, sms, true);
+  f.partial = static_cast<float*>(c.take(partial_bytes(f.shape, T, N)));
+  f.bytes = c.used;
+  return f;
+}
+
+struct Bwd {
+  gemm::Shape dx, dw;
+  void *x, *w, *dz;
+  float *part, *partial;
+  int64_t blocks, bytes;
+};
+Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, const void* dy, int64_t lddy, int act,
+                  uint32_t cut, bool need_dx, bool need_dw, bool need_db, int64_t T, int N, int K, int sms, void* ws) {
+  Bwd b = {};
+  Carver c(ws);
+  const int terms = dtype == PK_F32 ? gemm::kTerms32 : 1;
+  if (need_dw && !in_place(dtype, x, ldx)) b.x = c.take(copy_bytes(dtype, T, K));
+  if (need_dx && !in_place(dtype, w, K)) b.w = c.take(copy_bytes(dtype, N, K));
+  // dy itself is the operand when nothing changes it on the way
+  if ((need_dx || need_dw) && (act != PK_ACT_NONE || cut || !in_place(dtype, dy, lddy))) b.dz = c.take(copy_bytes(dtype, T, N));
+  b.blocks = (T + kDzRows - 1) / kDzRows;
+  if (need_db) b.part = static_cast<float*>(c.take(b.blocks * copy_ld(N) * 4));
+  int64_t partial = 0;
+  if (need_dx) {
+    b.dx = gemm::pick_shape(T, K, N, terms, sms, true);
+    partial = partial_bytes(b.dx, T, K);
+  }
+  if (need_dw) {
+    b.dw = gemm::pick_shape(N, K, T, terms, sms, true);
+    const int64_t m = partial_bytes(b.dw, N, K);
+    partial = m > partial ? m : partial;
+  }
+  b.partial = static_cast<float*>(c.take(partial));
+  b.bytes = c.used;
+  return b;
+}
+
+bool sizes_ok(int64_t T, int N, int K) {
+  return T >= 0 && T <= PK_ROWS_MAX_T && N >= 1 && N <= PK_ROWS_MAX_DIM && K >= 1 && K <= PK_ROWS_MAX_DIM;
+}
+bool act_ok(int act) { return act >= PK_ACT_NONE && act <= PK_ACT_SILU; }
+
+}  // namespace
+
+}  // namespace pk
+
+extern "C" {
+
+int pk_linear_workspace(int dtype, const void* x, int64_t ldx, const void* w, int64_t T, int N, int K, int64_t* bytes) {
+  using namespace pk;
+  if (!bytes || !rows::dtype_ok(dtype) || !sizes_ok(T, N, K) || ldx < K) return PK_ERR_ARG;
+  *bytes = 0;
+  if (T == 0) return PK_OK;
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  *bytes = plan_forward(dtype, x, ldx, w, T, N, K, d.sms, nullptr).bytes;
+  return PK_OK;
+}
+
+int pk_linear(int dtype, const void* x, int64_t ldx, const void* w, const void* bias, const void* residual, int64_t ldr,
+              int act, double p, uint64_t seed, uint64_t offset, int64_t T, int N, int K, void* y, int64_t ldy, void* pre,
+              void* workspace, int64_t workspace_bytes, int* status, struct CUstream_st* stream) {
+  using namespace pk;
+  LinParams ep = {};
+  if (!rows::dtype_ok(dtype) || !sizes_ok(T, N, K) || !act_ok(act) || !drop_args(p, seed, offset, &ep.drop)) return PK_ERR_ARG;
+  if (ldx < K || ldy < N || (residual && ldr < N) || workspace_bytes < 0) return PK_ERR_ARG;
+  if (T > 0 && (!x || !w || !y)) return PK_ERR_ARG;
+  const uintptr_t e = rows::elem_bytes(dtype);
+  if (!rows::aligned_to(x, e) || !rows::aligned_to(w, e) || !rows::aligned_to(bias, e) || !rows::aligned_to(residual, e) ||
+      !rows::aligned_to(y, e) || !rows::aligned_to(pre, e) || !rows::aligned_to(workspace, 256) || !rows::aligned_to(status, 4))
+    return PK_ERR_ALIGN;
+  if (T == 0) return status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess ? PK_ERR_CUDA : PK_OK;
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  const Fwd f = plan_forward(dtype, x, ldx, w, T, N, K, d.sms, workspace);
+  if (f.bytes > 0 && (!workspace || workspace_bytes < f.bytes)) return PK_ERR_NOMEM;
+  if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
+  if (f.x && rows::copy_operand(dtype, x, ldx, T, K, f.x, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  if (f.w && rows::copy_operand(dtype, w, K, N, K, f.w, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  ep.bias = bias;
+  ep.res = residual;
+  ep.ldres = ldr;
+  ep.y = y;
+  ep.ldy = ldy;
+  ep.pre = pre;
+  ep.ldpre = N;
+  ep.act = act;
+  gemm::Args a = {};
+  a.M = static_cast<int>(T);
+  a.N = N;
+  a.K = K;
+  a.status = status ? status : d.status;
+  a.timeout_ns = wait_limit_ns();
+  const gemm::Operand A = f.x ? rows::operand_of_copy(dtype, f.x, T, K, 0) : rows::operand(dtype, x, ldx, T, K, 0);
+  const gemm::Operand B = f.w ? rows::operand_of_copy(dtype, f.w, N, K, 0) : rows::operand(dtype, w, K, N, K, 0);
+  return rows::product(dtype, dtype, A, B, nullptr, a, ep, f.shape, f.partial, d.sms, stream) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+int pk_linear_backward_workspace(int dtype, const void* x, int64_t ldx, const void* w, const void* dy, int64_t lddy, int act,
+                                 double p, int need_dx, int need_dw, int need_db, int64_t T, int N, int K, int64_t* bytes) {
+  using namespace pk;
+  DropArgs drop;
+  if (!bytes || !rows::dtype_ok(dtype) || !sizes_ok(T, N, K) || !act_ok(act) || !drop_args(p, 0, 0, &drop) || ldx < K ||
+      lddy < N)
+    return PK_ERR_ARG;
+  *bytes = 0;
+  if (T == 0) return PK_OK;
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  *bytes = plan_backward(dtype, x, ldx, w, dy, lddy, act, drop.cut, need_dx != 0, need_dw != 0, need_db != 0, T, N, K, d.sms,
+                         nullptr)
+               .bytes;
+  return PK_OK;
+}
+
+int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, const void* dy, int64_t lddy, const void* pre,
+                       int act, double p, uint64_t seed, uint64_t offset, int64_t T, int N, int K, void* dx, void* dw,
+                       void* db, void* workspace, int64_t workspace_bytes, int* status, struct CUstream_st* stream) {
+  using namespace pk;
+  DzArgs z = {};
+  if (!rows::dtype_ok(dtype) || !sizes_ok(T, N, K) || !act_ok(act) || !drop_args(p, seed, offset, &z.drop)) return PK_ERR_ARG;
+  if (ldx < K || lddy < N || workspace_bytes < 0) return PK_ERR_ARG;
+  if (T > 0 && (!dy || (dw && !x) || (dx && !w) || (act != PK_ACT_NONE && !pre))) return PK_ERR_ARG;
+  const uintptr_t e = rows::elem_bytes(dtype);
+  if (!rows::aligned_to(x, e) || !rows::aligned_to(w, e) || !rows::aligned_to(dy, e) || !rows::aligned_to(pre, e) ||
+      !rows::aligned_to(dx, e) || !rows::aligned_to(dw, e) || !rows::aligned_to(db, e) || !rows::aligned_to(workspace, 256) ||
+      !rows::aligned_to(status, 4))
+    return PK_ERR_ALIGN;
+  if (T == 0) {
+    // no rows: the gradients of the weights are zero
+    if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (dw && cudaMemsetAsync(dw, 0, e * N * static_cast<size_t>(K), stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (db && cudaMemsetAsync(db, 0, e * N, stream) != cudaSuccess) return PK_ERR_CUDA;
+    return PK_OK;
+  }
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  const Bwd b = plan_backward(dtype, x, ldx, w, dy, lddy, act, z.drop.cut, dx != nullptr, dw != nullptr, db != nullptr, T, N,
+                              K, d.sms, workspace);
+  if (b.bytes > 0 && (!workspace || workspace_bytes < b.bytes)) return PK_ERR_NOMEM;
+  if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
+  if (b.dz || b.part) {
+    z.dy = dy;
+    z.lddy = lddy;
+    z.pre = pre;
+    z.ldpre = N;
+    z.T = T;
+    z.N = N;
+    z.act = act;
+    z.dz = static_cast<uint16_t*>(b.dz);
+    z.ldz = rows::copy_ld(N);
+    z.plane = T * z.ldz;
+    z.part = b.part;
+    if (dz_launch(dtype, z, stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (db && rows::sum_rows(dtype, b.part, b.blocks, N, z.ldz, nullptr, db, stream) != cudaSuccess) return PK_ERR_CUDA;
+  }
+  gemm::Args a = {};
+  a.status = status ? status : d.status;
+  a.timeout_ns = wait_limit_ns();
+  if (dx) {
+    if (b.w && rows::copy_operand(dtype, w, K, N, K, b.w, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+    const gemm::Operand A = b.dz ? rows::operand_of_copy(dtype, b.dz, T, N, 0) : rows::operand(dtype, dy, lddy, T, N, 0);
+    const gemm::Operand B = b.w ? rows::operand_of_copy(dtype, b.w, N, K, 1) : rows::operand(dtype, w, K, N, K, 1);
+    a.M = static_cast<int>(T);
+    a.N = K;
+    a.K = N;
+    LinParams ep = {};
+    ep.y = dx;
+    ep.ldy = K;
+    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dx, b.partial, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  }
+  if (dw) {
+    if (b.x && rows::copy_operand(dtype, x, ldx, T, K, b.x, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+    const gemm::Operand A = b.dz ? rows::operand_of_copy(dtype, b.dz, T, N, 1) : rows::operand(dtype, dy, lddy, T, N, 1);
+    const gemm::Operand B = b.x ? rows::operand_of_copy(dtype, b.x, T, K, 1) : rows::operand(dtype, x, ldx, T, K, 1);
+    a.M = N;
+    a.N = K;
+    a.K = static_cast<int>(T);
+    LinParams ep = {};
+    ep.y = dw;
+    ep.ldy = K;
+    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dw, b.partial, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  }
+  return PK_OK;
+}
+
+}  // extern "C"

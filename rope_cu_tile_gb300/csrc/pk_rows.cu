@@ -1,0 +1,324 @@
+// pk_rows.cu -- shared passes of the token-row operators: tensor maps, the cut of a product into tiles and splits, operand
+// copies, the sum of split partial sums with the epilogue, column sums, and the product's launches.
+#include <atomic>
+#include <mutex>
+
+#include "pk_rows.cuh"
+
+namespace pk {
+
+__device__ int g_rows_status;
+
+namespace gemm {
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+bool make_map(CUtensorMap* map, const Operand& o) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc || !operand_ok(o)) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
+                              static_cast<cuuint64_t>(o.planes)};
+  const cuuint64_t plane = o.planes > 1 ? o.plane : o.rows * o.ld;
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2, plane * 2};
+  const cuuint32_t box[3] = {64, o.mn ? 64u : 128u, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(o.p),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The cheapest cut by a model of the product's time in SM cycles: waves x (k steps x cycles a step + cycles a tile), plus
+// the partial sums' way through memory.
+Shape pick_shape(int64_t M, int64_t N, int64_t K, int terms, int sms, bool may_split) {
+  Shape best;
+  double best_cost = -1.0;
+  const int64_t kbs = (K + kBK - 1) / kBK;
+  for (int cg = 1; cg <= 2; ++cg) {
+    const int64_t tile = 128 * cg, tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
+    const int64_t slots = sms / cg;
+    // cycles a k step: the 256 x 256 pair runs at the tensor pipe's rate, the 128 x 128 tile at its operands' shared-memory reads
+    const double step = cg == 2 ? 280.0 : 270.0, over = cg == 2 ? 1500.0 : 1000.0;
+    for (int s = 1; s <= (may_split ? 32 : 1); ++s) {
+      if (s > 1 && (s > kbs || s * M * N > (int64_t(1) << 28))) break;
+      const int64_t per = (kbs + s - 1) / s, waves = (tiles * s + slots - 1) / slots;
+      if (s > 1 && (kbs + per - 1) / per != s) continue;  // the last splits would be empty
+      double cost = static_cast<double>(waves) * (static_cast<double>(per * terms) * step + over) + 3000.0;
+      if (s > 1) cost += 4000.0 + static_cast<double>(s * M * N) * 8.0 / 2500.0;  // another launch; write and read of L2
+      if (best_cost < 0.0 || cost < best_cost) {
+        best_cost = cost;
+        best.cg = cg;
+        best.splits = s;
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace gemm
+
+namespace rows {
+
+namespace {
+
+using namespace gemm;
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_ready[kMaxDevices];  // 0 unknown, 1 ready, 2 unsupported
+Device g_devices[kMaxDevices];
+std::mutex g_mu;
+
+}  // namespace
+
+cudaError_t prepare_products();
+cudaError_t prepare_xent();
+
+int device(Device* out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PK_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices) return PK_ERR_UNSUPPORTED;
+  int state = g_ready[dev].load(std::memory_order_acquire);
+  if (state == 0) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    state = g_ready[dev].load(std::memory_order_acquire);
+    if (state == 0) {
+      int major = 0, minor = 0, sms = 0;
+      if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+          cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+          cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PK_ERR_CUDA;
+      if (major != 10 || minor != 3) {
+        state = 2;
+      } else {
+        void* word = nullptr;
+        if (cudaGetSymbolAddress(&word, g_rows_status) != cudaSuccess || prepare_products() != cudaSuccess ||
+            prepare_xent() != cudaSuccess) {
+          cudaGetLastError();
+          return PK_ERR_CUDA;
+        }
+        g_devices[dev].sms = sms;
+        g_devices[dev].status = static_cast<int*>(word);
+        state = 1;
+      }
+      g_ready[dev].store(state, std::memory_order_release);
+    }
+  }
+  if (state == 2) return PK_ERR_UNSUPPORTED;
+  *out = g_devices[dev];
+  return PK_OK;
+}
+
+// The device's status word, read and cleared (the caller has synchronized what it asks about).
+int take_status(int dev) {
+  if (dev < 0 || dev >= kMaxDevices || g_ready[dev].load(std::memory_order_acquire) != 1) return PK_OK;
+  int st = 0, zero = 0;
+  if (cudaMemcpy(&st, g_devices[dev].status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) return PK_ERR_CUDA;
+  if (st != 0 && cudaMemcpy(g_devices[dev].status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
+    return PK_ERR_CUDA;
+  return st;
+}
+
+// ------------------------------------------------------------------------------------
+// operand copies
+
+namespace {
+
+// One thread: 8 columns of a row. Bound by bytes: 2 or 4 read and 2 or 6 written an element.
+template <int DT>
+__global__ void __launch_bounds__(256) pack_kernel(const void* __restrict__ src, int64_t ld, int64_t nrows, int cols,
+                                                   uint16_t* __restrict__ dst, int64_t ldp, int64_t plane, int vec,
+                                                   const int* idx, const int* count, int skip) {
+  griddep_wait();
+  int64_t live = nrows, total = nrows;
+  if (count) {
+    const int c = __ldcg(count);
+    if (c == skip) return;
+    live = c;
+    total = min((live + 255) / 256 * 256, (nrows + 255) / 256 * 256);
+  }
+  const int64_t groups = ldp / 8, n = total * groups;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / groups;
+    const int c = static_cast<int>(i - r * groups) * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint4* d = reinterpret_cast<uint4*>(dst + r * ldp + c);
+    if (r < live) {
+      const int64_t s = (idx ? static_cast<int64_t>(__ldcg(idx + r)) : r) * ld + c;
+      if constexpr (DT != PK_F32) {
+        if (vec && c + 8 <= cols) {
+          *d = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + s));
+          continue;
+        }
+      }
+      if (vec && c + 8 <= cols)
+        load8<DT>(src, s, v);
+      else
+        load8_any<DT>(src, s, cols - c, v);
+    }
+    if constexpr (DT == PK_F32) {
+      uint32_t h[3][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 a = make_float2(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          h[k][j] = Elem<true>::pack(a.x, a.y);
+          const float2 b = Elem<true>::unpack(h[k][j]);
+          a.x -= b.x;
+          a.y -= b.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint4*>(dst + k * plane + r * ldp + c) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+    } else {
+      store8<DT>(dst, r * ldp + c, v);
+    }
+  }
+}
+
+}  // namespace
+
+gemm::Operand operand(int dtype, const void* p, int64_t ld, int64_t nrows, int64_t cols, int mn) {
+  gemm::Operand o;
+  o.p = p;
+  o.rows = nrows;
+  o.cols = cols;
+  o.ld = ld;
+  o.plane = nrows * ld;
+  o.bf16 = dtype != PK_F16;
+  o.mn = mn;
+  return o;
+}
+gemm::Operand operand_of_copy(int dtype, const void* copy, int64_t nrows, int64_t cols, int mn) {
+  gemm::Operand o = operand(dtype, copy, copy_ld(cols), nrows, cols, mn);
+  o.planes = dtype == PK_F32 ? 3 : 1;
+  return o;
+}
+
+cudaError_t copy_operand(int dtype, const void* p, int64_t ld, int64_t nrows, int64_t cols, void* copy, const int* idx,
+                         const int* count, int skip, int sms, cudaStream_t stream) {
+  const int64_t ldp = copy_ld(cols), plane = nrows * ldp;
+  const int vec = rows16(p, ld, elem_bytes(dtype));
+  const int64_t n = nrows * (ldp / 8);
+  const int64_t most = static_cast<int64_t>(sms) * 8;
+  Launch l(n / 256 + 1 < most ? n / 256 + 1 : most, 256, stream);
+  uint16_t* d = static_cast<uint16_t*>(copy);
+  const int nc = static_cast<int>(cols);
+  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F32>, p, ld, nrows, nc, d, ldp, plane, vec, idx, count, skip);
+  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_BF16>, p, ld, nrows, nc, d, ldp, plane, vec, idx, count, skip);
+  return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F16>, p, ld, nrows, nc, d, ldp, plane, vec, idx, count, skip);
+}
+
+// ------------------------------------------------------------------------------------
+// split partial sums
+
+namespace {
+
+// y = epilogue(sum over splits of part[s]), the splits added in order: the result does not depend on which finished first.
+template <int ODT, int RDT>
+__global__ void __launch_bounds__(256) splits_kernel(const float* __restrict__ part, int splits, int64_t M, int N,
+                                                     int64_t ldp, const int* live, const __grid_constant__ LinParams p) {
+  griddep_wait();
+  const int64_t groups = ldp / 8, n = (live ? static_cast<int64_t>(__ldcg(live)) : M) * groups;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t r = i / groups;
+    const int c = static_cast<int>(i - r * groups) * 8;
+    float v[8];
+    load8<PK_F32>(part, r * ldp + c, v);
+    for (int s = 1; s < splits; ++s) {
+      float b[8];
+      load8<PK_F32>(part, (s * M + r) * ldp + c, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += b[j];
+    }
+    finish8<ODT, RDT>(p, v, r, c, N - c);
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) sum_rows_kernel(const float* __restrict__ part, int64_t nrows, int cols, int64_t ld,
+                                                       const float* alpha, void* out) {
+  // eight threads a column, each a strided eighth of the rows, joined in a fixed order
+  __shared__ float s[8][33];
+  griddep_wait();
+  const int c = blockIdx.x * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
+  float v = 0.0f;
+  if (c < cols)
+    for (int64_t r = g; r < nrows; r += 8) v += __ldcg(part + r * ld + c);
+  s[g][threadIdx.x % 32] = v;
+  __syncthreads();
+  if (g == 0 && c < cols) {
+    for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
+    Ty<DT>::put(out, c, alpha ? v * __ldcg(alpha) : v);
+  }
+}
+
+}  // namespace
+
+cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, int cols, int64_t ld, const float* alpha, void* out,
+                     cudaStream_t stream) {
+  Launch l((cols + 31) / 32, 256, stream);
+  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, sum_rows_kernel<PK_F32>, part, nrows, cols, ld, alpha, out);
+  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, sum_rows_kernel<PK_BF16>, part, nrows, cols, ld, alpha, out);
+  return cudaLaunchKernelEx(&l.cfg, sum_rows_kernel<PK_F16>, part, nrows, cols, ld, alpha, out);
+}
+
+// ------------------------------------------------------------------------------------
+// products
+
+cudaError_t prepare_products() {
+  cudaError_t e;
+  if ((e = gemm::prepare<LinEpi<PK_F32, PK_F32>>()) != cudaSuccess) return e;
+  if ((e = gemm::prepare<LinEpi<PK_BF16, PK_BF16>>()) != cudaSuccess) return e;
+  if ((e = gemm::prepare<LinEpi<PK_F16, PK_F16>>()) != cudaSuccess) return e;
+  if ((e = gemm::prepare<LinEpi<PK_BF16, PK_F32>>()) != cudaSuccess) return e;
+  return gemm::prepare<LinEpi<PK_F16, PK_F32>>();
+}
+
+cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt,
+                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int sms, cudaStream_t stream) {
+  const int e = elem_bytes(dtype);
+  ep.bias_vec = ep.bias && aligned_to(ep.bias, 16);
+  ep.res_vec = ep.res && rows16(ep.res, ep.ldres, elem_bytes(rdtype));
+  ep.pre_vec = ep.pre && rows16(ep.pre, ep.ldpre, e);
+  ep.y_vec = rows16(ep.y, ep.ldy, e);
+  if (s.splits > 1) {
+    LinParams part = {};
+    part.y = partial;
+    part.ldy = round_up(a.N, 8);
+    part.split_stride = a.M * part.ldy;
+    part.y_vec = 1;
+    cudaError_t r = gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, part, s, sms, stream);
+    if (r != cudaSuccess) return r;
+    const int64_t n = a.M * (part.ldy / 8), most = static_cast<int64_t>(sms) * 8;
+    Launch l(n / 256 + 1 < most ? n / 256 + 1 : most, 256, stream);
+    const float* cp = partial;
+    const int64_t M = a.M;
+    const int* live = a.dyn_axis == 0 ? a.dyn : nullptr;
+    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, cp, s.splits, M, a.N, part.ldy, live, ep); };
+    if (dtype == PK_F32) return run(splits_kernel<PK_F32, PK_F32>);
+    if (dtype == PK_BF16) return run(rdtype == PK_F32 ? splits_kernel<PK_BF16, PK_F32> : splits_kernel<PK_BF16, PK_BF16>);
+    return run(rdtype == PK_F32 ? splits_kernel<PK_F16, PK_F32> : splits_kernel<PK_F16, PK_F16>);
+  }
+  if (dtype == PK_F32) return gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, ep, s, sms, stream);
+  if (dtype == PK_BF16)
+    return rdtype == PK_F32 ? gemm::launch<LinEpi<PK_BF16, PK_F32>>(A, B, alt, a, ep, s, sms, stream)
+                            : gemm::launch<LinEpi<PK_BF16, PK_BF16>>(A, B, alt, a, ep, s, sms, stream);
+  return rdtype == PK_F32 ? gemm::launch<LinEpi<PK_F16, PK_F32>>(A, B, alt, a, ep, s, sms, stream)
+                          : gemm::launch<LinEpi<PK_F16, PK_F16>>(A, B, alt, a, ep, s, sms, stream);
+}
+
+}  // namespace rows
+}  // namespace pk

@@ -1,0 +1,81 @@
+// pk_rows.cuh -- host side shared by the token-row operators (pk_linear.cu, pk_dropout.cu, pk_xent.cu): the device check,
+// the status word, scratch carving, and the passes that lay an operand out for the tensor-core product.
+#pragma once
+
+#include "pk_epilogue.cuh"
+
+namespace pk {
+
+unsigned long long wait_limit_ns();  // pk_host.cu: the bound of a pipeline wait
+
+namespace rows {
+
+struct Device {
+  int sms = 0;
+  int* status = nullptr;  // the device's own status word, read by pk_last_status
+};
+// the current device, checked and set up once (PK_OK or an error code)
+int device(Device* out);
+
+// Carves 256-byte-aligned pieces out of a caller's workspace; with a null base it only adds up the bytes.
+struct Carver {
+  char* base;
+  int64_t used = 0;
+  explicit Carver(void* b) : base(static_cast<char*>(b)) {}
+  void* take(int64_t bytes) {
+    void* p = base ? base + used : nullptr;
+    used += (bytes + 255) & ~int64_t(255);
+    return p;
+  }
+};
+
+inline int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline int elem_bytes(int dtype) { return dtype == PK_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == PK_F32 || dtype == PK_BF16 || dtype == PK_F16; }
+
+// Whether a [rows, cols] matrix can be read by TMA where it lies, and the bytes of the copy that is made otherwise
+// (fp32: three bf16 planes; 16-bit with rows off the 16-byte grid: one padded plane).
+inline bool in_place(int dtype, const void* p, int64_t ld) {
+  return dtype != PK_F32 && aligned_to(p, 16) && (ld & 7) == 0;
+}
+inline int64_t copy_ld(int64_t cols) { return round_up(cols, 8); }
+inline int64_t copy_bytes(int dtype, int64_t rows, int64_t cols) {
+  return (dtype == PK_F32 ? 3 : 1) * rows * copy_ld(cols) * 2;
+}
+// The operand for p: p itself, or its copy at `copy` (filled by a launch on `stream`; rows `idx[0 .. *count)` of p when
+// idx is given, then zeros up to a multiple of 256 rows, nothing when *count == skip).
+gemm::Operand operand(int dtype, const void* p, int64_t ld, int64_t rows, int64_t cols, int mn);
+gemm::Operand operand_of_copy(int dtype, const void* copy, int64_t rows, int64_t cols, int mn);
+cudaError_t copy_operand(int dtype, const void* p, int64_t ld, int64_t rows, int64_t cols, void* copy, const int* idx,
+                         const int* count, int skip, int sms, cudaStream_t stream);
+
+// A product with the linear epilogue (type dtype out, residual of type rdtype), through split partial sums when s.splits
+// > 1 (`partial`: s.splits * M * round_up(N, 8) floats).
+cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt,
+                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int sms, cudaStream_t stream);
+inline int64_t partial_bytes(const gemm::Shape& s, int64_t M, int64_t N) {
+  return s.splits > 1 ? s.splits * M * round_up(N, 8) * 4 : 0;
+}
+
+// db[c] = sum_r part[r][c], rows added in order
+cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, int cols, int64_t ld, const float* alpha, void* out,
+                     cudaStream_t stream);
+
+// launch attributes of a kernel that may start under the previous one's tail
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  Launch(int64_t blocks, int threads, cudaStream_t stream) {
+    cfg.gridDim = dim3(static_cast<unsigned int>(blocks));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+};
+
+}  // namespace rows
+}  // namespace pk
