@@ -450,40 +450,32 @@ def _rope(qkv, cos, sin, cu, S, T, H, dims, traditional, inverse, out, status, s
 # token-row operators (the projection, dropout, the vocabulary cross entropy)
 
 
-class _OnDevice:
-    """The context of a token-row call: the tensors' device current and, when the caller names a stream, that stream
-    current, so that outputs and workspace are allocated for the stream that uses them (a workspace may then be freed as
-    soon as the call returns: its memory is handed out again in the order of that stream), and the given tensors are
-    held back from reuse until the stream is past them."""
+def _on_stream(dev, stream, tensors, call):
+    """call(raw stream) with the tensors' device current and, when the caller names a stream, that stream current, so that
+    outputs and workspace are allocated for the stream that uses them (a workspace may then be freed as soon as the call
+    returns: its memory is handed out again in the order of that stream); the given tensors are held back from reuse until
+    the stream is past them."""
+    torch = _torch()
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            h = int(stream)
+            stream = torch.cuda.ExternalStream(h, device=dev) if h else torch.cuda.default_stream(dev)
+        if stream != torch.cuda.current_stream():
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
-    __slots__ = ("dev", "stream", "entered", "tensors")
 
-    def __init__(self, dev, stream, tensors):
-        self.dev, self.stream, self.entered, self.tensors = dev, stream, (), tensors
-
-    def __enter__(self):
-        torch = _torch()
-        if self.stream is None and torch.cuda.current_device() == self.dev.index:
-            return torch.cuda.current_stream().cuda_stream
-        on = [torch.cuda.device(self.dev)]
-        on[0].__enter__()
-        self.entered = on
-        if self.stream is not None:
-            st = self.stream
-            if not hasattr(st, "cuda_stream"):
-                st = torch.cuda.ExternalStream(int(st), device=self.dev) if int(st) else torch.cuda.default_stream(self.dev)
-            if st != torch.cuda.current_stream():
-                for t in self.tensors:
-                    if t is not None:
-                        t.record_stream(st)
-            on.append(torch.cuda.stream(st))
-            on[1].__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.entered):
-            c.__exit__(*exc)
-        return False
+def _here(dev, stream):
+    """The raw current stream when the call runs on it and on the current device (the usual case), else None."""
+    cuda = _torch().cuda
+    if stream is None and cuda.current_device() == dev.index:
+        return _torch()._C._cuda_getCurrentRawStream(dev.index)
+    return None
 
 
 def _rows(t, cols, what, dtype=None, dev=None, rows=None):
@@ -592,14 +584,17 @@ def linear(x, w, bias=None, residual=None, act: str = "none", p: float = 0.0, se
     if out is not None:
         ldy = _rows(out, N, "out", dt, dev, T)
         _disjoint(out, "out", x, w, bias, None if _same_place(out, residual) else residual)
-    with _OnDevice(dev, stream, (x, w, bias, residual, out, status)) as st:
-        if out is None:
-            out = torch.empty((T, N), dtype=dt, device=dev)
+
+    def call(st):
+        y = torch.empty((T, N), dtype=dt, device=dev) if out is None else out
         pre = torch.empty((T, N), dtype=dt, device=dev) if return_pre else None
         ws, wp, wb = _workspace("pk_linear_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), T, N, K)
         _check(_lib.pk_linear(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), _ptr(residual), ldr, a, p, seed, offset, T,
-                              N, K, out.data_ptr(), ldy, _ptr(pre), wp, wb, _ptr(status), st), "pk_linear")
-    return (out, pre) if return_pre else out
+                              N, K, y.data_ptr(), ldy, _ptr(pre), wp, wb, _ptr(status), st), "pk_linear")
+        return (y, pre) if return_pre else y
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, bias, residual, out, status), call)
 
 
 def linear_backward(x, w, dy, pre=None, act: str = "none", p: float = 0.0, seed: int = 0, offset: int = 0,
@@ -626,7 +621,8 @@ def linear_backward(x, w, dy, pre=None, act: str = "none", p: float = 0.0, seed:
     _check_stream(stream, dev)
     if status is not None:
         _vector(status, 1, "status", torch.int32, dev)
-    with _OnDevice(dev, stream, (x, w, dy, pre, status)) as st:
+
+    def call(st):
         dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
         dw = torch.empty((N, K), dtype=dt, device=dev) if need_dw else None
         db = torch.empty(N, dtype=dt, device=dev) if need_db else None
@@ -635,7 +631,10 @@ def linear_backward(x, w, dy, pre=None, act: str = "none", p: float = 0.0, seed:
         _check(_lib.pk_linear_backward(code, x.data_ptr(), ldx, w.data_ptr(), dy.data_ptr(), lddy, _ptr(pre), a, p, seed,
                                        offset, T, N, K, _ptr(dx), _ptr(dw), _ptr(db), wp, wb, _ptr(status), st),
                "pk_linear_backward")
-    return dx, dw, db
+        return dx, dw, db
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, dy, pre, status), call)
 
 
 def dropout(x, p: float, seed: int, offset: int = 0, residual=None, out=None, stream=None):
@@ -656,12 +655,15 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, out=None, st
     if out is not None:
         ldy = _rows(out, N, "out", dt, dev, T)
         _disjoint(out, "out", None if _same_place(out, x) else x, None if _same_place(out, residual) else residual)
-    with _OnDevice(dev, stream, (x, residual, out)) as st:
-        if out is None:
-            out = torch.empty((T, N), dtype=dt, device=dev)
-        _check(load().pk_dropout(code, x.data_ptr(), ldx, _ptr(residual), ldr, p, seed, offset, T, N, out.data_ptr(), ldy, st),
+
+    def call(st):
+        y = torch.empty((T, N), dtype=dt, device=dev) if out is None else out
+        _check(load().pk_dropout(code, x.data_ptr(), ldx, _ptr(residual), ldr, p, seed, offset, T, N, y.data_ptr(), ldy, st),
                "pk_dropout")
-    return out
+        return y
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, residual, out), call)
 
 
 def dropout_backward(dy, p: float, seed: int, offset: int = 0, out=None, stream=None):
@@ -694,13 +696,17 @@ def cross_entropy(x, w, labels, bias=None, status=None, stream=None):
     gives a loss of NaN and PK_ERR_BAD_LABEL (in `status`, an int32 device tensor of one element, or last_status)."""
     torch = _torch()
     code, dt, dev, ldx, T, D, V = _xent_inputs(x, w, labels, bias, status, stream)
-    with _OnDevice(dev, stream, (x, w, labels, bias, status)) as st:
+
+    def call(st):
         loss = torch.empty(T, dtype=torch.float32, device=dev)
         lse = torch.empty(T, dtype=torch.float32, device=dev)
         ws, wp, wb = _workspace("pk_cross_entropy_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), 0, 0, T, D, V)
         _check(_lib.pk_cross_entropy(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), labels.data_ptr(), T, D, V,
                                      loss.data_ptr(), lse.data_ptr(), wp, wb, _ptr(status), st), "pk_cross_entropy")
-    return loss, lse
+        return loss, lse
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, labels, bias, status), call)
 
 
 def cross_entropy_backward(x, w, labels, lse, dloss, bias=None, need_dx: bool = True, need_dw: bool = True, status=None,
@@ -711,7 +717,8 @@ def cross_entropy_backward(x, w, labels, lse, dloss, bias=None, need_dx: bool = 
     code, dt, dev, ldx, T, D, V = _xent_inputs(x, w, labels, bias, status, stream)
     _vector(lse, T, "lse", torch.float32, dev)
     _vector(dloss, T, "dloss", torch.float32, dev)
-    with _OnDevice(dev, stream, (x, w, labels, lse, dloss, bias, status)) as st:
+
+    def call(st):
         dx = torch.empty((T, D), dtype=dt, device=dev) if need_dx else None
         dw = torch.empty((V, D), dtype=dt, device=dev) if need_dw else None
         db = torch.empty(V, dtype=dt, device=dev) if bias is not None else None
@@ -720,7 +727,10 @@ def cross_entropy_backward(x, w, labels, lse, dloss, bias=None, need_dx: bool = 
         _check(_lib.pk_cross_entropy_backward(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), labels.data_ptr(),
                                               lse.data_ptr(), dloss.data_ptr(), T, D, V, _ptr(dx), _ptr(dw), _ptr(db), wp, wb,
                                               _ptr(status), st), "pk_cross_entropy_backward")
-    return dx, dw, db
+        return dx, dw, db
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, labels, lse, dloss, bias, status), call)
 
 
 def schedule(cu, T: int, window: int, stream=None):

@@ -45,18 +45,19 @@ struct Ty<PK_F16> {
   static __device__ __forceinline__ void put(void* p, int64_t i, float v) { static_cast<__half*>(p)[i] = __float2half_rn(v); }
 };
 
-// Eight consecutive elements at a 16-byte boundary. Through L2 unless L1 is asked for: what a kernel earlier in a chain of
-// overlapping launches wrote must not be taken from a line that this SM read before, and only a bias is read often.
+// Eight consecutive elements at a 16-byte boundary: through L2, or with L1 where they are read often (a bias, a few rows).
+// Never by the read-only path, which asks that nothing wrote them since this kernel started: with overlapping launches an
+// earlier kernel of the chain may have.
 template <int DT, bool L1 = false>
 __device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
   if constexpr (DT == PK_F32) {
     const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = L1 ? __ldg(s) : __ldcg(s);
-    const float4 b = L1 ? __ldg(s + 1) : __ldcg(s + 1);
+    const float4 a = L1 ? *s : __ldcg(s);
+    const float4 b = L1 ? s[1] : __ldcg(s + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
     const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-    const uint4 q = L1 ? __ldg(s) : __ldcg(s);
+    const uint4 q = L1 ? *s : __ldcg(s);
     const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -94,24 +95,95 @@ __device__ __forceinline__ void store8_any(void* p, int64_t i, int n, const floa
 // ------------------------------------------------------------------------------------
 // activations (value, and slope at z)
 
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case PK_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case PK_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752f);
-    case PK_ACT_SILU: return z / (1.0f + __expf(-z));
-    default: return z;
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Phi(-u), u >= 0, of two values, for 16-bit results: 2 to a polynomial of degree 7 fitted (minimax, in the exponent) to
+// log2 Phi(-u) on [0, 6]. Relative error below 2^-17 there, so the negative tail of gelu keeps its digits; past 6 the value
+// only falls (from 1e-9), past 13 it is 0. 3.5 packed multiplications and one exponential an element, where the
+// complementary error function takes some forty instructions.
+__device__ __forceinline__ float2 tail2(float u0, float u1) {
+  const float2 u = make_float2(u0, u1);
+  float2 q = make_float2(-1.835213084e-06f, -1.835213084e-06f);
+  q = fma2(q, u, make_float2(6.160594057e-05f, 6.160594057e-05f));
+  q = fma2(q, u, make_float2(-9.305796120e-04f, -9.305796120e-04f));
+  q = fma2(q, u, make_float2(8.508067578e-03f, 8.508067578e-03f));
+  q = fma2(q, u, make_float2(-5.396029353e-02f, -5.396029353e-02f));
+  q = fma2(q, u, make_float2(-4.584644139e-01f, -4.584644139e-01f));
+  q = fma2(q, u, make_float2(-1.151250839e+00f, -1.151250839e+00f));
+  q = fma2(q, u, make_float2(-9.999952912e-01f, -9.999952912e-01f));
+  return make_float2(attn::ex2(q.x), attn::ex2(q.y));
+}
+
+// act(v) of a row's columns; DT: the type of the result, which says how exact it has to be
+template <int DT, int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+  if (act == PK_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] > 0.0f ? v[i] : (v[i] != v[i] ? v[i] : 0.0f);
+  } else if (act == PK_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      if constexpr (DT == PK_F32) {
+        v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678118654752f);
+        v[i + 1] = 0.5f * v[i + 1] * erfcf(v[i + 1] * -0.70710678118654752f);
+      } else {
+        // z Phi(z) = max(z, 0) - |z| Phi(-|z|), either sign (NaN and -inf through the second term)
+        const float2 e = tail2(fabsf(v[i]), fabsf(v[i + 1]));
+        v[i] = fmaf(-fabsf(v[i]), e.x, fmaxf(v[i], 0.0f));
+        v[i + 1] = fmaf(-fabsf(v[i + 1]), e.y, fmaxf(v[i + 1], 0.0f));
+      }
+    }
+  } else if (act == PK_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (DT == PK_F32)
+        v[i] = v[i] / (1.0f + __expf(-v[i]));
+      else
+        v[i] = v[i] * rcp_fast(1.0f + attn::ex2(v[i] * -1.4426950408889634f));
+    }
   }
 }
-__device__ __forceinline__ float act_slope(int act, float z) {
-  switch (act) {
-    case PK_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    case PK_ACT_GELU:
-      return 0.5f * erfcf(z * -0.70710678118654752f) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
-    case PK_ACT_SILU: {
-      const float h = 1.0f / (1.0f + __expf(-z));
-      return h * (1.0f + z * (1.0f - h));
+
+// d[i] *= act'(z[i])
+template <int DT, int N>
+__device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (&d)[N]) {
+  if (act == PK_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = z[i] > 0.0f ? d[i] : (z[i] != z[i] ? z[i] : 0.0f);
+  } else if (act == PK_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      // Phi(z) + z phi(z) is h or 1 - h with h = Phi(-u) - u phi(u), u = |z|
+      const float u0 = fabsf(z[i]), u1 = fabsf(z[i + 1]);
+      float2 e;
+      if constexpr (DT == PK_F32)
+        e = make_float2(0.5f * erfcf(u0 * 0.70710678118654752f), 0.5f * erfcf(u1 * 0.70710678118654752f));
+      else
+        e = tail2(u0, u1);
+      const float f0 = attn::ex2(u0 * u0 * -0.72134752044448170f), f1 = attn::ex2(u1 * u1 * -0.72134752044448170f);
+      const float h0 = fmaf(u0 * -0.39894228040143268f, f0, e.x), h1 = fmaf(u1 * -0.39894228040143268f, f1, e.y);
+      d[i] *= z[i] > 0.0f ? 1.0f - h0 : h0;
+      d[i + 1] *= z[i + 1] > 0.0f ? 1.0f - h1 : h1;
     }
-    default: return 1.0f;
+  } else if (act == PK_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float h = DT == PK_F32 ? 1.0f / (1.0f + __expf(-z[i])) : rcp_fast(1.0f + attn::ex2(z[i] * -1.4426950408889634f));
+      d[i] *= h * fmaf(z[i], 1.0f - h, 1.0f);
+    }
   }
 }
 
@@ -156,56 +228,45 @@ struct LinEpi {
     return reinterpret_cast<uint4*>(stage + r * 128 + ((u ^ (r & 7)) << 4));
   }
 
-  // 32 accumulator columns of this thread's row, with the bias
-  static __device__ __forceinline__ void take(const Params& p, uint32_t t, bool zero, int c, int N, float (&v)[32]) {
-    if (zero) {
+  // `n` columns (32 or 64) of this thread's row into the staging tile
+  template <int NV>
+  static __device__ __forceinline__ void put(uint8_t* stage, int lane, const float (&v)[NV]) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-    } else {
-      tmem_ld32(t, v);
-    }
-    if (p.bias) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float b[8];
-        bias8<ODT>(p, c + 8 * g, N - c - 8 * g, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * g + i] += b[i];
+    for (int i = 0; i < NV * kE / 16; ++i) {
+      if constexpr (kE == 4) {
+        *slot(stage, lane, i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                           __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+      } else {
+        using E = Elem<ODT == PK_BF16>;
+        *slot(stage, lane, i) = make_uint4(E::pack(v[8 * i], v[8 * i + 1]), E::pack(v[8 * i + 2], v[8 * i + 3]),
+                                           E::pack(v[8 * i + 4], v[8 * i + 5]), E::pack(v[8 * i + 6], v[8 * i + 7]));
       }
     }
   }
-  // 32 columns of this thread's row into the staging tile, units [u0, ..)
-  static __device__ __forceinline__ void put(uint8_t* stage, int lane, int u0, const float (&v)[32]) {
-    if constexpr (kE == 4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *slot(stage, lane, u0 + i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                                __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-    } else {
-      using E = Elem<ODT == PK_BF16>;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *slot(stage, lane, u0 + i) = make_uint4(E::pack(v[8 * i], v[8 * i + 1]), E::pack(v[8 * i + 2], v[8 * i + 3]),
-                                                E::pack(v[8 * i + 4], v[8 * i + 5]), E::pack(v[8 * i + 6], v[8 * i + 7]));
-    }
-  }
-  // the staging tile to rows of `out` (four rows a step, 16 bytes a lane)
+  // The staging tile to rows of `out`: a step takes four rows, 16 bytes a lane; all eight are read before the first is written.
   static __device__ __forceinline__ void flush(uint8_t* stage, int lane, void* out, int64_t ld, int vec, const int* rowmap,
                                                int r0, int c0, int M, int N) {
-    const int u = lane & 7, c = c0 + u * (16 / kE);
+    const int u = lane & 7, c = c0 + u * (16 / kE), r = r0 + (lane >> 3);
+    uint4 q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = *slot(stage, 4 * i + (lane >> 3), u);
+    if (vec && c0 + kChunk <= N && !rowmap) {
+      char* d = static_cast<char*>(out) + (r * ld + c) * kE;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r + 4 * i < M) *reinterpret_cast<uint4*>(d + 4 * i * ld * kE) = q[i];
+      return;
+    }
     const int n = min(N - c, 16 / kE);
-    if (n <= 0) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (r0 + r >= M) break;
-      const uint4 q = *slot(stage, r, u);
-      const int64_t row = rowmap ? __ldcg(rowmap + r0 + r) : r0 + r;
+      if (r + 4 * i >= M || n <= 0) continue;
+      const int64_t row = rowmap ? __ldcg(rowmap + r + 4 * i) : r + 4 * i;
       char* d = static_cast<char*>(out) + (row * ld + c) * kE;
       if (vec && n == 16 / kE) {
-        *reinterpret_cast<uint4*>(d) = q;
+        *reinterpret_cast<uint4*>(d) = q[i];
       } else {
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
         for (int j = 0; j < 16 / kE; ++j)
           if (j < n) {
@@ -217,113 +278,160 @@ struct LinEpi {
       }
     }
   }
-  // rows of the residual (of the output's type) into the staging tile
+  // Rows of the residual (of the output's type) into the staging tile in flush's layout, through asynchronous copies that
+  // take no registers and are waited for where the values are used.
   static __device__ __forceinline__ void fetch(uint8_t* stage, int lane, const void* in, int64_t ld, int vec, int r0, int c0,
                                                int M, int N) {
-    const int u = lane & 7, c = c0 + u * (16 / kE);
+    const int c = c0 + (lane & 7) * (16 / kE), r = r0 + (lane >> 3);
+    if (vec && c0 + kChunk <= N) {
+      const char* s = static_cast<const char*>(in) + (r * ld + c) * kE;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r + 4 * i < M)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, 4 * i + (lane >> 3), lane & 7))),
+                       "l"(s + 4 * i * ld * kE)
+                       : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return;
+    }
     const int n = min(N - c, 16 / kE);
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (r + 4 * i < M) {
+        const char* s = static_cast<const char*>(in) + ((r + 4 * i) * ld + c) * kE;
+#pragma unroll
+        for (int j = 0; j < 16 / kE; ++j)
+          if (j < n) {
+            if constexpr (kE == 4)
+              w[j] = reinterpret_cast<const uint32_t*>(s)[j];
+            else
+              w[j >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(s)[j]) << (16 * (j & 1));
+          }
+      }
+      *slot(stage, 4 * i + (lane >> 3), lane & 7) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // The bias of a chunk's columns, as stored (every lane the same).
+  static __device__ __forceinline__ void fetch_bias(uint4 (&q)[8], const void* bias, int vec, int c, int N) {
+    if (vec && c + kChunk <= N) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(bias) + static_cast<int64_t>(c) * kE);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = s[i];
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      uint4 q = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 + r < M && n > 0) {
-        const char* s = static_cast<const char*>(in) + ((r0 + r) * ld + c) * kE;
-        if (vec && n == 16 / kE) {
-          q = __ldcg(reinterpret_cast<const uint4*>(s));
-        } else {
-          uint32_t w[4] = {0u, 0u, 0u, 0u};
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int j = 0; j < 16 / kE; ++j)
-            if (j < n) {
-              if constexpr (kE == 4)
-                w[j] = reinterpret_cast<const uint32_t*>(s)[j];
-              else
-                w[j >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(s)[j]) << (16 * (j & 1));
-            }
-          q = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int j = 0; j < 16 / kE; ++j) {
+        const int at = c + i * (16 / kE) + j;
+        if (at < N) {
+          if constexpr (kE == 4)
+            w[j] = static_cast<const uint32_t*>(bias)[at];
+          else
+            w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(bias)[at]) << (16 * (j & 1));
         }
       }
-      *slot(stage, r, u) = q;
+      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  // v[.] += the elements of a 16-byte unit
+  static __device__ __forceinline__ void add_unit(const uint4& q, float* v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kE == 4) {
+        v[j] += __uint_as_float(w[j]);
+      } else {
+        const float2 f = Elem<ODT == PK_BF16>::unpack(w[j]);
+        v[2 * j] += f.x;
+        v[2 * j + 1] += f.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ void read_acc(uint32_t t, bool zero, float (&v)[kChunk]) {
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) v[i] = 0.0f;
+    } else if constexpr (kChunk == 64) {
+      tmem_ld64(t, v);
+    } else {
+      tmem_ld32(t, v);
     }
   }
 
-  static __device__ __forceinline__ void run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M,
-                                             int N, int split, int lane, uint8_t* stage) {
-    if (r0 >= M) return;
-    const int row = r0 + lane;
+  // `ready` waits for the accumulators (false: give up), `done` hands them back. What comes from memory (bias, residual) is asked for
+  // before the accumulators are waited for.
+  template <class Ready, class Done>
+  static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
+                                             int split, int lane, uint8_t* stage, const Ready& ready, const Done& done) {
+    if (r0 >= M || c0 >= N) {
+      if (!ready()) return false;
+      done();
+      return true;
+    }
     void* y = static_cast<char*>(p.y) + split * p.split_stride * kE;
     const float alpha = p.alpha ? __ldcg(p.alpha) : 1.0f;
-    for (int cc = 0; cc < cols && c0 + cc < N; cc += kChunk) {
+    const int end = min(cols, N - c0);
+#pragma unroll 1
+    for (int cc = 0; cc < end; cc += kChunk) {
       const int c = c0 + cc;
-      if (p.pre) {
+      float v[kChunk];
+      const bool res_staged = p.res && ODT == RDT;
+      if (res_staged && !p.pre) fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
+      {
+        uint4 bias[8];
+        if (p.bias) fetch_bias(bias, p.bias, p.bias_vec, c, N);
+        if (cc == 0 && !ready()) return false;
+        read_acc(tacc + cc, zero, v);
+        if (cc + kChunk >= end) done();
+        if (p.bias) {
 #pragma unroll
-        for (int h = 0; h < kChunk; h += 32) {
-          float v[32];
-          take(p, tacc + cc + h, zero, c + h, N, v);
-          put(stage, lane, h * kE / 16, v);
+          for (int i = 0; i < 8; ++i) add_unit(bias[i], v + i * (16 / kE));
         }
+      }
+      if (p.pre) {
+        put(stage, lane, v);
         __syncwarp();
         flush(stage, lane, p.pre, p.ldpre, p.pre_vec, nullptr, r0, c, M, N);
         __syncwarp();
+        if (res_staged) fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
       }
-      if (p.res && ODT == RDT) {
-        fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
+      act_values<ODT>(p.act, v);
+      if (p.drop.cut) {
+#pragma unroll
+        for (int g = 0; g < kChunk / 8; ++g) drop8(v + 8 * g, r0 + lane, c / 8 + g, p.drop);
+      }
+      if (res_staged) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) add_unit(*slot(stage, lane, i), v + i * (16 / kE));
+      } else if (p.res && r0 + lane < M) {
+#pragma unroll
+        for (int g = 0; g < kChunk / 8; ++g) {
+          float b[8];
+          const int64_t at = (r0 + lane) * p.ldres + c + 8 * g;
+          const int n = N - c - 8 * g;
+          if (p.res_vec && n >= 8)
+            load8<RDT>(p.res, at, b);
+          else
+            load8_any<RDT>(p.res, at, n, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[8 * g + i] += b[i];
+        }
       }
+      if (p.alpha) {
 #pragma unroll
-      for (int h = 0; h < kChunk; h += 32) {
-        float v[32];
-        take(p, tacc + cc + h, zero, c + h, N, v);
-        if (p.act != PK_ACT_NONE) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = act_value(p.act, v[i]);
-        }
-        if (p.drop.cut) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) drop8(v + 8 * g, row, (c + h) / 8 + g, p.drop);
-        }
-        if (p.res) {
-          if constexpr (ODT == RDT) {
-#pragma unroll
-            for (int i = 0; i < 32 * kE / 16; ++i) {
-              const uint4 q = *slot(stage, lane, h * kE / 16 + i);
-              const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if constexpr (kE == 4) {
-                  v[4 * i + j] += __uint_as_float(w[j]);
-                } else {
-                  const float2 f = Elem<ODT == PK_BF16>::unpack(w[j]);
-                  v[8 * i + 2 * j] += f.x;
-                  v[8 * i + 2 * j + 1] += f.y;
-                }
-              }
-            }
-          } else if (row < M) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float b[8];
-              const int64_t at = row * p.ldres + c + h + 8 * g;
-              const int n = N - c - h - 8 * g;
-              if (p.res_vec && n >= 8)
-                load8<RDT>(p.res, at, b);
-              else
-                load8_any<RDT>(p.res, at, n, b);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[8 * g + i] += b[i];
-            }
-          }
-        }
-        if (p.alpha) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= alpha;
-        }
-        put(stage, lane, h * kE / 16, v);
+        for (int i = 0; i < kChunk; ++i) v[i] *= alpha;
       }
+      put(stage, lane, v);
       __syncwarp();
       flush(stage, lane, y, p.ldy, p.y_vec, p.rowmap, r0, c, M, N);
       __syncwarp();
     }
+    return true;
   }
 };
 
@@ -342,10 +450,7 @@ __device__ __forceinline__ void finish8(const LinParams& p, float (&v)[8], int64
     else
       store8_any<ODT>(p.pre, row * p.ldpre + c, n, v);
   }
-  if (p.act != PK_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = act_value(p.act, v[i]);
-  }
+  act_values<ODT>(p.act, v);
   if (p.drop.cut) drop8(v, static_cast<uint32_t>(row), c / 8, p.drop);
   if (p.res) {
     float b[8];
@@ -366,6 +471,23 @@ __device__ __forceinline__ void finish8(const LinParams& p, float (&v)[8], int64
     store8<ODT>(p.y, row * p.ldy + c, v);
   else
     store8_any<ODT>(p.y, row * p.ldy + c, n, v);
+}
+
+// The same for one element.
+template <int ODT>
+__device__ __forceinline__ void finish1(const LinParams& p, float x, int64_t row, int c) {
+  if (p.bias) x += Ty<ODT>::get(p.bias, c);
+  if (p.pre) Ty<ODT>::put(p.pre, row * p.ldpre + c, x);
+  float v[2] = {x, 0.0f};
+  act_values<ODT>(p.act, v);
+  x = v[0];
+  if (p.drop.cut) {
+    const uint4 r = philox(c >> 3, static_cast<uint32_t>(row), p.drop);
+    const uint32_t w = (c & 4) ? ((c & 2) ? r.w : r.z) : ((c & 2) ? r.y : r.x);
+    x = ((c & 1) ? w >> 16 : w & 0xFFFFu) >= p.drop.cut ? x * p.drop.scale : 0.0f;
+  }
+  if (p.res) x += Ty<ODT>::get(p.res, row * p.ldres + c);
+  Ty<ODT>::put(p.y, row * p.ldy + c, x);
 }
 
 }  // namespace pk

@@ -314,8 +314,10 @@ __device__ __forceinline__ void issue(const Args& a, const Plan& p, uint8_t* sme
   }
 }
 
-// Epi: struct with `static __device__ void run(const Params&, tmem address of the warp's lanes and first column, zero,
-// first row, first column, columns, M, N, split, lane, staging)`.
+// Epi: struct with `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
+// are no accumulators: take zeros), first row, first column, columns, M, N, split, lane, staging, ready, done)`, called by
+// 32 lanes together; it calls ready() before it reads accumulators and done() once after the last of them, and
+// returns false when ready() did.
 template <int CG, class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -373,15 +375,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit t = unit_at<CG>(p, u);
       const bool zero = t.kbs == 0;
       const uint32_t buf = n & 1u;
-      if (!zero) {
+      // (the warp goes on or leaves as one: the accumulator loads are warp-wide)
+      const auto ready = [&]() {
+        if (zero) return true;
         const bool ok = wait(meta, a, &meta->acc_full[buf], (n >> 1) & 1u);
-        if (!__all_sync(0xffffffffu, ok)) break;  // (the warp leaves as one: the loads below are warp-wide)
+        if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
-      }
-      Epi::run(ep, tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + half * kCols, zero,
-               t.m0 + 128 * static_cast<int>(rank) + 32 * quarter, t.n0 + half * kCols, kCols, p.M, p.N, t.split, lane,
-               stage);
-      if (!zero) {
+        return true;
+      };
+      const auto done = [&]() {
+        if (zero) return;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -390,8 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             mbar_arrive(smem_u32(&meta->acc_empty[buf]));
         }
-        ++n;
-      }
+      };
+      if (!Epi::run(ep, tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + half * kCols, zero,
+                    t.m0 + 128 * static_cast<int>(rank) + 32 * quarter, t.n0 + half * kCols, kCols, p.M, p.N, t.split, lane,
+                    stage, ready, done))
+        break;
+      if (!zero) ++n;
     }
   }
   griddep_launch_dependents();

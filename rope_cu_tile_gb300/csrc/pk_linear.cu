@@ -60,8 +60,7 @@ __global__ void __launch_bounds__(kDzThreads) pk_dz_kernel(const __grid_constant
           load8<DT>(a.pre, r * a.ldpre + c, z);
         else
           load8_any<DT>(a.pre, r * a.ldpre + c, n, z);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= act_slope(a.act, z[j]);
+        act_slopes<DT>(a.act, z, v);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -112,6 +111,97 @@ cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------------------------
+// a few rows (serving): y for up to kFewRows rows of x
+
+// Bound by W's bytes, read once; x (at most 16 rows) stays in L1. A warp dots kR rows of W with every row of x, 8 elements a lane
+// and step, in fp32 on the CUDA cores (2 T operations an element of W are below the memory's time up to 16 rows, and fp32
+// inputs need no planes); where N alone gives too few warps, several share the rows and split k. One launch, no scratch.
+constexpr int kFewRows = 16;
+constexpr int kFewThreads = 256;
+
+struct FewArgs {
+  const void* x;
+  const void* w;
+  int64_t ldx;
+  int T, N, K;
+  int share;  // warps that split k: 1, 2, 4 or 8
+  int vec;    // rows of x and W on 16-byte boundaries
+  LinParams ep;
+};
+
+template <int DT, int TM, int R>
+__global__ void __launch_bounds__(kFewThreads) pk_linear_few_kernel(const __grid_constant__ FewArgs a) {
+  __shared__ float part[8][R * TM];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int group = w / a.share, sub = w % a.share, groups = 8 / a.share;
+  const int n0 = (blockIdx.x * groups + group) * R;
+  float acc[R][TM];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < TM; ++t) acc[r][t] = 0.0f;
+  griddep_wait();
+  if (n0 < a.N) {
+#pragma unroll 2
+    for (int k = sub * 256 + lane * 8; k < a.K; k += a.share * 256) {
+      float q[R][8];
+      const bool whole = a.vec && k + 8 <= a.K;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int64_t at = static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.K + k;
+        if (whole)
+          load8<DT>(a.w, at, q[r]);
+        else
+          load8_any<DT>(a.w, at, a.K - k, q[r]);
+      }
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        float x[8];
+        const int64_t at = min(t, a.T - 1) * a.ldx + k;
+        if (whole)
+          load8<DT, true>(a.x, at, x);
+        else
+          load8_any<DT>(a.x, at, a.K - k, x);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(q[r][j], x[j], acc[r][t]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], o);
+      if (lane == 0) part[w][r * TM + t] = acc[r][t];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < groups * R * TM; i += kFewThreads) {
+    const int g = i / (R * TM), e = i % (R * TM), t = e % TM, n = (blockIdx.x * groups + g) * R + e / TM;
+    if (t >= a.T || n >= a.N) continue;
+    float v = 0.0f;
+    for (int s = 0; s < a.share; ++s) v += part[g * a.share + s][e];
+    finish1<DT>(a.ep, v, t, n);
+  }
+}
+
+template <int DT>
+cudaError_t few_launch(FewArgs a, int sms, cudaStream_t stream) {
+  // as many rows of W a warp as amortise the reads of x, halved k until there are some 16 warps an SM
+  const int R = a.T <= 4 ? 2 : 4;
+  a.share = 1;
+  while (a.share < 8 && static_cast<int64_t>(a.N) / R * a.share < 16 * sms && a.K > 256 * a.share) a.share *= 2;
+  const int per_block = 8 / a.share * R;
+  Launch l((a.N + per_block - 1) / per_block, kFewThreads, stream);
+  if (a.T == 1) return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 1, 2>, a);
+  if (a.T <= 4) return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 4, 2>, a);
+  if (a.T <= 8) return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 8, 4>, a);
+  return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 16, 4>, a);
+}
+
+// ------------------------------------------------------------------------------------
 // plans: the scratch of a call, laid out the same way when its size is asked for and when it is used
 
 struct Fwd {
@@ -121,8 +211,9 @@ struct Fwd {
   int64_t bytes;
 };
 Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T, int N, int K, int sms, void* ws) {
-  Fwd f;
+  Fwd f = {};
   Carver c(ws);
+  if (T <= kFewRows) return f;
   f.x = in_place(dtype, x, ldx) ? nullptr : c.take(copy_bytes(dtype, T, K));
   f.w = in_place(dtype, w, K) ? nullptr : c.take(copy_bytes(dtype, N, K));
   f.shape = gemm::pick_shape(T, N, K, dtype == PK_F32 ? gemm::kTerms32 : 1, sms, true);
@@ -205,8 +296,6 @@ int pk_linear(int dtype, const void* x, int64_t ldx, const void* w, const void* 
   const Fwd f = plan_forward(dtype, x, ldx, w, T, N, K, d.sms, workspace);
   if (f.bytes > 0 && (!workspace || workspace_bytes < f.bytes)) return PK_ERR_NOMEM;
   if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
-  if (f.x && rows::copy_operand(dtype, x, ldx, T, K, f.x, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
-  if (f.w && rows::copy_operand(dtype, w, K, N, K, f.w, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   ep.bias = bias;
   ep.res = residual;
   ep.ldres = ldr;
@@ -215,6 +304,15 @@ int pk_linear(int dtype, const void* x, int64_t ldx, const void* w, const void* 
   ep.pre = pre;
   ep.ldpre = N;
   ep.act = act;
+  if (T <= kFewRows) {
+    const FewArgs fa = {x, w, ldx, static_cast<int>(T), N, K, 1, rows16(x, ldx, e) && rows16(w, K, e), ep};
+    const cudaError_t r = dtype == PK_F32    ? few_launch<PK_F32>(fa, d.sms, stream)
+                          : dtype == PK_BF16 ? few_launch<PK_BF16>(fa, d.sms, stream)
+                                             : few_launch<PK_F16>(fa, d.sms, stream);
+    return r == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+  }
+  if (f.x && rows::copy_operand(dtype, x, ldx, T, K, f.x, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  if (f.w && rows::copy_operand(dtype, w, K, N, K, f.w, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   gemm::Args a = {};
   a.M = static_cast<int>(T);
   a.N = N;

@@ -134,8 +134,8 @@ namespace {
 
 // One thread: 8 columns of a row. Bound by bytes: 2 or 4 read and 2 or 6 written an element.
 template <int DT>
-__global__ void __launch_bounds__(256) pack_kernel(const void* __restrict__ src, int64_t ld, int64_t nrows, int cols,
-                                                   uint16_t* __restrict__ dst, int64_t ldp, int64_t plane, int vec,
+__global__ void __launch_bounds__(256) pack_kernel(const void* src, int64_t ld, int64_t nrows, int cols,
+                                                   uint16_t* dst, int64_t ldp, int64_t plane, int vec,
                                                    const int* idx, const int* count, int skip) {
   griddep_wait();
   int64_t live = nrows, total = nrows;
@@ -227,7 +227,7 @@ namespace {
 
 // y = epilogue(sum over splits of part[s]), the splits added in order: the result does not depend on which finished first.
 template <int ODT, int RDT>
-__global__ void __launch_bounds__(256) splits_kernel(const float* __restrict__ part, int splits, int64_t M, int N,
+__global__ void __launch_bounds__(256) splits_kernel(const float* part, int splits, int64_t M, int N,
                                                      int64_t ldp, const int* live, const __grid_constant__ LinParams p) {
   griddep_wait();
   const int64_t groups = ldp / 8, n = (live ? static_cast<int64_t>(__ldcg(live)) : M) * groups;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) splits_kernel(const float* __restrict__ p
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float* __restrict__ part, int64_t nrows, int cols, int64_t ld,
+__global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int64_t nrows, int cols, int64_t ld,
                                                        const float* alpha, void* out) {
   // eight threads a column, each a strided eighth of the rows, joined in a fixed order
   __shared__ float s[8][33];

@@ -51,7 +51,7 @@ struct RowArgs {
 };
 
 __device__ __forceinline__ bool has_label(const RowArgs& a, int64_t t, long long& l) {
-  l = t < a.T ? __ldg(a.labels + t) : -1;
+  l = t < a.T ? __ldcg(a.labels + t) : -1;
   return l >= 0 && l < a.V;
 }
 
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kScan) pk_xent_count_kernel(const __grid_const
   long long l;
   const bool has = has_label(a, t, l);
   const int n = __syncthreads_count(has);
-  float m = has && a.dloss ? fabsf(__ldg(a.dloss + t)) : 0.0f;
+  float m = has && a.dloss ? fabsf(__ldcg(a.dloss + t)) : 0.0f;
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(kScan) pk_xent_index_kernel(const __grid_const
       a.idx[at] = static_cast<int>(t);
       a.lab[at] = static_cast<int>(l);
       if (a.dloss) {
-        a.coef[at] = __ldg(a.dloss + t) * scale;
-        a.lse_rows[at] = __ldg(a.lse_in + t);
+        a.coef[at] = __ldcg(a.dloss + t) * scale;
+        a.lse_rows[at] = __ldcg(a.lse_in + t);
       }
     } else {
       if (l >= a.V && a.status) atomicCAS(a.status, 0, PK_ERR_BAD_LABEL);
@@ -158,71 +158,92 @@ struct StatParams {
   int64_t cap;
 };
 
-// 32 logits of this thread's row: accumulators plus bias
+// v += the bias of 64 columns that was asked for earlier (16-bit: 8 units of 16 bytes; fp32: 16)
 template <int DT>
-__device__ __forceinline__ void logits32(uint32_t t, bool zero, const void* bias, int vec, int c, int N, float (&v)[32]) {
+struct Bias64 {
+  uint4 q[DT == PK_F32 ? 16 : 8];
+  __device__ __forceinline__ void fetch(const void* bias, int vec, int c, int N) {
+    using L = LinEpi<DT, DT>;
+    uint4(&lo)[8] = *reinterpret_cast<uint4(*)[8]>(&q[0]);
+    L::fetch_bias(lo, bias, vec, c, N);
+    if constexpr (DT == PK_F32) {
+      uint4(&hi)[8] = *reinterpret_cast<uint4(*)[8]>(&q[8]);
+      L::fetch_bias(hi, bias, vec, c + 32, N);
+    }
+  }
+  __device__ __forceinline__ void add(float (&v)[64]) const {
+    constexpr int kPer = DT == PK_F32 ? 4 : 8;
+#pragma unroll
+    for (int i = 0; i < 64 / kPer; ++i) LinEpi<DT, DT>::add_unit(q[i], v + kPer * i);
+  }
+};
+
+__device__ __forceinline__ void read64(uint32_t t, bool zero, float (&v)[64]) {
   if (zero) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
   } else {
-    tmem_ld32(t, v);
-  }
-  if (bias) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float b[8];
-      if (vec && N - c - 8 * g >= 8)
-        load8<DT, true>(bias, c + 8 * g, b);
-      else
-        load8_any<DT>(bias, c + 8 * g, N - c - 8 * g, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * g + i] += b[i];
-    }
+    tmem_ld64(t, v);
   }
 }
 
 template <int DT>
 struct StatEpi {
   using Params = StatParams;
-  static __device__ __forceinline__ void run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M,
-                                             int N, int, int lane, uint8_t*) {
-    if (r0 >= M || c0 >= N) return;
+  template <class Ready, class Done>
+  static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
+                                             int, int lane, uint8_t*, const Ready& ready, const Done& done) {
+    if (r0 >= M || c0 >= N) {
+      if (!ready()) return false;
+      done();
+      return true;
+    }
     const int row = r0 + lane;
     const int label = row < M ? __ldcg(p.lab + row) : -1;
+    const int end = min(cols, N - c0);
     float m = kFloor, l = 0.0f;
-    for (int cc = 0; cc < cols && c0 + cc < N; cc += 32) {
+#pragma unroll 1
+    for (int cc = 0; cc < end; cc += 64) {
       const int c = c0 + cc;
-      float v[32];
-      logits32<DT>(tacc + cc, zero, p.bias, p.bias_vec, c, N, v);
-      if (c + 32 > N) {
+      float v[64];
+      {
+        Bias64<DT> b;
+        if (p.bias) b.fetch(p.bias, p.bias_vec, c, N);
+        if (cc == 0 && !ready()) return false;
+        read64(tacc + cc, zero, v);
+        if (cc + 64 >= end) done();
+        if (p.bias) b.add(v);
+      }
+      if (c + 64 > N) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 64; ++i)
           if (c + i >= N) v[i] = -INFINITY;
       }
-      if (label >= c && label < c + 32) {
+      if (label >= c && label < c + 64) {
         float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) z = label == c + i ? v[i] : z;
+        for (int i = 0; i < 64; ++i) z = label == c + i ? v[i] : z;
         p.picked[row] = z;
       }
-      float top = v[0];
+      float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-      for (int i = 1; i < 32; ++i) top = fmaxf(top, v[i]);
-      const float mn = fmaxf(m, top);
-      float s = 0.0f;
+      for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+      const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s += exp2_fast((v[i] - mn) * kLog2e);
-      l = l * exp2_fast((m - mn) * kLog2e) + s;
+      for (int i = 0; i < 64; ++i) s[i & 3] += exp2_fast((v[i] - mn) * kLog2e);
+      l = l * exp2_fast((m - mn) * kLog2e) + ((s[0] + s[1]) + (s[2] + s[3]));
       m = mn;
     }
     if (row < M) p.part[static_cast<int64_t>(c0 / cols) * p.cap + row] = make_float2(m, l);
+    return true;
   }
 };
 
 // Joins the slices of each row, in a fixed order: 32 rows x 8 strided lanes of slices a block.
-__global__ void __launch_bounds__(256) pk_xent_join_kernel(const float2* __restrict__ part, int64_t cap, int slices,
-                                                           const float* __restrict__ picked, const int* __restrict__ idx,
-                                                           const int* __restrict__ count, float* loss, float* lse) {
+__global__ void __launch_bounds__(256) pk_xent_join_kernel(const float2* part, int64_t cap, int slices,
+                                                           const float* picked, const int* idx,
+                                                           const int* count, float* loss, float* lse) {
   __shared__ float2 s[8][32];
   const int r = threadIdx.x & 31, g = threadIdx.x >> 5;
   griddep_wait();
@@ -275,32 +296,39 @@ template <int DT>
 struct GradEpi {
   using Params = GradParams;
   using Lin = LinEpi<DT == PK_F16 ? PK_F16 : PK_BF16, PK_F32>;  // its staging, for 16-bit planes
-  static __device__ __forceinline__ void run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M,
-                                             int N, int, int lane, uint8_t* stage) {
-    if (r0 >= p.cap) return;
+  template <class Ready, class Done>
+  static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
+                                             int, int lane, uint8_t* stage, const Ready& ready, const Done& done) {
+    if (r0 >= p.cap || c0 >= N) {
+      if (!ready()) return false;
+      done();
+      return true;
+    }
     const int row = r0 + lane;
     const bool live = row < M;
     const float g = live ? __ldcg(p.coef + row) : 0.0f, lse = live ? __ldcg(p.lse + row) : 0.0f;
     const int label = live ? __ldcg(p.lab + row) - p.v0 : -1;
-    for (int cc = 0; cc < cols && c0 + cc < N; cc += 64) {
+    const int end = min(cols, N - c0);
+#pragma unroll 1
+    for (int cc = 0; cc < end; cc += 64) {
       const int c = c0 + cc;
       float v[64];
+      {
+        Bias64<DT> b;
+        if (p.bias) b.fetch(p.bias, p.bias_vec, c, N);
+        if (cc == 0 && !ready()) return false;
+        read64(tacc + cc, zero, v);
+        if (cc + 64 >= end) done();
+        if (p.bias) b.add(v);
+      }
 #pragma unroll
-      for (int h = 0; h < 64; h += 32) {
-        float z[32];
-        logits32<DT>(tacc + cc + h, zero, p.bias, p.bias_vec, c + h, N, z);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float e = exp2_fast((z[i] - lse) * kLog2e);
-          v[h + i] = live ? (label == c + h + i ? e - 1.0f : e) * g : 0.0f;  // rows past the count feed dW: zero
-        }
+      for (int i = 0; i < 64; ++i) {
+        const float e = exp2_fast((v[i] - lse) * kLog2e);
+        v[i] = live ? (label == c + i ? e - 1.0f : e) * g : 0.0f;  // rows past the count feed dW: zero
       }
 #pragma unroll
       for (int k = 0; k < (DT == PK_F32 ? 3 : 1); ++k) {
-        float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&v[0]);
-        float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&v[32]);
-        Lin::put(stage, lane, 0, lo);
-        Lin::put(stage, lane, 4, hi);
+        Lin::put(stage, lane, v);
         __syncwarp();
         Lin::flush(stage, lane, p.dz + k * p.plane, p.ld, 1, nullptr, r0, c, static_cast<int>(p.cap), N);
         __syncwarp();
@@ -312,13 +340,14 @@ struct GradEpi {
         }
       }
     }
+    return true;
   }
 };
 
 // Column sums of dz over blocks of rows (db): a warp takes 256 columns of a row, 8 a lane.
 constexpr int kColRows = 128;
 template <int DT>
-__global__ void __launch_bounds__(256) pk_xent_columns_kernel(const uint16_t* __restrict__ dz, int64_t ld, int64_t plane,
+__global__ void __launch_bounds__(256) pk_xent_columns_kernel(const uint16_t* dz, int64_t ld, int64_t plane,
                                                               int cols, const int* count, float* part) {
   __shared__ float sums[8][256];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
