@@ -204,6 +204,30 @@ struct LinParams {
   int bias_vec, res_vec, y_vec, pre_vec;  // 16-byte rows: vector access
 };
 
+// The same for the tensor-core product: outputs whose rows lie on 16-byte boundaries are stored by TMA.
+struct LinTiles : LinParams {
+  CUtensorMap map_y, map_pre;
+  int tma_y, tma_pre;
+};
+
+// A staged tile of 32 rows x 128 bytes (128-byte swizzle) to (x, y, plane) of a map, clipped at its ends. The warp's writes
+// are made visible to the copy; `stage` may be written again after stored().
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const uint8_t* stage, int x, int y, int plane, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(stage)), "r"(x), "r"(y), "r"(plane)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+__device__ __forceinline__ void stored(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+
 inline bool rows16(const void* p, int64_t ld, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ((ld * bytes) & 15) == 0;
 }
@@ -219,7 +243,7 @@ __device__ __forceinline__ void bias8(const LinParams& p, int c, int n, float (&
 
 template <int ODT, int RDT>
 struct LinEpi {
-  using Params = LinParams;
+  using Params = LinTiles;
   static constexpr int kE = Ty<ODT>::kBytes;
   static constexpr int kChunk = 128 / kE;  // columns of one staged row of 128 bytes
 
@@ -379,6 +403,7 @@ struct LinEpi {
       const int c = c0 + cc;
       float v[kChunk];
       const bool res_staged = p.res && ODT == RDT;
+      stored(lane);  // the previous chunk's tile has left the staging memory
       if (res_staged && !p.pre) fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
       {
         uint4 bias[8];
@@ -393,9 +418,14 @@ struct LinEpi {
       }
       if (p.pre) {
         put(stage, lane, v);
-        __syncwarp();
-        flush(stage, lane, p.pre, p.ldpre, p.pre_vec, nullptr, r0, c, M, N);
-        __syncwarp();
+        if (p.tma_pre) {
+          store_tile(&p.map_pre, stage, c, r0, 0, lane);
+          stored(lane);
+        } else {
+          __syncwarp();
+          flush(stage, lane, p.pre, p.ldpre, 0, nullptr, r0, c, M, N);
+          __syncwarp();
+        }
         if (res_staged) fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
       }
       act_values<ODT>(p.act, v);
@@ -427,9 +457,13 @@ struct LinEpi {
         for (int i = 0; i < kChunk; ++i) v[i] *= alpha;
       }
       put(stage, lane, v);
-      __syncwarp();
-      flush(stage, lane, y, p.ldy, p.y_vec, p.rowmap, r0, c, M, N);
-      __syncwarp();
+      if (p.tma_y) {
+        store_tile(&p.map_y, stage, c, r0, split, lane);
+      } else {
+        __syncwarp();
+        flush(stage, lane, y, p.ldy, p.y_vec, p.rowmap, r0, c, M, N);
+        __syncwarp();
+      }
     }
     return true;
   }

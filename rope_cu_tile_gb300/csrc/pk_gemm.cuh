@@ -400,6 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       if (!zero) ++n;
     }
+    // tiles stored by TMA are written before the CTA leaves
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
   griddep_launch_dependents();
   tc_fence_before();
@@ -430,6 +433,9 @@ inline bool operand_ok(const Operand& o) {
   return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && (o.ld & 7) == 0 && (o.plane & 7) == 0;
 }
 bool make_map(CUtensorMap* map, const Operand& o);
+// The map of an output of type dtype (enum pk_dtype) as the epilogue's warps store it: 32 rows x 128 bytes a box.
+bool make_out_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t planes,
+                  int64_t plane);
 
 // How a product of these sizes is cut up.
 struct Shape {

@@ -37,6 +37,22 @@ bool make_map(CUtensorMap* map, const Operand& o) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_out_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t planes,
+                  int64_t plane) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int e = dtype == PK_F32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * e, static_cast<cuuint64_t>(planes > 1 ? plane : rows * ld) * e};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / e), 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType t = dtype == PK_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : dtype == PK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, t, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The cheapest cut by a model of the product's time in SM cycles: waves x (k steps x cycles a step + cycles a tile), plus
 // the partial sums' way through memory.
 Shape pick_shape(int64_t M, int64_t N, int64_t K, int terms, int sms, bool may_split) {
@@ -295,11 +311,13 @@ cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::O
   ep.pre_vec = ep.pre && rows16(ep.pre, ep.ldpre, e);
   ep.y_vec = rows16(ep.y, ep.ldy, e);
   if (s.splits > 1) {
-    LinParams part = {};
+    LinTiles part = {};
     part.y = partial;
     part.ldy = round_up(a.N, 8);
     part.split_stride = a.M * part.ldy;
-    part.y_vec = 1;
+    part.tma_y = 1;
+    if (!gemm::make_out_map(&part.map_y, PK_F32, partial, a.M, a.N, part.ldy, s.splits, part.split_stride))
+      return cudaErrorInvalidValue;
     cudaError_t r = gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, part, s, sms, stream);
     if (r != cudaSuccess) return r;
     const int64_t n = a.M * (part.ldy / 8), most = static_cast<int64_t>(sms) * 8;
@@ -312,12 +330,19 @@ cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::O
     if (dtype == PK_BF16) return run(rdtype == PK_F32 ? splits_kernel<PK_BF16, PK_F32> : splits_kernel<PK_BF16, PK_BF16>);
     return run(rdtype == PK_F32 ? splits_kernel<PK_F16, PK_F32> : splits_kernel<PK_F16, PK_F16>);
   }
-  if (dtype == PK_F32) return gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, ep, s, sms, stream);
+  LinTiles t = {};
+  static_cast<LinParams&>(t) = ep;
+  t.tma_y = ep.y_vec && !ep.rowmap;
+  t.tma_pre = ep.pre_vec;
+  if ((t.tma_y && !gemm::make_out_map(&t.map_y, dtype, ep.y, a.M, a.N, ep.ldy, 1, 0)) ||
+      (t.tma_pre && !gemm::make_out_map(&t.map_pre, dtype, ep.pre, a.M, a.N, ep.ldpre, 1, 0)))
+    return cudaErrorInvalidValue;
+  if (dtype == PK_F32) return gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, t, s, sms, stream);
   if (dtype == PK_BF16)
-    return rdtype == PK_F32 ? gemm::launch<LinEpi<PK_BF16, PK_F32>>(A, B, alt, a, ep, s, sms, stream)
-                            : gemm::launch<LinEpi<PK_BF16, PK_BF16>>(A, B, alt, a, ep, s, sms, stream);
-  return rdtype == PK_F32 ? gemm::launch<LinEpi<PK_F16, PK_F32>>(A, B, alt, a, ep, s, sms, stream)
-                          : gemm::launch<LinEpi<PK_F16, PK_F16>>(A, B, alt, a, ep, s, sms, stream);
+    return rdtype == PK_F32 ? gemm::launch<LinEpi<PK_BF16, PK_F32>>(A, B, alt, a, t, s, sms, stream)
+                            : gemm::launch<LinEpi<PK_BF16, PK_BF16>>(A, B, alt, a, t, s, sms, stream);
+  return rdtype == PK_F32 ? gemm::launch<LinEpi<PK_F16, PK_F32>>(A, B, alt, a, t, s, sms, stream)
+                          : gemm::launch<LinEpi<PK_F16, PK_F16>>(A, B, alt, a, t, s, sms, stream);
 }
 
 }  // namespace rows

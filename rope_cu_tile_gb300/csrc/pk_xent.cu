@@ -288,8 +288,8 @@ struct GradParams {
   const float* coef;
   const float* lse;
   int v0;            // first word of the piece
-  uint16_t* dz;      // [cap, ld], `plane` elements between planes
-  int64_t ld, plane, cap;
+  CUtensorMap dz;    // [planes][cap, columns of the piece]
+  int64_t cap;
 };
 
 template <int DT>
@@ -328,10 +328,9 @@ struct GradEpi {
       }
 #pragma unroll
       for (int k = 0; k < (DT == PK_F32 ? 3 : 1); ++k) {
+        stored(lane);
         Lin::put(stage, lane, v);
-        __syncwarp();
-        Lin::flush(stage, lane, p.dz + k * p.plane, p.ld, 1, nullptr, r0, c, static_cast<int>(p.cap), N);
-        __syncwarp();
+        store_tile(&p.dz, stage, c, r0, k, lane);
         if constexpr (DT == PK_F32) {
           if (k < 2) {
 #pragma unroll
@@ -666,10 +665,10 @@ int pk_cross_entropy_backward(int dtype, const void* x, int64_t ldx, const void*
     gp.coef = b.coef;
     gp.lse = b.lse;
     gp.v0 = v0;
-    gp.dz = b.dz;
-    gp.ld = b.dz_ld;
-    gp.plane = b.dz_plane;
     gp.cap = b.m.cap;
+    if (!gemm::make_out_map(&gp.dz, dtype == PK_F16 ? PK_F16 : PK_BF16, b.dz, b.m.cap, n, b.dz_ld, dtype == PK_F32 ? 3 : 1,
+                            b.dz_plane))
+      return PK_ERR_CUDA;
     if (logits_product<GradEpi>(dtype, in.xc, words(in.w, v0, n, 0), alt, a, gp, b.dz_shape, d.sms, stream) != cudaSuccess)
       return PK_ERR_CUDA;
     gemm::Operand dz = rows::operand(dtype, b.dz, b.dz_ld, b.m.cap, n, 0);
