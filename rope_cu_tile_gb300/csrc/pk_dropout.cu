@@ -2,54 +2,73 @@
 // include/pk.h):  y = r + x keep / (1 - p),  keep drawn from (seed, offset, row, column) by pk_philox.cuh. The mask is
 // never stored: the backward pass draws it again from the same arguments.
 //
-// Bound by bytes (x and r read, y written); a thread draws once for the 8 columns it holds, 20 wide multiplications for
-// 8 elements.
+// Bound by bytes (x and r read, y written). A thread draws once for 8 columns, 20 wide multiplications for 8 elements, and
+// asks for several such groups before it uses the first.
 #include "pk_rows.cuh"
 
 namespace pk {
 
 namespace {
 
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // groups of 8 elements a thread has in flight (one, where that leaves SMs without a block)
+
 struct DropoutArgs {
   const void* x;
   const void* res;
   void* y;
-  int64_t ldx, ldr, ldy, T;
+  int64_t ldx, ldr, ldy;
+  uint32_t row0;  // of this launch
+  uint32_t total; // groups of this launch, below 2^31
   int N;
+  rows::FastDiv groups;
   DropArgs drop;
   int vec, res_vec;
 };
 
-template <int DT>
-__global__ void __launch_bounds__(256) pk_dropout_kernel(const __grid_constant__ DropoutArgs a) {
+template <int DT, int kB>
+__global__ void __launch_bounds__(kThreads) pk_dropout_kernel(const __grid_constant__ DropoutArgs a) {
   griddep_wait();
-  const int64_t groups = (a.N + 7) / 8, total = a.T * groups;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / groups;
-    const int g = static_cast<int>(i - r * groups), c = 8 * g, n = a.N - c;
-    float v[8], b[8];
-    const bool vec = a.vec && n >= 8;
-    if (vec)
-      load8<DT>(a.x, r * a.ldx + c, v);
-    else
-      load8_any<DT>(a.x, r * a.ldx + c, n, v);
-    if (a.res) {
-      if (a.res_vec && n >= 8)
-        load8<DT>(a.res, r * a.ldr + c, b);
-      else
-        load8_any<DT>(a.res, r * a.ldr + c, n, b);
-    }
-    if (a.drop.cut) drop8(v, static_cast<uint32_t>(r), static_cast<uint32_t>(g), a.drop);
-    if (a.res) {
+  const uint32_t i0 = blockIdx.x * (kThreads * kB) + threadIdx.x;
+  Raw8<DT> x[kB], res[kB];
+  uint32_t r[kB], g[kB];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += b[j];
-    }
-    if (vec)
-      store8<DT>(a.y, r * a.ldy + c, v);
-    else
-      store8_any<DT>(a.y, r * a.ldy + c, n, v);
+  for (int b = 0; b < kB; ++b) {
+    const uint32_t i = i0 + b * kThreads;
+    if (i >= a.total) break;
+    r[b] = a.groups.div(i);
+    g[b] = i - r[b] * a.groups.d;
+    r[b] += a.row0;
+    const int c = 8 * static_cast<int>(g[b]);
+    x[b].load(a.x, r[b] * a.ldx + c, a.vec, a.N - c);
+    if (a.res) res[b].load(a.res, r[b] * a.ldr + c, a.res_vec, a.N - c);
   }
+#pragma unroll
+  for (int b = 0; b < kB; ++b) {
+    if (i0 + b * kThreads >= a.total) break;
+    const int c = 8 * static_cast<int>(g[b]), n = a.N - c;
+    float v[8];
+    x[b].get(v);
+    if (a.drop.cut) drop8(v, r[b], g[b], a.drop);
+    if (a.res) {
+      float q[8];
+      res[b].get(q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += q[j];
+    }
+    if (a.vec && n >= 8)
+      store8<DT>(a.y, r[b] * a.ldy + c, v);
+    else
+      store8_any<DT>(a.y, r[b] * a.ldy + c, n, v);
+  }
+}
+
+template <int DT>
+cudaError_t dropout_launch(const DropoutArgs& a, int sms, cudaStream_t stream) {
+  const int batch = a.total >= static_cast<uint32_t>(2 * sms * kThreads * kBatch) ? kBatch : 1;
+  rows::Launch l((a.total + kThreads * batch - 1) / (kThreads * batch), kThreads, stream);
+  return batch == 1 ? cudaLaunchKernelEx(&l.cfg, pk_dropout_kernel<DT, 1>, a)
+                    : cudaLaunchKernelEx(&l.cfg, pk_dropout_kernel<DT, kBatch>, a);
 }
 
 }  // namespace
@@ -75,18 +94,18 @@ extern "C" int pk_dropout(int dtype, const void* x, int64_t ldx, const void* res
   a.ldx = ldx;
   a.ldr = ldr;
   a.ldy = ldy;
-  a.T = T;
   a.N = N;
   a.vec = rows16(x, ldx, e) && rows16(y, ldy, e);
   a.res_vec = residual && rows16(residual, ldr, e);
-  const int64_t total = T * ((N + 7) / 8), most = static_cast<int64_t>(d.sms) * 8;
-  rows::Launch l((total + 255) / 256 < most ? (total + 255) / 256 : most, 256, stream);
-  cudaError_t r;
-  if (dtype == PK_F32)
-    r = cudaLaunchKernelEx(&l.cfg, pk_dropout_kernel<PK_F32>, a);
-  else if (dtype == PK_BF16)
-    r = cudaLaunchKernelEx(&l.cfg, pk_dropout_kernel<PK_BF16>, a);
-  else
-    r = cudaLaunchKernelEx(&l.cfg, pk_dropout_kernel<PK_F16>, a);
-  return r == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+  const int64_t groups = (N + 7) / 8, most = (int64_t(1) << 30) / groups;  // rows of one launch
+  a.groups = rows::FastDiv(static_cast<uint32_t>(groups));
+  for (int64_t r0 = 0; r0 < T; r0 += most) {
+    a.row0 = static_cast<uint32_t>(r0);
+    a.total = static_cast<uint32_t>((T - r0 < most ? T - r0 : most) * groups);
+    const cudaError_t r = dtype == PK_F32    ? dropout_launch<PK_F32>(a, d.sms, stream)
+                          : dtype == PK_BF16 ? dropout_launch<PK_BF16>(a, d.sms, stream)
+                                             : dropout_launch<PK_F16>(a, d.sms, stream);
+    if (r != cudaSuccess) return PK_ERR_CUDA;
+  }
+  return PK_OK;
 }

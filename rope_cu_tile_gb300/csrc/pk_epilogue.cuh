@@ -79,6 +79,45 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) 
         make_uint4(E::pack(v[0], v[1]), E::pack(v[2], v[3]), E::pack(v[4], v[5]), E::pack(v[6], v[7]));
   }
 }
+// Eight elements as loaded, for loads that are asked for well before they are used.
+template <int DT>
+struct Raw8 {
+  uint4 q[DT == PK_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t i, bool vec, int n) {
+    if (vec && n >= 8) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * Ty<DT>::kBytes);
+      q[0] = __ldcg(s);
+      if constexpr (DT == PK_F32) q[1] = __ldcg(s + 1);
+      return;
+    }
+    uint32_t w[DT == PK_F32 ? 8 : 4] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) {
+        if constexpr (DT == PK_F32)
+          w[j] = static_cast<const uint32_t*>(p)[i + j];
+        else
+          w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i + j]) << (16 * (j & 1));
+      }
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (DT == PK_F32) q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+    if constexpr (DT == PK_F32) {
+      const uint32_t u[4] = {q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[j]), v[4 + j] = __uint_as_float(u[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = Elem<DT == PK_BF16>::unpack(w[j]);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+    }
+  }
+};
 // the same for any alignment, the elements at and past `n` left out (loaded as zero)
 template <int DT>
 __device__ __forceinline__ void load8_any(const void* p, int64_t i, int n, float (&v)[8]) {
@@ -196,7 +235,6 @@ struct LinParams {
   void* y;              // [M, N]
   void* pre;            // [M, N] in the output's type: bias added, before the activation; or null
   int64_t ldres, ldy, ldpre;
-  int64_t split_stride; // elements between the outputs of two splits of k (0: one split)
   const float* alpha;   // device factor of the whole, or null
   const int* rowmap;    // row of y (and of the mask) that row m goes to, or null
   int act;
@@ -395,7 +433,6 @@ struct LinEpi {
       done();
       return true;
     }
-    void* y = static_cast<char*>(p.y) + split * p.split_stride * kE;
     const float alpha = p.alpha ? __ldcg(p.alpha) : 1.0f;
     const int end = min(cols, N - c0);
 #pragma unroll 1
@@ -458,10 +495,10 @@ struct LinEpi {
       }
       put(stage, lane, v);
       if (p.tma_y) {
-        store_tile(&p.map_y, stage, c, r0, split, lane);
+        store_tile(&p.map_y, stage, c, r0 + split * gemm::split_rows(M), 0, lane);
       } else {
         __syncwarp();
-        flush(stage, lane, y, p.ldy, p.y_vec, p.rowmap, r0, c, M, N);
+        flush(stage, lane, p.y, p.ldy, p.y_vec, p.rowmap, r0, c, M, N);
         __syncwarp();
       }
     }

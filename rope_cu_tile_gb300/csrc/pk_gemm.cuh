@@ -53,7 +53,9 @@ struct Args {
   int a_mn, b_mn;   // operand layouts (0: K-major, 1: MN-major)
   int bf16;
   int terms;        // 1, or kTerms32
-  int splits;       // splits of k
+  int splits;       // splits of k (with a device count of rows: the most that the device may choose)
+  int part_rows;    // with a device count of rows: rows of the partial sums' memory
+  int slots;        // tiles that run at the same time
   const int* dyn;   // when not null, a device count that replaces M (dyn_axis 0) or K (dyn_axis 1)
   int dyn_axis;
   int alt_count;    // when dyn is not null and *dyn equals this, the alternative map replaces the operand below
@@ -73,6 +75,26 @@ struct Plan {
   int M, N, tiles_m, tiles_n, kb_all, kb_per, units, splits;
 };
 
+// Rows between the partial sums of two splits.
+__device__ __forceinline__ int split_rows(int M) { return (M + 255) & ~255; }
+
+// The splits of k for a count of rows that only the device knows: the fewest waves x steps, the host's model on the device.
+template <int CG>
+__device__ __forceinline__ int choose_splits(const Args& a, int M) {
+  if (!a.dyn || a.dyn_axis != 0 || a.splits == 1) return a.splits;
+  constexpr int kTile = 128 * CG;
+  const int tiles = ((M + kTile - 1) / kTile) * ((a.N + kTile - 1) / kTile), kbs = (a.K + kBK - 1) / kBK;
+  int best = 1, best_cost = 0x7fffffff;
+  for (int s = 1; s <= a.splits && s * split_rows(M) <= a.part_rows; ++s) {
+    const int cost = (tiles * s + a.slots - 1) / a.slots * ((kbs + s - 1) / s * a.terms + 4) + s;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
 template <int CG>
 __device__ __forceinline__ Plan make_plan(const Args& a) {
   Plan p;
@@ -90,9 +112,9 @@ __device__ __forceinline__ Plan make_plan(const Args& a) {
   p.tiles_m = (p.M + kTile - 1) / kTile;
   p.tiles_n = (p.N + kTile - 1) / kTile;
   p.kb_all = (K + kBK - 1) / kBK;
-  p.splits = a.splits;
-  p.kb_per = (p.kb_all + a.splits - 1) / a.splits;
-  p.units = p.tiles_m * p.tiles_n * a.splits;
+  p.splits = choose_splits<CG>(a, p.M);
+  p.kb_per = (p.kb_all + p.splits - 1) / p.splits;
+  p.units = p.tiles_m * p.tiles_n * p.splits;
   return p;
 }
 
@@ -468,6 +490,7 @@ cudaError_t launch(const Operand& A, const Operand& B, const Operand* alt, Args 
   a.bf16 = A.bf16;
   a.terms = A.planes == 3 ? kTerms32 : 1;
   a.splits = s.splits;
+  a.slots = sms / s.cg;
   const int64_t tile = 128 * s.cg;
   const int64_t units = ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile) * s.splits;
   int64_t ctas = units < sms / s.cg ? units : sms / s.cg;

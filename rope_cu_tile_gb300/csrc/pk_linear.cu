@@ -21,6 +21,7 @@ using namespace rows;
 
 constexpr int kDzThreads = 256;
 constexpr int kDzRows = 128;  // rows of a block: 16 a thread, then a fixed-order sum over the block's eight row lanes
+constexpr int kDzBatch = 4;   // rows whose loads are in flight together
 
 struct DzArgs {
   const void* dy;
@@ -48,18 +49,25 @@ __global__ void __launch_bounds__(kDzThreads) pk_dz_kernel(const __grid_constant
   griddep_wait();
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (c < a.ldz) {
-    for (int64_t r = r0 + w; r < r0 + kDzRows && r < a.T; r += 8) {
-      float v[8], z[8];
-      if (a.dy_vec && n >= 8)
-        load8<DT>(a.dy, r * a.lddy + c, v);
-      else
-        load8_any<DT>(a.dy, r * a.lddy + c, n, v);
+#pragma unroll 1
+    for (int64_t rb = r0 + w; rb < r0 + kDzRows && rb < a.T; rb += 8 * kDzBatch) {
+      Raw8<DT> dy[kDzBatch], pre[kDzBatch];
+#pragma unroll
+      for (int i = 0; i < kDzBatch; ++i)
+        if (rb + 8 * i < a.T) {
+          dy[i].load(a.dy, (rb + 8 * i) * a.lddy + c, a.dy_vec, n);
+          if (a.act != PK_ACT_NONE) pre[i].load(a.pre, (rb + 8 * i) * a.ldpre + c, a.pre_vec, n);
+        }
+#pragma unroll
+      for (int i = 0; i < kDzBatch; ++i) {
+      const int64_t r = rb + 8 * i;
+      if (r >= a.T) break;
+      float v[8];
+      dy[i].get(v);
       if (a.drop.cut) drop8(v, static_cast<uint32_t>(r), c / 8, a.drop);
       if (a.act != PK_ACT_NONE) {
-        if (a.pre_vec && n >= 8)
-          load8<DT>(a.pre, r * a.ldpre + c, z);
-        else
-          load8_any<DT>(a.pre, r * a.ldpre + c, n, z);
+        float z[8];
+        pre[i].get(z);
         act_slopes<DT>(a.act, z, v);
       }
 #pragma unroll
@@ -84,6 +92,7 @@ __global__ void __launch_bounds__(kDzThreads) pk_dz_kernel(const __grid_constant
         } else {
           store8<DT>(a.dz, r * a.ldz + c, v);
         }
+      }
       }
     }
   }
@@ -321,7 +330,7 @@ int pk_linear(int dtype, const void* x, int64_t ldx, const void* w, const void* 
   a.timeout_ns = wait_limit_ns();
   const gemm::Operand A = f.x ? rows::operand_of_copy(dtype, f.x, T, K, 0) : rows::operand(dtype, x, ldx, T, K, 0);
   const gemm::Operand B = f.w ? rows::operand_of_copy(dtype, f.w, N, K, 0) : rows::operand(dtype, w, K, N, K, 0);
-  return rows::product(dtype, dtype, A, B, nullptr, a, ep, f.shape, f.partial, d.sms, stream) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+  return rows::product(dtype, dtype, A, B, nullptr, a, ep, f.shape, f.partial, rows::partial_rows(f.shape, T), d.sms, stream) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
 int pk_linear_backward_workspace(int dtype, const void* x, int64_t ldx, const void* w, const void* dy, int64_t lddy, int act,
@@ -397,7 +406,7 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     LinParams ep = {};
     ep.y = dx;
     ep.ldy = K;
-    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dx, b.partial, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dx, b.partial, rows::partial_rows(b.dx, T), d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
   if (dw) {
     if (b.x && rows::copy_operand(dtype, x, ldx, T, K, b.x, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
@@ -409,7 +418,7 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     LinParams ep = {};
     ep.y = dw;
     ep.ldy = K;
-    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dw, b.partial, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dw, b.partial, rows::partial_rows(b.dw, N), d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
   return PK_OK;
 }

@@ -35,14 +35,15 @@ __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, const DropArgs
   return make_uint4(x, y, z, w);
 }
 
-// v[0 .. 7] (columns 8 group ..) with the dropped ones zero and the kept ones scaled.
+// v[0 .. 7] (columns 8 group ..) with the dropped ones zero and the kept ones scaled. (A high half is at least `cut` exactly
+// when its word is at least cut 2^16, so half of the comparisons need no extraction.)
 __device__ __forceinline__ void drop8(float* v, uint32_t row, uint32_t group, const DropArgs& d) {
   const uint4 r = philox(group, row, d);
-  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w}, cut = d.cut << 16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = (u[i] & 0xFFFFu) >= d.cut ? v[2 * i] * d.scale : 0.0f;
-    v[2 * i + 1] = (u[i] >> 16) >= d.cut ? v[2 * i + 1] * d.scale : 0.0f;
+    v[2 * i] = (u[i] << 16) >= cut ? v[2 * i] * d.scale : 0.0f;
+    v[2 * i + 1] = u[i] >= cut ? v[2 * i + 1] * d.scale : 0.0f;
   }
 }
 

@@ -151,7 +151,7 @@ namespace {
 // One thread: 8 columns of a row. Bound by bytes: 2 or 4 read and 2 or 6 written an element.
 template <int DT>
 __global__ void __launch_bounds__(256) pack_kernel(const void* src, int64_t ld, int64_t nrows, int cols,
-                                                   uint16_t* dst, int64_t ldp, int64_t plane, int vec,
+                                                   uint16_t* dst, int64_t ldp, int64_t plane, int vec, FastDiv div,
                                                    const int* idx, const int* count, int skip) {
   griddep_wait();
   int64_t live = nrows, total = nrows;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const void* src, int64_t ld, 
   const int64_t groups = ldp / 8, n = total * groups;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / groups;
+    const int64_t r = n < (int64_t(1) << 31) ? div.div(static_cast<uint32_t>(i)) : i / groups;
     const int c = static_cast<int>(i - r * groups) * 8;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     uint4* d = reinterpret_cast<uint4*>(dst + r * ldp + c);
@@ -231,9 +231,10 @@ cudaError_t copy_operand(int dtype, const void* p, int64_t ld, int64_t nrows, in
   Launch l(n / 256 + 1 < most ? n / 256 + 1 : most, 256, stream);
   uint16_t* d = static_cast<uint16_t*>(copy);
   const int nc = static_cast<int>(cols);
-  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F32>, p, ld, nrows, nc, d, ldp, plane, vec, idx, count, skip);
-  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_BF16>, p, ld, nrows, nc, d, ldp, plane, vec, idx, count, skip);
-  return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F16>, p, ld, nrows, nc, d, ldp, plane, vec, idx, count, skip);
+  const FastDiv div(static_cast<uint32_t>(ldp / 8));
+  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F32>, p, ld, nrows, nc, d, ldp, plane, vec, div, idx, count, skip);
+  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_BF16>, p, ld, nrows, nc, d, ldp, plane, vec, div, idx, count, skip);
+  return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F16>, p, ld, nrows, nc, d, ldp, plane, vec, div, idx, count, skip);
 }
 
 // ------------------------------------------------------------------------------------
@@ -243,23 +244,27 @@ namespace {
 
 // y = epilogue(sum over splits of part[s]), the splits added in order: the result does not depend on which finished first.
 template <int ODT, int RDT>
-__global__ void __launch_bounds__(256) splits_kernel(const float* part, int splits, int64_t M, int N,
-                                                     int64_t ldp, const int* live, const __grid_constant__ LinParams p) {
+__global__ void __launch_bounds__(256) splits_kernel(const float* part, int cg, int64_t ldp, FastDiv groups,
+                                                     const __grid_constant__ gemm::Args a, const __grid_constant__ LinParams p) {
   griddep_wait();
-  const int64_t groups = ldp / 8, n = (live ? static_cast<int64_t>(__ldcg(live)) : M) * groups;
+  const int M = a.dyn && a.dyn_axis == 0 ? __ldcg(a.dyn) : a.M;
+  const int splits = cg == 2 ? gemm::choose_splits<2>(a, M) : gemm::choose_splits<1>(a, M);
+  const int64_t stride = gemm::split_rows(M) * ldp, n = M * static_cast<int64_t>(groups.d);
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / groups;
-    const int c = static_cast<int>(i - r * groups) * 8;
+    const int64_t r = n < (int64_t(1) << 31) ? groups.div(static_cast<uint32_t>(i)) : i / groups.d;
+    const int c = static_cast<int>(i - r * groups.d) * 8;
+    const float* at = part + r * ldp + c;
     float v[8];
-    load8<PK_F32>(part, r * ldp + c, v);
+    load8<PK_F32>(at, 0, v);
+#pragma unroll 4
     for (int s = 1; s < splits; ++s) {
       float b[8];
-      load8<PK_F32>(part, (s * M + r) * ldp + c, b);
+      load8<PK_F32>(at, s * stride, b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += b[j];
     }
-    finish8<ODT, RDT>(p, v, r, c, N - c);
+    finish8<ODT, RDT>(p, v, r, c, a.N - c);
   }
 }
 
@@ -304,7 +309,7 @@ cudaError_t prepare_products() {
 }
 
 cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt,
-                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int sms, cudaStream_t stream) {
+                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int64_t part_rows, int sms, cudaStream_t stream) {
   const int e = elem_bytes(dtype);
   ep.bias_vec = ep.bias && aligned_to(ep.bias, 16);
   ep.res_vec = ep.res && rows16(ep.res, ep.ldres, elem_bytes(rdtype));
@@ -314,18 +319,19 @@ cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::O
     LinTiles part = {};
     part.y = partial;
     part.ldy = round_up(a.N, 8);
-    part.split_stride = a.M * part.ldy;
     part.tma_y = 1;
-    if (!gemm::make_out_map(&part.map_y, PK_F32, partial, a.M, a.N, part.ldy, s.splits, part.split_stride))
-      return cudaErrorInvalidValue;
+    a.part_rows = static_cast<int>(part_rows);
+    if (!gemm::make_out_map(&part.map_y, PK_F32, partial, part_rows, a.N, part.ldy, 1, 0)) return cudaErrorInvalidValue;
     cudaError_t r = gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, part, s, sms, stream);
     if (r != cudaSuccess) return r;
+    a.terms = A.planes == 3 ? gemm::kTerms32 : 1;  // what the launch above told the product
+    a.splits = s.splits;
+    a.slots = sms / s.cg;
     const int64_t n = a.M * (part.ldy / 8), most = static_cast<int64_t>(sms) * 8;
     Launch l(n / 256 + 1 < most ? n / 256 + 1 : most, 256, stream);
     const float* cp = partial;
-    const int64_t M = a.M;
-    const int* live = a.dyn_axis == 0 ? a.dyn : nullptr;
-    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, cp, s.splits, M, a.N, part.ldy, live, ep); };
+    const FastDiv groups(static_cast<uint32_t>(part.ldy / 8));
+    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, cp, s.cg, part.ldy, groups, a, ep); };
     if (dtype == PK_F32) return run(splits_kernel<PK_F32, PK_F32>);
     if (dtype == PK_BF16) return run(rdtype == PK_F32 ? splits_kernel<PK_BF16, PK_F32> : splits_kernel<PK_BF16, PK_BF16>);
     return run(rdtype == PK_F32 ? splits_kernel<PK_F16, PK_F32> : splits_kernel<PK_F16, PK_F16>);

@@ -51,16 +51,29 @@ cudaError_t copy_operand(int dtype, const void* p, int64_t ld, int64_t rows, int
                          const int* count, int skip, int sms, cudaStream_t stream);
 
 // A product with the linear epilogue (type dtype out, residual of type rdtype), through split partial sums when s.splits
-// > 1 (`partial`: s.splits * M * round_up(N, 8) floats).
+// > 1 (`partial`: `part_rows` rows of round_up(N, 8) floats, part_rows >= splits x round_up(M, 256); with a device count of
+// rows the device takes as many splits, up to s.splits, as are worth it and have room).
 cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt,
-                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int sms, cudaStream_t stream);
-inline int64_t partial_bytes(const gemm::Shape& s, int64_t M, int64_t N) {
-  return s.splits > 1 ? s.splits * M * round_up(N, 8) * 4 : 0;
-}
+                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int64_t part_rows, int sms, cudaStream_t stream);
+inline int64_t partial_rows(const gemm::Shape& s, int64_t M) { return s.splits > 1 ? s.splits * round_up(M, 256) : 0; }
+inline int64_t partial_bytes(const gemm::Shape& s, int64_t M, int64_t N) { return partial_rows(s, M) * round_up(N, 8) * 4; }
 
 // db[c] = sum_r part[r][c], rows added in order
 cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, int cols, int64_t ld, const float* alpha, void* out,
                      cudaStream_t stream);
+
+// n / d and n % d for n < 2^31 by a multiplication (d >= 1): with s = ceil(log2 d) and m = ceil(2^(31 + s) / d), m fits 32
+// bits and m n / 2^(31 + s) exceeds n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t d, m, s;
+  explicit FastDiv(uint32_t divisor = 1) : d(divisor), m(0), s(0) {
+    while ((uint64_t(1) << s) < d) ++s;
+    m = static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> (31 + s));
+  }
+};
 
 // launch attributes of a kernel that may start under the previous one's tail
 struct Launch {

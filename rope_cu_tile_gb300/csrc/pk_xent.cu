@@ -430,7 +430,7 @@ struct Bwd {
   gemm::Shape dz_shape, dx_shape, dw_shape;
   float *coef, *lse, *unscale, *acc, *part, *partial;
   uint16_t* dz;
-  int64_t dz_ld, dz_plane, blocks, bytes;
+  int64_t dz_ld, dz_plane, dx_rows, blocks, bytes;
 };
 Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, bool need_db, int64_t T, int D, int V, int sms,
                   void* ws) {
@@ -454,9 +454,17 @@ Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, bool nee
   b.blocks = (T + kColRows - 1) / kColRows;
   if (need_db) b.part = static_cast<float*>(c.take(b.blocks * b.dz_ld * 4));
   b.dz_shape = gemm::pick_shape(T, widest, D, terms, sms, false);
-  b.dx_shape = gemm::pick_shape(T, D, widest, terms, sms, true);
+  // how many rows dx has is the device's to know: where even all of them would fill the SMs only a few times over, it may
+  // split k as far as the memory of the partial sums goes
+  b.dx_shape = gemm::pick_shape(T, D, widest, terms, sms, false);
+  const int64_t tile = 128 * b.dx_shape.cg, tiles = ((T + tile - 1) / tile) * ((D + tile - 1) / tile);
+  b.dx_rows = 0;
+  if (tiles < 8 * (sms / b.dx_shape.cg) && widest > 512) {
+    b.dx_shape.splits = 8;
+    b.dx_rows = round_up(T, 256) * 2 > 8 * 2048 ? round_up(T, 256) * 2 : 8 * round_up(T < 2048 ? T : 2048, 256);
+  }
   b.dw_shape = gemm::pick_shape(widest, D, T, terms, sms, true);
-  const int64_t p1 = partial_bytes(b.dx_shape, T, D), p2 = partial_bytes(b.dw_shape, widest, D);
+  const int64_t p1 = b.dx_rows * round_up(D, 8) * 4, p2 = partial_bytes(b.dw_shape, widest, D);
   b.partial = static_cast<float*>(c.take(p1 > p2 ? p1 : p2));
   b.bytes = c.used;
   return b;
@@ -687,7 +695,8 @@ int pk_cross_entropy_backward(int dtype, const void* x, int64_t ldx, const void*
       ep.y = static_cast<char*>(dw) + static_cast<int64_t>(v0) * D * e;
       ep.ldy = D;
       ep.alpha = alpha;
-      if (rows::product(dtype, dtype, dz, xb, in.alt ? &xa : nullptr, a, ep, b.dw_shape, b.partial, d.sms, stream) != cudaSuccess)
+      if (rows::product(dtype, dtype, dz, xb, in.alt ? &xa : nullptr, a, ep, b.dw_shape, b.partial,
+                        rows::partial_rows(b.dw_shape, n), d.sms, stream) != cudaSuccess)
         return PK_ERR_CUDA;
     }
     if (dx) {
@@ -704,8 +713,8 @@ int pk_cross_entropy_backward(int dtype, const void* x, int64_t ldx, const void*
       ep.ldy = D;
       ep.alpha = last ? alpha : nullptr;
       ep.rowmap = last ? b.m.idx : nullptr;
-      if (rows::product(last ? dtype : PK_F32, PK_F32, dz, words(in.w, v0, n, 1), nullptr, a, ep, b.dx_shape, b.partial, d.sms,
-                        stream) != cudaSuccess)
+      if (rows::product(last ? dtype : PK_F32, PK_F32, dz, words(in.w, v0, n, 1), nullptr, a, ep, b.dx_shape, b.partial, b.dx_rows,
+                        d.sms, stream) != cudaSuccess)
         return PK_ERR_CUDA;
     }
     if (db) {
