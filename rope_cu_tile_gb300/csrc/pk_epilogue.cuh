@@ -248,7 +248,7 @@ struct LinTiles : LinParams {
   int tma_y, tma_pre;
 };
 
-// A staged tile of 32 rows x 128 bytes (128-byte swizzle) to (x, y, plane) of a map, clipped at its ends. The warp's writes
+// A staged tile of 32 rows x 32 columns (64- or 128-byte rows, swizzled) to (x, y, plane) of a map, clipped at its ends. The warp's writes
 // are made visible to the copy; `stage` may be written again after stored().
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, const uint8_t* stage, int x, int y, int plane, int lane) {
   fence_proxy_async_smem();
@@ -279,117 +279,138 @@ __device__ __forceinline__ void bias8(const LinParams& p, int c, int n, float (&
     load8_any<DT>(p.bias, c, n, b);
 }
 
-template <int ODT, int RDT>
-struct LinEpi {
-  using Params = LinTiles;
-  static constexpr int kE = Ty<ODT>::kBytes;
-  static constexpr int kChunk = 128 / kE;  // columns of one staged row of 128 bytes
-
-  // staging: 16-byte unit u of row r sits at unit u ^ (r & 7) of its 128-byte row
-  static __device__ __forceinline__ uint4* slot(uint8_t* stage, int r, int u) {
-    return reinterpret_cast<uint4*>(stage + r * 128 + ((u ^ (r & 7)) << 4));
+// Staging of a warp's 32 rows x 32 columns of type DT: rows of 64 or 128 bytes in the swizzle that TMA reads (16-byte unit u
+// of row r at unit u ^ (r / 2 mod 4), or u ^ (r mod 8)), which also keeps a column of lanes free of bank conflicts.
+template <int DT>
+struct Stage {
+  static constexpr int kE = Ty<DT>::kBytes;
+  static constexpr int kRow = 32 * kE;          // bytes
+  static constexpr int kUnits = kRow / 16;      // of a row
+  static constexpr int kPer = 16 / kE;          // elements of a unit
+  static constexpr int kStep = 32 / kUnits;     // rows that a warp moves at once, 16 bytes a lane
+  static __device__ __forceinline__ uint8_t* slot(uint8_t* stage, int r, int u) {
+    return stage + r * kRow + ((u ^ (kE == 4 ? r & 7 : (r >> 1) & 3)) << 4);
   }
-
-  // `n` columns (32 or 64) of this thread's row into the staging tile
+  // columns from unit u0 of this thread's row
   template <int NV>
-  static __device__ __forceinline__ void put(uint8_t* stage, int lane, const float (&v)[NV]) {
+  static __device__ __forceinline__ void put(uint8_t* stage, int lane, const float (&v)[NV], int u0 = 0) {
 #pragma unroll
-    for (int i = 0; i < NV * kE / 16; ++i) {
+    for (int i = 0; i < NV / kPer; ++i) {
+      uint4 q;
       if constexpr (kE == 4) {
-        *slot(stage, lane, i) = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                           __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+        q = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                       __float_as_uint(v[4 * i + 3]));
       } else {
-        using E = Elem<ODT == PK_BF16>;
-        *slot(stage, lane, i) = make_uint4(E::pack(v[8 * i], v[8 * i + 1]), E::pack(v[8 * i + 2], v[8 * i + 3]),
-                                           E::pack(v[8 * i + 4], v[8 * i + 5]), E::pack(v[8 * i + 6], v[8 * i + 7]));
+        using E = Elem<DT == PK_BF16>;
+        q = make_uint4(E::pack(v[8 * i], v[8 * i + 1]), E::pack(v[8 * i + 2], v[8 * i + 3]),
+                       E::pack(v[8 * i + 4], v[8 * i + 5]), E::pack(v[8 * i + 6], v[8 * i + 7]));
+      }
+      *reinterpret_cast<uint4*>(slot(stage, lane, u0 + i)) = q;
+    }
+  }
+  // v[0 ..] += the elements of a unit
+  static __device__ __forceinline__ void add_unit(const uint4& q, float* v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kE == 4) {
+        v[j] += __uint_as_float(w[j]);
+      } else {
+        const float2 f = Elem<DT == PK_BF16>::unpack(w[j]);
+        v[2 * j] += f.x;
+        v[2 * j + 1] += f.y;
       }
     }
   }
-  // The staging tile to rows of `out`: a step takes four rows, 16 bytes a lane; all eight are read before the first is written.
-  static __device__ __forceinline__ void flush(uint8_t* stage, int lane, void* out, int64_t ld, int vec, const int* rowmap,
+  template <int NV>
+  static __device__ __forceinline__ void add(uint8_t* stage, int lane, float (&v)[NV], int u0) {
+#pragma unroll
+    for (int i = 0; i < NV / kPer; ++i) add_unit(*reinterpret_cast<const uint4*>(slot(stage, lane, u0 + i)), v + i * kPer);
+  }
+  static __device__ __forceinline__ char* element(uint8_t* stage, int r, int c) {
+    return reinterpret_cast<char*>(slot(stage, r, c / kPer)) + (c % kPer) * kE;
+  }
+  // The staged rows to rows of `out` where TMA cannot: a row map, or rows off the 16-byte grid (a column a lane).
+  static __device__ __noinline__ void flush(uint8_t* stage, int lane, void* out, int64_t ld, int vec, const int* rowmap,
                                                int r0, int c0, int M, int N) {
-    const int u = lane & 7, c = c0 + u * (16 / kE), r = r0 + (lane >> 3);
-    uint4 q[8];
+    const int rows = min(32, M - r0);
+    if (vec && c0 + 32 <= N) {
+      const int u = lane % kUnits;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = *slot(stage, 4 * i + (lane >> 3), u);
-    if (vec && c0 + kChunk <= N && !rowmap) {
-      char* d = static_cast<char*>(out) + (r * ld + c) * kE;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r + 4 * i < M) *reinterpret_cast<uint4*>(d + 4 * i * ld * kE) = q[i];
+      for (int i = 0; i < 32 / kStep; ++i) {
+        const int r = i * kStep + lane / kUnits;
+        if (r >= rows) break;
+        const int64_t row = rowmap ? __ldcg(rowmap + r0 + r) : r0 + r;
+        *reinterpret_cast<uint4*>(static_cast<char*>(out) + (row * ld + c0 + u * kPer) * kE) =
+            *reinterpret_cast<const uint4*>(slot(stage, r, u));
+      }
       return;
     }
-    const int n = min(N - c, 16 / kE);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (r + 4 * i >= M || n <= 0) continue;
-      const int64_t row = rowmap ? __ldcg(rowmap + r + 4 * i) : r + 4 * i;
-      char* d = static_cast<char*>(out) + (row * ld + c) * kE;
-      if (vec && n == 16 / kE) {
-        *reinterpret_cast<uint4*>(d) = q[i];
-      } else {
-        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-        for (int j = 0; j < 16 / kE; ++j)
-          if (j < n) {
-            if constexpr (kE == 4)
-              reinterpret_cast<uint32_t*>(d)[j] = w[j];
-            else
-              reinterpret_cast<uint16_t*>(d)[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-          }
-      }
+    if (c0 + lane >= N) return;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const int64_t row = rowmap ? __ldcg(rowmap + r0 + r) : r0 + r;
+      char* d = static_cast<char*>(out) + (row * ld + c0 + lane) * kE;
+      if constexpr (kE == 4)
+        *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(element(stage, r, lane));
+      else
+        *reinterpret_cast<uint16_t*>(d) = *reinterpret_cast<const uint16_t*>(element(stage, r, lane));
     }
   }
-  // Rows of the residual (of the output's type) into the staging tile in flush's layout, through asynchronous copies that
-  // take no registers and are waited for where the values are used.
+  // Rows of `in` into the staging memory, by asynchronous copies (waited for where the values are used) where the rows allow.
   static __device__ __forceinline__ void fetch(uint8_t* stage, int lane, const void* in, int64_t ld, int vec, int r0, int c0,
                                                int M, int N) {
-    const int c = c0 + (lane & 7) * (16 / kE), r = r0 + (lane >> 3);
-    if (vec && c0 + kChunk <= N) {
-      const char* s = static_cast<const char*>(in) + (r * ld + c) * kE;
+    const int rows = min(32, M - r0);
+    if (vec && c0 + 32 <= N) {
+      const int u = lane % kUnits;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (r + 4 * i < M)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, 4 * i + (lane >> 3), lane & 7))),
-                       "l"(s + 4 * i * ld * kE)
+      for (int i = 0; i < 32 / kStep; ++i) {
+        const int r = i * kStep + lane / kUnits;
+        if (r < rows)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, r, u))),
+                       "l"(static_cast<const char*>(in) + ((static_cast<int64_t>(r0) + r) * ld + c0 + u * kPer) * kE)
                        : "memory");
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
       return;
     }
-    const int n = min(N - c, 16 / kE);
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (r + 4 * i < M) {
-        const char* s = static_cast<const char*>(in) + ((r + 4 * i) * ld + c) * kE;
-#pragma unroll
-        for (int j = 0; j < 16 / kE; ++j)
-          if (j < n) {
-            if constexpr (kE == 4)
-              w[j] = reinterpret_cast<const uint32_t*>(s)[j];
-            else
-              w[j >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(s)[j]) << (16 * (j & 1));
-          }
-      }
-      *slot(stage, 4 * i + (lane >> 3), lane & 7) = make_uint4(w[0], w[1], w[2], w[3]);
+    fetch_ragged(stage, lane, in, ld, r0, c0, rows, N);
+  }
+  static __device__ __noinline__ void fetch_ragged(uint8_t* stage, int lane, const void* in, int64_t ld, int r0, int c0,
+                                                   int rows, int N) {
+    if (c0 + lane >= N) return;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const char* s = static_cast<const char*>(in) + ((static_cast<int64_t>(r0) + r) * ld + c0 + lane) * kE;
+      if constexpr (kE == 4)
+        *reinterpret_cast<uint32_t*>(element(stage, r, lane)) = __ldcg(reinterpret_cast<const uint32_t*>(s));
+      else
+        *reinterpret_cast<uint16_t*>(element(stage, r, lane)) = __ldcg(reinterpret_cast<const unsigned short*>(s));
     }
   }
-  // The bias of a chunk's columns, as stored (every lane the same).
-  static __device__ __forceinline__ void fetch_bias(uint4 (&q)[8], const void* bias, int vec, int c, int N) {
-    if (vec && c + kChunk <= N) {
-      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(bias) + static_cast<int64_t>(c) * kE);
+};
+
+// The bias of NC columns, asked for as stored (every lane the same) before the accumulators are waited for.
+template <int DT, int NC>
+struct Bias {
+  using S = Stage<DT>;
+  static constexpr int kUnits = NC / S::kPer;
+  uint4 q[kUnits];
+  __device__ __forceinline__ void fetch(const void* bias, int vec, int c, int N) {
+    if (vec && c + NC <= N) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(bias) + static_cast<int64_t>(c) * S::kE);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = s[i];
+      for (int i = 0; i < kUnits; ++i) q[i] = s[i];
       return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kUnits; ++i) {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < 16 / kE; ++j) {
-        const int at = c + i * (16 / kE) + j;
+      for (int j = 0; j < S::kPer; ++j) {
+        const int at = c + i * S::kPer + j;
         if (at < N) {
-          if constexpr (kE == 4)
+          if constexpr (S::kE == 4)
             w[j] = static_cast<const uint32_t*>(bias)[at];
           else
             w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(bias)[at]) << (16 * (j & 1));
@@ -398,33 +419,37 @@ struct LinEpi {
       q[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // v[.] += the elements of a 16-byte unit
-  static __device__ __forceinline__ void add_unit(const uint4& q, float* v) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  __device__ __forceinline__ void add(float (&v)[NC]) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (kE == 4) {
-        v[j] += __uint_as_float(w[j]);
-      } else {
-        const float2 f = Elem<ODT == PK_BF16>::unpack(w[j]);
-        v[2 * j] += f.x;
-        v[2 * j + 1] += f.y;
-      }
-    }
+    for (int i = 0; i < kUnits; ++i) S::add_unit(q[i], v + i * S::kPer);
   }
-  static __device__ __forceinline__ void read_acc(uint32_t t, bool zero, float (&v)[kChunk]) {
-    if (zero) {
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) v[i] = 0.0f;
-    } else if constexpr (kChunk == 64) {
-      tmem_ld64(t, v);
-    } else {
-      tmem_ld32(t, v);
-    }
-  }
+};
 
-  // `ready` waits for the accumulators (false: give up), `done` hands them back. What comes from memory (bias, residual) is asked for
-  // before the accumulators are waited for.
+template <int NC>
+__device__ __forceinline__ void read_acc(uint32_t t, bool zero, float (&v)[NC]) {
+  if (zero) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] = 0.0f;
+  } else if constexpr (NC == 32) {
+    tmem_ld32(t, v);
+  } else {
+    tmem_ld16(t, v);
+  }
+}
+
+template <int ODT, int RDT>
+struct LinEpi {
+  using Params = LinTiles;
+  using S = Stage<ODT>;
+  // Sixteen columns at a time in a rolled loop: the four code streams of an SM sub-partition share its instruction cache
+  // with the one that issues the MMAs, and a wider body (every activation unrolled over 32 or 64 columns) starves it: even
+  // jumping over the unused parts cost 5 of 87 us. Sixteen warps cover each other's latencies; fp32's staging is twice as
+  // large and has room for eight.
+  static constexpr int kG = 16;
+  static constexpr int kWarps = ODT == PK_F32 ? 8 : 16;
+
+  // `ready` waits for the accumulators (false: give up), `done` hands them back. What comes from memory (bias, residual) is
+  // asked for before the accumulators are waited for.
   template <class Ready, class Done>
   static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
                                              int split, int lane, uint8_t* stage, const Ready& ready, const Done& done) {
@@ -433,72 +458,79 @@ struct LinEpi {
       done();
       return true;
     }
-    const float alpha = p.alpha ? __ldcg(p.alpha) : 1.0f;
     const int end = min(cols, N - c0);
+    const bool res_staged = p.res && ODT == RDT;
 #pragma unroll 1
-    for (int cc = 0; cc < end; cc += kChunk) {
+    for (int cc = 0; cc < end; cc += 32) {
       const int c = c0 + cc;
-      float v[kChunk];
-      const bool res_staged = p.res && ODT == RDT;
       stored(lane);  // the previous chunk's tile has left the staging memory
-      if (res_staged && !p.pre) fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
-      {
-        uint4 bias[8];
-        if (p.bias) fetch_bias(bias, p.bias, p.bias_vec, c, N);
-        if (cc == 0 && !ready()) return false;
-        read_acc(tacc + cc, zero, v);
-        if (cc + kChunk >= end) done();
-        if (p.bias) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) add_unit(bias[i], v + i * (16 / kE));
-        }
-      }
+      if (res_staged && !p.pre) S::fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
+      if (cc == 0 && !ready()) return false;
       if (p.pre) {
-        put(stage, lane, v);
+#pragma unroll 1
+        for (int g = 0; g < 32; g += kG) {
+          float v[kG];
+          Bias<ODT, kG> bias;
+          if (p.bias) bias.fetch(p.bias, p.bias_vec, c + g, N);
+          read_acc(tacc + cc + g, zero, v);
+          if (p.bias) bias.add(v);
+          S::put(stage, lane, v, g / S::kPer);
+        }
         if (p.tma_pre) {
           store_tile(&p.map_pre, stage, c, r0, 0, lane);
           stored(lane);
         } else {
           __syncwarp();
-          flush(stage, lane, p.pre, p.ldpre, 0, nullptr, r0, c, M, N);
+          S::flush(stage, lane, p.pre, p.ldpre, 0, nullptr, r0, c, M, N);
           __syncwarp();
         }
-        if (res_staged) fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
+        if (res_staged) S::fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
       }
-      act_values<ODT>(p.act, v);
-      if (p.drop.cut) {
+#pragma unroll 1
+      for (int g = 0; g < 32; g += kG) {
+        float v[kG];
+        Bias<ODT, kG> bias;
+        if (p.bias) bias.fetch(p.bias, p.bias_vec, c + g, N);
+        read_acc(tacc + cc + g, zero, v);
+        if (g + kG == 32 && cc + 32 >= end) done();
+        if (p.bias) bias.add(v);
+        act_values<ODT>(p.act, v);
+        if (p.drop.cut) {
 #pragma unroll
-        for (int g = 0; g < kChunk / 8; ++g) drop8(v + 8 * g, r0 + lane, c / 8 + g, p.drop);
-      }
-      if (res_staged) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) add_unit(*slot(stage, lane, i), v + i * (16 / kE));
-      } else if (p.res && r0 + lane < M) {
-#pragma unroll
-        for (int g = 0; g < kChunk / 8; ++g) {
-          float b[8];
-          const int64_t at = (r0 + lane) * p.ldres + c + 8 * g;
-          const int n = N - c - 8 * g;
-          if (p.res_vec && n >= 8)
-            load8<RDT>(p.res, at, b);
-          else
-            load8_any<RDT>(p.res, at, n, b);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[8 * g + i] += b[i];
+          for (int i = 0; i < kG / 8; ++i) drop8(v + 8 * i, r0 + lane, (c + g) / 8 + i, p.drop);
         }
-      }
-      if (p.alpha) {
+        if (res_staged) {
+          if (g == 0) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+          }
+          S::add(stage, lane, v, g / S::kPer);
+        } else if (p.res && r0 + lane < M) {
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) v[i] *= alpha;
+          for (int i = 0; i < kG / 8; ++i) {
+            float b[8];
+            const int64_t at = (r0 + lane) * p.ldres + c + g + 8 * i;
+            const int n = N - c - g - 8 * i;
+            if (p.res_vec && n >= 8)
+              load8<RDT>(p.res, at, b);
+            else
+              load8_any<RDT>(p.res, at, n, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * i + j] += b[j];
+          }
+        }
+        if (p.alpha) {
+          const float alpha = __ldcg(p.alpha);
+#pragma unroll
+          for (int i = 0; i < kG; ++i) v[i] *= alpha;
+        }
+        S::put(stage, lane, v, g / S::kPer);
       }
-      put(stage, lane, v);
       if (p.tma_y) {
         store_tile(&p.map_y, stage, c, r0 + split * gemm::split_rows(M), 0, lane);
       } else {
         __syncwarp();
-        flush(stage, lane, p.y, p.ldy, p.y_vec, p.rowmap, r0, c, M, N);
+        S::flush(stage, lane, p.y, p.ldy, p.y_vec, p.rowmap, r0, c, M, N);
         __syncwarp();
       }
     }

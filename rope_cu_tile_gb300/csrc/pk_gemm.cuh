@@ -9,8 +9,8 @@
 //
 // Tile and roles: a pair of CTAs (cta_group::2) owns 256 x 256 of D -- each holds 128 rows of A and 128 of B per 64-wide
 // k step, so a k step moves 64 KB for 256 * 256 * 64 products -- or, where that leaves SMs idle, one CTA owns 128 x 128.
-// Both use the same shared memory: six stages of 16 + 16 KB filled by TMA (128-byte swizzle) and 4 KB a warp for the
-// epilogue. Warp 0 loads, warp 1 of the leader issues the MMAs, warps 4-11 empty the accumulators; two accumulators
+// Both use the same shared memory: six stages of 16 + 16 KB filled by TMA (128-byte swizzle) and 32 KB for the epilogue's
+// warps. Warp 0 loads, warp 1 of the leader issues the MMAs, warps from 4 on empty the accumulators; two accumulators
 // in tensor memory let the epilogue of one tile run under the products of the next. Persistent: a grid of one CTA per SM
 // walks the work units (output tile x split of k) in a fixed order, tiles grouped so that concurrent units share
 // operands in L2. A split of k writes fp32 partial sums, added in a fixed order afterwards.
@@ -25,14 +25,12 @@ namespace gemm {
 
 constexpr int kStages = 6;
 constexpr int kBK = 64;                       // k step: 128 bytes, one swizzle row
-constexpr int kThreads = 384;                 // 12 warps
-constexpr int kEpiWarps = 8;
-constexpr int kEpiWarp0 = 4;
+constexpr int kEpiWarp0 = 4;                  // warps 0-3: load, issue, allocate; then Epi::kWarps (8 or 16) of the epilogue
 constexpr uint32_t kOpBytes = 128 * 128;      // one operand's share of a stage: 128 rows x 64 elements
 constexpr uint32_t kStageBytes = 2 * kOpBytes;
-constexpr uint32_t kEpiBytes = 32 * 128;      // staging of one epilogue warp: 32 rows x 128 bytes
+constexpr uint32_t kEpiBytes = 32 * 1024;     // staging of the epilogue's warps
 constexpr uint32_t kOffEpi = kStages * kStageBytes;
-constexpr uint32_t kOffMeta = kOffEpi + kEpiWarps * kEpiBytes;
+constexpr uint32_t kOffMeta = kOffEpi + kEpiBytes;
 constexpr int kTerms32 = 6;                   // plane pairs of an fp32 product
 constexpr int kGroupM = 8;                    // tile rows walked together
 
@@ -156,18 +154,8 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+  // (no cluster-wide release: what it hands back is tensor memory, ordered by the tcgen05 fences)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // 3-D tile load at (x, y, plane); `bar` is a shared::cluster address (the leader's barrier for a pair)
 template <int CG>
@@ -225,13 +213,14 @@ __device__ __forceinline__ void free_tmem(uint32_t t) {
     tmem_dealloc(t, 512);
 }
 
-// Bounded wait; false once the CTA gave up or after the time limit (which makes it give up).
+// Bounded wait; false once the CTA gave up or after the time limit (which makes it give up). What these barriers guard is
+// written by TMA, the tensor pipe or to tensor memory: no acquire wider than the CTA, which would invalidate L1 each time.
 __device__ __forceinline__ bool wait(Meta* m, const Args& a, uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_u32(bar);
-  if (mbar_try_wait_cluster(addr, parity)) return true;
+  if (mbar_try_wait(addr, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(addr, parity)) return true;
+    if (mbar_try_wait(addr, parity)) return true;
     if ((i & 15u) == 0u) {
       if (attn::aborted(&m->abort)) return false;
       if (globaltimer_ns() - t0 > a.timeout_ns) {
@@ -336,12 +325,12 @@ __device__ __forceinline__ void issue(const Args& a, const Plan& p, uint8_t* sme
   }
 }
 
-// Epi: struct with `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
+// Epi: struct with kWarps and `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
 // are no accumulators: take zeros), first row, first column, columns, M, N, split, lane, staging, ready, done)`, called by
 // 32 lanes together; it calls ready() before it reads accumulators and done() once after the last of them, and
 // returns false when ready() did.
 template <int CG, class Epi>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                 const __grid_constant__ CUtensorMap map_alt, const __grid_constant__ Args a,
                 const __grid_constant__ typename Epi::Params ep) {
@@ -357,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&meta->acc_full[i]), 1);
-      mbar_init(smem_u32(&meta->acc_empty[i]), CG * kEpiWarps);
+      mbar_init(smem_u32(&meta->acc_empty[i]), CG * Epi::kWarps);
     }
     mbar_init(smem_u32(&meta->drain), 1);
     meta->abort = 0;
@@ -387,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && rank == 0) issue<CG>(a, p, smem, meta, tmem, unit0, unit_step);
     __syncwarp();
   } else if (warp >= kEpiWarp0) {
-    const int w = warp - kEpiWarp0, quarter = w & 3, half = w >> 2;
-    constexpr int kCols = 64 * CG;  // columns a warp empties
-    uint8_t* stage = smem + kOffEpi + w * kEpiBytes;
+    const int w = warp - kEpiWarp0, quarter = w & 3, part = w >> 2;
+    constexpr int kCols = 128 * CG / (Epi::kWarps / 4);  // columns a warp empties
+    uint8_t* stage = smem + kOffEpi + w * (kEpiBytes / Epi::kWarps);
     uint32_t n = 0;
     uint32_t empty0 = smem_u32(&meta->acc_empty[0]);
     if constexpr (CG == 2) empty0 = mapa(empty0, 0);
@@ -416,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(smem_u32(&meta->acc_empty[buf]));
         }
       };
-      if (!Epi::run(ep, tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + half * kCols, zero,
-                    t.m0 + 128 * static_cast<int>(rank) + 32 * quarter, t.n0 + half * kCols, kCols, p.M, p.N, t.split, lane,
+      if (!Epi::run(ep, tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + part * kCols, zero,
+                    t.m0 + 128 * static_cast<int>(rank) + 32 * quarter, t.n0 + part * kCols, kCols, p.M, p.N, t.split, lane,
                     stage, ready, done))
         break;
       if (!zero) ++n;
@@ -455,7 +444,7 @@ inline bool operand_ok(const Operand& o) {
   return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && (o.ld & 7) == 0 && (o.plane & 7) == 0;
 }
 bool make_map(CUtensorMap* map, const Operand& o);
-// The map of an output of type dtype (enum pk_dtype) as the epilogue's warps store it: 32 rows x 128 bytes a box.
+// The map of an output of type dtype (enum pk_dtype) as the epilogue's warps store it: 32 rows x 32 columns a box.
 bool make_out_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t planes,
                   int64_t plane);
 
@@ -498,7 +487,7 @@ cudaError_t launch(const Operand& A, const Operand& B, const Operand* alt, Args 
   if (ctas <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned int>(ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * (kEpiWarp0 + Epi::kWarps));
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];

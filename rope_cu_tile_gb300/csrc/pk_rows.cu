@@ -44,13 +44,13 @@ bool make_out_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int6
   const int e = dtype == PK_F32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * e, static_cast<cuuint64_t>(planes > 1 ? plane : rows * ld) * e};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / e), 32, 1};
+  const cuuint32_t box[3] = {32, 32, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType t = dtype == PK_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                 : dtype == PK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return enc(map, t, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             e == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The cheapest cut by a model of the product's time in SM cycles: waves x (k steps x cycles a step + cycles a tile), plus

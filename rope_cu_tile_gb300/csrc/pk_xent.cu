@@ -158,38 +158,10 @@ struct StatParams {
   int64_t cap;
 };
 
-// v += the bias of 64 columns that was asked for earlier (16-bit: 8 units of 16 bytes; fp32: 16)
-template <int DT>
-struct Bias64 {
-  uint4 q[DT == PK_F32 ? 16 : 8];
-  __device__ __forceinline__ void fetch(const void* bias, int vec, int c, int N) {
-    using L = LinEpi<DT, DT>;
-    uint4(&lo)[8] = *reinterpret_cast<uint4(*)[8]>(&q[0]);
-    L::fetch_bias(lo, bias, vec, c, N);
-    if constexpr (DT == PK_F32) {
-      uint4(&hi)[8] = *reinterpret_cast<uint4(*)[8]>(&q[8]);
-      L::fetch_bias(hi, bias, vec, c + 32, N);
-    }
-  }
-  __device__ __forceinline__ void add(float (&v)[64]) const {
-    constexpr int kPer = DT == PK_F32 ? 4 : 8;
-#pragma unroll
-    for (int i = 0; i < 64 / kPer; ++i) LinEpi<DT, DT>::add_unit(q[i], v + kPer * i);
-  }
-};
-
-__device__ __forceinline__ void read64(uint32_t t, bool zero, float (&v)[64]) {
-  if (zero) {
-#pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
-  } else {
-    tmem_ld64(t, v);
-  }
-}
-
 template <int DT>
 struct StatEpi {
   using Params = StatParams;
+  static constexpr int kWarps = 8;  // wide slices: half the partial results
   template <class Ready, class Done>
   static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
                                              int, int lane, uint8_t*, const Ready& ready, const Done& done) {
@@ -203,35 +175,35 @@ struct StatEpi {
     const int end = min(cols, N - c0);
     float m = kFloor, l = 0.0f;
 #pragma unroll 1
-    for (int cc = 0; cc < end; cc += 64) {
+    for (int cc = 0; cc < end; cc += 32) {
       const int c = c0 + cc;
-      float v[64];
+      float v[32];
       {
-        Bias64<DT> b;
+        Bias<DT, 32> b;
         if (p.bias) b.fetch(p.bias, p.bias_vec, c, N);
         if (cc == 0 && !ready()) return false;
-        read64(tacc + cc, zero, v);
-        if (cc + 64 >= end) done();
+        read_acc(tacc + cc, zero, v);
+        if (cc + 32 >= end) done();
         if (p.bias) b.add(v);
       }
-      if (c + 64 > N) {
+      if (c + 32 > N) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
+        for (int i = 0; i < 32; ++i)
           if (c + i >= N) v[i] = -INFINITY;
       }
-      if (label >= c && label < c + 64) {
+      if (label >= c && label < c + 32) {
         float z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) z = label == c + i ? v[i] : z;
+        for (int i = 0; i < 32; ++i) z = label == c + i ? v[i] : z;
         p.picked[row] = z;
       }
       float top[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-      for (int i = 4; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+      for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
       const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < 64; ++i) s[i & 3] += exp2_fast((v[i] - mn) * kLog2e);
+      for (int i = 0; i < 32; ++i) s[i & 3] += exp2_fast((v[i] - mn) * kLog2e);
       l = l * exp2_fast((m - mn) * kLog2e) + ((s[0] + s[1]) + (s[2] + s[3]));
       m = mn;
     }
@@ -295,7 +267,8 @@ struct GradParams {
 template <int DT>
 struct GradEpi {
   using Params = GradParams;
-  using Lin = LinEpi<DT == PK_F16 ? PK_F16 : PK_BF16, PK_F32>;  // its staging, for 16-bit planes
+  using S = Stage<DT == PK_F16 ? PK_F16 : PK_BF16>;
+  static constexpr int kWarps = 16;
   template <class Ready, class Done>
   static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
                                              int, int lane, uint8_t* stage, const Ready& ready, const Done& done) {
@@ -310,31 +283,31 @@ struct GradEpi {
     const int label = live ? __ldcg(p.lab + row) - p.v0 : -1;
     const int end = min(cols, N - c0);
 #pragma unroll 1
-    for (int cc = 0; cc < end; cc += 64) {
+    for (int cc = 0; cc < end; cc += 32) {
       const int c = c0 + cc;
-      float v[64];
+      float v[32];
       {
-        Bias64<DT> b;
+        Bias<DT, 32> b;
         if (p.bias) b.fetch(p.bias, p.bias_vec, c, N);
         if (cc == 0 && !ready()) return false;
-        read64(tacc + cc, zero, v);
-        if (cc + 64 >= end) done();
+        read_acc(tacc + cc, zero, v);
+        if (cc + 32 >= end) done();
         if (p.bias) b.add(v);
       }
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
+      for (int i = 0; i < 32; ++i) {
         const float e = exp2_fast((v[i] - lse) * kLog2e);
         v[i] = live ? (label == c + i ? e - 1.0f : e) * g : 0.0f;  // rows past the count feed dW: zero
       }
 #pragma unroll
       for (int k = 0; k < (DT == PK_F32 ? 3 : 1); ++k) {
         stored(lane);
-        Lin::put(stage, lane, v);
+        S::put(stage, lane, v);
         store_tile(&p.dz, stage, c, r0, k, lane);
         if constexpr (DT == PK_F32) {
           if (k < 2) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+            for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
           }
         }
       }
