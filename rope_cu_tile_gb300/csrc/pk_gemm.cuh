@@ -232,6 +232,24 @@ __device__ __forceinline__ bool wait(Meta* m, const Args& a, uint64_t* bar, uint
   }
 }
 
+// One lane of a converged warp. The loops of the loading and the issuing warp are run by all 32 lanes, with only the TMA and
+// MMA instructions under this: the compiler then sees loop counters and descriptors as the same in every lane and keeps
+// them in the uniform registers that those instructions take. (One lane in a divergent branch spent some 60 cycles an MMA
+// moving operands over, 700 a k step where the tensor pipe needs 512.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)::"memory");
+  return ok != 0;
+}
+// (a warp goes on or gives up as one)
+__device__ __forceinline__ bool wait_warp(Meta* m, const Args& a, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(m, a, bar, parity));
+}
+
 // ------------------------------------------------------------------------------------
 // roles
 
@@ -248,14 +266,15 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
     for (int term = 0; term < a.terms && !bad; ++term) {
       const int pa = term_a(a.terms, term), pb = term_b(a.terms, term);
       for (int kb = t.kb0; kb < t.kb0 + t.kbs; ++kb) {
-        if (!wait(meta, a, &meta->empty[st], ph ^ 1u)) {
+        if (!wait_warp(meta, a, &meta->empty[st], ph ^ 1u)) {
           bad = true;
           break;
         }
         const uint32_t bar = full0 + 8 * st;
-        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&meta->full[st]), CG * kStageBytes);
         const uint32_t sa = smem_u32(smem + st * kStageBytes), sb = sa + kOpBytes;
         const int k = kb * kBK;
+        if (elect_one()) {
+        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&meta->full[st]), CG * kStageBytes);
         if (a.a_mn) {
           tma_load_3d<CG>(sa, ma, bar, ra, k, pa);
           tma_load_3d<CG>(sa + kOpBytes / 2, ma, bar, ra + 64, k, pa);
@@ -268,6 +287,8 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
         } else {
           tma_load_3d<CG>(sb, mb, bar, k, rb, pb);
         }
+        }
+        __syncwarp();
         st = st + 1 == kStages ? 0 : st + 1;
         ph ^= st == 0 ? 1u : 0u;
       }
@@ -278,7 +299,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
   for (int i = 0; i < kStages; ++i) {
     if (bad)
       mbar_wait(smem_u32(&meta->empty[st]), ph ^ 1u, a.timeout_ns);
-    else if (!wait(meta, a, &meta->empty[st], ph ^ 1u))
+    else if (!wait_warp(meta, a, &meta->empty[st], ph ^ 1u))
       bad = true;
     st = st + 1 == kStages ? 0 : st + 1;
     ph ^= st == 0 ? 1u : 0u;
@@ -301,26 +322,30 @@ __device__ __forceinline__ void issue(const Args& a, const Plan& p, uint8_t* sme
     const int steps = t.kbs * a.terms;
     if (steps == 0) continue;  // an empty split: the epilogue takes zeros
     const uint32_t buf = n & 1u;
-    if (!(ok = wait(meta, a, &meta->acc_empty[buf], ((n >> 1) & 1u) ^ 1u))) break;
+    if (!(ok = wait_warp(meta, a, &meta->acc_empty[buf], ((n >> 1) & 1u) ^ 1u))) break;
     tc_fence_after();
     const uint32_t d = tmem + buf * 256;
     for (int i = 0; i < steps; ++i) {
-      if (!(ok = wait(meta, a, &meta->full[st], ph))) break;
+      if (!(ok = wait_warp(meta, a, &meta->full[st], ph))) break;
       tc_fence_after();
       const uint64_t xa = da + st * (kStageBytes >> 4), xb = db + st * (kStageBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (uint32_t k = 0; k < kBK / 16; ++k) mma<CG>(d, xa + k * sa, xb + k * sb, idesc, (i | k) != 0 ? 1u : 0u);
-      commit<CG>(smem_u32(&meta->empty[st]));
+        for (uint32_t k = 0; k < kBK / 16; ++k) mma<CG>(d, xa + k * sa, xb + k * sb, idesc, (i | k) != 0 ? 1u : 0u);
+        commit<CG>(smem_u32(&meta->empty[st]));
+        if (i + 1 == steps) commit<CG>(smem_u32(&meta->acc_full[buf]));
+      }
+      __syncwarp();
       st = st + 1 == kStages ? 0 : st + 1;
       ph ^= st == 0 ? 1u : 0u;
     }
     if (!ok) break;
-    commit<CG>(smem_u32(&meta->acc_full[buf]));
     ++n;
   }
   if (!ok) {
     // gave up: the MMAs in flight end before the tensor memory is freed
-    commit<CG>(smem_u32(&meta->drain));
+    if (elect_one()) commit<CG>(smem_u32(&meta->drain));
+    __syncwarp();
     mbar_wait(smem_u32(&meta->drain), 0, a.timeout_ns);
   }
 }
@@ -337,7 +362,7 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   Meta* meta = reinterpret_cast<Meta*>(smem + kOffMeta);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -359,22 +384,18 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = meta->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, meta->tmem, 0);
   griddep_wait();  // the previous kernel's results (operands, counts) from here on
   const Plan p = make_plan<CG>(a);
   const int unit0 = blockIdx.x / CG, unit_step = gridDim.x / CG;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const bool alt = a.dyn && __ldcg(a.dyn) == a.alt_count;
-      const CUtensorMap* ma = alt && a.alt_operand == 0 ? &map_alt : &map_a;
-      const CUtensorMap* mb = alt && a.alt_operand == 1 ? &map_alt : &map_b;
-      produce<CG>(ma, mb, a, p, smem, meta, rank, unit0, unit_step);
-    }
-    __syncwarp();
+    const bool alt = a.dyn && __ldcg(a.dyn) == a.alt_count;
+    const CUtensorMap* ma = alt && a.alt_operand == 0 ? &map_alt : &map_a;
+    const CUtensorMap* mb = alt && a.alt_operand == 1 ? &map_alt : &map_b;
+    produce<CG>(ma, mb, a, p, smem, meta, rank, unit0, unit_step);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) issue<CG>(a, p, smem, meta, tmem, unit0, unit_step);
-    __syncwarp();
+    if (rank == 0) issue<CG>(a, p, smem, meta, tmem, unit0, unit_step);
   } else if (warp >= kEpiWarp0) {
     const int w = warp - kEpiWarp0, quarter = w & 3, part = w >> 2;
     constexpr int kCols = 128 * CG / (Epi::kWarps / 4);  // columns a warp empties
@@ -389,8 +410,7 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
       // (the warp goes on or leaves as one: the accumulator loads are warp-wide)
       const auto ready = [&]() {
         if (zero) return true;
-        const bool ok = wait(meta, a, &meta->acc_full[buf], (n >> 1) & 1u);
-        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (!wait_warp(meta, a, &meta->acc_full[buf], (n >> 1) & 1u)) return false;
         tc_fence_after();
         return true;
       };
