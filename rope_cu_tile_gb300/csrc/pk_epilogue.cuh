@@ -143,6 +143,20 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ void add2(float& x, float& y, float2 b) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(b.x), "f"(b.y));
+}
 __device__ __forceinline__ float rcp_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -205,17 +219,22 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
   } else if (act == PK_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      // Phi(z) + z phi(z) is h or 1 - h with h = Phi(-u) - u phi(u), u = |z|
-      const float u0 = fabsf(z[i]), u1 = fabsf(z[i + 1]);
+      // Phi(z) + z phi(z) is 1/2 +- (1/2 - h), the sign z's, with h = Phi(-u) - u phi(u), u = |z| (h < 1/2)
+      const float2 u = make_float2(fabsf(z[i]), fabsf(z[i + 1]));
       float2 e;
       if constexpr (DT == PK_F32)
-        e = make_float2(0.5f * erfcf(u0 * 0.70710678118654752f), 0.5f * erfcf(u1 * 0.70710678118654752f));
+        e = make_float2(0.5f * erfcf(u.x * 0.70710678118654752f), 0.5f * erfcf(u.y * 0.70710678118654752f));
       else
-        e = tail2(u0, u1);
-      const float f0 = attn::ex2(u0 * u0 * -0.72134752044448170f), f1 = attn::ex2(u1 * u1 * -0.72134752044448170f);
-      const float h0 = fmaf(u0 * -0.39894228040143268f, f0, e.x), h1 = fmaf(u1 * -0.39894228040143268f, f1, e.y);
-      d[i] *= z[i] > 0.0f ? 1.0f - h0 : h0;
-      d[i + 1] *= z[i + 1] > 0.0f ? 1.0f - h1 : h1;
+        e = tail2(u.x, u.y);
+      const float2 q = mul2(mul2(u, u), make_float2(-0.72134752044448170f, -0.72134752044448170f));
+      const float2 f = make_float2(attn::ex2(q.x), attn::ex2(q.y));
+      const float2 h = fma2(mul2(u, make_float2(-0.39894228040143268f, -0.39894228040143268f)), f, e);
+      float2 w = fma2(h, make_float2(-1.0f, -1.0f), make_float2(0.5f, 0.5f));
+      w.x = __uint_as_float(__float_as_uint(w.x) ^ (__float_as_uint(z[i]) & 0x80000000u));
+      w.y = __uint_as_float(__float_as_uint(w.y) ^ (__float_as_uint(z[i + 1]) & 0x80000000u));
+      const float2 v = mul2(fma2(w, make_float2(1.0f, 1.0f), make_float2(0.5f, 0.5f)), make_float2(d[i], d[i + 1]));
+      d[i] = v.x;
+      d[i + 1] = v.y;
     }
   } else if (act == PK_ACT_SILU) {
 #pragma unroll
@@ -316,9 +335,7 @@ struct Stage {
       if constexpr (kE == 4) {
         v[j] += __uint_as_float(w[j]);
       } else {
-        const float2 f = Elem<DT == PK_BF16>::unpack(w[j]);
-        v[2 * j] += f.x;
-        v[2 * j + 1] += f.y;
+        add2(v[2 * j], v[2 * j + 1], Elem<DT == PK_BF16>::unpack(w[j]));
       }
     }
   }
@@ -441,11 +458,9 @@ template <int ODT, int RDT>
 struct LinEpi {
   using Params = LinTiles;
   using S = Stage<ODT>;
-  // Sixteen columns at a time in a rolled loop: the four code streams of an SM sub-partition share its instruction cache
-  // with the one that issues the MMAs, and a wider body (every activation unrolled over 32 or 64 columns) starves it: even
-  // jumping over the unused parts cost 5 of 87 us. Sixteen warps cover each other's latencies; fp32's staging is twice as
-  // large and has room for eight.
-  static constexpr int kG = 16;
+  // A chunk of 32 columns is a chain of a tensor-memory load, arithmetic and a staged store; four warps a scheduler cover each
+  // other's (131072 x 1024 x 4096 with gelu and kept pre-activation: 1031 us on eight warps of 128 columns, 895 on sixteen of 64, at
+  // the same time otherwise). fp32's staging is twice as large and has room for eight.
   static constexpr int kWarps = ODT == PK_F32 ? 8 : 16;
 
   // `ready` waits for the accumulators (false: give up), `done` hands them back. What comes from memory (bias, residual) is
@@ -465,17 +480,17 @@ struct LinEpi {
       const int c = c0 + cc;
       stored(lane);  // the previous chunk's tile has left the staging memory
       if (res_staged && !p.pre) S::fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
-      if (cc == 0 && !ready()) return false;
+      float v[32];
+      {
+        Bias<ODT, 32> bias;
+        if (p.bias) bias.fetch(p.bias, p.bias_vec, c, N);
+        if (cc == 0 && !ready()) return false;
+        read_acc(tacc + cc, zero, v);
+        if (cc + 32 >= end) done();
+        if (p.bias) bias.add(v);
+      }
       if (p.pre) {
-#pragma unroll 1
-        for (int g = 0; g < 32; g += kG) {
-          float v[kG];
-          Bias<ODT, kG> bias;
-          if (p.bias) bias.fetch(p.bias, p.bias_vec, c + g, N);
-          read_acc(tacc + cc + g, zero, v);
-          if (p.bias) bias.add(v);
-          S::put(stage, lane, v, g / S::kPer);
-        }
+        S::put(stage, lane, v);
         if (p.tma_pre) {
           store_tile(&p.map_pre, stage, c, r0, 0, lane);
           stored(lane);
@@ -486,46 +501,35 @@ struct LinEpi {
         }
         if (res_staged) S::fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
       }
-#pragma unroll 1
-      for (int g = 0; g < 32; g += kG) {
-        float v[kG];
-        Bias<ODT, kG> bias;
-        if (p.bias) bias.fetch(p.bias, p.bias_vec, c + g, N);
-        read_acc(tacc + cc + g, zero, v);
-        if (g + kG == 32 && cc + 32 >= end) done();
-        if (p.bias) bias.add(v);
-        act_values<ODT>(p.act, v);
-        if (p.drop.cut) {
+      act_values<ODT>(p.act, v);
+      if (p.drop.cut) {
 #pragma unroll
-          for (int i = 0; i < kG / 8; ++i) drop8(v + 8 * i, r0 + lane, (c + g) / 8 + i, p.drop);
-        }
-        if (res_staged) {
-          if (g == 0) {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-          }
-          S::add(stage, lane, v, g / S::kPer);
-        } else if (p.res && r0 + lane < M) {
-#pragma unroll
-          for (int i = 0; i < kG / 8; ++i) {
-            float b[8];
-            const int64_t at = (r0 + lane) * p.ldres + c + g + 8 * i;
-            const int n = N - c - g - 8 * i;
-            if (p.res_vec && n >= 8)
-              load8<RDT>(p.res, at, b);
-            else
-              load8_any<RDT>(p.res, at, n, b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * i + j] += b[j];
-          }
-        }
-        if (p.alpha) {
-          const float alpha = __ldcg(p.alpha);
-#pragma unroll
-          for (int i = 0; i < kG; ++i) v[i] *= alpha;
-        }
-        S::put(stage, lane, v, g / S::kPer);
+        for (int i = 0; i < 4; ++i) drop8(v + 8 * i, r0 + lane, c / 8 + i, p.drop);
       }
+      if (res_staged) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        S::add(stage, lane, v, 0);
+      } else if (p.res && r0 + lane < M) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float b[8];
+          const int64_t at = (r0 + lane) * p.ldres + c + 8 * i;
+          const int n = N - c - 8 * i;
+          if (p.res_vec && n >= 8)
+            load8<RDT>(p.res, at, b);
+          else
+            load8_any<RDT>(p.res, at, n, b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[8 * i + j] += b[j];
+        }
+      }
+      if (p.alpha) {
+        const float alpha = __ldcg(p.alpha);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= alpha;
+      }
+      S::put(stage, lane, v);
       if (p.tma_y) {
         store_tile(&p.map_y, stage, c, r0 + split * gemm::split_rows(M), 0, lane);
       } else {

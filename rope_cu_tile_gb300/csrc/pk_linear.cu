@@ -20,8 +20,10 @@ using namespace rows;
 // dz and its column sums
 
 constexpr int kDzThreads = 256;
-constexpr int kDzRows = 128;  // rows of a block: 16 a thread, then a fixed-order sum over the block's eight row lanes
+constexpr int kDzRows = 128;  // rows of a block: 16 a thread, then a fixed-order sum over the block's eight row lanes; for
+constexpr int kDzFew = 32;    // fewer rows than give every SM a block, 32
 constexpr int kDzBatch = 4;   // rows whose loads are in flight together
+int dz_rows(int64_t T, int64_t ldz, int sms) { return (T + kDzRows - 1) / kDzRows * ((ldz + 255) / 256) < 2 * sms ? kDzFew : kDzRows; }
 
 struct DzArgs {
   const void* dy;
@@ -35,6 +37,7 @@ struct DzArgs {
   int64_t ldz, plane;
   float* part;  // [blocks of rows, ldz] column sums, or null
   int dy_vec, pre_vec;
+  int rows;    // of a block
 };
 
 // A warp takes 256 columns of a row (8 a lane: one draw of the generator); a block eight rows at a time.
@@ -45,12 +48,12 @@ __global__ void __launch_bounds__(kDzThreads) pk_dz_kernel(const __grid_constant
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.y * 256 + lane * 8;
   const int n = a.N - c;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kDzRows;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   griddep_wait();
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (c < a.ldz) {
 #pragma unroll 1
-    for (int64_t rb = r0 + w; rb < r0 + kDzRows && rb < a.T; rb += 8 * kDzBatch) {
+    for (int64_t rb = r0 + w; rb < r0 + a.rows && rb < a.T; rb += 8 * kDzBatch) {
       Raw8<DT> dy[kDzBatch], pre[kDzBatch];
 #pragma unroll
       for (int i = 0; i < kDzBatch; ++i)
@@ -60,22 +63,24 @@ __global__ void __launch_bounds__(kDzThreads) pk_dz_kernel(const __grid_constant
         }
 #pragma unroll
       for (int i = 0; i < kDzBatch; ++i) {
-      const int64_t r = rb + 8 * i;
-      if (r >= a.T) break;
-      float v[8];
-      dy[i].get(v);
-      if (a.drop.cut) drop8(v, static_cast<uint32_t>(r), c / 8, a.drop);
-      if (a.act != PK_ACT_NONE) {
-        float z[8];
-        pre[i].get(z);
-        act_slopes<DT>(a.act, z, v);
-      }
+        const int64_t r = rb + 8 * i;
+        if (r >= a.T) break;
+        float v[8];
+        dy[i].get(v);
+        if (a.drop.cut) drop8(v, static_cast<uint32_t>(r), c / 8, a.drop);
+        if (a.act != PK_ACT_NONE) {
+          float z[8];
+          pre[i].get(z);
+          act_slopes<DT>(a.act, z, v);
+        }
+        if (n < 8) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j >= n) v[j] = 0.0f;  // the operand's padding
-        sum[j] += v[j];
-      }
-      if (a.dz) {
+          for (int j = 0; j < 8; ++j)
+            if (j >= n) v[j] = 0.0f;  // the operand's padding
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) add2(sum[j], sum[j + 1], make_float2(v[j], v[j + 1]));
+        if (!a.dz) continue;
         if constexpr (DT == PK_F32) {
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
@@ -92,7 +97,6 @@ __global__ void __launch_bounds__(kDzThreads) pk_dz_kernel(const __grid_constant
         } else {
           store8<DT>(a.dz, r * a.ldz + c, v);
         }
-      }
       }
     }
   }
@@ -113,7 +117,7 @@ cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
   a.dy_vec = rows16(a.dy, a.lddy, elem_bytes(dtype));
   a.pre_vec = a.pre && rows16(a.pre, a.ldpre, elem_bytes(dtype));
   Launch l(1, kDzThreads, stream);
-  l.cfg.gridDim = dim3(static_cast<unsigned int>((a.T + kDzRows - 1) / kDzRows), static_cast<unsigned int>((a.ldz + 255) / 256));
+  l.cfg.gridDim = dim3(static_cast<unsigned int>((a.T + a.rows - 1) / a.rows), static_cast<unsigned int>((a.ldz + 255) / 256));
   if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F32>, a);
   if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_BF16>, a);
   return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F16>, a);
@@ -235,6 +239,7 @@ struct Bwd {
   gemm::Shape dx, dw;
   void *x, *w, *dz;
   float *part, *partial;
+  int rows;  // of a block of dz
   int64_t blocks, bytes;
 };
 Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, const void* dy, int64_t lddy, int act,
@@ -246,7 +251,8 @@ Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, const vo
   if (need_dx && !in_place(dtype, w, K)) b.w = c.take(copy_bytes(dtype, N, K));
   // dy itself is the operand when nothing changes it on the way
   if ((need_dx || need_dw) && (act != PK_ACT_NONE || cut || !in_place(dtype, dy, lddy))) b.dz = c.take(copy_bytes(dtype, T, N));
-  b.blocks = (T + kDzRows - 1) / kDzRows;
+  b.rows = dz_rows(T, copy_ld(N), sms);
+  b.blocks = (T + b.rows - 1) / b.rows;
   if (need_db) b.part = static_cast<float*>(c.take(b.blocks * copy_ld(N) * 4));
   int64_t partial = 0;
   if (need_dx) {
@@ -320,8 +326,10 @@ int pk_linear(int dtype, const void* x, int64_t ldx, const void* w, const void* 
                                              : few_launch<PK_F16>(fa, d.sms, stream);
     return r == cudaSuccess ? PK_OK : PK_ERR_CUDA;
   }
-  if (f.x && rows::copy_operand(dtype, x, ldx, T, K, f.x, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
-  if (f.w && rows::copy_operand(dtype, w, K, N, K, f.w, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  rows::Copies copies(dtype);
+  if (f.x) copies.add(x, ldx, T, K, f.x);
+  if (f.w) copies.add(w, K, N, K, f.w);
+  if (copies.launch(d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   gemm::Args a = {};
   a.M = static_cast<int>(T);
   a.N = N;
@@ -390,14 +398,18 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     z.ldz = rows::copy_ld(N);
     z.plane = T * z.ldz;
     z.part = b.part;
+    z.rows = b.rows;
     if (dz_launch(dtype, z, stream) != cudaSuccess) return PK_ERR_CUDA;
-    if (db && rows::sum_rows(dtype, b.part, b.blocks, N, z.ldz, nullptr, db, stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (db && rows::sum_rows(dtype, b.part, b.blocks, nullptr, 1, N, z.ldz, nullptr, db, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
+  rows::Copies copies(dtype);
+  if (b.w) copies.add(w, K, N, K, b.w);
+  if (b.x) copies.add(x, ldx, T, K, b.x);
+  if (copies.launch(d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   gemm::Args a = {};
   a.status = status ? status : d.status;
   a.timeout_ns = wait_limit_ns();
   if (dx) {
-    if (b.w && rows::copy_operand(dtype, w, K, N, K, b.w, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
     const gemm::Operand A = b.dz ? rows::operand_of_copy(dtype, b.dz, T, N, 0) : rows::operand(dtype, dy, lddy, T, N, 0);
     const gemm::Operand B = b.w ? rows::operand_of_copy(dtype, b.w, N, K, 1) : rows::operand(dtype, w, K, N, K, 1);
     a.M = static_cast<int>(T);
@@ -409,7 +421,6 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dx, b.partial, rows::partial_rows(b.dx, T), d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
   if (dw) {
-    if (b.x && rows::copy_operand(dtype, x, ldx, T, K, b.x, nullptr, nullptr, 0, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
     const gemm::Operand A = b.dz ? rows::operand_of_copy(dtype, b.dz, T, N, 1) : rows::operand(dtype, dy, lddy, T, N, 1);
     const gemm::Operand B = b.x ? rows::operand_of_copy(dtype, b.x, T, K, 1) : rows::operand(dtype, x, ldx, T, K, 1);
     a.M = N;

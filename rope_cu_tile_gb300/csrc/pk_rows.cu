@@ -148,57 +148,60 @@ int take_status(int dev) {
 
 namespace {
 
+struct CopyJobs {
+  CopyJob job[2];
+};
+
 // One thread: 8 columns of a row. Bound by bytes: 2 or 4 read and 2 or 6 written an element.
 template <int DT>
-__global__ void __launch_bounds__(256) pack_kernel(const void* src, int64_t ld, int64_t nrows, int cols,
-                                                   uint16_t* dst, int64_t ldp, int64_t plane, int vec, FastDiv div,
-                                                   const int* idx, const int* count, int skip) {
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ CopyJobs jobs) {
+  const CopyJob& j = jobs.job[blockIdx.y];
   griddep_wait();
-  int64_t live = nrows, total = nrows;
-  if (count) {
-    const int c = __ldcg(count);
-    if (c == skip) return;
+  int64_t live = j.rows, total = j.rows;
+  if (j.count) {
+    const int c = __ldcg(j.count);
+    if (c == j.skip) return;
     live = c;
-    total = min((live + 255) / 256 * 256, (nrows + 255) / 256 * 256);
+    total = min((live + 255) / 256 * 256, (j.rows + 255) / 256 * 256);
   }
-  const int64_t groups = ldp / 8, n = total * groups;
+  const int64_t groups = j.ldp / 8, n = total * groups;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = n < (int64_t(1) << 31) ? div.div(static_cast<uint32_t>(i)) : i / groups;
+    const int64_t r = n < (int64_t(1) << 31) ? j.div.div(static_cast<uint32_t>(i)) : i / groups;
     const int c = static_cast<int>(i - r * groups) * 8;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    uint4* d = reinterpret_cast<uint4*>(dst + r * ldp + c);
+    uint4* d = reinterpret_cast<uint4*>(j.dst + r * j.ldp + c);
     if (r < live) {
-      const int64_t s = (idx ? static_cast<int64_t>(__ldcg(idx + r)) : r) * ld + c;
+      const int64_t s = (j.idx ? static_cast<int64_t>(__ldcg(j.idx + r)) : r) * j.ld + c;
       if constexpr (DT != PK_F32) {
-        if (vec && c + 8 <= cols) {
-          *d = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + s));
+        if (j.vec && c + 8 <= j.cols) {
+          *d = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(j.src) + s));
           continue;
         }
       }
-      if (vec && c + 8 <= cols)
-        load8<DT>(src, s, v);
+      if (j.vec && c + 8 <= j.cols)
+        load8<DT>(j.src, s, v);
       else
-        load8_any<DT>(src, s, cols - c, v);
+        load8_any<DT>(j.src, s, j.cols - c, v);
     }
     if constexpr (DT == PK_F32) {
       uint32_t h[3][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 a = make_float2(v[2 * j], v[2 * j + 1]);
+      for (int i2 = 0; i2 < 4; ++i2) {
+        float2 a = make_float2(v[2 * i2], v[2 * i2 + 1]);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          h[k][j] = Elem<true>::pack(a.x, a.y);
-          const float2 b = Elem<true>::unpack(h[k][j]);
+          h[k][i2] = Elem<true>::pack(a.x, a.y);
+          const float2 b = Elem<true>::unpack(h[k][i2]);
           a.x -= b.x;
           a.y -= b.y;
         }
       }
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint4*>(dst + k * plane + r * ldp + c) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+        *reinterpret_cast<uint4*>(j.dst + k * j.plane + r * j.ldp + c) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
     } else {
-      store8<DT>(dst, r * ldp + c, v);
+      store8<DT>(j.dst, r * j.ldp + c, v);
     }
   }
 }
@@ -222,19 +225,38 @@ gemm::Operand operand_of_copy(int dtype, const void* copy, int64_t nrows, int64_
   return o;
 }
 
-cudaError_t copy_operand(int dtype, const void* p, int64_t ld, int64_t nrows, int64_t cols, void* copy, const int* idx,
-                         const int* count, int skip, int sms, cudaStream_t stream) {
-  const int64_t ldp = copy_ld(cols), plane = nrows * ldp;
-  const int vec = rows16(p, ld, elem_bytes(dtype));
-  const int64_t n = nrows * (ldp / 8);
-  const int64_t most = static_cast<int64_t>(sms) * 8;
-  Launch l(n / 256 + 1 < most ? n / 256 + 1 : most, 256, stream);
-  uint16_t* d = static_cast<uint16_t*>(copy);
-  const int nc = static_cast<int>(cols);
-  const FastDiv div(static_cast<uint32_t>(ldp / 8));
-  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F32>, p, ld, nrows, nc, d, ldp, plane, vec, div, idx, count, skip);
-  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_BF16>, p, ld, nrows, nc, d, ldp, plane, vec, div, idx, count, skip);
-  return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F16>, p, ld, nrows, nc, d, ldp, plane, vec, div, idx, count, skip);
+void Copies::add(const void* p, int64_t ld, int64_t nrows, int64_t cols, void* copy, const int* idx, const int* count,
+                 int skip) {
+  const int64_t ldp = copy_ld(cols);
+  job[n++] = CopyJob{p,
+                     ld,
+                     nrows,
+                     ldp,
+                     nrows * ldp,
+                     static_cast<uint16_t*>(copy),
+                     static_cast<int>(cols),
+                     rows16(p, ld, elem_bytes(dtype)),
+                     FastDiv(static_cast<uint32_t>(ldp / 8)),
+                     idx,
+                     count,
+                     skip};
+}
+
+cudaError_t Copies::launch(int sms, cudaStream_t stream) {
+  if (n == 0) return cudaSuccess;
+  CopyJobs jobs = {};
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    jobs.job[i] = job[i];
+    const int64_t m = job[i].rows * (job[i].ldp / 8);
+    most = m > most ? m : most;
+  }
+  const int64_t blocks = most / 256 + 1, cap = static_cast<int64_t>(sms) * 8;
+  Launch l(blocks < cap ? blocks : cap, 256, stream);
+  l.cfg.gridDim.y = n;
+  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F32>, jobs);
+  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_BF16>, jobs);
+  return cudaLaunchKernelEx(&l.cfg, pack_kernel<PK_F16>, jobs);
 }
 
 // ------------------------------------------------------------------------------------
@@ -269,14 +291,16 @@ __global__ void __launch_bounds__(256) splits_kernel(const float* part, int cg, 
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int64_t nrows, int cols, int64_t ld,
-                                                       const float* alpha, void* out) {
+__global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int64_t nrows, const int* count, int per, int cols,
+                                                       int64_t ld, const float* alpha, void* out) {
   // eight threads a column, each a strided eighth of the rows, joined in a fixed order
   __shared__ float s[8][33];
   griddep_wait();
   const int c = blockIdx.x * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
+  if (count) nrows = min(nrows, static_cast<int64_t>((__ldcg(count) + per - 1) / per));
   float v = 0.0f;
   if (c < cols)
+#pragma unroll 8
     for (int64_t r = g; r < nrows; r += 8) v += __ldcg(part + r * ld + c);
   s[g][threadIdx.x % 32] = v;
   __syncthreads();
@@ -288,12 +312,13 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int64_
 
 }  // namespace
 
-cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, int cols, int64_t ld, const float* alpha, void* out,
-                     cudaStream_t stream) {
+cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, const int* count, int per, int cols, int64_t ld,
+                     const float* alpha, void* out, cudaStream_t stream) {
   Launch l((cols + 31) / 32, 256, stream);
-  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, sum_rows_kernel<PK_F32>, part, nrows, cols, ld, alpha, out);
-  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, sum_rows_kernel<PK_BF16>, part, nrows, cols, ld, alpha, out);
-  return cudaLaunchKernelEx(&l.cfg, sum_rows_kernel<PK_F16>, part, nrows, cols, ld, alpha, out);
+  const auto run = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, part, nrows, count, per, cols, ld, alpha, out); };
+  if (dtype == PK_F32) return run(sum_rows_kernel<PK_F32>);
+  if (dtype == PK_BF16) return run(sum_rows_kernel<PK_BF16>);
+  return run(sum_rows_kernel<PK_F16>);
 }
 
 // ------------------------------------------------------------------------------------

@@ -43,24 +43,9 @@ inline int64_t copy_ld(int64_t cols) { return round_up(cols, 8); }
 inline int64_t copy_bytes(int dtype, int64_t rows, int64_t cols) {
   return (dtype == PK_F32 ? 3 : 1) * rows * copy_ld(cols) * 2;
 }
-// The operand for p: p itself, or its copy at `copy` (filled by a launch on `stream`; rows `idx[0 .. *count)` of p when
-// idx is given, then zeros up to a multiple of 256 rows, nothing when *count == skip).
+// The operand for p itself, and for its copy.
 gemm::Operand operand(int dtype, const void* p, int64_t ld, int64_t rows, int64_t cols, int mn);
 gemm::Operand operand_of_copy(int dtype, const void* copy, int64_t rows, int64_t cols, int mn);
-cudaError_t copy_operand(int dtype, const void* p, int64_t ld, int64_t rows, int64_t cols, void* copy, const int* idx,
-                         const int* count, int skip, int sms, cudaStream_t stream);
-
-// A product with the linear epilogue (type dtype out, residual of type rdtype), through split partial sums when s.splits
-// > 1 (`partial`: `part_rows` rows of round_up(N, 8) floats, part_rows >= splits x round_up(M, 256); with a device count of
-// rows the device takes as many splits, up to s.splits, as are worth it and have room).
-cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt,
-                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int64_t part_rows, int sms, cudaStream_t stream);
-inline int64_t partial_rows(const gemm::Shape& s, int64_t M) { return s.splits > 1 ? s.splits * round_up(M, 256) : 0; }
-inline int64_t partial_bytes(const gemm::Shape& s, int64_t M, int64_t N) { return partial_rows(s, M) * round_up(N, 8) * 4; }
-
-// db[c] = sum_r part[r][c], rows added in order
-cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, int cols, int64_t ld, const float* alpha, void* out,
-                     cudaStream_t stream);
 
 // n / d and n % d for n < 2^31 by a multiplication (d >= 1): with s = ceil(log2 d) and m = ceil(2^(31 + s) / d), m fits 32
 // bits and m n / 2^(31 + s) exceeds n / d by less than 1 / d.
@@ -74,6 +59,38 @@ struct FastDiv {
     return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> (31 + s));
   }
 };
+
+// Up to two operand copies in one launch (none: no launch).
+struct CopyJob {
+  const void* src;
+  int64_t ld, rows, ldp, plane;
+  uint16_t* dst;
+  int cols, vec;
+  FastDiv div;
+  const int* idx;    // with idx: rows idx[0 .. *count) of src, then zeros up to a multiple of 256 rows; nothing when
+  const int* count;  // *count == skip
+  int skip;
+};
+struct Copies {
+  int dtype, n = 0;
+  CopyJob job[2];
+  explicit Copies(int dt) : dtype(dt) {}
+  void add(const void* p, int64_t ld, int64_t rows, int64_t cols, void* copy, const int* idx = nullptr,
+           const int* count = nullptr, int skip = 0);
+  cudaError_t launch(int sms, cudaStream_t stream);
+};
+
+// A product with the linear epilogue (type dtype out, residual of type rdtype), through split partial sums when s.splits
+// > 1 (`partial`: `part_rows` rows of round_up(N, 8) floats, part_rows >= splits x round_up(M, 256); with a device count of
+// rows the device takes as many splits, up to s.splits, as are worth it and have room).
+cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt,
+                    gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int64_t part_rows, int sms, cudaStream_t stream);
+inline int64_t partial_rows(const gemm::Shape& s, int64_t M) { return s.splits > 1 ? s.splits * round_up(M, 256) : 0; }
+inline int64_t partial_bytes(const gemm::Shape& s, int64_t M, int64_t N) { return partial_rows(s, M) * round_up(N, 8) * 4; }
+
+// out[c] = sum over rows of part[r][c], in a fixed order; with `count`, only the first ceil(*count / per) rows
+cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, const int* count, int per, int cols, int64_t ld,
+                     const float* alpha, void* out, cudaStream_t stream);
 
 // launch attributes of a kernel that may start under the previous one's tail
 struct Launch {

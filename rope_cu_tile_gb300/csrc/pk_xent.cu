@@ -327,15 +327,29 @@ __global__ void __launch_bounds__(256) pk_xent_columns_kernel(const uint16_t* dz
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kColRows;
   griddep_wait();
   const int64_t n = __ldcg(count);
+  if (r0 >= n) return;  // (the sum stops at the count too)
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int kPlanes = DT == PK_F32 ? 3 : 1, kBatch = DT == PK_F32 ? 2 : 8;  // rows in flight
+  constexpr int kT = DT == PK_F16 ? PK_F16 : PK_BF16;
   if (c < cols) {
-    for (int64_t r = r0 + w; r < r0 + kColRows && r < n; r += 8) {
+#pragma unroll 1
+    for (int64_t rb = r0 + w; rb < r0 + kColRows && rb < n; rb += 8 * kBatch) {
+      Raw8<kT> q[kBatch][kPlanes];
 #pragma unroll
-      for (int k = 0; k < (DT == PK_F32 ? 3 : 1); ++k) {
-        float v[8];
-        load8<DT == PK_F16 ? PK_F16 : PK_BF16>(dz + k * plane, r * ld + c, v);
+      for (int i = 0; i < kBatch; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        for (int k = 0; k < kPlanes; ++k)
+          if (rb + 8 * i < n) q[i][k].load(dz + k * plane, (rb + 8 * i) * ld + c, true, 8);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (rb + 8 * i >= n) break;
+#pragma unroll
+        for (int k = 0; k < kPlanes; ++k) {
+          float v[8];
+          q[i][k].get(v);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) add2(sum[j], sum[j + 1], make_float2(v[j], v[j + 1]));
+        }
       }
     }
   }
@@ -455,19 +469,14 @@ struct Inputs {
 cudaError_t lay_out(int dtype, const Common& m, const void* x, int64_t ldx, const void* w, int64_t T, int D, int V, int sms,
                     cudaStream_t stream, Inputs* in) {
   // gathered rows; nothing to gather when all have labels and x can be read where it lies
-  cudaError_t e = cudaSuccess;
   in->alt = m.x_in_place;
-  e = copy_operand(dtype, x, ldx, m.cap, D, m.x, m.idx, m.count, m.x_in_place ? static_cast<int>(T) : -1, sms, stream);
-  if (e != cudaSuccess) return e;
+  Copies copies(dtype);
+  copies.add(x, ldx, m.cap, D, m.x, m.idx, m.count, m.x_in_place ? static_cast<int>(T) : -1);
+  if (m.w) copies.add(w, D, V, D, m.w);
   in->xc = operand_of_copy(dtype, m.x, m.cap, D, 0);
   in->xd = operand(dtype, x, ldx, T, D, 0);
-  if (m.w) {
-    if ((e = copy_operand(dtype, w, D, V, D, m.w, nullptr, nullptr, 0, sms, stream)) != cudaSuccess) return e;
-    in->w = operand_of_copy(dtype, m.w, V, D, 0);
-  } else {
-    in->w = operand(dtype, w, D, V, D, 0);
-  }
-  return cudaSuccess;
+  in->w = m.w ? operand_of_copy(dtype, m.w, V, D, 0) : operand(dtype, w, D, V, D, 0);
+  return copies.launch(sms, stream);
 }
 
 // rows [v0, v0 + n) of W
@@ -702,7 +711,7 @@ int pk_cross_entropy_backward(int dtype, const void* x, int64_t ldx, const void*
         ce = cudaLaunchKernelEx(&l.cfg, pk_xent_columns_kernel<PK_BF16>, z, b.dz_ld, b.dz_plane, n, count, b.part);
       else
         ce = cudaLaunchKernelEx(&l.cfg, pk_xent_columns_kernel<PK_F16>, z, b.dz_ld, b.dz_plane, n, count, b.part);
-      if (ce != cudaSuccess || rows::sum_rows(dtype, b.part, b.blocks, n, b.dz_ld, alpha, static_cast<char*>(db) + v0 * e,
+      if (ce != cudaSuccess || rows::sum_rows(dtype, b.part, b.blocks, count, kColRows, n, b.dz_ld, alpha, static_cast<char*>(db) + v0 * e,
                                               stream) != cudaSuccess)
         return PK_ERR_CUDA;
     }
