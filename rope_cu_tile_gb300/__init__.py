@@ -507,7 +507,8 @@ def _vector(t, n, what, dtype, dev):
 
 
 def _dense(t, rows, cols, what, dtype, dev):
-    if _rows(t, cols, what, dtype, dev, rows) != max(cols, 1) or not t.is_contiguous():
+    if tuple(t.shape) != (rows, cols) or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+        _rows(t, cols, what, dtype, dev, rows)
         raise ValueError(f"{what} must be contiguous")
 
 

@@ -78,9 +78,15 @@ __global__ void __launch_bounds__(kScan) pk_xent_index_kernel(const __grid_const
   __shared__ float top[32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   griddep_wait();
-  // labelled rows before this block, and the largest |dloss| of all
+  // labelled rows before this block, and the largest |dloss| of all (one block finds its own; more read what
+  // pk_xent_count_kernel found)
   int before = 0;
   float m = 0.0f;
+  if (gridDim.x == 1) {
+    const int64_t t = threadIdx.x;
+    long long l;
+    if (has_label(a, t, l) && a.dloss) m = fabsf(__ldcg(a.dloss + t));
+  } else
   for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += kScan) {
     if (b < static_cast<int>(blockIdx.x)) before += __ldcg(a.counts + b);
     m = fmaxf(m, __ldcg(a.maxima + b));
@@ -141,8 +147,11 @@ __global__ void __launch_bounds__(kScan) pk_xent_index_kernel(const __grid_const
 
 cudaError_t rows_launch(const RowArgs& a, cudaStream_t stream) {
   Launch l((a.T + kScan - 1) / kScan, kScan, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, pk_xent_count_kernel, a);
-  return e != cudaSuccess ? e : cudaLaunchKernelEx(&l.cfg, pk_xent_index_kernel, a);
+  if (a.T > kScan) {
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, pk_xent_count_kernel, a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&l.cfg, pk_xent_index_kernel, a);
 }
 
 // ------------------------------------------------------------------------------------
@@ -212,35 +221,29 @@ struct StatEpi {
   }
 };
 
-// Joins the slices of each row, in a fixed order: 32 rows x 8 strided lanes of slices a block.
-__global__ void __launch_bounds__(256) pk_xent_join_kernel(const float2* part, int64_t cap, int slices,
-                                                           const float* picked, const int* idx,
-                                                           const int* count, float* loss, float* lse) {
-  __shared__ float2 s[8][32];
-  const int r = threadIdx.x & 31, g = threadIdx.x >> 5;
+// Joins the slices of each row, in a fixed order: 8 rows x 32 strided lanes of slices a block.
+__global__ void __launch_bounds__(256) pk_xent_join_kernel(const float2* part, int64_t cap, int slices, const float* picked,
+                                                           const int* idx, const int* count, float* loss, float* lse) {
+  __shared__ float2 s[32][8];
+  const int r = threadIdx.x & 7, g = threadIdx.x >> 3;
   griddep_wait();
   const int n = __ldcg(count);
-  for (int64_t r0 = blockIdx.x * 32LL; r0 < n; r0 += gridDim.x * 32LL) {
+  const auto join = [](float& m, float& l, float2 q) {
+    const float mn = fmaxf(m, q.x);
+    l = l * exp2f((m - mn) * kLog2e) + q.y * exp2f((q.x - mn) * kLog2e);
+    m = mn;
+  };
+  for (int64_t r0 = blockIdx.x * 8LL; r0 < n; r0 += gridDim.x * 8LL) {
     const int64_t row = r0 + r;
     float m = kFloor, l = 0.0f;
     if (row < n) {
 #pragma unroll 4
-      for (int i = g; i < slices; i += 8) {
-        const float2 q = __ldcg(part + i * cap + row);
-        const float mn = fmaxf(m, q.x);
-        l = l * exp2f((m - mn) * kLog2e) + q.y * exp2f((q.x - mn) * kLog2e);
-        m = mn;
-      }
+      for (int i = g; i < slices; i += 32) join(m, l, __ldcg(part + i * cap + row));
     }
     s[g][r] = make_float2(m, l);
     __syncthreads();
     if (g == 0 && row < n) {
-      for (int i = 1; i < 8; ++i) {
-        const float2 q = s[i][r];
-        const float mn = fmaxf(m, q.x);
-        l = l * exp2f((m - mn) * kLog2e) + q.y * exp2f((q.x - mn) * kLog2e);
-        m = mn;
-      }
+      for (int i = 1; i < 32; ++i) join(m, l, s[i][r]);
       const float all = m + logf(l);
       const int t = __ldcg(idx + row);
       lse[t] = all;
@@ -319,7 +322,7 @@ struct GradEpi {
 // Column sums of dz over blocks of rows (db): a warp takes 256 columns of a row, 8 a lane.
 constexpr int kColRows = 128;
 template <int DT>
-__global__ void __launch_bounds__(256) pk_xent_columns_kernel(const uint16_t* dz, int64_t ld, int64_t plane,
+__global__ void __launch_bounds__(256, 4) pk_xent_columns_kernel(const uint16_t* dz, int64_t ld, int64_t plane,
                                                               int cols, const int* count, float* part) {
   __shared__ float sums[8][256];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -579,7 +582,7 @@ int pk_cross_entropy(int dtype, const void* x, int64_t ldx, const void* w, const
   sp.cap = f.m.cap;
   if (logits_product<StatEpi>(dtype, in.xc, in.w, in.alt ? &in.xd : nullptr, a, sp, f.shape, d.sms, stream) != cudaSuccess)
     return PK_ERR_CUDA;
-  const int64_t blocks = (T + 31) / 32, most = static_cast<int64_t>(d.sms) * 8;
+  const int64_t blocks = (T + 7) / 8, most = static_cast<int64_t>(d.sms) * 8;
   rows::Launch l(blocks < most ? blocks : most, 256, stream);
   const float2* part = f.part;
   const float* picked = f.picked;
