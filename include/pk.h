@@ -64,7 +64,8 @@
  *   PK_DEBUG_SKIP_ARRIVE=1 test hook of the tensor-core kernels, read at every call: the
  *                          producer of each CTA withholds its first work-item hand-off, so
  *                          the call ends with PK_ERR_TIMEOUT after one wait bound and writes
- *                          no valid output; later calls without it are unaffected.
+ *                          no valid output; later calls without it are unaffected. In the
+ *                          token-row operators' products it withholds the first operand stage.
  *   PK_ATTN=q4|tc_single   pk_attend and its typed forms run PK_KERNEL_Q4 or
  *                          PK_KERNEL_TC_SINGLE instead of PK_KERNEL_TC for bf16 / fp16 inputs
  *                          outside the narrow windows (read at every call).
@@ -399,7 +400,7 @@ int pk_linear_backward_workspace(int dtype, const void *x, int64_t ldx, const vo
                                  double p, int need_dx, int need_dw, int need_db, int64_t T, int N, int K, int64_t *bytes);
 
 /*
- * Dropout: y = r + x keep / (1 - p), 0 <= p < 1 taken to the nearest multiple of 2^-16. keep(t, n)
+ * Dropout: y = r + x keep / (1 - p), 0 <= p < 1 - 2^-17, taken to the nearest multiple of 2^-16. keep(t, n)
  * depends on seed, offset, t and n alone (Philox4x32-10 of Salmon, Moraes, Dror and Shaw, SC 2011:
  * key seed, counter (n / 8, t, offset), element n the (n mod 8)th 16 bits of the four words, low
  * half first, kept when they are at least p 65536). The gradient is the same call on dy

@@ -519,8 +519,8 @@ def _act_code(act):
 
 
 def _drop_check(p, seed, offset):
-    if not 0.0 <= p < 1.0:
-        raise ValueError(f"p must be in [0, 1), not {p}")
+    if not 0.0 <= p < 1.0 - 2.0**-17:
+        raise ValueError(f"p must be in [0, 1 - 2^-17), not {p}")
     if not 0 <= seed < 1 << 64 or not 0 <= offset < 1 << 64:
         raise ValueError("seed and offset must be unsigned 64-bit numbers")
 
@@ -541,9 +541,8 @@ def _ptr(t):
 
 def _disjoint(out, what, *inputs):
     """An output that the caller gives must not share memory with what the call reads while it writes it."""
-    a, b = out.data_ptr(), out.data_ptr() + _extent(out)
     for t in inputs:
-        if t is not None and t.data_ptr() < b and a < t.data_ptr() + _extent(t):
+        if t is not None and _overlap(out, t):
             raise ValueError(f"{what} overlaps an input")
 
 
@@ -551,6 +550,20 @@ def _extent(t):
     if t.numel() == 0:
         return 0
     return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _overlap(a, b):
+    """Whether two tensors can share an element: their address ranges meet and they are not different columns of rows of
+    one stride (slices of one wider matrix)."""
+    pa, pb = a.data_ptr(), b.data_ptr()
+    if not (pa < pb + _extent(b) and pb < pa + _extent(a)):
+        return False
+    if a.dim() == 2 and b.dim() == 2 and a.stride(0) == b.stride(0) and a.element_size() == b.element_size():
+        row = a.stride(0) * a.element_size()
+        d = (pb - pa) % row  # b's first column, counted from a's
+        if d >= a.shape[1] * a.element_size() and d + b.shape[1] * b.element_size() <= row:
+            return False
+    return True
 
 
 def _same_place(a, b):

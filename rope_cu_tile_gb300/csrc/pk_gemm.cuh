@@ -60,6 +60,7 @@ struct Args {
   int alt_operand;  // 0: A, 1: B
   int* status;
   unsigned long long timeout_ns;
+  int skip_first_arrive;  // test hook (PK_DEBUG_SKIP_ARRIVE=1): the loading warp withholds its first arrival
 };
 
 // One unit of work: an output tile and its range of k steps.
@@ -257,7 +258,7 @@ template <int CG>
 __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap* mb, const Args& a, const Plan& p,
                                         uint8_t* smem, Meta* meta, uint32_t rank, int unit0, int unit_step) {
   uint32_t st = 0, ph = 0;
-  bool bad = false;
+  bool bad = false, withhold = a.skip_first_arrive != 0;
   uint32_t full0 = smem_u32(&meta->full[0]);
   if constexpr (CG == 2) full0 = mapa(full0, 0);
   for (int u = unit0; u < p.units && !bad; u += unit_step) {
@@ -274,20 +275,21 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
         const uint32_t sa = smem_u32(smem + st * kStageBytes), sb = sa + kOpBytes;
         const int k = kb * kBK;
         if (elect_one()) {
-        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&meta->full[st]), CG * kStageBytes);
-        if (a.a_mn) {
-          tma_load_3d<CG>(sa, ma, bar, ra, k, pa);
-          tma_load_3d<CG>(sa + kOpBytes / 2, ma, bar, ra + 64, k, pa);
-        } else {
-          tma_load_3d<CG>(sa, ma, bar, k, ra, pa);
+          if (rank == 0 && !withhold) mbar_arrive_expect_tx(smem_u32(&meta->full[st]), CG * kStageBytes);
+          if (a.a_mn) {
+            tma_load_3d<CG>(sa, ma, bar, ra, k, pa);
+            tma_load_3d<CG>(sa + kOpBytes / 2, ma, bar, ra + 64, k, pa);
+          } else {
+            tma_load_3d<CG>(sa, ma, bar, k, ra, pa);
+          }
+          if (a.b_mn) {
+            tma_load_3d<CG>(sb, mb, bar, rb, k, pb);
+            tma_load_3d<CG>(sb + kOpBytes / 2, mb, bar, rb + 64, k, pb);
+          } else {
+            tma_load_3d<CG>(sb, mb, bar, k, rb, pb);
+          }
         }
-        if (a.b_mn) {
-          tma_load_3d<CG>(sb, mb, bar, rb, k, pb);
-          tma_load_3d<CG>(sb + kOpBytes / 2, mb, bar, rb + 64, k, pb);
-        } else {
-          tma_load_3d<CG>(sb, mb, bar, k, rb, pb);
-        }
-        }
+        withhold = false;
         __syncwarp();
         st = st + 1 == kStages ? 0 : st + 1;
         ph ^= st == 0 ? 1u : 0u;
@@ -393,6 +395,8 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
     const bool alt = a.dyn && __ldcg(a.dyn) == a.alt_count;
     const CUtensorMap* ma = alt && a.alt_operand == 0 ? &map_alt : &map_a;
     const CUtensorMap* mb = alt && a.alt_operand == 1 ? &map_alt : &map_b;
+    // operands that an earlier kernel wrote with ordinary stores, before TMA reads them
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     produce<CG>(ma, mb, a, p, smem, meta, rank, unit0, unit_step);
   } else if (warp == 1) {
     if (rank == 0) issue<CG>(a, p, smem, meta, tmem, unit0, unit_step);
@@ -431,7 +435,8 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
         break;
       if (!zero) ++n;
     }
-    // tiles stored by TMA are written before the CTA leaves
+    // copies in flight (a warp that gave up) land, and tiles stored by TMA are written, before the CTA leaves
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
   }
@@ -450,6 +455,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn encode_fn();
+int debug_skip_arrive();  // PK_DEBUG_SKIP_ARRIVE, read at every call
 
 // A 16-bit operand as the product reads it: `rows` x `cols` with cols contiguous, `ld` elements apart, `planes` of them
 // `plane` elements apart. Base 16-byte aligned, ld and plane multiples of 8.
@@ -500,6 +506,7 @@ cudaError_t launch(const Operand& A, const Operand& B, const Operand* alt, Args 
   a.terms = A.planes == 3 ? kTerms32 : 1;
   a.splits = s.splits;
   a.slots = sms / s.cg;
+  a.skip_first_arrive = debug_skip_arrive();
   const int64_t tile = 128 * s.cg;
   const int64_t units = ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile) * s.splits;
   int64_t ctas = units < sms / s.cg ? units : sms / s.cg;

@@ -1,6 +1,7 @@
 // pk_rows.cu -- shared passes of the token-row operators: tensor maps, the cut of a product into tiles and splits, operand
 // copies, the sum of split partial sums with the epilogue, column sums, and the product's launches.
 #include <atomic>
+#include <cstdlib>
 #include <mutex>
 
 #include "pk_rows.cuh"
@@ -21,6 +22,11 @@ EncodeTiledFn encode_fn() {
     return reinterpret_cast<EncodeTiledFn>(p);
   }();
   return fn;
+}
+
+int debug_skip_arrive() {
+  const char* e = std::getenv("PK_DEBUG_SKIP_ARRIVE");
+  return e && e[0] == '1' ? 1 : 0;
 }
 
 bool make_map(CUtensorMap* map, const Operand& o) {

@@ -18,20 +18,29 @@ U = {torch.bfloat16: 2.0**-9 * 2, torch.float16: 2.0**-12 * 2, torch.float32: 2.
 # (torch.finfo(t).eps / 2: 2^-8, 2^-11, 2^-24)
 
 
-def keep_mask(T, N, p, seed, offset):
-    """bool [T, N] from the published generator, in Python-independent uint64 arithmetic."""
+def pieces(col8, row, seed, offset):
+    """uint64 [len, 8]: the generator's 16-bit pieces for arrays of column groups and rows, in unsigned 64-bit arithmetic."""
     u = np.uint64
     m = u(0xFFFFFFFF)
-    G = (N + 7) // 8
-    c = [np.tile(np.arange(G, dtype=u), T), np.repeat(np.arange(T, dtype=u), G), np.full(T * G, offset & 0xFFFFFFFF, dtype=u),
-         np.full(T * G, offset >> 32, dtype=u)]
+    c = [np.asarray(col8, dtype=u), np.asarray(row, dtype=u)]
+    c += [np.full(c[0].shape, offset & 0xFFFFFFFF, dtype=u), np.full(c[0].shape, offset >> 32, dtype=u)]
     k = [seed & 0xFFFFFFFF, seed >> 32]
     for _ in range(10):
         a, b = c[0] * u(0xD2511F53), c[2] * u(0xCD9E8D57)
         c = [(b >> u(32)) ^ c[1] ^ u(k[0]), b & m, (a >> u(32)) ^ c[3] ^ u(k[1]), a & m]
         k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
-    bits = np.stack([h for w in c for h in (w & u(0xFFFF), w >> u(16))], -1).reshape(T, G * 8)[:, :N]
-    return bits >= u(math.floor(p * 65536 + 0.5))
+    return np.stack([h for w in c for h in (w & u(0xFFFF), w >> u(16))], -1)
+
+
+def keep_mask(T, N, p, seed, offset):
+    """bool [T, N]: the elements that dropout keeps."""
+    G = (N + 7) // 8
+    bits = pieces(np.tile(np.arange(G), T), np.repeat(np.arange(T), G), seed, offset).reshape(T, G * 8)[:, :N]
+    return bits >= np.uint64(math.floor(p * 65536 + 0.5))
+
+
+def keep_mask_at(col8, row, cut, seed, offset):
+    return pieces([col8], [row], seed, offset)[0] >= np.uint64(cut)
 
 
 def drop_factor(T, N, p, seed, offset, device):

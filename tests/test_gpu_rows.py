@@ -390,3 +390,44 @@ def test_no_rows(pk):
         assert loss.shape == (0,)
         dx, dw, db = pk.cross_entropy_backward(x, w, labels, lse, loss, bias=torch.ones(40, dtype=dtype, device="cuda"))
         assert dx.shape == (0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
+
+
+_STALL_SCRIPT = r"""
+import json, os, sys
+sys.path.insert(0, os.environ["ROOT"])
+import torch
+import rope_cu_tile_gb300 as pk
+torch.manual_seed(3)
+got = []
+for T, K, N in ((300, 256, 264), (9000, 128, 1024)):  # one CTA a tile, and pairs
+    x, w = torch.randn(T, K, device="cuda").bfloat16(), torch.randn(N, K, device="cuda").bfloat16()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = pk.linear(x, w)
+    os.environ["PK_DEBUG_SKIP_ARRIVE"] = "1"
+    pk.linear(x, w, status=status)
+    torch.cuda.synchronize()
+    pk.linear(x, w)
+    torch.cuda.synchronize()
+    del os.environ["PK_DEBUG_SKIP_ARRIVE"]
+    word = pk.last_status()
+    after = pk.linear(x, w)
+    torch.cuda.synchronize()
+    got.append([int(status), word, pk.last_status(), bool(torch.equal(after, want))])
+print(json.dumps(got))
+"""
+
+
+def test_withheld_stage_times_out_and_the_context_stays_usable():
+    """The loading warp withholds its first arrival (test hook): every wait of the product runs out, the call ends with
+    PK_ERR_TIMEOUT in the status word given or the device's, and the next call is right. Nothing traps or hangs."""
+    import json
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, ROOT=root, PK_TIMEOUT_MS="100")
+    env.pop("PK_DEBUG_SKIP_ARRIVE", None)
+    p = subprocess.run([sys.executable, "-c", _STALL_SCRIPT], env=env, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-3000:]
+    assert json.loads(p.stdout.strip().splitlines()[-1]) == [[6, 6, 0, True]] * 2
