@@ -381,7 +381,10 @@ enum pk_act {
  *   pre [T, N] or NULL: z = x W^T + b, which pk_linear_backward needs when act is not PK_ACT_NONE.
  *   p, seed, offset: dropout of act(z) before the residual, as pk_dropout (p = 0: none).
  *   y may be residual itself (ldy = ldr).
+ * A few rows (serving: up to PK_LINEAR_FEW_T of fp32, half of that in 16 bits) run on the CUDA cores in
+ * one launch, fp32 throughout, without a workspace; more on the tensor cores.
  */
+#define PK_LINEAR_FEW_T 8
 int pk_linear(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, const void *residual, int64_t ldr,
               int act, double p, uint64_t seed, uint64_t offset, int64_t T, int N, int K, void *y, int64_t ldy, void *pre,
               void *workspace, int64_t workspace_bytes, int *status, struct CUstream_st *stream);

@@ -32,6 +32,7 @@ STATUS = {
 }
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NOALLOC_MAX_T = 1048576
+LINEAR_FEW_T = 8  # include/pk.h: half as many rows of any type need no workspace in linear
 
 # names declared in include/pk.h
 EXPORTS = ("pk_attend", "pk_attend_bf16", "pk_attend_f16", "pk_attend_f32", "pk_attend_dt",
@@ -131,7 +132,7 @@ def status_string(code: int) -> str:
 
 
 def _check(rc: int, what: str):
-    if rc != 0:
+    if rc:
         raise PKError(rc, what)
 
 
@@ -602,8 +603,9 @@ def linear(x, w, bias=None, residual=None, act: str = "none", p: float = 0.0, se
     def call(st):
         y = torch.empty((T, N), dtype=dt, device=dev) if out is None else out
         pre = torch.empty((T, N), dtype=dt, device=dev) if return_pre else None
-        ws, wp, wb = _workspace("pk_linear_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), T, N, K)
-        _check(_lib.pk_linear(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), _ptr(residual), ldr, a, p, seed, offset, T,
+        ws, wp, wb = (None, None, 0) if 2 * T <= LINEAR_FEW_T else _workspace("pk_linear_workspace", dev, code, x.data_ptr(), ldx,
+                                                                          w.data_ptr(), T, N, K)
+        _check(load().pk_linear(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), _ptr(residual), ldr, a, p, seed, offset, T,
                               N, K, y.data_ptr(), ldy, _ptr(pre), wp, wb, _ptr(status), st), "pk_linear")
         return (y, pre) if return_pre else y
 

@@ -127,11 +127,13 @@ cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
 // ------------------------------------------------------------------------------------
 // a few rows (serving): y for up to kFewRows rows of x
 
-// Bound by W's bytes, read once; x (at most 16 rows) stays in L1. A warp dots kR rows of W with every row of x, 8 elements a lane
-// and step, in fp32 on the CUDA cores (2 T operations an element of W are below the memory's time up to 16 rows, and fp32
-// inputs need no planes); where N alone gives too few warps, several share the rows and split k. One launch, no scratch.
-constexpr int kFewRows = 16;
+// Bound by W's bytes, read once; x stays in L1. A warp dots kR rows of W with every row of x, 8 elements a lane and step, in
+// fp32 on the CUDA cores (fp32 inputs need no planes); where N alone gives too few warps, several share the rows and split
+// k, so that most of W is on its way at once. One launch, no scratch. Past a few rows its arithmetic and the reads of x
+// outweigh the tensor cores' fixed costs: W [4096, 1024] in bf16 took 3.5 us at 1 row, 6.5 at 4, 11.9 at 8, and 7.3 there;
+// fp32 10.5 at 8 rows here and some 19 there, with its plane copies.
 constexpr int kFewThreads = 256;
+bool few_rows(int dtype, int64_t T) { return T <= (dtype == PK_F32 ? PK_LINEAR_FEW_T : PK_LINEAR_FEW_T / 2); }
 
 struct FewArgs {
   const void* x;
@@ -143,48 +145,60 @@ struct FewArgs {
   LinParams ep;
 };
 
-template <int DT, int TM, int R>
+// rows of W a warp, and steps of k asked for together: as many 16-byte loads in flight as the registers of 16 warps an SM hold
+__host__ __device__ constexpr int few_r(int dt, int tm) { return dt == PK_F32 && tm < 8 ? 2 : 4; }
+__host__ __device__ constexpr int few_steps(int dt) { return dt == PK_F32 ? 1 : 2; }
+
+template <int DT, int TM>
 __global__ void __launch_bounds__(kFewThreads) pk_linear_few_kernel(const __grid_constant__ FewArgs a) {
-  __shared__ float part[8][R * TM];
+  constexpr int kR = few_r(DT, TM), kFewSteps = few_steps(DT);
+  __shared__ float part[8][kR * TM];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int group = w / a.share, sub = w % a.share, groups = 8 / a.share;
-  const int n0 = (blockIdx.x * groups + group) * R;
-  float acc[R][TM];
+  const int n0 = (blockIdx.x * groups + group) * kR;
+  float acc[kR][TM];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < kR; ++r)
 #pragma unroll
     for (int t = 0; t < TM; ++t) acc[r][t] = 0.0f;
   griddep_wait();
   if (n0 < a.N) {
-#pragma unroll 2
-    for (int k = sub * 256 + lane * 8; k < a.K; k += a.share * 256) {
-      float q[R][8];
-      const bool whole = a.vec && k + 8 <= a.K;
+    const int step = a.share * 256;
+#pragma unroll 1
+    for (int k0 = sub * 256 + lane * 8; k0 < a.K; k0 += kFewSteps * step) {
+      Raw8<DT> q[kFewSteps][kR];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int64_t at = static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.K + k;
-        if (whole)
-          load8<DT>(a.w, at, q[r]);
-        else
-          load8_any<DT>(a.w, at, a.K - k, q[r]);
-      }
+      for (int s = 0; s < kFewSteps; ++s)
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        float x[8];
-        const int64_t at = min(t, a.T - 1) * a.ldx + k;
-        if (whole)
-          load8<DT, true>(a.x, at, x);
-        else
-          load8_any<DT>(a.x, at, a.K - k, x);
+        for (int r = 0; r < kR; ++r) {
+          const int k = k0 + s * step;
+          if (k < a.K) q[s][r].load(a.w, static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.K + k, a.vec, a.K - k);
+        }
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+      for (int s = 0; s < kFewSteps; ++s) {
+        const int k = k0 + s * step;
+        if (k >= a.K) break;
+        float v[kR][8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(q[r][j], x[j], acc[r][t]);
+        for (int r = 0; r < kR; ++r) q[s][r].get(v[r]);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+          float x[8];
+          const int64_t at = min(t, a.T - 1) * a.ldx + k;
+          if (a.vec && k + 8 <= a.K)
+            load8<DT, true>(a.x, at, x);
+          else
+            load8_any<DT>(a.x, at, a.K - k, x);
+#pragma unroll
+          for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(v[r][j], x[j], acc[r][t]);
+        }
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < kR; ++r)
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
 #pragma unroll
@@ -192,8 +206,8 @@ __global__ void __launch_bounds__(kFewThreads) pk_linear_few_kernel(const __grid
       if (lane == 0) part[w][r * TM + t] = acc[r][t];
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < groups * R * TM; i += kFewThreads) {
-    const int g = i / (R * TM), e = i % (R * TM), t = e % TM, n = (blockIdx.x * groups + g) * R + e / TM;
+  for (int i = threadIdx.x; i < groups * kR * TM; i += kFewThreads) {
+    const int g = i / (kR * TM), e = i % (kR * TM), t = e % TM, n = (blockIdx.x * groups + g) * kR + e / TM;
     if (t >= a.T || n >= a.N) continue;
     float v = 0.0f;
     for (int s = 0; s < a.share; ++s) v += part[g * a.share + s][e];
@@ -201,18 +215,22 @@ __global__ void __launch_bounds__(kFewThreads) pk_linear_few_kernel(const __grid
   }
 }
 
-template <int DT>
-cudaError_t few_launch(FewArgs a, int sms, cudaStream_t stream) {
-  // as many rows of W a warp as amortise the reads of x, halved k until there are some 16 warps an SM
-  const int R = a.T <= 4 ? 2 : 4;
+template <int DT, int TM>
+cudaError_t few_launch_rows(FewArgs a, int sms, cudaStream_t stream) {
+  constexpr int kR = few_r(DT, TM);
   a.share = 1;
-  while (a.share < 8 && static_cast<int64_t>(a.N) / R * a.share < 16 * sms && a.K > 256 * a.share) a.share *= 2;
-  const int per_block = 8 / a.share * R;
+  while (a.share < 8 && static_cast<int64_t>(a.N) / kR * a.share < 16 * sms && a.K > 256 * a.share) a.share *= 2;
+  const int per_block = 8 / a.share * kR;
   Launch l((a.N + per_block - 1) / per_block, kFewThreads, stream);
-  if (a.T == 1) return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 1, 2>, a);
-  if (a.T <= 4) return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 4, 2>, a);
-  if (a.T <= 8) return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 8, 4>, a);
-  return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, 16, 4>, a);
+  return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, TM>, a);
+}
+template <int DT>
+cudaError_t few_launch(const FewArgs& a, int sms, cudaStream_t stream) {
+  if (a.T == 1) return few_launch_rows<DT, 1>(a, sms, stream);
+  if (a.T == 2) return few_launch_rows<DT, 2>(a, sms, stream);
+  if constexpr (DT == PK_F32)
+    if (a.T > 4) return few_launch_rows<DT, 8>(a, sms, stream);
+  return few_launch_rows<DT, 4>(a, sms, stream);
 }
 
 // ------------------------------------------------------------------------------------
@@ -227,7 +245,7 @@ struct Fwd {
 Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T, int N, int K, int sms, void* ws) {
   Fwd f = {};
   Carver c(ws);
-  if (T <= kFewRows) return f;
+  if (few_rows(dtype, T)) return f;
   f.x = in_place(dtype, x, ldx) ? nullptr : c.take(copy_bytes(dtype, T, K));
   f.w = in_place(dtype, w, K) ? nullptr : c.take(copy_bytes(dtype, N, K));
   f.shape = gemm::pick_shape(T, N, K, dtype == PK_F32 ? gemm::kTerms32 : 1, sms, true);
@@ -320,7 +338,7 @@ int pk_linear(int dtype, const void* x, int64_t ldx, const void* w, const void* 
   ep.pre = pre;
   ep.ldpre = N;
   ep.act = act;
-  if (T <= kFewRows) {
+  if (few_rows(dtype, T)) {
     const FewArgs fa = {x, w, ldx, static_cast<int>(T), N, K, 1, rows16(x, ldx, e) && rows16(w, K, e), ep};
     const cudaError_t r = dtype == PK_F32    ? few_launch<PK_F32>(fa, d.sms, stream)
                           : dtype == PK_BF16 ? few_launch<PK_BF16>(fa, d.sms, stream)

@@ -30,7 +30,7 @@ def check_status(pk):
 
 # ------------------------------------------------------------------------------------------ the projection
 
-SIZES = [(1, 8, 8), (1, 1, 1), (2, 64, 40), (5, 129, 3), (16, 256, 513), (17, 100, 264), (128, 64, 128), (129, 72, 136),
+SIZES = [(1, 8, 8), (1, 1, 1), (1, 4096, 77), (2, 64, 40), (3, 2056, 4100), (4, 300, 33), (5, 129, 3), (8, 264, 100), (16, 256, 513), (17, 100, 264), (128, 64, 128), (129, 72, 136),
          (251, 768, 768), (300, 65, 257), (1000, 515, 1003), (513, 1024, 264), (4096, 128, 512), (20000, 64, 256)]
 
 
