@@ -264,7 +264,8 @@ struct GradParams {
   const float* lse;
   int v0;            // first word of the piece
   CUtensorMap dz;    // [planes][cap, columns of the piece]
-  int64_t cap;
+  float* col;        // [cap / 32, ldcol] column sums of 32 rows each, or null
+  int64_t cap, ldcol;
 };
 
 template <int DT>
@@ -302,11 +303,20 @@ struct GradEpi {
         const float e = exp2_fast((v[i] - lse) * kLog2e);
         v[i] = live ? (label == c + i ? e - 1.0f : e) * g : 0.0f;  // rows past the count feed dW: zero
       }
+      // db: the column sums of the staged (rounded) tile, two columns and every other row a lane
+      const int pair = lane & 15, odd = lane >> 4;
+      float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < (DT == PK_F32 ? 3 : 1); ++k) {
         stored(lane);
         S::put(stage, lane, v);
         store_tile(&p.dz, stage, c, r0, k, lane);
+        if (p.col) {
+#pragma unroll
+          for (int r = 0; r < 32; r += 2)
+            add2(sum.x, sum.y,
+                 Elem<DT != PK_F16>::unpack(*reinterpret_cast<const uint32_t*>(S::slot(stage, r + odd, pair >> 2) + (pair & 3) * 4)));
+        }
         if constexpr (DT == PK_F32) {
           if (k < 2) {
 #pragma unroll
@@ -314,59 +324,17 @@ struct GradEpi {
           }
         }
       }
+      if (p.col) {
+        sum.x += __shfl_xor_sync(0xffffffffu, sum.x, 16);
+        sum.y += __shfl_xor_sync(0xffffffffu, sum.y, 16);
+        float* d = p.col + (r0 >> 5) * p.ldcol + c + 2 * pair;
+        if (odd == 0 && c + 2 * pair < N) d[0] = sum.x;
+        if (odd == 1 && c + 2 * pair + 1 < N) d[1] = sum.y;
+      }
     }
     return true;
   }
 };
-
-// Column sums of dz over blocks of rows (db): a warp takes 256 columns of a row, 8 a lane.
-constexpr int kColRows = 128;
-template <int DT>
-__global__ void __launch_bounds__(256, 4) pk_xent_columns_kernel(const uint16_t* dz, int64_t ld, int64_t plane,
-                                                              int cols, const int* count, float* part) {
-  __shared__ float sums[8][256];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.y * 256 + lane * 8;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kColRows;
-  griddep_wait();
-  const int64_t n = __ldcg(count);
-  if (r0 >= n) return;  // (the sum stops at the count too)
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  constexpr int kPlanes = DT == PK_F32 ? 3 : 1, kBatch = DT == PK_F32 ? 2 : 8;  // rows in flight
-  constexpr int kT = DT == PK_F16 ? PK_F16 : PK_BF16;
-  if (c < cols) {
-#pragma unroll 1
-    for (int64_t rb = r0 + w; rb < r0 + kColRows && rb < n; rb += 8 * kBatch) {
-      Raw8<kT> q[kBatch][kPlanes];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int k = 0; k < kPlanes; ++k)
-          if (rb + 8 * i < n) q[i][k].load(dz + k * plane, (rb + 8 * i) * ld + c, true, 8);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (rb + 8 * i >= n) break;
-#pragma unroll
-        for (int k = 0; k < kPlanes; ++k) {
-          float v[8];
-          q[i][k].get(v);
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) add2(sum[j], sum[j + 1], make_float2(v[j], v[j + 1]));
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sums[w][lane * 8 + j] = sum[j];
-  __syncthreads();
-  const int col = blockIdx.y * 256 + threadIdx.x;
-  if (col < cols) {
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v += sums[i][threadIdx.x];
-    part[static_cast<int64_t>(blockIdx.x) * ld + col] = v;
-  }
-}
 
 // ------------------------------------------------------------------------------------
 // plans
@@ -420,7 +388,7 @@ struct Bwd {
   gemm::Shape dz_shape, dx_shape, dw_shape;
   float *coef, *lse, *unscale, *acc, *part, *partial;
   uint16_t* dz;
-  int64_t dz_ld, dz_plane, dx_rows, blocks, bytes;
+  int64_t dz_ld, dz_plane, dx_rows, bytes;
 };
 Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, bool need_db, int64_t T, int D, int V, int sms,
                   void* ws) {
@@ -441,8 +409,7 @@ Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, bool nee
   b.dz_plane = b.m.cap * b.dz_ld;
   b.dz = static_cast<uint16_t*>(c.take(planes * b.dz_plane * 2));
   if (b.pieces > 1) b.acc = static_cast<float*>(c.take(b.m.cap * D * 4));
-  b.blocks = (T + kColRows - 1) / kColRows;
-  if (need_db) b.part = static_cast<float*>(c.take(b.blocks * b.dz_ld * 4));
+  if (need_db) b.part = static_cast<float*>(c.take(b.m.cap / 32 * b.dz_ld * 4));
   b.dz_shape = gemm::pick_shape(T, widest, D, terms, sms, false);
   // how many rows dx has is the device's to know: where even all of them would fill the SMs only a few times over, it may
   // split k as far as the memory of the partial sums goes
@@ -659,6 +626,8 @@ int pk_cross_entropy_backward(int dtype, const void* x, int64_t ldx, const void*
     gp.lse = b.lse;
     gp.v0 = v0;
     gp.cap = b.m.cap;
+    gp.col = db ? b.part : nullptr;
+    gp.ldcol = b.dz_ld;
     if (!gemm::make_out_map(&gp.dz, dtype == PK_F16 ? PK_F16 : PK_BF16, b.dz, b.m.cap, n, b.dz_ld, dtype == PK_F32 ? 3 : 1,
                             b.dz_plane))
       return PK_ERR_CUDA;
@@ -702,22 +671,9 @@ int pk_cross_entropy_backward(int dtype, const void* x, int64_t ldx, const void*
                         d.sms, stream) != cudaSuccess)
         return PK_ERR_CUDA;
     }
-    if (db) {
-      rows::Launch l(1, 256, stream);
-      l.cfg.gridDim = dim3(static_cast<unsigned int>(b.blocks), static_cast<unsigned int>((n + 255) / 256));
-      const uint16_t* z = b.dz;
-      const int* count = b.m.count;
-      cudaError_t ce;
-      if (dtype == PK_F32)
-        ce = cudaLaunchKernelEx(&l.cfg, pk_xent_columns_kernel<PK_F32>, z, b.dz_ld, b.dz_plane, n, count, b.part);
-      else if (dtype == PK_BF16)
-        ce = cudaLaunchKernelEx(&l.cfg, pk_xent_columns_kernel<PK_BF16>, z, b.dz_ld, b.dz_plane, n, count, b.part);
-      else
-        ce = cudaLaunchKernelEx(&l.cfg, pk_xent_columns_kernel<PK_F16>, z, b.dz_ld, b.dz_plane, n, count, b.part);
-      if (ce != cudaSuccess || rows::sum_rows(dtype, b.part, b.blocks, count, kColRows, n, b.dz_ld, alpha, static_cast<char*>(db) + v0 * e,
-                                              stream) != cudaSuccess)
-        return PK_ERR_CUDA;
-    }
+    if (db && rows::sum_rows(dtype, b.part, b.m.cap / 32, b.m.count, 32, n, b.dz_ld, alpha, static_cast<char*>(db) + v0 * e,
+                             stream) != cudaSuccess)
+      return PK_ERR_CUDA;
   }
   return PK_OK;
 }
