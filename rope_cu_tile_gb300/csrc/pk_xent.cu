@@ -167,6 +167,17 @@ struct StatParams {
   int64_t cap;
 };
 
+// v[i] = exp(v[i] + shift)
+__device__ __forceinline__ void exponentials(float (&v)[32], float shift) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    add2(v[i], v[i + 1], make_float2(shift, shift));
+    const float2 q = mul2(make_float2(v[i], v[i + 1]), make_float2(kLog2e, kLog2e));
+    v[i] = exp2_fast(q.x);
+    v[i + 1] = exp2_fast(q.y);
+  }
+}
+
 template <int DT>
 struct StatEpi {
   using Params = StatParams;
@@ -211,8 +222,12 @@ struct StatEpi {
       for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
       const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      exponentials(v, -mn);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s[i & 3] += exp2_fast((v[i] - mn) * kLog2e);
+      for (int i = 0; i < 32; i += 4) {
+        add2(s[0], s[1], make_float2(v[i], v[i + 1]));
+        add2(s[2], s[3], make_float2(v[i + 2], v[i + 3]));
+      }
       l = l * exp2_fast((m - mn) * kLog2e) + ((s[0] + s[1]) + (s[2] + s[3]));
       m = mn;
     }
@@ -283,7 +298,8 @@ struct GradEpi {
     }
     const int row = r0 + lane;
     const bool live = row < M;
-    const float g = live ? __ldcg(p.coef + row) : 0.0f, lse = live ? __ldcg(p.lse + row) : 0.0f;
+    // rows past the count feed dW: zero, as exp(z - inf) times 0
+    const float g = live ? __ldcg(p.coef + row) : 0.0f, lse = live ? __ldcg(p.lse + row) : INFINITY;
     const int label = live ? __ldcg(p.lab + row) - p.v0 : -1;
     const int end = min(cols, N - c0);
 #pragma unroll 1
@@ -298,10 +314,16 @@ struct GradEpi {
         if (cc + 32 >= end) done();
         if (p.bias) b.add(v);
       }
+      exponentials(v, -lse);
+      if (label >= c && label < c + 32) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float e = exp2_fast((v[i] - lse) * kLog2e);
-        v[i] = live ? (label == c + i ? e - 1.0f : e) * g : 0.0f;  // rows past the count feed dW: zero
+        for (int i = 0; i < 32; ++i) v[i] = label == c + i ? v[i] - 1.0f : v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 q = mul2(make_float2(v[i], v[i + 1]), make_float2(g, g));
+        v[i] = q.x;
+        v[i + 1] = q.y;
       }
       // db: the column sums of the staged (rounded) tile, two columns and every other row a lane
       const int pair = lane & 15, odd = lane >> 4;
