@@ -392,6 +392,43 @@ def test_no_rows(pk):
         assert dx.shape == (0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
 
 
+def test_offsets_past_32_bits(pk, gen):
+    """600000 rows of 4096: 2.4e9 elements a matrix. The last rows against the definition, the first beside them."""
+    T, K, N, dtype = 600000, 32, 4096, torch.bfloat16
+    rows = torch.tensor([0, 1, 299999, 524287, 524288, T - 2, T - 1], device="cuda")
+    x, w, bias = rand(gen, T, K, dtype=dtype), rand(gen, N, K, std=K**-0.5, dtype=dtype), rand(gen, N, dtype=dtype)
+    big = torch.empty(T, N, dtype=dtype, device="cuda").normal_(generator=gen)
+    y, pre = pk.linear(x, w, bias, big, "gelu", return_pre=True)
+    want, z, by, bz = ref.linear(x[rows], w, bias, big[rows], "gelu", 0.0, 0, 0)
+    assert ref.worst(y[rows], want, by) <= 1 and ref.worst(pre[rows], z, bz) <= 1
+    dx, dw, db = pk.linear_backward(x, w, big, pre, "gelu")
+    wx, bx = ref.linear_backward(x[rows], w, big[rows], pre[rows], "gelu", 0.0, 0, 0)
+    assert ref.worst(dx[rows], wx[0], bx[0]) <= 1
+    dz = torch.cat([b.float() * ref.act_slope(p.float(), "gelu").float() for b, p in
+                    zip(big[:, 4000:].split(100000), pre[:, 4000:].split(100000))]).double()
+    u = ref.U[dtype]
+    bound = u * db[4000:].double().abs() + (T * 2.0**-23 + 2.0**-16) * dz.abs().sum(0)
+    assert ref.worst(db[4000:], dz.sum(0), bound) <= 1
+    del y, dx, dw, db, dz
+    y = pk.dropout(big, 0.25, SEED, OFFSET, residual=pre)
+    keep = torch.from_numpy(ref.pieces(list(range(512)) * len(rows), [int(r) for r in rows for _ in range(512)], SEED, OFFSET)
+                            .reshape(len(rows), N).astype("int32")).cuda() >= 16384
+    want = big[rows].double() * keep / 0.75 + pre[rows].double()
+    assert ref.worst(y[rows], want, 2.0**-22 * (want.abs() + 2 * big[rows].double().abs()) + u * want.abs()) <= 1
+    del y, big, pre
+    V = 5000
+    x, w = x[:, :16].contiguous(), rand(gen, V, 16, dtype=dtype)
+    labels = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    loss, lse = pk.cross_entropy(x, w, labels)
+    (wl, ws), bound = ref.cross_entropy(x[rows], w, labels[rows], None)
+    assert ref.worst(lse[rows], ws, bound) <= 1 and ref.worst(loss[rows], wl, 2 * bound) <= 1
+    dloss = torch.ones(T, device="cuda")
+    dx, dw, _ = pk.cross_entropy_backward(x, w, labels, lse, dloss)
+    wx, bx = ref.cross_entropy_backward(x[rows], w, labels[rows], lse[rows], dloss[rows], None)
+    assert ref.worst(dx[rows], wx[0], bx[0]) <= 1
+    check_status(pk)
+
+
 _STALL_SCRIPT = r"""
 import json, os, sys
 sys.path.insert(0, os.environ["ROOT"])
