@@ -33,6 +33,11 @@ constexpr uint32_t kOffEpi = kStages * kStageBytes;
 constexpr uint32_t kOffMeta = kOffEpi + kEpiBytes;
 constexpr int kTerms32 = 6;                   // plane pairs of an fp32 product
 constexpr int kGroupM = 8;                    // tile rows walked together
+// The tensor pipe truncates when it adds to an accumulator, so a long sum drifts towards zero by some 2^-25 of itself a step
+// of 16: nothing beside a 16-bit result, but 8e-5 over 100000 terms where fp32 allows 1e-5. fp32 operands therefore add up
+// at most this many k steps (1024 terms) before the epilogue's warps take the sum over, rounding to nearest, into the other
+// accumulator's tensor memory.
+constexpr int kPhase = 16;
 
 struct Meta {
   uint64_t full[kStages], empty[kStages];
@@ -72,6 +77,8 @@ struct Unit {
 
 struct Plan {
   int M, N, tiles_m, tiles_n, kb_all, kb_per, units, splits;
+  int phase;   // k steps that the tensor pipe adds up by itself
+  bool phased; // more than one phase a unit: accumulator 0 only, sums in accumulator 1's place
 };
 
 // Rows between the partial sums of two splits.
@@ -114,6 +121,8 @@ __device__ __forceinline__ Plan make_plan(const Args& a) {
   p.splits = choose_splits<CG>(a, p.M);
   p.kb_per = (p.kb_all + p.splits - 1) / p.splits;
   p.units = p.tiles_m * p.tiles_n * p.splits;
+  p.phased = a.terms > 1 && p.kb_per > kPhase;
+  p.phase = p.phased ? kPhase : p.kb_per;
   return p;
 }
 
@@ -264,9 +273,11 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
   for (int u = unit0; u < p.units && !bad; u += unit_step) {
     const Unit t = unit_at<CG>(p, u);
     const int ra = t.m0 + 128 * static_cast<int>(rank), rb = t.n0 + 128 * static_cast<int>(rank);
-    for (int term = 0; term < a.terms && !bad; ++term) {
+    const int end = t.kb0 + t.kbs;
+    // the passes of one phase, then the next phase's (`kb` runs over a phase `terms` times)
+    for (int k0 = t.kb0, term = 0; k0 < end && !bad;) {
       const int pa = term_a(a.terms, term), pb = term_b(a.terms, term);
-      for (int kb = t.kb0; kb < t.kb0 + t.kbs; ++kb) {
+      for (int kb = k0; kb < min(k0 + p.phase, end); ++kb) {
         if (!wait_warp(meta, a, &meta->empty[st], ph ^ 1u)) {
           bad = true;
           break;
@@ -293,6 +304,10 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
         __syncwarp();
         st = st + 1 == kStages ? 0 : st + 1;
         ph ^= st == 0 ? 1u : 0u;
+      }
+      if (++term == a.terms) {
+        term = 0;
+        k0 += p.phase;
       }
     }
   }
@@ -321,28 +336,29 @@ __device__ __forceinline__ void issue(const Args& a, const Plan& p, uint8_t* sme
   bool ok = true;
   for (int u = unit0; u < p.units && ok; u += unit_step) {
     const Unit t = unit_at<CG>(p, u);
-    const int steps = t.kbs * a.terms;
-    if (steps == 0) continue;  // an empty split: the epilogue takes zeros
-    const uint32_t buf = n & 1u;
-    if (!(ok = wait_warp(meta, a, &meta->acc_empty[buf], ((n >> 1) & 1u) ^ 1u))) break;
-    tc_fence_after();
-    const uint32_t d = tmem + buf * 256;
-    for (int i = 0; i < steps; ++i) {
-      if (!(ok = wait_warp(meta, a, &meta->full[st], ph))) break;
+    // (an empty split issues nothing: the epilogue takes zeros)
+    for (int k0 = 0; k0 < t.kbs && ok; k0 += p.phase) {
+      const int steps = min(p.phase, t.kbs - k0) * a.terms;
+      const uint32_t buf = p.phased ? 0u : n & 1u, use = p.phased ? n : n >> 1;
+      if (!(ok = wait_warp(meta, a, &meta->acc_empty[buf], (use & 1u) ^ 1u))) break;
       tc_fence_after();
-      const uint64_t xa = da + st * (kStageBytes >> 4), xb = db + st * (kStageBytes >> 4);
-      if (elect_one()) {
+      const uint32_t d = tmem + buf * 256;
+      for (int i = 0; i < steps; ++i) {
+        if (!(ok = wait_warp(meta, a, &meta->full[st], ph))) break;
+        tc_fence_after();
+        const uint64_t xa = da + st * (kStageBytes >> 4), xb = db + st * (kStageBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t k = 0; k < kBK / 16; ++k) mma<CG>(d, xa + k * sa, xb + k * sb, idesc, (i | k) != 0 ? 1u : 0u);
-        commit<CG>(smem_u32(&meta->empty[st]));
-        if (i + 1 == steps) commit<CG>(smem_u32(&meta->acc_full[buf]));
+          for (uint32_t k = 0; k < kBK / 16; ++k) mma<CG>(d, xa + k * sa, xb + k * sb, idesc, (i | k) != 0 ? 1u : 0u);
+          commit<CG>(smem_u32(&meta->empty[st]));
+          if (i + 1 == steps) commit<CG>(smem_u32(&meta->acc_full[buf]));
+        }
+        __syncwarp();
+        st = st + 1 == kStages ? 0 : st + 1;
+        ph ^= st == 0 ? 1u : 0u;
       }
-      __syncwarp();
-      st = st + 1 == kStages ? 0 : st + 1;
-      ph ^= st == 0 ? 1u : 0u;
+      ++n;
     }
-    if (!ok) break;
-    ++n;
   }
   if (!ok) {
     // gave up: the MMAs in flight end before the tensor memory is freed
@@ -352,7 +368,28 @@ __device__ __forceinline__ void issue(const Args& a, const Plan& p, uint8_t* sme
   }
 }
 
-// Epi: struct with kWarps and `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
+// The `kCols` columns of a finished phase (accumulator 0) added to the sums 256 columns further, or put there.
+template <int kCols>
+__device__ __forceinline__ void add_phase(uint32_t acc, bool first) {
+#pragma unroll 1
+  for (int c = 0; c < kCols; c += 32) {
+    float v[32];
+    tmem_ld32(acc + c, v);
+    if (!first) {
+      float sum[32];
+      tmem_ld32(acc + 256 + c, sum);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += sum[i];
+    }
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+    tmem_st32(acc + 256 + c, w);
+  }
+  tmem_wait_st();
+}
+
+// Epi: struct with kWarps, kPlanes (fp32 operands: a sum may come in phases) and `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
 // are no accumulators: take zeros), first row, first column, columns, M, N, split, lane, staging, ready, done)`, called by
 // 32 lanes together; it calls ready() before it reads accumulators and done() once after the last of them, and
 // returns false when ready() did.
@@ -410,16 +447,15 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
     for (int u = unit0; u < p.units; u += unit_step) {
       const Unit t = unit_at<CG>(p, u);
       const bool zero = t.kbs == 0;
-      const uint32_t buf = n & 1u;
+      const uint32_t buf = p.phased ? 0u : n & 1u;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * kCols;
       // (the warp goes on or leaves as one: the accumulator loads are warp-wide)
-      const auto ready = [&]() {
-        if (zero) return true;
-        if (!wait_warp(meta, a, &meta->acc_full[buf], (n >> 1) & 1u)) return false;
+      const auto full = [&]() {
+        if (!wait_warp(meta, a, &meta->acc_full[buf], (p.phased ? n : n >> 1) & 1u)) return false;
         tc_fence_after();
         return true;
       };
-      const auto done = [&]() {
-        if (zero) return;
+      const auto empty = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -429,11 +465,23 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
             mbar_arrive(smem_u32(&meta->acc_empty[buf]));
         }
       };
-      if (!Epi::run(ep, tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * 256 + part * kCols, zero,
-                    t.m0 + 128 * static_cast<int>(rank) + 32 * quarter, t.n0 + part * kCols, kCols, p.M, p.N, t.split, lane,
-                    stage, ready, done))
+      bool ok = true;
+      if constexpr (Epi::kPlanes) {
+        // each phase's sums onto those of the phases before, in accumulator 1's place
+        for (int k0 = 0; p.phased && k0 < t.kbs && (ok = full()); k0 += p.phase) {
+          add_phase<kCols>(acc, k0 == 0);
+          empty();
+          ++n;
+        }
+      }
+      const auto ready = [&]() { return zero || p.phased || full(); };
+      const auto done = [&]() {
+        if (!zero && !p.phased) empty();
+      };
+      if (!ok || !Epi::run(ep, acc + (p.phased ? 256 : buf * 256), zero, t.m0 + 128 * static_cast<int>(rank) + 32 * quarter,
+                           t.n0 + part * kCols, kCols, p.M, p.N, t.split, lane, stage, ready, done))
         break;
-      if (!zero) ++n;
+      if (!zero && !p.phased) ++n;
     }
     // copies in flight (a warp that gave up) land, and tiles stored by TMA are written, before the CTA leaves
     asm volatile("cp.async.wait_all;" ::: "memory");

@@ -51,7 +51,8 @@ gemm::Operand operand_of_copy(int dtype, const void* copy, int64_t rows, int64_t
 // bits and m n / 2^(31 + s) exceeds n / d by less than 1 / d.
 struct FastDiv {
   uint32_t d, m, s;
-  explicit FastDiv(uint32_t divisor = 1) : d(divisor), m(0), s(0) {
+  FastDiv() : FastDiv(1) {}
+  explicit FastDiv(uint32_t divisor) : d(divisor), m(0), s(0) {
     while ((uint64_t(1) << s) < d) ++s;
     m = static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d);
   }

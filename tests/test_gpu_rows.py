@@ -248,6 +248,23 @@ def test_cross_entropy_bad_and_extreme(pk, gen, dtype):
     assert pk.last_status() == 11 and pk.last_status() == 0
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [90, 3000])
+def test_rows_without_a_label_do_not_leak(pk, gen, dtype, T):
+    """NaN and infinities in the rows that have no label (x, lse, dloss) reach nothing."""
+    D, V = 72, 700
+    x, w, bias, labels = xent_case(gen, dtype, T, D, V, 0.4, True)
+    _, lse = pk.cross_entropy(x, w, labels, bias)
+    dloss = torch.rand(T, generator=gen, device="cuda")
+    want = pk.cross_entropy(x, w, labels, bias) + pk.cross_entropy_backward(x, w, labels, lse, dloss, bias)
+    out = labels < 0
+    x[out], lse[out], dloss[out] = float("nan"), float("inf"), float("nan")
+    x[out.nonzero()[::2, 0]] = float("inf")
+    got = pk.cross_entropy(x, w, labels, bias) + pk.cross_entropy_backward(x, w, labels, lse, dloss, bias)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------------------ a run of them, streams, graphs
 
 
@@ -390,6 +407,24 @@ def test_no_rows(pk):
         assert loss.shape == (0,)
         dx, dw, db = pk.cross_entropy_backward(x, w, labels, lse, loss, bias=torch.ones(40, dtype=dtype, device="cuda"))
         assert dx.shape == (0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
+
+
+@pytest.mark.parametrize("T,K,N", [(300, 1024, 264), (130, 1100, 264), (40, 65536, 128), (2000, 40000, 520)])
+def test_long_fp32_sums_do_not_drift(pk, gen, T, K, N):
+    """Positive terms: an accumulator that truncates loses up to 2^-23 of the sum a step of 16. The tensor pipe adds up at
+    most 64 such steps (of the largest pass; the smaller passes 2^-8 of that each) before a rounding sum takes over, so the
+    result is off by at most (64 (1 + 5 2^-8) + K / 1024) 2^-23 of itself, however long it is."""
+    bound = (64 * (1 + 5 * 2.0**-8) + K / 1024 + 4) * 2.0**-23
+    x, w = torch.rand(T, K, generator=gen, device="cuda"), torch.rand(N, K, generator=gen, device="cuda")
+    want = x.double() @ w.double().T
+    assert ref.worst(pk.linear(x, w), want, bound * want) <= 1
+    # the same sums as the gradients take them: over the outputs (dx) and over the rows (dw)
+    dx, _, _ = pk.linear_backward(torch.zeros(T, N, device="cuda"), w.T.contiguous(), x, need_dw=False, need_db=False)
+    assert ref.worst(dx, want, bound * want) <= 1
+    _, dw, _ = pk.linear_backward(x.T.contiguous(), torch.zeros(N, T, device="cuda"), w.T.contiguous(), need_dx=False, need_db=False)
+    want = w.double() @ x.double().T
+    assert ref.worst(dw, want, bound * want) <= 1
+    check_status(pk)
 
 
 def test_offsets_past_32_bits(pk, gen):
