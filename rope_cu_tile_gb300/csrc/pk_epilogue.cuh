@@ -462,7 +462,6 @@ struct LinEpi {
   // other's (131072 x 1024 x 4096 with gelu and kept pre-activation: 1031 us on eight warps of 128 columns, 895 on sixteen of 64, at
   // the same time otherwise). fp32's staging is twice as large and has room for eight.
   static constexpr int kWarps = ODT == PK_F32 ? 8 : 16;
-  static constexpr bool kPlanes = ODT == PK_F32;
 
   // `ready` waits for the accumulators (false: give up), `done` hands them back. What comes from memory (bias, residual) is
   // asked for before the accumulators are waited for.

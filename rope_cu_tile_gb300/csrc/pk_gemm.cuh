@@ -34,10 +34,12 @@ constexpr uint32_t kOffMeta = kOffEpi + kEpiBytes;
 constexpr int kTerms32 = 6;                   // plane pairs of an fp32 product
 constexpr int kGroupM = 8;                    // tile rows walked together
 // The tensor pipe truncates when it adds to an accumulator, so a long sum drifts towards zero by some 2^-25 of itself a step
-// of 16: nothing beside a 16-bit result, but 8e-5 over 100000 terms where fp32 allows 1e-5. fp32 operands therefore add up
-// at most this many k steps (1024 terms) before the epilogue's warps take the sum over, rounding to nearest, into the other
-// accumulator's tensor memory.
-constexpr int kPhase = 16;
+// of 16: 8e-5 over 100000 terms, where fp32 allows 1e-5 and a rounding to fp16 costs 2e-4. At most this many k steps add
+// up there before the epilogue's warps take the sum over, rounding to nearest, into the other accumulator's tensor memory:
+// 1024 terms of fp32 operands (the drift stays below 2e-6), 16384 of 16-bit ones (3e-5; a hand-over costs some 2000
+// cycles of 131000).
+constexpr int kPhase32 = 16;
+constexpr int kPhase16 = 256;
 
 struct Meta {
   uint64_t full[kStages], empty[kStages];
@@ -121,8 +123,9 @@ __device__ __forceinline__ Plan make_plan(const Args& a) {
   p.splits = choose_splits<CG>(a, p.M);
   p.kb_per = (p.kb_all + p.splits - 1) / p.splits;
   p.units = p.tiles_m * p.tiles_n * p.splits;
-  p.phased = a.terms > 1 && p.kb_per > kPhase;
-  p.phase = p.phased ? kPhase : p.kb_per;
+  const int most = a.terms > 1 ? kPhase32 : kPhase16;
+  p.phased = p.kb_per > most;
+  p.phase = p.phased ? most : p.kb_per;
   return p;
 }
 
@@ -389,7 +392,7 @@ __device__ __forceinline__ void add_phase(uint32_t acc, bool first) {
   tmem_wait_st();
 }
 
-// Epi: struct with kWarps, kPlanes (fp32 operands: a sum may come in phases) and `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
+// Epi: struct with kWarps and `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
 // are no accumulators: take zeros), first row, first column, columns, M, N, split, lane, staging, ready, done)`, called by
 // 32 lanes together; it calls ready() before it reads accumulators and done() once after the last of them, and
 // returns false when ready() did.
@@ -466,9 +469,9 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
         }
       };
       bool ok = true;
-      if constexpr (Epi::kPlanes) {
+      if (p.phased) {
         // each phase's sums onto those of the phases before, in accumulator 1's place
-        for (int k0 = 0; p.phased && k0 < t.kbs && (ok = full()); k0 += p.phase) {
+        for (int k0 = 0; k0 < t.kbs && (ok = full()); k0 += p.phase) {
           add_phase<kCols>(acc, k0 == 0);
           empty();
           ++n;

@@ -23,7 +23,7 @@ constexpr int kDzThreads = 256;
 constexpr int kDzBlocks = 4;  // resident blocks of an SM
 constexpr int kDzLeast = 16;  // rows of a block
 // Rows of a block: one wave of resident blocks, all of the same length (fixed blocks of 128 rows left part of the SMs
-// idle at the end). Measured: 65536 x 2048 bf16, gelu and dropout, 167 us (0.71 of the copy rate; issue slots 64 % full).
+// idle at the end). Measured: 65536 x 2048 bf16, gelu and dropout, 159 us (0.75 of the copy rate; issue slots 63 % full).
 int dz_rows(int64_t T, int64_t ldz, int sms) {
   const int64_t blocks = kDzBlocks * sms / ((ldz + 255) / 256);
   const int64_t rows = blocks > 1 ? round_up((T + blocks - 1) / blocks, 8) : T;
@@ -125,7 +125,7 @@ cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------------------------
-// a few rows (serving): y for up to kFewRows rows of x
+// a few rows (serving)
 
 // Bound by W's bytes, read once; x stays in L1. A warp dots kR rows of W with every row of x, 8 elements a lane and step, in
 // fp32 on the CUDA cores (fp32 inputs need no planes); where N alone gives too few warps, several share the rows and split

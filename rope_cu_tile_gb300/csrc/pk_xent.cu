@@ -182,7 +182,6 @@ template <int DT>
 struct StatEpi {
   using Params = StatParams;
   static constexpr int kWarps = 8;  // wide slices: half the partial results
-  static constexpr bool kPlanes = DT == PK_F32;
   template <class Ready, class Done>
   static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
                                              int, int lane, uint8_t*, const Ready& ready, const Done& done) {
@@ -289,7 +288,6 @@ struct GradEpi {
   using Params = GradParams;
   using S = Stage<DT == PK_F16 ? PK_F16 : PK_BF16>;
   static constexpr int kWarps = 16;
-  static constexpr bool kPlanes = DT == PK_F32;
   template <class Ready, class Done>
   static __device__ __forceinline__ bool run(const Params& p, uint32_t tacc, bool zero, int r0, int c0, int cols, int M, int N,
                                              int, int lane, uint8_t* stage, const Ready& ready, const Done& done) {

@@ -427,6 +427,18 @@ def test_long_fp32_sums_do_not_drift(pk, gen, T, K, N):
     check_status(pk)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_long_16_bit_sums_do_not_drift(pk, gen, dtype):
+    """At most 1024 truncating steps of 16 terms, 2^-23 of the sum each, before a rounding sum takes over, and the result's own
+    rounding, at K = 200000 positive terms (without it: 12500 steps)."""
+    K, M, N = 200000, 136, 264
+    x, w = (torch.rand(K, n, generator=gen, device="cuda").mul_(0.01).to(dtype) for n in (N, M))
+    _, dw, _ = pk.linear_backward(x, torch.zeros(M, N, dtype=dtype, device="cuda"), w, need_dx=False, need_db=False)
+    want = w.double().T @ x.double()
+    assert ref.worst(dw, want, ((1024 + 16) * 2.0**-23 + ref.U[dtype]) * want) <= 1
+    check_status(pk)
+
+
 def test_offsets_past_32_bits(pk, gen):
     """600000 rows of 4096: 2.4e9 elements a matrix. The last rows against the definition, the first beside them."""
     T, K, N, dtype = 600000, 32, 4096, torch.bfloat16
