@@ -190,13 +190,16 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       if constexpr (DT == PK_F32) {
-        v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678118654752f);
-        v[i + 1] = 0.5f * v[i + 1] * erfcf(v[i + 1] * -0.70710678118654752f);
+        // (z kept finite below: -inf times the 0 of its tail has no value)
+        v[i] = fmaxf(v[i], -3.0e38f) * (0.5f * erfcf(v[i] * -0.70710678118654752f));
+        v[i + 1] = fmaxf(v[i + 1], -3.0e38f) * (0.5f * erfcf(v[i + 1] * -0.70710678118654752f));
       } else {
-        // z Phi(z) = max(z, 0) - |z| Phi(-|z|), either sign (NaN and -inf through the second term)
-        const float2 e = tail2(fabsf(v[i]), fabsf(v[i + 1]));
-        v[i] = fmaf(-fabsf(v[i]), e.x, fmaxf(v[i], 0.0f));
-        v[i + 1] = fmaf(-fabsf(v[i + 1]), e.y, fmaxf(v[i + 1], 0.0f));
+        // z Phi(z) = max(z, 0) - |z| Phi(-|z|), either sign. The factor |z| stays finite, so that infinity gives infinity;
+        // NaN comes through the tail.
+        const float u0 = fabsf(v[i]), u1 = fabsf(v[i + 1]);
+        const float2 e = tail2(u0, u1);
+        v[i] = fmaf(-fminf(u0, 3.0e38f), e.x, fmaxf(v[i], 0.0f));
+        v[i + 1] = fmaf(-fminf(u1, 3.0e38f), e.y, fmaxf(v[i + 1], 0.0f));
       }
     }
   } else if (act == PK_ACT_SILU) {

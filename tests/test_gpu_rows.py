@@ -63,6 +63,22 @@ def test_linear_epilogue(pk, gen, dtype, act, T, K, N):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [2, 200])
+def test_activations_at_infinity(pk, gen, dtype, T):
+    """A pre-activation of +inf, -inf or NaN (through the bias) beside finite ones: relu and gelu take their limits, NaN stays."""
+    K, N = 64, 40
+    x, w, bias = rand(gen, T, K, dtype=dtype), rand(gen, N, K, dtype=dtype), torch.zeros(N, dtype=dtype, device="cuda")
+    bias[3], bias[4], bias[5] = float("inf"), float("-inf"), float("nan")
+    ok = [i for i in range(N) if i not in (3, 4, 5)]
+    for act in ("relu", "gelu"):
+        y = pk.linear(x, w, bias, act=act)
+        assert bool((y[:, 3] == float("inf")).all()) and bool((y[:, 4] == 0).all()) and bool(y[:, 5].isnan().all())
+        assert bool(y[:, ok].isfinite().all())
+    y = pk.linear(x, w, bias, act="silu")
+    assert bool((y[:, 3] == float("inf")).all()) and bool(y[:, 5].isnan().all()) and bool(y[:, ok].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T", [1, 7, 300])
 def test_linear_strided_rows(pk, gen, dtype, T):
     """x a slice of wider rows (the v part of a packed qkv), out and the residual slices too; what lies beside is kept."""
