@@ -222,7 +222,8 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
   } else if (act == PK_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      // Phi(z) + z phi(z) is 1/2 +- (1/2 - h), the sign z's, with h = Phi(-u) - u phi(u), u = |z| (h < 1/2)
+      // Phi(z) + z phi(z) is h = Phi(-u) - u phi(u), u = |z|, for z < 0 and 1 - h otherwise: h as it stands, so that the
+      // negative tail keeps its digits (1/2 - (1/2 - h) keeps 2^-25 of 1: 4 % of the slope at -5.5, nothing past -6.5)
       const float2 u = make_float2(fabsf(z[i]), fabsf(z[i + 1]));
       float2 e;
       if constexpr (DT == PK_F32)
@@ -232,10 +233,8 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
       const float2 q = mul2(mul2(u, u), make_float2(-0.72134752044448170f, -0.72134752044448170f));
       const float2 f = make_float2(attn::ex2(q.x), attn::ex2(q.y));
       const float2 h = fma2(mul2(u, make_float2(-0.39894228040143268f, -0.39894228040143268f)), f, e);
-      float2 w = fma2(h, make_float2(-1.0f, -1.0f), make_float2(0.5f, 0.5f));
-      w.x = __uint_as_float(__float_as_uint(w.x) ^ (__float_as_uint(z[i]) & 0x80000000u));
-      w.y = __uint_as_float(__float_as_uint(w.y) ^ (__float_as_uint(z[i + 1]) & 0x80000000u));
-      const float2 v = mul2(fma2(w, make_float2(1.0f, 1.0f), make_float2(0.5f, 0.5f)), make_float2(d[i], d[i + 1]));
+      const float2 w = fma2(h, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+      const float2 v = mul2(make_float2(z[i] < 0.0f ? h.x : w.x, z[i + 1] < 0.0f ? h.y : w.y), make_float2(d[i], d[i + 1]));
       d[i] = v.x;
       d[i + 1] = v.y;
     }

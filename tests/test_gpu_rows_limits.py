@@ -1,0 +1,72 @@
+"""The token-row operators at the edges of their types: tails and infinities of the activations, values near the ends of fp16
+and fp32, masked words, padding rows, long features, pieces of the vocabulary, the streams' status words, bounded waits."""
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import rows_ref as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+INF, NAN = float("inf"), float("nan")
+
+
+def rand(gen, *shape, std=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=gen, device="cuda") * std).to(dtype)
+
+
+@pytest.fixture
+def gen():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4321)
+    return g
+
+
+def rounded(err, want, dtype):
+    """The bound of a value off by err before its rounding to the type (fp16: half a step of its smallest numbers)."""
+    return err * (1 + ref.U[dtype]) + ref.U[dtype] * want.abs() + (2.0**-25 if dtype == torch.float16 else 0.0)
+
+
+# ------------------------------------------------------------------------------------------ activations
+
+
+def act_of(pk, z, act, rows):
+    """act at the values z: a product of nothing, z its bias."""
+    x, w = torch.ones(rows, 8, dtype=z.dtype, device="cuda"), torch.zeros(z.numel(), 8, dtype=z.dtype, device="cuda")
+    return pk.linear(x, w, z, act=act)
+
+
+def slope_of(pk, z, act, d=1.0):
+    """act' at the values z: db of one row (the sum of one dz, rounded once)."""
+    n, dt = z.numel(), z.dtype
+    x, w = torch.ones(1, 8, dtype=dt, device="cuda"), torch.zeros(n, 8, dtype=dt, device="cuda")
+    dy = torch.full((1, n), d, dtype=dt, device="cuda")
+    return pk.linear_backward(x, w, dy, z[None].contiguous(), act, need_dx=False, need_dw=False)[2]
+
+
+def tail_and_density(z):
+    u = z.abs()
+    return 0.5 * torch.special.erfc(u / math.sqrt(2)), u * torch.exp(-u * u / 2) / math.sqrt(2 * math.pi)
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gelu_slope_keeps_its_tail(pk, dtype):
+    """gelu' of z < 0 is h = Phi(-u) - u phi(u), u = -z, of z > 0 1 - h. Relative errors of the two terms, 0 <= u <= 6:
+    16 bits: Phi by the fit, 2^-17; phi by an exponential whose argument's base-2 logarithm (at most 26) is off by three
+    roundings, 26 * 3 * 2^-24 * ln 2 < 2^-18, and the function's 2^-22. fp32: the complementary error function's four units
+    of 2^-23 and its argument's 1.5 2^-24 relative, which is 1.5 u^2 2^-24 of the value; phi as above or better."""
+    z = torch.linspace(-6, 6, 4801, device="cuda").to(dtype)
+    want = ref.act_slope(z.double(), "gelu")
+    tail, dens = tail_and_density(z.double())
+    if dtype == torch.float32:
+        err = tail * (2.0**-21 + 1.5 * z.double() ** 2 * 2.0**-24) + dens * (2.0**-18 + 2.0**-22)
+    else:
+        err = tail * 2.0**-17 + dens * (2.0**-18 + 2.0**-22)
+    err = err + 2.0**-23 * torch.where(z < 0, tail + dens, 2.0)  # the additions
+    assert ref.worst(slope_of(pk, z, "gelu"), want, rounded(err, want, dtype)) <= 1
+    far = torch.linspace(-60, -6, 500, device="cuda").to(dtype)
+    # |gelu'(-6)| = 3.6e-8, and it falls (fp16: to the nearest multiple of 2^-24, at most half a step further)
+    assert float(slope_of(pk, far, "gelu").double().abs().max()) <= 4e-8 + (2.0**-25 if dtype == torch.float16 else 0.0)
