@@ -205,10 +205,11 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
   } else if (act == PK_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      // (z kept finite below, as gelu's)
       if constexpr (DT == PK_F32)
-        v[i] = v[i] / (1.0f + __expf(-v[i]));
+        v[i] = fmaxf(v[i], -3.0e38f) / (1.0f + __expf(-v[i]));
       else
-        v[i] = v[i] * rcp_fast(1.0f + attn::ex2(v[i] * -1.4426950408889634f));
+        v[i] = fmaxf(v[i], -3.0e38f) * rcp_fast(1.0f + attn::ex2(v[i] * -1.4426950408889634f));
     }
   }
 }
@@ -232,7 +233,9 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
         e = tail2(u.x, u.y);
       const float2 q = mul2(mul2(u, u), make_float2(-0.72134752044448170f, -0.72134752044448170f));
       const float2 f = make_float2(attn::ex2(q.x), attn::ex2(q.y));
-      const float2 h = fma2(mul2(u, make_float2(-0.39894228040143268f, -0.39894228040143268f)), f, e);
+      // (the factor u kept finite, so that an infinite z has the limits 0 and 1; NaN comes through e)
+      const float2 g = make_float2(fminf(u.x, 3.0e38f), fminf(u.y, 3.0e38f));
+      const float2 h = fma2(mul2(g, make_float2(-0.39894228040143268f, -0.39894228040143268f)), f, e);
       const float2 w = fma2(h, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
       const float2 v = mul2(make_float2(z[i] < 0.0f ? h.x : w.x, z[i + 1] < 0.0f ? h.y : w.y), make_float2(d[i], d[i + 1]));
       d[i] = v.x;
@@ -242,7 +245,8 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float h = DT == PK_F32 ? 1.0f / (1.0f + __expf(-z[i])) : rcp_fast(1.0f + attn::ex2(z[i] * -1.4426950408889634f));
-      d[i] *= h * fmaf(z[i], 1.0f - h, 1.0f);
+      // (z kept finite: infinity times the 0 of h or 1 - h has no value; NaN comes through h)
+      d[i] *= h * fmaf(fminf(fmaxf(z[i], -3.0e38f), 3.0e38f), 1.0f - h, 1.0f);
     }
   }
 }

@@ -70,3 +70,29 @@ def test_gelu_slope_keeps_its_tail(pk, dtype):
     far = torch.linspace(-60, -6, 500, device="cuda").to(dtype)
     # |gelu'(-6)| = 3.6e-8, and it falls (fp16: to the nearest multiple of 2^-24, at most half a step further)
     assert float(slope_of(pk, far, "gelu").double().abs().max()) <= 4e-8 + (2.0**-25 if dtype == torch.float16 else 0.0)
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act,value,slope", [("relu", (0.0, INF), (0.0, 1.0)), ("gelu", (0.0, INF), (0.0, 1.0)),
+                                             ("silu", (0.0, INF), (0.0, 1.0))])
+def test_limits_at_infinity(pk, dtype, act, value, slope):
+    """Values and slopes of infinite and of the largest finite pre-activations are their limits; NaN stays NaN."""
+    top = torch.finfo(dtype).max
+    z = torch.tensor([-INF, INF, -top, top, NAN, 1.0], dtype=dtype, device="cuda")
+    for rows in (1, 9, 300):
+        y = act_of(pk, z, act, rows).float().cpu()
+        assert bool((y[:, 0] == value[0]).all()) and bool((y[:, 1] == value[1]).all()), y[0]
+        assert bool((y[:, 2] == 0).all()) and bool((y[:, 3] == top).all()) and bool(y[:, 4].isnan().all())
+    d = slope_of(pk, z, act).float().cpu()
+    assert d[0] == slope[0] and d[1] == slope[1] and d[2] == 0 and d[3] == 1 and d[4].isnan(), d
+    d = slope_of(pk, z[:4], act, 0.0)
+    assert bool((d == 0).all())
+
+
+def test_half_precision_overflow_of_the_kept_pre_activation(pk):
+    """z = -80000 is finite in fp32 and -inf in fp16: y is 0, and so is every gradient."""
+    x, w = torch.full((9, 8), 200.0, device="cuda").half(), torch.full((16, 8), -50.0, device="cuda").half()
+    for act in ("gelu", "silu"):
+        y, pre = pk.linear(x, w, act=act, return_pre=True)
+        assert bool((y == 0).all()) and bool((pre == -INF).all())
+        for g in pk.linear_backward(x, w, torch.ones_like(y), pre, act, p=0.25, seed=3):
+            assert bool((g == 0).all()), act
