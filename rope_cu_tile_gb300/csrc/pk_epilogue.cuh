@@ -132,7 +132,9 @@ __device__ __forceinline__ void store8_any(void* p, int64_t i, int n, const floa
 }
 
 // ------------------------------------------------------------------------------------
-// activations (value, and slope at z)
+// activations (value, and slope at z). fp32 results take the full-precision functions (erfcf, expf). 16-bit ones take
+// short exponentials and reciprocals, good to some 2^-17 relative where the result's rounding is 2^-11 or 2^-8: dz of a
+// feed-forward layer is bound by issue slots.
 
 // Two fp32 operations an instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -207,7 +209,7 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
     for (int i = 0; i < N; ++i) {
       // (z kept finite below, as gelu's)
       if constexpr (DT == PK_F32)
-        v[i] = fmaxf(v[i], -3.0e38f) / (1.0f + __expf(-v[i]));
+        v[i] = fmaxf(v[i], -3.0e38f) / (1.0f + expf(-v[i]));
       else
         v[i] = fmaxf(v[i], -3.0e38f) * rcp_fast(1.0f + attn::ex2(v[i] * -1.4426950408889634f));
     }
@@ -231,8 +233,13 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
         e = make_float2(0.5f * erfcf(u.x * 0.70710678118654752f), 0.5f * erfcf(u.y * 0.70710678118654752f));
       else
         e = tail2(u.x, u.y);
-      const float2 q = mul2(mul2(u, u), make_float2(-0.72134752044448170f, -0.72134752044448170f));
-      const float2 f = make_float2(attn::ex2(q.x), attn::ex2(q.y));
+      float2 f = mul2(u, u);
+      if constexpr (DT == PK_F32) {
+        f = make_float2(expf(-0.5f * f.x), expf(-0.5f * f.y));
+      } else {
+        f = mul2(f, make_float2(-0.72134752044448170f, -0.72134752044448170f));
+        f = make_float2(attn::ex2(f.x), attn::ex2(f.y));
+      }
       // (the factor u kept finite, so that an infinite z has the limits 0 and 1; NaN comes through e)
       const float2 g = make_float2(fminf(u.x, 3.0e38f), fminf(u.y, 3.0e38f));
       const float2 h = fma2(mul2(g, make_float2(-0.39894228040143268f, -0.39894228040143268f)), f, e);
@@ -244,9 +251,19 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
   } else if (act == PK_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float h = DT == PK_F32 ? 1.0f / (1.0f + __expf(-z[i])) : rcp_fast(1.0f + attn::ex2(z[i] * -1.4426950408889634f));
+      // 1 - h as the difference: off by some 2^-24 of 1, which counts times z: within 16 bits' rounding. In fp32 e h instead
+      // for z > 0, where it is small.
+      float h, rest;
+      if constexpr (DT == PK_F32) {
+        const float e = expf(-z[i]);
+        h = 1.0f / (1.0f + e);
+        rest = z[i] > 0.0f ? e * h : 1.0f - h;
+      } else {
+        h = rcp_fast(1.0f + attn::ex2(z[i] * -1.4426950408889634f));
+        rest = 1.0f - h;
+      }
       // (z kept finite: infinity times the 0 of h or 1 - h has no value; NaN comes through h)
-      d[i] *= h * fmaf(fminf(fmaxf(z[i], -3.0e38f), 3.0e38f), 1.0f - h, 1.0f);
+      d[i] *= h * fmaf(fminf(fmaxf(z[i], -3.0e38f), 3.0e38f), rest, 1.0f);
     }
   }
 }

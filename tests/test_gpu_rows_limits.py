@@ -96,3 +96,32 @@ def test_half_precision_overflow_of_the_kept_pre_activation(pk):
         assert bool((y == 0).all()) and bool((pre == -INF).all())
         for g in pk.linear_backward(x, w, torch.ones_like(y), pre, act, p=0.25, seed=3):
             assert bool((g == 0).all()), act
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_activations_are_as_exact_as_their_type(pk, dtype, act):
+    """Relative to the terms of each value. fp32: the complementary error function of at most four units of 2^-23 on an argument
+    off by 1.5 2^-24 of itself; exponentials of at most two units, one addition and one division. 16 bits: as the fit (2^-17) and the short exponentials (2^-22, the argument
+    times log2 e off by 1.5 2^-24 of itself) allow; gelu's fit holds to 6."""
+    lo = 6 if act == "gelu" else 20
+    z = torch.linspace(-lo, lo, 4001, device="cuda").to(dtype)
+    u = z.double().abs()
+    f32 = dtype == torch.float32
+    want = ref.act(z.double(), act)
+    slope = ref.act_slope(z.double(), act)
+    if act == "gelu":
+        tail, dens = tail_and_density(z.double())
+        t = 2.0**-21 + 1.5 * u * u * 2.0**-24 if f32 else 2.0**-17  # of Phi(-u)
+        g = 2.0**-22 + u * u * 2.0**-24 if f32 else 2.0**-18 + 2.0**-22  # of phi(u)
+        err = u * tail * t + 4 * 2.0**-24 * want.abs()
+        serr = tail * t + dens * g + 2.0**-23 * torch.where(z < 0, tail + dens, 2.0)
+    else:
+        h = torch.sigmoid(z.double())
+        r = 4 * 2.0**-23 if f32 else (1.5 * u + 16) * 2.0**-24  # of h
+        err = want.abs() * r
+        # 1 - h: of itself in fp32, as the difference of the rounded h in 16 bits
+        serr = h * ((1 + u * (1 - h)) * (r + 2.0**-22) + (0.0 if f32 else u * h * (r + 2.0**-24)))
+    for rows in (1, 9):
+        y = act_of(pk, z, act, rows)
+        assert ref.worst(y[rows - 1], want, rounded(err, want, dtype)) <= 1
+    assert ref.worst(slope_of(pk, z, act), slope, rounded(serr, slope, dtype)) <= 1
