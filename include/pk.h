@@ -394,7 +394,8 @@ int pk_linear_workspace(int dtype, const void *x, int64_t ldx, const void *w, in
  * Its gradients: dz = act'(pre) drop(dy);  dx = dz W,  dw = dz^T x,  db = column sums of dz (the
  * residual's gradient is dy). pre: the forward's, in the element type (may be NULL for
  * PK_ACT_NONE); p, seed, offset as in the forward. dx [T, K], dw [N, K], db [N]: each may be NULL.
- * dz is rounded to the element type before the products (db sums it unrounded).
+ * dz is rounded to the element type before the products (db sums it unrounded), in fp16 times a
+ * power of two where its largest finite element is outside [2^-10, 65504].
  */
 int pk_linear_backward(int dtype, const void *x, int64_t ldx, const void *w, const void *dy, int64_t lddy, const void *pre,
                        int act, double p, uint64_t seed, uint64_t offset, int64_t T, int N, int K, void *dx, void *dw,

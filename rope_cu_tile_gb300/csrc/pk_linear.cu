@@ -43,11 +43,39 @@ struct DzArgs {
   float* part;  // [blocks of rows, ldz] column sums, or null
   int dy_vec, pre_vec;
   int rows;    // of a block
+  float* tops;     // [blocks] fp16: each block's largest finite |dz|, or null
+  float* unscale;  // the inverse of dz's scale
 };
 
+// The power of two that fp16's dz is multiplied by: 1 while the largest |dz| is within [2^-10, 65504], where it overflows
+// nothing and every element within 2^-4 of it keeps its 11 bits (half a step of the smallest numbers, 2^-25, is 2^-15 of it at
+// most); past either end the one that brings it to [2^14, 2^15).
+__device__ __forceinline__ int dz_exponent(float top) {
+  if (!(top > 0.0f) || (top >= 0.0009765625f && top <= 65504.0f)) return 0;
+  return max(-100, min(100, 14 - ilogbf(top)));
+}
+
+// The largest of a block's values, in every thread; `shared` holds a value a warp.
+__device__ __forceinline__ float block_top(float v, float* shared) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = shared[0];
+#pragma unroll
+  for (int i = 1; i < kDzThreads / 32; ++i) v = fmaxf(v, shared[i]);
+  return v;
+}
+
 // A warp takes 256 columns of a row (8 a lane: one draw of the generator); a block eight rows at a time.
-// Bound by bytes: dy and z read, dz written.
-template <int DT>
+// Moves dy, z and dz; bound by issue slots with dropout and gelu (64 % of them, 0.75 of the copy rate).
+// dz is rounded to the element type once: it is an operand of tensor-core products of that type, as x and W are. bf16
+// results are then off by 2.3e-3 of their norm (1.7e-3 of it their own rounding); two planes of dz would undo that at twice
+// the products' time.
+// fp16: a dz of ordinary size is stored as it is. How large the largest is, is known after this kernel only: a second launch
+// (kScale) stores dz again, times a power of two, where that has to be, and else ends at once (some 2 us); the products' results are
+// multiplied by the inverse. (A pass over dy before this one would cost its reading every time.)
+template <int DT, bool kScale>
 __global__ void __launch_bounds__(kDzThreads, kDzBlocks) pk_dz_kernel(const __grid_constant__ DzArgs a) {
   __shared__ float sums[8][256];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -56,6 +84,16 @@ __global__ void __launch_bounds__(kDzThreads, kDzBlocks) pk_dz_kernel(const __gr
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   griddep_wait();
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float top = 0.0f, scale = 1.0f;
+  if constexpr (kScale) {
+    const int blocks = gridDim.x * gridDim.y;
+    for (int i = threadIdx.x; i < blocks; i += kDzThreads) top = fmaxf(top, __ldcg(a.tops + i));
+    top = block_top(top, &sums[0][0]);
+    const int e = dz_exponent(top);
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) *a.unscale = scalbnf(1.0f, -e);
+    if (e == 0) return;
+    scale = scalbnf(1.0f, e);
+  }
   if (c < a.ldz) {
     // the next row's values are asked for before this one's are used (two rows ahead, or batches of rows, take longer: the
     // body is copied for each and no longer fits the instruction cache)
@@ -80,9 +118,21 @@ __global__ void __launch_bounds__(kDzThreads, kDzBlocks) pk_dz_kernel(const __gr
         for (int j = 0; j < 8; ++j)
           if (j >= n) v[j] = 0.0f;  // the operand's padding
       }
+      if constexpr (kScale) {
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) add2(sum[j], sum[j + 1], make_float2(v[j], v[j + 1]));
-      if (!a.dz) continue;
+        for (int j = 0; j < 8; ++j) v[j] *= scale;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) add2(sum[j], sum[j + 1], make_float2(v[j], v[j + 1]));
+        if constexpr (DT == PK_F16) {
+          // (an infinite or undefined element is none that a scale could hold)
+          if (a.tops) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fabsf(v[j]) <= 3.4e38f ? fmaxf(top, fabsf(v[j])) : top;
+          }
+        }
+        if (!a.dz) continue;
+      }
       if constexpr (DT == PK_F32) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -99,6 +149,14 @@ __global__ void __launch_bounds__(kDzThreads, kDzBlocks) pk_dz_kernel(const __gr
       } else {
         store8<DT>(a.dz, r * a.ldz + c, v);
       }
+    }
+  }
+  if constexpr (kScale) return;
+  if constexpr (DT == PK_F16) {
+    if (a.tops) {
+      top = block_top(top, &sums[0][0]);
+      if (threadIdx.x == 0) a.tops[blockIdx.y * gridDim.x + blockIdx.x] = top;
+      __syncthreads();
     }
   }
   if (!a.part) return;
@@ -119,9 +177,10 @@ cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
   a.pre_vec = a.pre && rows16(a.pre, a.ldpre, elem_bytes(dtype));
   Launch l(1, kDzThreads, stream);
   l.cfg.gridDim = dim3(static_cast<unsigned int>((a.T + a.rows - 1) / a.rows), static_cast<unsigned int>((a.ldz + 255) / 256));
-  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F32>, a);
-  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_BF16>, a);
-  return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F16>, a);
+  if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F32, false>, a);
+  if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_BF16, false>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F16, false>, a);
+  return e != cudaSuccess || !a.tops ? e : cudaLaunchKernelEx(&l.cfg, pk_dz_kernel<PK_F16, true>, a);
 }
 
 // ------------------------------------------------------------------------------------
@@ -258,6 +317,8 @@ struct Bwd {
   gemm::Shape dx, dw;
   void *x, *w, *dz;
   float *part, *partial;
+  float *tops, *unscale;  // of a dz that may need a scale
+  bool scaled;
   int rows;  // of a block of dz
   int64_t blocks, bytes;
 };
@@ -269,9 +330,16 @@ Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, const vo
   if (need_dw && !in_place(dtype, x, ldx)) b.x = c.take(copy_bytes(dtype, T, K));
   if (need_dx && !in_place(dtype, w, K)) b.w = c.take(copy_bytes(dtype, N, K));
   // dy itself is the operand when nothing changes it on the way
-  if ((need_dx || need_dw) && (act != PK_ACT_NONE || cut || !in_place(dtype, dy, lddy))) b.dz = c.take(copy_bytes(dtype, T, N));
+  const bool made = (need_dx || need_dw) && (act != PK_ACT_NONE || cut || !in_place(dtype, dy, lddy));
+  if (made) b.dz = c.take(copy_bytes(dtype, T, N));
   b.rows = dz_rows(T, copy_ld(N), sms);
   b.blocks = (T + b.rows - 1) / b.rows;
+  // (without dropout dz of relu, or of no activation, is made of dy's elements and zeros: exact)
+  b.scaled = made && dtype == PK_F16 && (cut || act == PK_ACT_GELU || act == PK_ACT_SILU);
+  if (b.scaled) {
+    b.tops = static_cast<float*>(c.take(b.blocks * ((copy_ld(N) + 255) / 256) * 4));
+    b.unscale = static_cast<float*>(c.take(4));
+  }
   if (need_db) b.part = static_cast<float*>(c.take(b.blocks * copy_ld(N) * 4));
   int64_t partial = 0;
   if (need_dx) {
@@ -418,6 +486,8 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     z.plane = T * z.ldz;
     z.part = b.part;
     z.rows = b.rows;
+    z.tops = b.tops;
+    z.unscale = b.unscale;
     if (dz_launch(dtype, z, stream) != cudaSuccess) return PK_ERR_CUDA;
     if (db && rows::sum_rows(dtype, b.part, b.blocks, nullptr, 1, N, z.ldz, nullptr, db, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
@@ -437,6 +507,7 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     LinParams ep = {};
     ep.y = dx;
     ep.ldy = K;
+    ep.alpha = b.scaled ? b.unscale : nullptr;
     if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dx, b.partial, rows::partial_rows(b.dx, T), d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
   if (dw) {
@@ -448,6 +519,7 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     LinParams ep = {};
     ep.y = dw;
     ep.ldy = K;
+    ep.alpha = b.scaled ? b.unscale : nullptr;
     if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dw, b.partial, rows::partial_rows(b.dw, N), d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
   return PK_OK;

@@ -125,3 +125,49 @@ def test_activations_are_as_exact_as_their_type(pk, dtype, act):
         y = act_of(pk, z, act, rows)
         assert ref.worst(y[rows - 1], want, rounded(err, want, dtype)) <= 1
     assert ref.worst(slope_of(pk, z, act), slope, rounded(serr, slope, dtype)) <= 1
+
+@pytest.mark.parametrize("act,p", [("none", 0.5), ("gelu", 0.0), ("silu", 0.25), ("relu", 0.4), ("relu", 0.0)])
+@pytest.mark.parametrize("size", [3e-8, 1e-6, 1e-4, 2.0**-10, 0.03, 1.0, 3e4])
+def test_half_precision_gradients_keep_their_range(pk, gen, act, p, size):
+    """dz in fp16 is scaled by a power of two where its largest element would be past 65504, or below 2^-10 (where half a
+    step of fp16's smallest numbers, 2^-25, would be over 2^-15 of it): so each element is off by 2^-11 of itself or
+    2^-15 of the largest one, whichever is more, and the products as everywhere."""
+    T, K, N, dt = 300, 72, 136, torch.float16
+    x, w = rand(gen, T, K, std=0.05, dtype=dt), rand(gen, N, K, std=0.05, dtype=dt)
+    dy = (torch.rand(T, N, generator=gen, device="cuda") * 2 - 1).mul_(2 * size).to(dt)
+    pre = None if act == "none" else rand(gen, T, N, dtype=dt)
+    got = pk.linear_backward(x, w, dy, pre, act, p, 5, 6)
+    d = dy.double() * ref.drop_factor(T, N, p, 5, 6, "cuda")
+    err = 2.0**-22 * d.abs()
+    if act != "none":
+        z = pre.double()
+        err = err * ref.LIPSCHITZ + (2.0**-16 * (1 + z.abs()) * d.abs() if act != "relu" else 0.0)
+        d = d * ref.act_slope(z, act)
+    rd = err + torch.maximum(ref.U[dt] * d.abs(), 2.0**-15 * d.abs().max())
+    X, W = x.double(), w.double()
+    want = (d @ W, d.T @ X, d.sum(0))
+    ex = rd @ W.abs() + ref.sum_bound(N, dt) * ((d.abs() + rd) @ W.abs())
+    ew = rd.T @ X.abs() + ref.sum_bound(T, dt) * ((d.abs() + rd).T @ X.abs())
+    eb = err.sum(0) + T * 2.0**-23 * d.abs().sum(0)
+    for name, g, v, e in zip(("dx", "dw", "db"), got, want, (ex, ew, eb)):
+        fits = v.abs() < 65000
+        assert ref.worst(g[fits], v[fits], rounded(e, v, dt)[fits]) <= 1, name
+    assert pk.last_status() == 0
+
+
+def test_half_precision_gradients_beside_an_infinite_one(pk, gen):
+    """One infinite dy: its own row of dx, and db and dw of its column; the rest as without it, with a dz past 65504 beside it."""
+    T, K, N, dt = 40, 16, 24, torch.float16
+    x, w = rand(gen, T, K, std=0.01, dtype=dt), rand(gen, N, K, std=0.01, dtype=dt)
+    dy = rand(gen, T, N, dtype=dt)
+    dy[2, 3] = 60000.0
+    keep = torch.from_numpy(ref.keep_mask(T, N, 0.5, 1, 2)).cuda()
+    dy[~keep] = 1.0
+    at = int(keep[7].nonzero()[0])
+    a = pk.linear_backward(x, w, dy, p=0.5, seed=1, offset=2)
+    dy[7, at] = INF
+    b = pk.linear_backward(x, w, dy, p=0.5, seed=1, offset=2)
+    rows, cols = torch.arange(T, device="cuda") != 7, torch.arange(N, device="cuda") != at
+    assert bool(a[0].isfinite().all()) and bool(a[1].isfinite().all())
+    assert torch.equal(a[0][rows], b[0][rows]) and torch.equal(a[1][cols], b[1][cols]) and torch.equal(a[2][cols], b[2][cols])
+    assert not bool(b[0][7].isfinite().any()) and bool(b[2][at].isinf())
