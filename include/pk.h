@@ -427,7 +427,7 @@ int pk_cross_entropy(int dtype, const void *x, int64_t ldx, const void *w, const
 /*
  * The gradient of sum_t dloss[t] loss[t] for the forward's lse: dz = dloss (exp(z - lse) - onehot),
  * dx = dz W [T, D], dw = dz^T x [V, D], db = column sums of dz [V]; each may be NULL. dz is
- * rounded to the element type before the products and the sums.
+ * rounded to the element type before the products (db sums it unrounded).
  */
 int pk_cross_entropy_backward(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, const int64_t *labels,
                               const float *lse, const float *dloss, int64_t T, int D, int V, void *dx, void *dw, void *db,

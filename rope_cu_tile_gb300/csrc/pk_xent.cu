@@ -283,6 +283,24 @@ struct GradParams {
   int64_t cap, ldcol;
 };
 
+// The sum over a warp's lanes (rows) of each of their 32 columns: column `lane` in lane `lane`. Five steps, in each of which a
+// lane keeps half of its columns and hands over the other half.
+__device__ __forceinline__ float column_sum(const float (&v)[32], int lane) {
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const bool up = (lane & 16) != 0;
+    t[i] = (up ? v[i + 16] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 16], 16);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) t[i] = (up ? t[i + o] : t[i]) + __shfl_xor_sync(0xffffffffu, up ? t[i] : t[i + o], o);
+  }
+  return t[0];
+}
+
 template <int DT>
 struct GradEpi {
   using Params = GradParams;
@@ -325,33 +343,23 @@ struct GradEpi {
         v[i] = q.x;
         v[i + 1] = q.y;
       }
-      // db: the column sums of the staged (rounded) tile, two columns and every other row a lane
-      const int pair = lane & 15, odd = lane >> 4;
-      float2 sum = make_float2(0.0f, 0.0f);
+      // db: the column sums before dz is rounded (sums of the rounded tile, read back from the staging memory, left db with the
+      // roundings wherever labels and probabilities cancel in a column)
+      if (p.col) {
+        const float sum = column_sum(v, lane);
+        if (c + lane < N) p.col[(r0 >> 5) * p.ldcol + c + lane] = sum;
+      }
 #pragma unroll
       for (int k = 0; k < (DT == PK_F32 ? 3 : 1); ++k) {
         stored(lane);
         S::put(stage, lane, v);
         store_tile(&p.dz, stage, c, r0, k, lane);
-        if (p.col) {
-#pragma unroll
-          for (int r = 0; r < 32; r += 2)
-            add2(sum.x, sum.y,
-                 Elem<DT != PK_F16>::unpack(*reinterpret_cast<const uint32_t*>(S::slot(stage, r + odd, pair >> 2) + (pair & 3) * 4)));
-        }
         if constexpr (DT == PK_F32) {
           if (k < 2) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
           }
         }
-      }
-      if (p.col) {
-        sum.x += __shfl_xor_sync(0xffffffffu, sum.x, 16);
-        sum.y += __shfl_xor_sync(0xffffffffu, sum.y, 16);
-        float* d = p.col + (r0 >> 5) * p.ldcol + c + 2 * pair;
-        if (odd == 0 && c + 2 * pair < N) d[0] = sum.x;
-        if (odd == 1 && c + 2 * pair + 1 < N) d[1] = sum.y;
       }
     }
     return true;

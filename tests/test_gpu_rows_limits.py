@@ -171,3 +171,23 @@ def test_half_precision_gradients_beside_an_infinite_one(pk, gen):
     assert bool(a[0].isfinite().all()) and bool(a[1].isfinite().all())
     assert torch.equal(a[0][rows], b[0][rows]) and torch.equal(a[1][cols], b[1][cols]) and torch.equal(a[2][cols], b[2][cols])
     assert not bool(b[0][7].isfinite().any()) and bool(b[2][at].isinf())
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [4096, 4001])
+def test_cross_entropy_bias_gradient_sums_unrounded(pk, gen, dtype, T):
+    """Every word is as often a label as it is likely, so each column of dz nearly cancels: db is off by the exponentials'
+    and the sum's fp32 errors (32 rows, then strided eighths of the blocks of 32, then eight), not by a rounding of dz."""
+    D, V = 64, 64
+    x, w = rand(gen, T, D, std=0.1, dtype=dtype), rand(gen, V, D, dtype=dtype)
+    bias = torch.zeros(V, device="cuda", dtype=dtype)
+    labels = torch.arange(T, device="cuda") % V
+    _, lse = pk.cross_entropy(x, w, labels, bias)
+    dloss = torch.ones(T, device="cuda")
+    _, _, db = pk.cross_entropy_backward(x, w, labels, lse, dloss, bias)
+    z, dz = ref.logits(x, w, bias)
+    q = torch.exp(z - lse.double()[:, None])
+    e = q * (dz + (z.abs() + lse.double().abs()[:, None] + 2) * 2.0**-21)
+    q[torch.arange(T, device="cuda"), labels] -= 1.0
+    err = e.sum(0) + (32 + T / 256 + 9 + 2) * 2.0**-24 * (q.abs() + e).sum(0)
+    want = q.sum(0)
+    assert ref.worst(db, want, rounded(err, want, dtype)) <= 1
