@@ -207,7 +207,8 @@ int64_t pk_schedule_capacity(int64_t T);
 
 /*
  * Synchronizes `stream`, returns the first device-detected error recorded for it since
- * the last call (PK_OK if none) and clears it.
+ * the last call (PK_OK if none) and clears it. The token-row operators record theirs apart from the
+ * attention's: where there is one of each, the attention's is returned and the other stays for the next call.
  */
 int pk_last_status(struct CUstream_st *stream);
 
@@ -357,8 +358,9 @@ int pk_rope(int dtype, const void *x, void *y, const void *cos, const void *sin,
  *     the call's own launches: two calls that may run at the same time (other streams, two
  *     captured graphs) need two workspaces. Nothing is kept in it between calls.
  *   - `status`: optional device int (NULL: none), set to PK_OK in stream order and then to the first
- *     error that the device finds (PK_ERR_TIMEOUT, PK_ERR_BAD_LABEL). With NULL such errors go to a
- *     word of the device that pk_last_status of any of its streams reads.
+ *     error that the device finds (PK_ERR_TIMEOUT, PK_ERR_BAD_LABEL). With NULL such errors go to the
+ *     stream's own word (a captured call's: the word of the stream it was captured on), read by
+ *     pk_last_status(stream). A device has 1024 words; the streams that come after share the last one.
  *   - T (rows) <= PK_ROWS_MAX_T, other sizes <= PK_ROWS_MAX_DIM. T = 0 is a valid call: gradients of
  *     weights are set to zero, nothing else is written.
  *   - Results do not depend on timing: no sum's order does. Nothing is allocated. A call can be

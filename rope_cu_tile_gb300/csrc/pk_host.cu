@@ -167,7 +167,7 @@ unsigned long long wait_limit_ns() {
 }
 
 namespace rows {
-int take_status(int dev);  // the token-row operators' status word of a device (pk_rows.cu)
+int take_status(int dev, cudaStream_t stream);  // the token-row operators' status word of a stream (pk_rows.cu)
 }
 
 int select_forward_kernel(int dtype, int window) {
@@ -728,14 +728,15 @@ int pk_last_status(struct CUstream_st* stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PK_ERR_CUDA;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return PK_ERR_CUDA;
-  const int row_st = rows::take_status(dev);
   auto it = g_ws.find(std::make_pair(dev, static_cast<cudaStream_t>(stream)));
-  if (it == g_ws.end() || !it->second.base) return row_st;
-  int st = 0, zero = 0;
-  if (cudaMemcpy(&st, &it->second.ctl->status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemcpy(&it->second.ctl->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
-    return PK_ERR_CUDA;
-  return st != PK_OK ? st : row_st;
+  if (it != g_ws.end() && it->second.base) {
+    int st = 0, zero = 0;
+    if (cudaMemcpy(&st, &it->second.ctl->status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess ||
+        cudaMemcpy(&it->second.ctl->status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
+      return PK_ERR_CUDA;
+    if (st != PK_OK) return st;
+  }
+  return rows::take_status(dev, stream);  // (after the attention's: an error that is not returned now stays for the next query)
 }
 
 int pk_profile_start(int n) {

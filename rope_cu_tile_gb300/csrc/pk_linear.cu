@@ -421,7 +421,7 @@ int pk_linear(int dtype, const void* x, int64_t ldx, const void* w, const void* 
   a.M = static_cast<int>(T);
   a.N = N;
   a.K = K;
-  a.status = status ? status : d.status;
+  a.status = status ? status : rows::stream_status(d, stream);
   a.timeout_ns = wait_limit_ns();
   const gemm::Operand A = f.x ? rows::operand_of_copy(dtype, f.x, T, K, 0) : rows::operand(dtype, x, ldx, T, K, 0);
   const gemm::Operand B = f.w ? rows::operand_of_copy(dtype, f.w, N, K, 0) : rows::operand(dtype, w, K, N, K, 0);
@@ -496,7 +496,7 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
   if (b.x) copies.add(x, ldx, T, K, b.x);
   if (copies.launch(d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   gemm::Args a = {};
-  a.status = status ? status : d.status;
+  a.status = status ? status : rows::stream_status(d, stream);
   a.timeout_ns = wait_limit_ns();
   if (dx) {
     const gemm::Operand A = b.dz ? rows::operand_of_copy(dtype, b.dz, T, N, 0) : rows::operand(dtype, dy, lddy, T, N, 0);

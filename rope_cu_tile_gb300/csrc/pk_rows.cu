@@ -2,13 +2,16 @@
 // copies, the sum of split partial sums with the epilogue, column sums, and the product's launches.
 #include <atomic>
 #include <cstdlib>
+#include <map>
 #include <mutex>
 
 #include "pk_rows.cuh"
 
 namespace pk {
 
-__device__ int g_rows_status;
+// Status words of the calls that are given none: one a stream, the last one shared by all streams past the others.
+constexpr int kStatusWords = 1024;
+__device__ int g_rows_status[kStatusWords];
 
 namespace gemm {
 
@@ -97,6 +100,8 @@ using namespace gemm;
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_ready[kMaxDevices];  // 0 unknown, 1 ready, 2 unsupported
 Device g_devices[kMaxDevices];
+int* g_words[kMaxDevices];  // g_rows_status of each
+std::map<cudaStream_t, int> g_word_of[kMaxDevices];  // g_mu
 std::mutex g_mu;
 
 }  // namespace
@@ -127,8 +132,9 @@ int device(Device* out) {
           cudaGetLastError();
           return PK_ERR_CUDA;
         }
+        g_devices[dev].index = dev;
         g_devices[dev].sms = sms;
-        g_devices[dev].status = static_cast<int*>(word);
+        g_words[dev] = static_cast<int*>(word);
         state = 1;
       }
       g_ready[dev].store(state, std::memory_order_release);
@@ -139,13 +145,27 @@ int device(Device* out) {
   return PK_OK;
 }
 
-// The device's status word, read and cleared (the caller has synchronized what it asks about).
-int take_status(int dev) {
+int* stream_status(const Device& d, cudaStream_t stream) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  std::map<cudaStream_t, int>& words = g_word_of[d.index];
+  const int next = static_cast<int>(words.size());
+  return g_words[d.index] + words.emplace(stream, next < kStatusWords ? next : kStatusWords - 1).first->second;
+}
+
+// The stream's status word, read and cleared (the caller has synchronized the stream). Kernels write a word only while it is
+// PK_OK, so what is cleared is what was read.
+int take_status(int dev, cudaStream_t stream) {
   if (dev < 0 || dev >= kMaxDevices || g_ready[dev].load(std::memory_order_acquire) != 1) return PK_OK;
+  int* word;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    const auto it = g_word_of[dev].find(stream);
+    if (it == g_word_of[dev].end()) return PK_OK;
+    word = g_words[dev] + it->second;
+  }
   int st = 0, zero = 0;
-  if (cudaMemcpy(&st, g_devices[dev].status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) return PK_ERR_CUDA;
-  if (st != 0 && cudaMemcpy(g_devices[dev].status, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess)
-    return PK_ERR_CUDA;
+  if (cudaMemcpy(&st, word, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) return PK_ERR_CUDA;
+  if (st != 0 && cudaMemcpy(word, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return PK_ERR_CUDA;
   return st;
 }
 

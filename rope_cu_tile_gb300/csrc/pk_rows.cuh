@@ -11,11 +11,13 @@ unsigned long long wait_limit_ns();  // pk_host.cu: the bound of a pipeline wait
 namespace rows {
 
 struct Device {
+  int index = 0;
   int sms = 0;
-  int* status = nullptr;  // the device's own status word, read by pk_last_status
 };
 // the current device, checked and set up once (PK_OK or an error code)
 int device(Device* out);
+// the stream's status word, for a call that is given none: read by pk_last_status
+int* stream_status(const Device& d, cudaStream_t stream);
 
 // Carves 256-byte-aligned pieces out of a caller's workspace; with a null base it only adds up the bytes.
 struct Carver {

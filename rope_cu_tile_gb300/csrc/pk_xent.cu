@@ -556,7 +556,7 @@ int pk_cross_entropy(int dtype, const void* x, int64_t ldx, const void* w, const
   r.count = f.m.count;
   r.loss = loss;
   r.lse = lse;
-  r.status = status ? status : d.status;
+  r.status = status ? status : rows::stream_status(d, stream);
   if (rows_launch(r, stream) != cudaSuccess) return PK_ERR_CUDA;
   Inputs in;
   if (lay_out(dtype, f.m, x, ldx, w, T, D, V, d.sms, stream, &in) != cudaSuccess) return PK_ERR_CUDA;
@@ -627,7 +627,7 @@ int pk_cross_entropy_backward(int dtype, const void* x, int64_t ldx, const void*
   r.lse_rows = b.lse;
   r.unscale = b.unscale;
   r.scaled = dtype == PK_F16;
-  r.status = status ? status : d.status;
+  r.status = status ? status : rows::stream_status(d, stream);
   if (rows_launch(r, stream) != cudaSuccess) return PK_ERR_CUDA;
   Inputs in;
   if (lay_out(dtype, b.m, x, ldx, w, T, D, V, d.sms, stream, &in) != cudaSuccess) return PK_ERR_CUDA;

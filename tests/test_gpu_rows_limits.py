@@ -191,3 +191,63 @@ def test_cross_entropy_bias_gradient_sums_unrounded(pk, gen, dtype, T):
     err = e.sum(0) + (32 + T / 256 + 9 + 2) * 2.0**-24 * (q.abs() + e).sum(0)
     want = q.sum(0)
     assert ref.worst(db, want, rounded(err, want, dtype)) <= 1
+
+def test_status_belongs_to_the_call_s_stream(pk, gen):
+    """A bad label on one stream is no other stream's error; a query takes one error and leaves the other for the next."""
+    x, w = torch.ones(1, 8, device="cuda"), torch.ones(2, 8, device="cuda")
+    bad = torch.tensor([5], device="cuda")
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pk.cross_entropy(x, w, bad, stream=a)
+    a.synchronize()
+    assert pk.last_status() == 0 and pk.last_status(b) == 0
+    assert pk.last_status(a) == 11 and pk.last_status(a) == 0
+    # the attention's error and the loss's on one stream: both are told, one after the other
+    T, H = 8, 1
+    qkv = torch.zeros(T, 3 * H * 64, device="cuda", dtype=torch.bfloat16)
+    cos = torch.ones(16, 32, device="cuda", dtype=torch.bfloat16)
+    cu = torch.tensor([0, 6, 4, 8], device="cuda", dtype=torch.int32)
+    torch.cuda.synchronize()
+    pk.attend(qkv, cos, torch.zeros_like(cos), cu, H, 0, 0.125, stream=b, max_len=8)
+    pk.cross_entropy(x, w, bad, stream=b)
+    b.synchronize()
+    assert pk.last_status() == 0 and pk.last_status(a) == 0
+    assert [pk.last_status(b) for _ in range(3)] == [5, 11, 0]
+
+
+_MANY_STREAMS_SCRIPT = r"""
+import ctypes, json, os, sys
+sys.path.insert(0, os.environ["ROOT"])
+import torch
+import rope_cu_tile_gb300 as pk
+x, w = torch.ones(1, 8, device="cuda"), torch.ones(2, 8, device="cuda")
+good, bad = torch.tensor([1], device="cuda"), torch.tensor([5], device="cuda")
+torch.cuda.synchronize()
+streams = []
+for _ in range(1030):
+    p = ctypes.c_void_p()
+    assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(p))) == 0
+    streams.append(p.value)
+    pk.cross_entropy(x, w, good, stream=p.value)
+torch.cuda.synchronize()
+got = []
+for s in (streams[0], streams[500], streams[1028]):
+    pk.cross_entropy(x, w, bad, stream=s)
+    torch.cuda.synchronize()
+    got.append([pk.last_status(), pk.last_status(streams[7]), pk.last_status(s), pk.last_status(s)])
+print(json.dumps(got))
+"""
+
+
+def test_status_of_more_streams_than_words():
+    """A device has 1024 words; the streams past them share the last. Each is still told its errors."""
+    import json
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", _MANY_STREAMS_SCRIPT], env=dict(os.environ, ROOT=root), capture_output=True, text=True,
+                       timeout=300)
+    assert p.returncode == 0, p.stderr[-3000:]
+    assert json.loads(p.stdout.strip().splitlines()[-1]) == [[0, 0, 11, 0]] * 3
