@@ -65,7 +65,8 @@
  *                          producer of each CTA withholds its first work-item hand-off, so
  *                          the call ends with PK_ERR_TIMEOUT after one wait bound and writes
  *                          no valid output; later calls without it are unaffected. In the
- *                          token-row operators' products it withholds the first operand stage.
+ *                          token-row operators' products it withholds the first operand stage;
+ *                          each product of such a call ends after two wait bounds at most.
  *   PK_ATTN=q4|tc_single   pk_attend and its typed forms run PK_KERNEL_Q4 or
  *                          PK_KERNEL_TC_SINGLE instead of PK_KERNEL_TC for bf16 / fp16 inputs
  *                          outside the narrow windows (read at every call).

@@ -315,12 +315,17 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
     }
   }
   // every stage released before leaving (one never filled counts as released): no copy and no arrival is on its way to
-  // this CTA any more
+  // this CTA any more. After giving up, one wait bound for all of them together: nobody releases a stage that was filled, and
+  // its copies have landed long before.
+  uint64_t t0 = 0;
   for (int i = 0; i < kStages; ++i) {
-    if (bad)
-      mbar_wait(smem_u32(&meta->empty[st]), ph ^ 1u, a.timeout_ns);
-    else if (!wait_warp(meta, a, &meta->empty[st], ph ^ 1u))
+    if (bad) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      mbar_wait(smem_u32(&meta->empty[st]), ph ^ 1u, now - t0 < a.timeout_ns ? a.timeout_ns - (now - t0) : 0);
+    } else if (!wait_warp(meta, a, &meta->empty[st], ph ^ 1u)) {
       bad = true;
+    }
     st = st + 1 == kStages ? 0 : st + 1;
     ph ^= st == 0 ? 1u : 0u;
   }

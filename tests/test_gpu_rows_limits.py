@@ -251,3 +251,43 @@ def test_status_of_more_streams_than_words():
                        timeout=300)
     assert p.returncode == 0, p.stderr[-3000:]
     assert json.loads(p.stdout.strip().splitlines()[-1]) == [[0, 0, 11, 0]] * 3
+
+_STALL_SCRIPT = r"""
+import json, os, sys, time
+sys.path.insert(0, os.environ["ROOT"])
+import torch
+import rope_cu_tile_gb300 as pk
+torch.manual_seed(3)
+got = []
+for T, K, N in ((300, 1024, 264), (9000, 1024, 1024)):  # one CTA a tile, and pairs; more k steps than stages
+    x, w = torch.randn(T, K, device="cuda").bfloat16(), torch.randn(N, K, device="cuda").bfloat16()
+    want = pk.linear(x, w)
+    torch.cuda.synchronize()
+    os.environ["PK_DEBUG_SKIP_ARRIVE"] = "1"
+    t = time.time()
+    pk.linear(x, w)
+    torch.cuda.synchronize()
+    t = time.time() - t
+    del os.environ["PK_DEBUG_SKIP_ARRIVE"]
+    word = pk.last_status()
+    after = pk.linear(x, w)
+    torch.cuda.synchronize()
+    got.append([word, pk.last_status(), bool(torch.equal(after, want)), t])
+print(json.dumps(got))
+"""
+
+
+def test_a_product_that_gives_up_ends_within_two_wait_bounds():
+    """One bound for the wait that runs out, one for what is still on its way (bound 200 ms, and 100 ms for the host)."""
+    import json
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, ROOT=root, PK_TIMEOUT_MS="200")
+    env.pop("PK_DEBUG_SKIP_ARRIVE", None)
+    p = subprocess.run([sys.executable, "-c", _STALL_SCRIPT], env=env, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-3000:]
+    for word, later, same, t in json.loads(p.stdout.strip().splitlines()[-1]):
+        assert (word, later, same) == (6, 0, True) and t <= 0.5, t
