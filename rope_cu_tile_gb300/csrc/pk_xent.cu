@@ -21,7 +21,9 @@ namespace {
 using namespace rows;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFloor = -1.0e30f;  // running maximum of nothing: finite, so that a row of -inf logits stays defined
+// running maximum of nothing: the lowest finite value, so that a row of -inf logits stays defined and one of words masked by
+// that value has it as its maximum
+constexpr float kFloor = -3.402823466e38f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return attn::ex2(x); }
 
@@ -259,10 +261,10 @@ __global__ void __launch_bounds__(256) pk_xent_join_kernel(const float2* part, i
     __syncthreads();
     if (g == 0 && row < n) {
       for (int i = 1; i < 32; ++i) join(m, l, s[i][r]);
-      const float all = m + logf(l);
+      const float rest = logf(l);
       const int t = __ldcg(idx + row);
-      lse[t] = all;
-      loss[t] = all - __ldcg(picked + row);
+      lse[t] = m + rest;
+      loss[t] = (m - __ldcg(picked + row)) + rest;  // not lse - z: large logits would leave the loss their rounding
     }
     __syncthreads();
   }

@@ -291,3 +291,25 @@ def test_a_product_that_gives_up_ends_within_two_wait_bounds():
     assert p.returncode == 0, p.stderr[-3000:]
     for word, later, same, t in json.loads(p.stdout.strip().splitlines()[-1]):
         assert (word, later, same) == (6, 0, True) and t <= 0.5, t
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", [(20, 100), (300, 4099)])
+def test_words_masked_by_the_lowest_value(pk, gen, dtype, T, V):
+    """A bias of the type's lowest value masks words; where it masks all of them the row's lse is still its log-sum-exp (the
+    lowest value, to fp32's precision) and the loss that of equal logits."""
+    D = 32
+    x, w = rand(gen, T, D, dtype=dtype), rand(gen, V, D, std=D**-0.5, dtype=dtype)
+    low = torch.finfo(dtype).min
+    labels = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    some = torch.zeros(V, device="cuda", dtype=dtype)
+    some[V // 2:] = low
+    loss, lse = pk.cross_entropy(x, w, labels.clamp(max=V // 2 - 1), some)
+    (wl, ws), bound = ref.cross_entropy(x, w[:V // 2].contiguous(), labels.clamp(max=V // 2 - 1), None)
+    assert ref.worst(lse, ws, bound) <= 1 and ref.worst(loss, wl, 2 * bound) <= 1
+    every = torch.full((V,), low, device="cuda", dtype=dtype)
+    zero = torch.zeros_like(x)
+    loss, lse = pk.cross_entropy(zero, w, labels, every)
+    assert ref.worst(lse, torch.full_like(lse, 1.0, dtype=torch.float64) * low + math.log(V), torch.full_like(lse, abs(low) * 2.0**-23)) <= 1
+    # equal logits: ln V, within the sums' errors (64 + V / 32 additions, of V ones) and the logarithm's; fp16's lowest value is
+    # small enough for the logits to differ by the products' zero only
+    assert ref.worst(loss, torch.full_like(loss, math.log(V), dtype=torch.float64), torch.full_like(loss, (64 + V / 32) * 2.0**-23 + 2.0**-20)) <= 1
