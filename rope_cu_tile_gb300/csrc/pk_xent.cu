@@ -318,8 +318,8 @@ struct GradEpi {
     }
     const int row = r0 + lane;
     const bool live = row < M;
-    // rows past the count feed dW: zero, as exp(z - inf) times 0
-    const float g = live ? __ldcg(p.coef + row) : 0.0f, lse = live ? __ldcg(p.lse + row) : INFINITY;
+    // (rows past the count feed dW and db: set to zero below)
+    const float g = live ? __ldcg(p.coef + row) : 0.0f, lse = live ? __ldcg(p.lse + row) : 0.0f;
     const int label = live ? __ldcg(p.lab + row) - p.v0 : -1;
     const int end = min(cols, N - c0);
 #pragma unroll 1
@@ -344,6 +344,10 @@ struct GradEpi {
         const float2 q = mul2(make_float2(v[i], v[i + 1]), make_float2(g, g));
         v[i] = q.x;
         v[i + 1] = q.y;
+      }
+      if (r0 + 32 > M) {  // (their logits are 0 W^T + b: undefined beside infinite weights, and so times 0)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = live ? v[i] : 0.0f;
       }
       // db: the column sums before dz is rounded (sums of the rounded tile, read back from the staging memory, left db with the
       // roundings wherever labels and probabilities cancel in a column)

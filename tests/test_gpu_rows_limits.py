@@ -313,3 +313,20 @@ def test_words_masked_by_the_lowest_value(pk, gen, dtype, T, V):
     # equal logits: ln V, within the sums' errors (64 + V / 32 additions, of V ones) and the logarithm's; fp16's lowest value is
     # small enough for the logits to differ by the products' zero only
     assert ref.worst(loss, torch.full_like(loss, math.log(V), dtype=torch.float64), torch.full_like(loss, (64 + V / 32) * 2.0**-23 + 2.0**-20)) <= 1
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("labelled", [1.0, 0.6])
+def test_a_word_of_infinite_weights_gets_no_gradient_from_padding(pk, gen, dtype, labelled):
+    """A word whose weights are -inf has the logit -inf in every row (x > 0): probability 0, and a gradient of 0 in its row of
+    dw and db. Rows that only fill a tile have x = 0 and would have a logit of 0 (-inf)."""
+    T, D, V = 70, 32, 300
+    x, w = rand(gen, T, D, dtype=dtype).abs() + 0.125, rand(gen, V, D, std=D**-0.5, dtype=dtype)
+    w[7] = -INF
+    bias = rand(gen, V, dtype=dtype)
+    labels = torch.randint(8, V, (T,), generator=gen, device="cuda")
+    labels[torch.rand(T, generator=gen, device="cuda") >= labelled] = -100
+    _, lse = pk.cross_entropy(x, w, labels, bias)
+    assert bool(lse.isfinite().all())
+    _, dw, db = pk.cross_entropy_backward(x, w, labels, lse, torch.ones(T, device="cuda"), bias, need_dx=False)
+    assert bool((dw[7] == 0).all()) and float(db[7]) == 0
+    assert bool(dw.isfinite().all()) and bool(db.isfinite().all())
