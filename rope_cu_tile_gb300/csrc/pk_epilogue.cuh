@@ -131,6 +131,23 @@ __device__ __forceinline__ void store8_any(void* p, int64_t i, int n, const floa
     if (j < n) Ty<DT>::put(p, i + j, v[j]);
 }
 
+// Eight fp32 values as three planes of bf16, v = hi + mid + lo. hi stays finite where v is: the values past bf16's largest
+// would round to infinity, and mid holds what is left of them (as of infinity, which thus stays non-finite).
+__device__ __forceinline__ void planes8(float (&v)[8], uint32_t (&h)[3][4]) {
+  constexpr float kMost = 3.3895313892515355e38f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[0][i] = Elem<true>::pack(fminf(fmaxf(v[2 * i], -kMost), kMost), fminf(fmaxf(v[2 * i + 1], -kMost), kMost));
+#pragma unroll
+    for (int k = 1; k < 3; ++k) {
+      const float2 b = Elem<true>::unpack(h[k - 1][i]);
+      v[2 * i] -= b.x;
+      v[2 * i + 1] -= b.y;
+      h[k][i] = Elem<true>::pack(v[2 * i], v[2 * i + 1]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------------
 // activations (value, and slope at z). fp32 results take the full-precision functions (erfcf, expf). 16-bit ones take
 // short exponentials and reciprocals, good to some 2^-17 relative where the result's rounding is 2^-11 or 2^-8: dz of a

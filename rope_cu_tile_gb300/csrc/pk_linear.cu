@@ -134,18 +134,11 @@ __global__ void __launch_bounds__(kDzThreads, kDzBlocks) pk_dz_kernel(const __gr
         if (!a.dz) continue;
       }
       if constexpr (DT == PK_F32) {
+        uint32_t h[3][4];
+        planes8(v, h);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[j] = Elem<true>::pack(v[2 * j], v[2 * j + 1]);
-            const float2 b = Elem<true>::unpack(h[j]);
-            v[2 * j] -= b.x;
-            v[2 * j + 1] -= b.y;
-          }
-          *reinterpret_cast<uint4*>(a.dz + k * a.plane + r * a.ldz + c) = make_uint4(h[0], h[1], h[2], h[3]);
-        }
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(a.dz + k * a.plane + r * a.ldz + c) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
       } else {
         store8<DT>(a.dz, r * a.ldz + c, v);
       }

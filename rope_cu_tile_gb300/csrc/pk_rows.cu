@@ -212,17 +212,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ CopyJ
     }
     if constexpr (DT == PK_F32) {
       uint32_t h[3][4];
-#pragma unroll
-      for (int i2 = 0; i2 < 4; ++i2) {
-        float2 a = make_float2(v[2 * i2], v[2 * i2 + 1]);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          h[k][i2] = Elem<true>::pack(a.x, a.y);
-          const float2 b = Elem<true>::unpack(h[k][i2]);
-          a.x -= b.x;
-          a.y -= b.y;
-        }
-      }
+      planes8(v, h);
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         *reinterpret_cast<uint4*>(j.dst + k * j.plane + r * j.ldp + c) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);

@@ -330,3 +330,24 @@ def test_a_word_of_infinite_weights_gets_no_gradient_from_padding(pk, gen, dtype
     _, dw, db = pk.cross_entropy_backward(x, w, labels, lse, torch.ones(T, device="cuda"), bias, need_dx=False)
     assert bool((dw[7] == 0).all()) and float(db[7]) == 0
     assert bool(dw.isfinite().all()) and bool(db.isfinite().all())
+
+@pytest.mark.parametrize("T", [5, 16, 300])
+def test_largest_fp32_operands(pk, gen, T):
+    """The largest finite values round to infinity in bf16; their products with small weights are finite all the same."""
+    K, N = 64, 40
+    top = torch.finfo(torch.float32).max
+    x, w = rand(gen, T, K), rand(gen, N, K)
+    x[:, 0] = top
+    x[::2, 0] = -top
+    w[:, 0] = 2.0**-100
+    want, _, bound, _ = ref.linear(x, w, None, None, "none", 0.0, 0, 0)
+    assert ref.worst(pk.linear(x, w), want, bound) <= 1
+    dy = torch.full((T, N), 2.0**-100, device="cuda")
+    _, dw, _ = pk.linear_backward(x, w, dy, need_dx=False, need_db=False)
+    (_, want, _), (_, bound, _) = ref.linear_backward(x, w, dy, None, "none", 0.0, 0, 0)
+    assert ref.worst(dw, want, bound) <= 1
+    dy = x[:, :1].expand(-1, N).contiguous()  # the gradient itself at the end of the range, through the activation
+    wx = torch.full((N, K), 2.0**-100, device="cuda")
+    dx, _, _ = pk.linear_backward(x, wx, dy, torch.ones(T, N, device="cuda"), "relu", need_dw=False, need_db=False)
+    want = dy.double() @ wx.double()
+    assert ref.worst(dx, want, (2 * ref.sum_bound(N, torch.float32) + ref.U[torch.float32]) * dy.double().abs() @ wx.double()) <= 1
