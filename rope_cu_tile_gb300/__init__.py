@@ -559,7 +559,7 @@ def _overlap(a, b):
     pa, pb = a.data_ptr(), b.data_ptr()
     if not (pa < pb + _extent(b) and pb < pa + _extent(a)):
         return False
-    if a.dim() == 2 and b.dim() == 2 and a.stride(0) == b.stride(0) and a.element_size() == b.element_size():
+    if a.dim() == 2 and b.dim() == 2 and a.stride(0) == b.stride(0) > 0 and a.element_size() == b.element_size():
         row = a.stride(0) * a.element_size()
         d = (pb - pa) % row  # b's first column, counted from a's
         if d >= a.shape[1] * a.element_size() and d + b.shape[1] * b.element_size() <= row:
