@@ -351,3 +351,72 @@ def test_largest_fp32_operands(pk, gen, T):
     dx, _, _ = pk.linear_backward(x, wx, dy, torch.ones(T, N, device="cuda"), "relu", need_dw=False, need_db=False)
     want = dy.double() @ wx.double()
     assert ref.worst(dx, want, (2 * ref.sum_bound(N, torch.float32) + ref.U[torch.float32]) * dy.double().abs() @ wx.double()) <= 1
+
+@pytest.mark.parametrize("dtype,T,D,V,labelled", [(torch.float32, 300, 1100, 700, 1.0), (torch.float32, 700, 1100, 1003, 0.4),
+                                                  (torch.float32, 1500, 2056, 9000, 0.9), (torch.bfloat16, 130, 16456, 300, 0.5),
+                                                  (torch.float16, 300, 20000, 264, 1.0)])
+def test_cross_entropy_of_long_features(pk, gen, dtype, T, D, V, labelled):
+    """More terms than the tensor pipe adds up by itself: the sums are taken over in phases, for the loss and its gradient."""
+    x, w = rand(gen, T, D, dtype=dtype), rand(gen, V, D, std=2 * D**-0.5, dtype=dtype)
+    bias = rand(gen, V, dtype=dtype)
+    labels = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    labels[torch.rand(T, generator=gen, device="cuda") >= labelled] = -100
+    loss, lse = pk.cross_entropy(x, w, labels, bias)
+    (wl, ws), bound = ref.cross_entropy(x, w, labels, bias)
+    assert ref.worst(lse, ws, bound) <= 1 and ref.worst(loss, wl, 2 * bound) <= 1
+    # closer than the worst case of any order: the pipe truncates 2^-23 of a partial sum a step of 16, at most 1024 steps (fp32:
+    # 64, and five passes 2^-8 as large) before a rounding sum takes over; a phase's partial sums are differences of two of the
+    # whole's. Some rows, their partial sums in 64 bits.
+    rows = (labels >= 0).nonzero()[:32, 0]
+    k = D // 16 * 16
+    parts = torch.einsum("tgk,vgk->tvg", x[rows, :k].double().view(len(rows), -1, 16), w[:, :k].double().view(V, -1, 16)[:, :])
+    most = 2 * float(parts.cumsum(2).abs().max()) + 1
+    steps = 64 * (1 + 5 * 2.0**-8) + D / 1024 + 4 if dtype == torch.float32 else 1024 + D / 16384 + 4
+    zerr = steps * 2.0**-23 * most + (2.0**-24 * float((x[rows].double().abs() @ w.double().abs().T).max()) if dtype == torch.float32 else 0)
+    rest = (float(ref.logits(x[rows], w, bias)[0].abs().max()) + 1) * 2.0**-21 + (64 + V / 32) * 2.0**-23 + 2.0**-22 * ws[rows].abs()
+    assert ref.worst(lse[rows], ws[rows], zerr + rest) <= 1
+    del parts
+    dloss = torch.rand(T, generator=gen, device="cuda") + 0.5
+    got = pk.cross_entropy_backward(x, w, labels, lse, dloss, bias)
+    want, bounds = ref.cross_entropy_backward(x, w, labels, lse, dloss, bias)
+    for name, g, v, b in zip(("dx", "dw", "db"), got, want, bounds):
+        assert ref.worst(g, v, b) <= 1, name
+        off = float((g.double() - v).norm() / v.norm())
+        assert off <= {torch.float32: 2.0**-16, torch.bfloat16: 2.0**-7, torch.float16: 2.0**-10}[dtype], (name, off)
+    assert pk.last_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("labelled", [1.0, 0.3])
+def test_gradient_over_several_pieces_of_the_vocabulary(pk, gen, dtype, labelled):
+    """Pieces of at least 4096 words: the gradient's fp32 sums between them, fp16's scale on the last one, fp32's planes, the map
+    of labelled rows, with a last piece narrower than the others. Some rows and words against 64 bits."""
+    T, D, V = (40001 if dtype == torch.float32 else 131073), 40, 9001 if dtype == torch.float32 else 13001
+    x, w = rand(gen, T, D, dtype=dtype), rand(gen, V, D, std=2 * D**-0.5, dtype=dtype)
+    bias = rand(gen, V, dtype=dtype)
+    labels = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    labels[torch.rand(T, generator=gen, device="cuda") >= labelled] = -100
+    _, lse = pk.cross_entropy(x, w, labels, bias)
+    dloss = torch.rand(T, generator=gen, device="cuda") * 1e-4
+    dx, dw, db = pk.cross_entropy_backward(x, w, labels, lse, dloss, bias)
+    some = torch.arange(0, T, 1013, device="cuda")
+    want, bound = ref.cross_entropy_backward(x[some], w, labels[some], lse[some], dloss[some], bias)
+    assert ref.worst(dx[some], want[0], bound[0]) <= 1
+    assert bool((dx[labels < 0] == 0).all())
+    words = torch.tensor([0, 1, 4095, 4096, 4351, 4352, 4608, 8191, 8192, V - 300, V - 1], device="cuda")
+    z, dz = ref.logits(x, w[words].contiguous(), bias[words])
+    has = (labels >= 0)[:, None]
+    q = torch.exp(z - lse.double()[:, None])
+    e = q * (dz + (z.abs() + lse.double().abs()[:, None] + 2) * 2.0**-21)
+    g = dloss.double()[:, None]
+    q = torch.where(has, (q - (labels[:, None] == words[None, :]).double()) * g, 0.0)
+    e = torch.where(has, e * g, 0.0) + 2.0**-22 * q.abs()
+    u = ref.U[dtype] if dtype != torch.float32 else 2.0**-23
+    if dtype == torch.float16:
+        e = e + has * 2.0**-25 * float(dloss.max()) * 2.0**-14
+    r = e + u * q.abs()  # dz as stored
+    X = x.double()
+    for name, got, v, b in (("dw", dw[words], q.T @ X, r.T @ X.abs() + ref.sum_bound(16384, dtype) * ((q.abs() + r).T @ X.abs())),
+                            ("db", db[words], q.sum(0), r.sum(0) + 2.0**-13 * q.abs().sum(0))):
+        assert ref.worst(got, v, rounded(b, v, dtype)) <= 1, name
+    assert pk.last_status() == 0
