@@ -301,13 +301,15 @@ struct LinParams {
   int bias_vec, res_vec, y_vec, pre_vec;  // 16-byte rows: vector access
 };
 
-// The same for the tensor-core product: outputs whose rows lie on 16-byte boundaries are stored by TMA.
+// The same for the tensor-core product: outputs whose rows begin and end on 16-byte boundaries are stored by TMA.
 struct LinTiles : LinParams {
   CUtensorMap map_y, map_pre;
   int tma_y, tma_pre;
 };
 
-// A staged tile of 32 rows x 32 columns (64- or 128-byte rows, swizzled) to (x, y, plane) of a map, clipped at its ends. The warp's writes
+// A staged tile of 32 rows x 32 columns (64- or 128-byte rows, swizzled) to (x, y, plane) of a map, clipped at its ends: at the
+// last row, and at the end of the last 16 bytes that a row's columns touch (the store fills those up with what is staged, so
+// the memory behind a row that ends inside them has to be padding of the library's own). The warp's writes
 // are made visible to the copy; `stage` may be written again after stored().
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, const uint8_t* stage, int x, int y, int plane, int lane) {
   fence_proxy_async_smem();

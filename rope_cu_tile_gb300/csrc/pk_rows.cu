@@ -379,7 +379,9 @@ cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::O
   }
   LinTiles t = {};
   static_cast<LinParams&>(t) = ep;
-  t.tma_y = ep.y_vec && !ep.rowmap;
+  // (a TMA store clips a row's end to whole 16 bytes only: where the rows of y end inside one and go on in a wider matrix, the
+  // warps store the last columns themselves)
+  t.tma_y = ep.y_vec && !ep.rowmap && (a.N * e & 15) == 0;
   t.tma_pre = ep.pre_vec;
   if ((t.tma_y && !gemm::make_out_map(&t.map_y, dtype, ep.y, a.M, a.N, ep.ldy, 1, 0)) ||
       (t.tma_pre && !gemm::make_out_map(&t.map_pre, dtype, ep.pre, a.M, a.N, ep.ldpre, 1, 0)))

@@ -420,3 +420,27 @@ def test_gradient_over_several_pieces_of_the_vocabulary(pk, gen, dtype, labelled
                             ("db", db[words], q.sum(0), r.sum(0) + 2.0**-13 * q.abs().sum(0))):
         assert ref.worst(got, v, rounded(b, v, dtype)) <= 1, name
     assert pk.last_status() == 0
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,K", [(1, 64), (16, 64), (122, 40), (300, 2048), (9000, 64)])
+def test_columns_beside_an_output_stay_as_they_were(pk, gen, dtype, T, K):
+    """out as some columns of a wider matrix whose rows are whole 16 bytes: what stands left and right of them is not written,
+    whatever the number of columns; alone, and as residual and output in one."""
+    for N, off, wide in ((41, 0, 48), (33, 0, 40), (36, 8, 56), (34, 0, 40), (44, 0, 48), (1, 0, 8), (39, 16, 56), (589, 0, 592), (130, 8, 144),
+                         (64, 0, 72), (31, 0, 32)):
+        x, w = rand(gen, T, K, dtype=dtype), rand(gen, N, K, std=K**-0.5, dtype=dtype)
+        want = pk.linear(x, w)
+        for residual in (False, True):
+            base = torch.full((T + 1, wide), 7.0, dtype=dtype, device="cuda")
+            out = base[:T, off:off + N]
+            if residual:
+                out.copy_(rand(gen, T, N, dtype=dtype))
+                want = pk.linear(x, w, residual=out.clone())
+            got = pk.linear(x, w, residual=out if residual else None, out=out)
+            assert torch.equal(got, want) and torch.equal(out, want), (N, off, wide)
+            base[:T, off:off + N] = 7.0
+            assert bool((base == 7).all()), (N, off, wide)
+            got = pk.dropout(want, 0.25, 3, out=out)
+            assert torch.equal(got, pk.dropout(want, 0.25, 3))
+            base[:T, off:off + N] = 7.0
+            assert bool((base == 7).all()), (N, off, wide)
