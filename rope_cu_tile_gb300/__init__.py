@@ -577,7 +577,8 @@ def linear(x, w, bias=None, residual=None, act: str = "none", p: float = 0.0, se
     of one type); act "none", "relu", "gelu" or "silu"; dropout of probability p with the bits of (seed, offset), as
     `dropout`. x, residual and out may have strided rows; out may be residual itself. return_pre: also the
     pre-activation x w^T + bias [T, N], which linear_backward needs when act is not "none". `status`: optional int32
-    device tensor of one element (otherwise last_status tells of device-detected errors)."""
+    device tensor of one element (otherwise last_status of the call's stream tells of device-detected errors; a captured
+    call's are those of the stream it was captured on)."""
     torch = _torch()
     dt, dev = x.dtype, x.device
     code = dtype_code(x)
@@ -709,7 +710,7 @@ def _xent_inputs(x, w, labels, bias, status, stream):
 def cross_entropy(x, w, labels, bias=None, status=None, stream=None):
     """(loss [T], lse [T]), float32: the softmax cross entropy of the logits x w^T + bias, x [T, D], w [V, D], against
     int64 labels [T], without storing the logits. A negative label leaves its row out (loss 0, no work); a label >= V
-    gives a loss of NaN and PK_ERR_BAD_LABEL (in `status`, an int32 device tensor of one element, or last_status)."""
+    gives a loss of NaN and PK_ERR_BAD_LABEL (in `status`, an int32 device tensor of one element, or last_status of the call's stream)."""
     torch = _torch()
     code, dt, dev, ldx, T, D, V = _xent_inputs(x, w, labels, bias, status, stream)
 

@@ -1,6 +1,6 @@
 // pk_epilogue.cuh -- what happens to the fp32 accumulators of a product before they are stored: bias, activation,
 // dropout, residual, one rounding to the element type. The same steps serve the tensor-core product (a thread holds 32
-// columns of one row), the sum of the splits of k and the few-row kernel (a thread holds 8 columns of one row).
+// columns of one row), the sum of the splits of k (8 columns of one row) and the few-row kernel (one element).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -295,7 +295,7 @@ struct LinParams {
   void* pre;            // [M, N] in the output's type: bias added, before the activation; or null
   int64_t ldres, ldy, ldpre;
   const float* alpha;   // device factor of the whole, or null
-  const int* rowmap;    // row of y (and of the mask) that row m goes to, or null
+  const int* rowmap;    // row of y that row m goes to, or null
   int act;
   DropArgs drop;
   int bias_vec, res_vec, y_vec, pre_vec;  // 16-byte rows: vector access
@@ -484,15 +484,12 @@ struct Bias {
   }
 };
 
-template <int NC>
-__device__ __forceinline__ void read_acc(uint32_t t, bool zero, float (&v)[NC]) {
+__device__ __forceinline__ void read_acc(uint32_t t, bool zero, float (&v)[32]) {
   if (zero) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) v[i] = 0.0f;
-  } else if constexpr (NC == 32) {
-    tmem_ld32(t, v);
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
   } else {
-    tmem_ld16(t, v);
+    tmem_ld32(t, v);
   }
 }
 

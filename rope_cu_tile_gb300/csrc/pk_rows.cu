@@ -62,8 +62,11 @@ bool make_out_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int6
              e == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The cheapest cut by a model of the product's time in SM cycles: waves x (k steps x cycles a step + cycles a tile), plus
-// the partial sums' way through memory.
+// The cheapest cut by a model of the product's time: waves x (k steps x cost of a step + cost of a tile), plus the partial
+// sums' way through memory. The costs are fitted, in a unit of their own: a step of either tile takes 500 to 600 cycles, the
+// pair's (four times the products) at the tensor pipe's rate of 512, the lone tile's at its operands' way through L2, twice
+// the bytes a product. Lone tile and pair, bf16, us: 300 x 768 -> 768 6.7, 8.4; 2304 x 768 -> 2304 12.9, 12.3;
+// 2400 x 1024 -> 4096 19.7, 20.0 (taken, 2 % off); 4096 x 1024 -> 4096 31.0, 24.9; 16931 x 768 -> 2304 53.0, 38.8.
 Shape pick_shape(int64_t M, int64_t N, int64_t K, int terms, int sms, bool may_split) {
   Shape best;
   double best_cost = -1.0;
@@ -71,7 +74,6 @@ Shape pick_shape(int64_t M, int64_t N, int64_t K, int terms, int sms, bool may_s
   for (int cg = 1; cg <= 2; ++cg) {
     const int64_t tile = 128 * cg, tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
     const int64_t slots = sms / cg;
-    // cycles a k step: the 256 x 256 pair runs at the tensor pipe's rate, the 128 x 128 tile at its operands' shared-memory reads
     const double step = cg == 2 ? 280.0 : 270.0, over = cg == 2 ? 1500.0 : 1000.0;
     for (int s = 1; s <= (may_split ? 32 : 1); ++s) {
       if (s > 1 && (s > kbs || s * M * N > (int64_t(1) << 28))) break;
