@@ -444,3 +444,35 @@ def test_columns_beside_an_output_stay_as_they_were(pk, gen, dtype, T, K):
             assert torch.equal(got, pk.dropout(want, 0.25, 3))
             base[:T, off:off + N] = 7.0
             assert bool((base == 7).all()), (N, off, wide)
+
+def test_captured_calls_decide_on_the_device(pk, gen):
+    """Replayed with other contents, a captured fp16 gradient takes the scale that those need, and a captured loss tells of a bad
+    label in the word of the stream it was captured on."""
+    T, K, N, V = 200, 64, 136, 300
+    x, w, wv = rand(gen, T, K, std=0.05).half(), rand(gen, N, K, std=0.05).half(), rand(gen, V, K).half()
+    dy, pre = rand(gen, T, N).half(), rand(gen, T, N).half()
+    labels = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        return [*pk.linear_backward(x, w, dy, pre, "gelu", 0.5, 3, 4), *pk.cross_entropy(x, wv, labels)]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    for size in (1.0, 2e4, 1e-6, 0.1):
+        dy.copy_((torch.rand(T, N, generator=gen, device="cuda") * 2 * size).half())
+        graph.replay()
+        want = step()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), size
+    assert bool(got[0].isfinite().all())
+    assert pk.last_status() == 0 and pk.last_status(side) == 0
+    labels[3] = V
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool(got[3][3].isnan()) and pk.last_status() == 0
+    assert pk.last_status(side) == 11 and pk.last_status(side) == 0
