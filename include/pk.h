@@ -99,7 +99,7 @@ enum pk_status {
     PK_ERR_TOO_LARGE = 9,    /* pk_attend_noalloc: T above PK_NOALLOC_MAX_T */
     PK_ERR_CAPTURE = 10,     /* the stream is being captured and its workspace would have to
                                 be allocated or grown: make one uncaptured call first */
-    PK_ERR_BAD_LABEL = 11    /* device: pk_cross_entropy: a label at or past V */
+    PK_ERR_BAD_LABEL = 11    /* device: a label or a target word at or past V */
 };
 
 enum pk_dtype { PK_F32 = 0, PK_BF16 = 1, PK_F16 = 2 };
@@ -438,6 +438,54 @@ int pk_cross_entropy_backward(int dtype, const void *x, int64_t ldx, const void 
 /* backward: 0 or 1; need_db: whether the backward call has db. */
 int pk_cross_entropy_workspace(int dtype, const void *x, int64_t ldx, const void *w, int backward, int need_db, int64_t T,
                                int D, int V, int64_t *bytes);
+
+/*
+ * Root-mean-square norm with the residual's addition: h = x + r, y = w h / sqrt(mean(h^2) + eps).
+ *   x [T, D] (ldx), residual [T, D] (ldr) or NULL, w [D], y [T, D] (ldy), h [T, D] (ldh) or NULL. D <= PK_NORM_MAX_D; eps
+ *   positive and finite. Sums are fp32, of the unrounded h; y and h are rounded once. h may be x or residual itself (of the
+ *   same row stride).
+ * pk_rms_norm_q8 writes the rows in 8 bits for pk_linear_q8: scale[t] = max |y| / 448 of the row (fp32), q [T, D] (ldq,
+ * in bytes) = y / scale rounded to e4m3. A row of zeros has scale 0; one with a NaN, scale NaN; one with an infinity, scale
+ * infinity. pk_quantize_rows does that to x itself (a weight matrix, other activations). These calls take no
+ * workspace and find no errors on the device.
+ */
+#define PK_NORM_MAX_D 16384
+int pk_rms_norm(int dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *w, float eps, int64_t T,
+                int D, void *y, int64_t ldy, void *h, int64_t ldh, struct CUstream_st *stream);
+int pk_rms_norm_q8(int dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *w, float eps, int64_t T,
+                   int D, void *q, int64_t ldq, float *scale, void *h, int64_t ldh, struct CUstream_st *stream);
+int pk_quantize_rows(int dtype, const void *x, int64_t ldx, int64_t T, int D, void *q, int64_t ldq, float *scale,
+                     struct CUstream_st *stream);
+/*
+ * The norm's gradient for its h (x where there was no residual): with n = h / sqrt(mean(h^2) + eps) and g = dy w,
+ * dx = (g - n mean(g n)) / sqrt(mean(h^2) + eps) + dh (the gradient of x and of residual alike; dh, the gradient that arrives
+ * on h itself, may be NULL), dw = sum over rows of dy n. dx [T, D] (lddx), dw [D]: each may be NULL. dx may be dy or
+ * dh itself (of the same row stride). need_dw: whether the call has dw.
+ */
+int pk_rms_norm_backward(int dtype, const void *h, int64_t ldh, const void *w, const void *dy, int64_t lddy, const void *dh,
+                         int64_t lddh, float eps, int64_t T, int D, void *dx, int64_t lddx, void *dw, void *workspace,
+                         int64_t workspace_bytes, struct CUstream_st *stream);
+int pk_rms_norm_backward_workspace(int dtype, int64_t T, int D, int need_dw, int64_t *bytes);
+
+/*
+ * Of rows of logits z [T, V] (ld): lse = ln sum_v exp z_v, logp[t] = z[t, labels[t]] - lse (0 for a negative label; NaN and
+ * PK_ERR_BAD_LABEL for one at or past V), entropy = -sum_v p_v ln p_v with p = exp(z - lse), all fp32 [T]; and the `top`
+ * likeliest words, the likeliest first and equal ones by their index: top_idx [T, top] int64 and top_logp [T, top]
+ * (top <= PK_LOGPROBS_MAX_TOP and <= V; 0: both may be NULL). NaN is ranked above all numbers. A logit of -inf is a word
+ * that cannot be: probability 0. A row of nothing else has lse and log probabilities -inf and entropy 0; one with a NaN or
+ * +inf has NaN. No workspace.
+ */
+#define PK_LOGPROBS_MAX_TOP 64
+int pk_token_logprobs(int dtype, const void *logits, int64_t ld, const int64_t *labels, int64_t T, int V, int top, float *logp,
+                      float *lse, float *entropy, float *top_logp, int64_t *top_idx, int *status, struct CUstream_st *stream);
+/*
+ * The gradient of sum_t dlogp[t] logp[t] + dentropy[t] entropy[t] with respect to the logits, for the forward's lse and
+ * entropy: dz_v = dlogp ([v = label] - p_v) - dentropy p_v (ln p_v + entropy). dentropy may be NULL (entropy then too). A row
+ * whose label is negative or past V has no part in logp. dlogits [T, V] (lddz) may be logits itself (lddz = ld).
+ */
+int pk_token_logprobs_backward(int dtype, const void *logits, int64_t ld, const int64_t *labels, const float *lse,
+                               const float *entropy, const float *dlogp, const float *dentropy, int64_t T, int V, void *dlogits,
+                               int64_t lddz, struct CUstream_st *stream);
 
 /* Text of a status code (static storage). */
 const char *pk_status_string(int status);

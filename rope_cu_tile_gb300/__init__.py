@@ -32,6 +32,8 @@ STATUS = {
 }
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NOALLOC_MAX_T = 1048576
+NORM_MAX_D = 16384
+LOGPROBS_MAX_TOP = 64
 LINEAR_FEW_T = 8  # include/pk.h: half as many rows of any type need no workspace in linear
 
 # names declared in include/pk.h
@@ -41,7 +43,9 @@ EXPORTS = ("pk_attend", "pk_attend_bf16", "pk_attend_f16", "pk_attend_f32", "pk_
            "pk_attend_backward", "pk_attend_tuned", "pk_tune_pick", "pk_tune_key", "pk_tune_clear",
            "pk_forward_kernel", "pk_kernel_name", "pk_attend_mixed_ops",
            "pk_linear", "pk_linear_workspace", "pk_linear_backward", "pk_linear_backward_workspace", "pk_dropout",
-           "pk_cross_entropy", "pk_cross_entropy_backward", "pk_cross_entropy_workspace")
+           "pk_cross_entropy", "pk_cross_entropy_backward", "pk_cross_entropy_workspace",
+           "pk_rms_norm", "pk_rms_norm_q8", "pk_quantize_rows", "pk_rms_norm_backward", "pk_rms_norm_backward_workspace",
+           "pk_token_logprobs", "pk_token_logprobs_backward")
 KERNELS = {0: "band", 1: "f32", 2: "tc", 3: "q4", 4: "tc_single", 5: "split"}
 
 _lib = None
@@ -120,6 +124,13 @@ def load(path: str | None = None):
         "pk_cross_entropy": [i32, vp, i64, vp, vp, vp, i64, i32, i32, vp, vp] + tail,
         "pk_cross_entropy_backward": [i32, vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp] + tail,
         "pk_cross_entropy_workspace": [i32, vp, i64, vp, i32, i32, i64, i32, i32, pi64],
+        "pk_rms_norm": [i32, vp, i64, vp, i64, vp, f32, i64, i32, vp, i64, vp, i64, vp],
+        "pk_rms_norm_q8": [i32, vp, i64, vp, i64, vp, f32, i64, i32, vp, i64, vp, vp, i64, vp],
+        "pk_quantize_rows": [i32, vp, i64, i64, i32, vp, i64, vp, vp],
+        "pk_rms_norm_backward": [i32, vp, i64, vp, vp, i64, vp, i64, f32, i64, i32, vp, i64, vp, vp, i64, vp],
+        "pk_rms_norm_backward_workspace": [i32, i64, i32, i32, pi64],
+        "pk_token_logprobs": [i32, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp],
+        "pk_token_logprobs_backward": [i32, vp, i64, vp, vp, vp, vp, vp, i64, i32, vp, i64, vp],
     }.items():
         getattr(L, name).argtypes = args
         getattr(L, name).restype = i32
@@ -748,6 +759,210 @@ def cross_entropy_backward(x, w, labels, lse, dloss, bias=None, need_dx: bool = 
 
     st = _here(dev, stream)
     return call(st) if st is not None else _on_stream(dev, stream, (x, w, labels, lse, dloss, bias, status), call)
+
+
+# ------------------------------------------------------------------------------------------
+# norms and 8-bit rows
+
+
+def _norm_inputs(x, w, residual, eps, stream):
+    dt, dev = x.dtype, x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, D = x.shape
+    if not 1 <= D <= NORM_MAX_D:
+        raise ValueError(f"x must have 1 to {NORM_MAX_D} columns, not {D}")
+    _vector(w, D, "w", dt, dev)
+    ldr = _rows(residual, D, "residual", dt, dev, T) if residual is not None else D
+    _eps_check(eps)
+    _check_stream(stream, dev)
+    return code, dt, dev, ldx, ldr, T, D
+
+
+def _eps_check(eps):
+    if not 1e-45 < eps < 3.4e38:
+        raise ValueError(f"eps must be positive and finite in fp32, not {eps}")
+
+
+def _sum_rows(h_out, x, w, residual, T, D, dt, dev):
+    """The row stride of a given h_out, which may be x or the residual itself."""
+    ldh = _rows(h_out, D, "h_out", dt, dev, T)
+    _disjoint(h_out, "h_out", None if _same_place(h_out, x) else x, w, None if _same_place(h_out, residual) else residual)
+    return ldh
+
+
+def rms_norm(x, w, residual=None, eps: float = 1e-6, out=None, h_out=None, stream=None):
+    """y [T, D] = w h / sqrt(mean(h^2) + eps) with h = x + residual, for x [T, D] and w [D] (float32, bfloat16 or float16,
+    everything of one type, D up to 16384). With a residual: (y, h), the sum being what the next layer adds to. x, residual, out
+    and h_out may have strided rows; h_out may be x or residual itself (the residual stream updated in place)."""
+    torch = _torch()
+    code, dt, dev, ldx, ldr, T, D = _norm_inputs(x, w, residual, eps, stream)
+    ldy = ldh = D
+    if h_out is not None:
+        if residual is None:
+            raise ValueError("h_out needs a residual: without one h is x")
+        ldh = _sum_rows(h_out, x, w, residual, T, D, dt, dev)
+    if out is not None:
+        ldy = _rows(out, D, "out", dt, dev, T)
+        _disjoint(out, "out", x, w, residual, h_out)
+
+    def call(st):
+        y = torch.empty((T, D), dtype=dt, device=dev) if out is None else out
+        h = h_out if h_out is not None or residual is None else torch.empty((T, D), dtype=dt, device=dev)
+        _check(load().pk_rms_norm(code, x.data_ptr(), ldx, _ptr(residual), ldr, w.data_ptr(), eps, T, D, y.data_ptr(), ldy, _ptr(h),
+                                  ldh, st), "pk_rms_norm")
+        return y if residual is None else (y, h)
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, residual, out, h_out), call)
+
+
+def rms_norm_q8(x, w, residual=None, eps: float = 1e-6, h_out=None, stream=None):
+    """`rms_norm` with its rows in 8 bits, for `linear_q8`: (q [T, D] float8_e4m3fn, scale [T] float32), and h with a
+    residual; row t stands for q[t] scale[t], scale being the row's largest magnitude / 448."""
+    torch = _torch()
+    code, dt, dev, ldx, ldr, T, D = _norm_inputs(x, w, residual, eps, stream)
+    ldh = D
+    if h_out is not None:
+        if residual is None:
+            raise ValueError("h_out needs a residual: without one h is x")
+        ldh = _sum_rows(h_out, x, w, residual, T, D, dt, dev)
+
+    def call(st):
+        q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty(T, dtype=torch.float32, device=dev)
+        h = h_out if h_out is not None or residual is None else torch.empty((T, D), dtype=dt, device=dev)
+        _check(load().pk_rms_norm_q8(code, x.data_ptr(), ldx, _ptr(residual), ldr, w.data_ptr(), eps, T, D, q.data_ptr(), D,
+                                     scale.data_ptr(), _ptr(h), ldh, st), "pk_rms_norm_q8")
+        return (q, scale) if residual is None else (q, scale, h)
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, residual, h_out), call)
+
+
+def quantize_rows(x, stream=None):
+    """(q [T, D] float8_e4m3fn, scale [T] float32) for x [T, D]: row t is q[t] scale[t] to 8 bits, scale the row's largest
+    magnitude / 448. For the weights of `linear_q8` and for activations that come from no norm."""
+    torch = _torch()
+    dev = x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, D = x.shape
+    if not 1 <= D <= NORM_MAX_D:
+        raise ValueError(f"x must have 1 to {NORM_MAX_D} columns, not {D}")
+    _check_stream(stream, dev)
+
+    def call(st):
+        q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(load().pk_quantize_rows(code, x.data_ptr(), ldx, T, D, q.data_ptr(), D, scale.data_ptr(), st), "pk_quantize_rows")
+        return q, scale
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x,), call)
+
+
+def rms_norm_backward(h, w, dy, dh=None, eps: float = 1e-6, need_dx: bool = True, need_dw: bool = True, out=None, stream=None):
+    """(dx [T, D], dw [D]) of `rms_norm` for the gradient dy of its output, each None where not needed; h is the forward's sum
+    (x where there was no residual), dh the gradient that arrives on h itself. dx is the gradient of x and of the residual
+    alike; `out` for it may be dy or dh itself."""
+    torch = _torch()
+    dt, dev = h.dtype, h.device
+    code = dtype_code(h)
+    ldh = _rows(h, None, "h")
+    T, D = h.shape
+    if not 1 <= D <= NORM_MAX_D:
+        raise ValueError(f"h must have 1 to {NORM_MAX_D} columns, not {D}")
+    _vector(w, D, "w", dt, dev)
+    lddy = _rows(dy, D, "dy", dt, dev, T)
+    lddh = _rows(dh, D, "dh", dt, dev, T) if dh is not None else D
+    _eps_check(eps)
+    _check_stream(stream, dev)
+    lddx = D
+    if out is not None:
+        if not need_dx:
+            raise ValueError("out is dx's, which is not needed")
+        lddx = _rows(out, D, "out", dt, dev, T)
+        _disjoint(out, "out", h, w, None if _same_place(out, dy) else dy, None if dh is None or _same_place(out, dh) else dh)
+
+    def call(st):
+        dx = out if out is not None or not need_dx else torch.empty((T, D), dtype=dt, device=dev)
+        dw = torch.empty(D, dtype=dt, device=dev) if need_dw else None
+        ws, wp, wb = _workspace("pk_rms_norm_backward_workspace", dev, code, T, D, bool(need_dw))
+        _check(load().pk_rms_norm_backward(code, h.data_ptr(), ldh, w.data_ptr(), dy.data_ptr(), lddy, _ptr(dh), lddh, eps, T, D,
+                                           _ptr(dx), lddx, _ptr(dw), wp, wb, st), "pk_rms_norm_backward")
+        return dx, dw
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (h, w, dy, dh, out), call)
+
+
+# ------------------------------------------------------------------------------------------
+# log probabilities of rows of logits
+
+
+def token_logprobs(logits, labels, top: int = 0, status=None, stream=None):
+    """(logp [T], lse [T], entropy [T], top_logp [T, top], top_idx [T, top]) of logits [T, V] and int64 labels [T]: the log
+    probability of each row's label (0 for a negative label; NaN and PK_ERR_BAD_LABEL for one >= V, in `status` or last_status
+    of the call's stream), the row's log-sum-exp and entropy (float32), and its `top` (at most 64) likeliest words, the
+    likeliest first and equal ones by index (int64; None, None for top 0). logits may have strided rows."""
+    torch = _torch()
+    dev = logits.device
+    code = dtype_code(logits)
+    ld = _rows(logits, None, "logits")
+    T, V = logits.shape
+    if V < 1:
+        raise ValueError("logits must have at least one column")
+    _vector(labels, T, "labels", torch.int64, dev)
+    if not 0 <= top <= min(LOGPROBS_MAX_TOP, V):
+        raise ValueError(f"top must be in [0, min({LOGPROBS_MAX_TOP}, V)], not {top}")
+    if status is not None:
+        _vector(status, 1, "status", torch.int32, dev)
+    _check_stream(stream, dev)
+
+    def call(st):
+        logp, lse, entropy = torch.empty((3, T), dtype=torch.float32, device=dev).unbind(0)
+        best = torch.empty((T, top), dtype=torch.float32, device=dev) if top else None
+        idx = torch.empty((T, top), dtype=torch.int64, device=dev) if top else None
+        _check(load().pk_token_logprobs(code, logits.data_ptr(), ld, labels.data_ptr(), T, V, top, logp.data_ptr(), lse.data_ptr(),
+                                        entropy.data_ptr(), _ptr(best), _ptr(idx), _ptr(status), st), "pk_token_logprobs")
+        return logp, lse, entropy, best, idx
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (logits, labels, status), call)
+
+
+def token_logprobs_backward(logits, labels, lse, entropy, dlogp, dentropy=None, out=None, stream=None):
+    """dlogits [T, V]: the gradient of sum(dlogp * logp) + sum(dentropy * entropy) of `token_logprobs` for its lse and entropy
+    (entropy may be None without dentropy). `out` may be logits itself."""
+    torch = _torch()
+    dt, dev = logits.dtype, logits.device
+    code = dtype_code(logits)
+    ld = _rows(logits, None, "logits")
+    T, V = logits.shape
+    if V < 1:
+        raise ValueError("logits must have at least one column")
+    _vector(labels, T, "labels", torch.int64, dev)
+    for name, t in (("lse", lse), ("dlogp", dlogp), ("entropy", entropy), ("dentropy", dentropy)):
+        if t is not None:
+            _vector(t, T, name, torch.float32, dev)
+        elif name == "lse" or name == "dlogp" or (name == "entropy" and dentropy is not None):
+            raise ValueError(f"{name} is needed")
+    _check_stream(stream, dev)
+    ldo = V
+    if out is not None:
+        ldo = _rows(out, V, "out", dt, dev, T)
+        _disjoint(out, "out", None if _same_place(out, logits) else logits, labels, lse, entropy, dlogp, dentropy)
+
+    def call(st):
+        d = torch.empty((T, V), dtype=dt, device=dev) if out is None else out
+        _check(load().pk_token_logprobs_backward(code, logits.data_ptr(), ld, labels.data_ptr(), lse.data_ptr(), _ptr(entropy),
+                                                 dlogp.data_ptr(), _ptr(dentropy), T, V, d.data_ptr(), ldo, st),
+               "pk_token_logprobs_backward")
+        return d
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (logits, labels, lse, entropy, dlogp, dentropy, out), call)
 
 
 def schedule(cu, T: int, window: int, stream=None):

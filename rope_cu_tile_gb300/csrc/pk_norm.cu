@@ -1,0 +1,548 @@
+// pk_norm.cu -- the root-mean-square norm of token rows with the residual's addition, its gradient, and its form with rows in
+// 8 bits (pk_rms_norm, pk_rms_norm_backward, pk_rms_norm_q8, pk_quantize_rows in include/pk.h).
+//
+//     h = x + r,   y = w h / sqrt(mean(h^2) + eps)                        x, r, h, y [T, D], w [D]
+//     n = h / sqrt(mean(h^2) + eps),  g = dy w:   dx = (g - n mean(g n)) / sqrt(mean(h^2) + eps) + dh,   dw = sum over rows of dy n
+//     8 bits: s = max |y| / 448 of a row, q = e4m3(y / s)
+//
+// All of it is bound by bytes: each element is read once and held in registers, a row's sums go through shuffles (and
+// shared memory where a row takes more than a warp), and everything is written once.
+#include <cfloat>
+
+#include "pk_rows.cuh"
+
+namespace pk {
+
+namespace {
+
+using namespace rows;
+
+constexpr int kMaxD = PK_NORM_MAX_D;
+
+enum Mode { kNorm, kNormQ8, kQuantize };
+
+struct NormArgs {
+  const void* x;
+  const void* res;
+  const void* w;
+  void* y;       // in the element type, or 8 bits
+  void* h;       // x + res, or null
+  float* scale;  // of the 8-bit rows
+  int64_t ldx, ldr, ldy, ldh;
+  int64_t T;
+  int D;
+  float eps, inv_d;
+};
+
+// A row belongs to kTpr threads, each with kNv groups of eight elements kTpr groups apart: 8 threads for the shortest rows,
+// so that a warp's lanes all have something to load, a block of 1024 for the longest, whose elements must fit the registers.
+template <int kTpr>
+constexpr int kBlock = kTpr <= 32 ? 256 : kTpr;
+
+// The eight elements of a group: 16 bytes of a row where every row of every matrix begins and ends on such a boundary (kVec),
+// else eight columns kTpr apart, so that a warp's scalar accesses are of neighbours. `n`: columns of the row from the first.
+template <int DT, int kTpr, bool kVec>
+struct Group {
+  uint4 q[DT == PK_F32 ? 2 : 1];
+  static __device__ __forceinline__ int column(int i, int t) { return kVec ? (i * kTpr + t) * 8 : i * 8 * kTpr + t; }
+  __device__ __forceinline__ void load(const void* p, int64_t at, int n) {
+    if constexpr (kVec) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes);
+      q[0] = __ldcg(s);
+      if constexpr (DT == PK_F32) q[1] = __ldcg(s + 1);
+    } else {
+      uint32_t w[DT == PK_F32 ? 8 : 4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (DT == PK_F32) {
+          w[j] = j * kTpr < n ? __ldcg(static_cast<const unsigned int*>(p) + at + j * kTpr) : 0u;
+        } else {
+          const uint32_t x = j * kTpr < n ? __ldcg(static_cast<const unsigned short*>(p) + at + j * kTpr) : 0u;
+          w[j >> 1] = j & 1 ? w[j >> 1] | x << 16 : x;
+        }
+      }
+      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (DT == PK_F32) q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+  // the weights, which every row reads again: through L1
+  __device__ __forceinline__ void load_shared(const void* p, int at, int n) {
+    if constexpr (kVec) {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes);
+      q[0] = *s;
+      if constexpr (DT == PK_F32) q[1] = s[1];
+    } else {
+      load(p, at, n);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    Raw8<DT> r;
+    r.q[0] = q[0];
+    if constexpr (DT == PK_F32) r.q[1] = q[1];
+    r.get(v);
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t at, int n, const float (&v)[8]) {
+    if constexpr (kVec) {
+      store8<DT>(p, at, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j * kTpr < n) Ty<DT>::put(p, at + j * kTpr, v[j]);
+    }
+  }
+};
+
+// N sums (or maxima, where bit i of kMax is set) over a row's threads, in every one of them. `red`: 2 x 32 x N floats, used
+// alternately so that one barrier a row is enough.
+template <int kTpr, int N, int kMax>
+__device__ __forceinline__ void row_reduce(float (&v)[N], float* red, int& turn) {
+#pragma unroll
+  for (int o = (kTpr < 32 ? kTpr : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float u = __shfl_xor_sync(0xffffffffu, v[i], o);
+      v[i] = (kMax >> i) & 1 ? fmaxf(v[i], u) : v[i] + u;
+    }
+  if constexpr (kTpr > 32) {
+    constexpr int kWarps = kTpr / 32;
+    float* r = red + turn * 32 * N;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[(threadIdx.x >> 5) * N + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = r[i];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) v[i] = (kMax >> i) & 1 ? fmaxf(v[i], r[k * N + i]) : v[i] + r[k * N + i];
+    }
+  }
+}
+
+__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8]) {
+  uint16_t p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+  return make_uint2(p[0] | static_cast<uint32_t>(p[1]) << 16, p[2] | static_cast<uint32_t>(p[3]) << 16);
+}
+
+template <int DT, int kMode, int kTpr, int kNv, bool kVec>
+__global__ void __launch_bounds__(kBlock<kTpr>, kTpr > 256 ? 1 : DT == PK_F32 ? 2 : 3)
+    pk_norm_kernel(const __grid_constant__ NormArgs a) {
+  using G = Group<DT, kTpr, kVec>;
+  __shared__ float red[kTpr > 32 ? 2 * 32 * 2 : 1];
+  constexpr int kRows = kBlock<kTpr> / kTpr;
+  const int t = threadIdx.x % kTpr;
+  int turn = 0;
+  griddep_wait();
+  // (the rows of one warp go round together: the shuffles are warp-wide)
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.T; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t row = r0 + threadIdx.x / kTpr;
+    const int D = row < a.T ? a.D : 0;  // (no columns of a row that is not there)
+    float h[kNv][8];
+    {
+      G x[kNv], res[kNv];
+#pragma unroll
+      for (int i = 0; i < kNv; ++i) {
+        const int c = G::column(i, t);
+        if (c < D) {
+          x[i].load(a.x, row * a.ldx + c, D - c);
+          if (kMode != kQuantize && a.res) res[i].load(a.res, row * a.ldr + c, D - c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kNv; ++i) {
+        const int c = G::column(i, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
+        if (c < D) {
+          x[i].get(h[i]);
+          if (kMode != kQuantize && a.res) {
+            float b[8];
+            res[i].get(b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] += b[j];
+          }
+          if (kMode != kQuantize && a.h) G::store(a.h, row * a.ldh + c, D - c, h[i]);
+        }
+      }
+    }
+    if constexpr (kMode != kQuantize) {
+      float s[1];
+      const auto squares = [&]() {
+        s[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);
+        row_reduce<kTpr, 1, 0>(s, red, turn);
+      };
+      squares();
+      // squares past fp32's range (elements past 2^58 or so): the row times a power of two, beside which eps is nothing
+      const bool past = s[0] > FLT_MAX;
+      float eps = a.eps;
+      if (kTpr > 32 ? past : __any_sync(0xffffffffu, past)) {
+        const float down = past ? 0x1p-80f : 1.0f;
+        eps = past ? 0.0f : eps;
+#pragma unroll
+        for (int i = 0; i < kNv; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] *= down;
+        squares();
+      }
+      const float f = rsqrtf(fmaf(s[0], a.inv_d, eps));
+#pragma unroll
+      for (int i = 0; i < kNv; ++i) {
+        const int c = G::column(i, t);
+        if (c < D) {
+          G w;
+          w.load_shared(a.w, c, D - c);
+          float b[8];
+          w.get(b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * f * b[j];
+          if constexpr (kMode == kNorm) G::store(a.y, row * a.ldy + c, D - c, h[i]);
+        }
+      }
+    }
+    if constexpr (kMode != kNorm) {
+      // (a maximum passes over NaN: a row that holds one gets a NaN scale, so that nobody takes the others for its values)
+      float m[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kNv; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          m[0] = fmaxf(m[0], fabsf(h[i][j]));
+          m[1] = h[i][j] != h[i][j] ? 1.0f : m[1];
+        }
+      row_reduce<kTpr, 2, 3>(m, red, turn);
+      const float scale = m[1] != 0.0f ? __int_as_float(0x7fc00000) : m[0] * (1.0f / 448.0f);
+      // the inverse of a scale near fp32's smallest numbers would be infinite: two factors then
+      const float up = scale < 0x1p-100f ? 0x1p60f : 1.0f;
+      const float inv = scale > 0.0f ? 1.0f / (scale * up) : (scale == 0.0f ? 0.0f : scale);
+#pragma unroll
+      for (int i = 0; i < kNv; ++i) {
+        const int c = G::column(i, t);
+        if (c < D) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * up * inv;
+          const uint2 q = to_e4m3(h[i]);
+          uint8_t* d = static_cast<uint8_t*>(a.y) + row * a.ldy + c;
+          if constexpr (kVec) {
+            *reinterpret_cast<uint2*>(d) = q;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j * kTpr < D - c) d[j * kTpr] = static_cast<uint8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+          }
+        }
+      }
+      if (D > 0 && t == 0) a.scale[row] = scale;
+    }
+  }
+}
+
+struct NormBackArgs {
+  const void* h;
+  const void* w;
+  const void* dy;
+  const void* dh;
+  void* dx;     // or null
+  float* part;  // [blocks, D] sums of dy n over a block's rows, or null
+  int64_t ldh, lddy, lddh, lddx;
+  int64_t T;
+  int D;
+  float eps, inv_d;
+};
+
+// A block keeps its columns' sums of dy n in registers over all of its rows.
+template <int DT, int kTpr>
+constexpr int kBackResident = kTpr > 256 || (DT == PK_F32 && kTpr <= 32) ? 1 : 2;  // blocks of an SM
+
+template <int DT, int kTpr, int kNv, bool kVec>
+__global__ void __launch_bounds__(kBlock<kTpr>, (kBackResident<DT, kTpr>)) pk_norm_backward_kernel(const __grid_constant__ NormBackArgs a) {
+  using G = Group<DT, kTpr, kVec>;
+  __shared__ float red[kTpr > 32 ? 2 * 32 * 2 : 1];
+  constexpr int kRows = kBlock<kTpr> / kTpr, kCols = kTpr * kNv * 8;
+  __shared__ float cols[kTpr <= 32 ? kRows * kCols : 1];
+  const int t = threadIdx.x % kTpr;
+  int turn = 0;
+  float sum[kNv][8];
+  G w[kNv];
+  griddep_wait();
+#pragma unroll
+  for (int i = 0; i < kNv; ++i) {
+    const int c = G::column(i, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[i][j] = 0.0f;
+    if (c < a.D) w[i].load(a.w, c, a.D - c);
+  }
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.T; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t row = r0 + threadIdx.x / kTpr;
+    const int D = row < a.T ? a.D : 0;
+    G xh[kNv], xd[kNv], xr[kNv];
+#pragma unroll
+    for (int i = 0; i < kNv; ++i) {
+      const int c = G::column(i, t);
+      if (c < D) {
+        xh[i].load(a.h, row * a.ldh + c, D - c);
+        xd[i].load(a.dy, row * a.lddy + c, D - c);
+        if (a.dh) xr[i].load(a.dh, row * a.lddh + c, D - c);
+      }
+    }
+    float s[2], down = 1.0f, eps = a.eps;
+    const auto sums = [&]() {
+      s[0] = s[1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kNv; ++i)
+        if (G::column(i, t) < D) {
+          float h[8], d[8], g[8];
+          xh[i].get(h);
+          xd[i].get(d);
+          w[i].get(g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            h[j] *= down;
+            s[0] = fmaf(h[j], h[j], s[0]);
+            s[1] = fmaf(h[j], d[j] * g[j], s[1]);
+          }
+        }
+      row_reduce<kTpr, 2, 0>(s, red, turn);
+    };
+    sums();
+    // (as forwards: squares past fp32's range)
+    const bool past = s[0] > FLT_MAX;
+    if (kTpr > 32 ? past : __any_sync(0xffffffffu, past)) {
+      down = past ? 0x1p-80f : 1.0f;
+      eps = past ? 0.0f : eps;
+      sums();
+    }
+    const float f = rsqrtf(fmaf(s[0], a.inv_d, eps));  // of h times `down`
+    const float mean = s[1] * a.inv_d * f;             // of g n
+#pragma unroll
+    for (int i = 0; i < kNv; ++i) {
+      const int c = G::column(i, t);
+      if (c < D) {
+        float n[8], d[8], g[8];
+        xh[i].get(n);
+        xd[i].get(d);
+        w[i].get(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          n[j] = n[j] * down * f;
+          sum[i][j] = fmaf(d[j], n[j], sum[i][j]);
+          d[j] = (d[j] * g[j] - n[j] * mean) * f * down;
+        }
+        if (a.dx) {
+          if (a.dh) {
+            xr[i].get(n);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] += n[j];
+          }
+          G::store(a.dx, row * a.lddx + c, D - c, d);
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.D;
+#pragma unroll
+  for (int i = 0; i < kNv; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = G::column(i, t) + (kVec ? j : j * kTpr);
+      if constexpr (kTpr > 32) {
+        if (c < a.D) part[c] = sum[i][j];
+      } else {
+        cols[threadIdx.x / kTpr * kCols + c] = sum[i][j];
+      }
+    }
+  if constexpr (kTpr <= 32) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.D; c += kBlock<kTpr>) {
+      float v = 0.0f;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) v += cols[r * kCols + c];
+      part[c] = v;
+    }
+  }
+}
+
+// How a row of D elements is shared out: calls f(threads a row, groups of eight a thread).
+template <int A, int B>
+struct Cut {
+  static constexpr int kTpr = A, kNv = B;
+};
+template <class F>
+cudaError_t by_length(int D, const F& f) {
+  if (D <= 64) return f(Cut<8, 1>());
+  if (D <= 256) return f(Cut<8, 4>());
+  if (D <= 1024) return f(Cut<32, 4>());
+  if (D <= 4096) return f(Cut<256, 2>());
+  return f(Cut<1024, 2>());
+}
+static_assert(1024 * 2 * 8 == kMaxD, "the longest row");
+
+template <int DT, int kMode>
+cudaError_t norm_launch(const NormArgs& a, bool vec, int sms, cudaStream_t stream) {
+  return by_length(a.D, [&](auto cut) {
+    constexpr int kTpr = decltype(cut)::kTpr, kNv = decltype(cut)::kNv, kRows = kBlock<kTpr> / kTpr;
+    const int64_t blocks = (a.T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * (2048 / kBlock<kTpr>);
+    Launch l(blocks < most ? blocks : most, kBlock<kTpr>, stream);
+    return vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNv, true>, a)
+               : cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNv, false>, a);
+  });
+}
+
+// Blocks of the backward pass: as many as are resident at once, each with its own partial column sums.
+template <int DT>
+int64_t back_blocks_of(int64_t T, int D, int sms) {
+  int64_t n = 0;
+  by_length(D, [&](auto cut) {
+    constexpr int kTpr = decltype(cut)::kTpr, kRows = kBlock<kTpr> / kTpr;
+    const int64_t blocks = (T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * kBackResident<DT, kTpr>;
+    n = blocks < most ? blocks : most;
+    return cudaSuccess;
+  });
+  return n;
+}
+int64_t back_blocks(int dtype, int64_t T, int D, int sms) {
+  return dtype == PK_F32 ? back_blocks_of<PK_F32>(T, D, sms) : back_blocks_of<PK_BF16>(T, D, sms);
+}
+
+template <int DT>
+cudaError_t back_launch(const NormBackArgs& a, bool vec, int64_t blocks, cudaStream_t stream) {
+  return by_length(a.D, [&](auto cut) {
+    constexpr int kTpr = decltype(cut)::kTpr, kNv = decltype(cut)::kNv;
+    Launch l(blocks, kBlock<kTpr>, stream);
+    return vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNv, true>, a)
+               : cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNv, false>, a);
+  });
+}
+
+bool sizes_ok(int dtype, int64_t T, int D) { return dtype_ok(dtype) && T >= 0 && T <= PK_ROWS_MAX_T && D >= 1 && D <= kMaxD; }
+bool eps_ok(float eps) { return eps > 0.0f && eps <= FLT_MAX; }
+
+int run_norm(int mode, int dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* w, float eps,
+             int64_t T, int D, void* y, int64_t ldy, float* scale, void* h, int64_t ldh, cudaStream_t stream) {
+  if (!sizes_ok(dtype, T, D) || (mode != kQuantize && !eps_ok(eps)) || ldx < D || ldy < D || (residual && ldr < D) || (h && ldh < D))
+    return PK_ERR_ARG;
+  if (T > 0 && (!x || !y || (mode != kQuantize && !w) || (mode != kNorm && !scale))) return PK_ERR_ARG;
+  const int e = elem_bytes(dtype);
+  if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned_to(w, e) || !aligned_to(h, e) || !aligned_to(scale, 4) ||
+      (mode == kNorm && !aligned_to(y, e)))
+    return PK_ERR_ALIGN;
+  if (T == 0) return PK_OK;
+  Device d;
+  const int rc = device(&d);
+  if (rc != PK_OK) return rc;
+  NormArgs a = {};
+  a.x = x;
+  a.res = residual;
+  a.w = w;
+  a.y = y;
+  a.h = h;
+  a.scale = scale;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldy = ldy;
+  a.ldh = ldh;
+  a.T = T;
+  a.D = D;
+  a.eps = eps;
+  a.inv_d = 1.0f / static_cast<float>(D);
+  const bool vec = (D & 7) == 0 && rows16(x, ldx, e) && (!residual || rows16(residual, ldr, e)) && (!h || rows16(h, ldh, e)) &&
+                   aligned_to(w, 16) && (mode == kNorm ? rows16(y, ldy, e) : aligned_to(y, 8) && (ldy & 7) == 0);
+  const auto run = [&](auto type) {
+    constexpr int DT = decltype(type)::value;
+    if (mode == kNorm) return norm_launch<DT, kNorm>(a, vec, d.sms, stream);
+    if (mode == kNormQ8) return norm_launch<DT, kNormQ8>(a, vec, d.sms, stream);
+    return norm_launch<DT, kQuantize>(a, vec, d.sms, stream);
+  };
+  const cudaError_t r = dtype == PK_F32    ? run(std::integral_constant<int, PK_F32>())
+                        : dtype == PK_BF16 ? run(std::integral_constant<int, PK_BF16>())
+                                           : run(std::integral_constant<int, PK_F16>());
+  return r == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace pk
+
+extern "C" {
+
+int pk_rms_norm(int dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* w, float eps, int64_t T,
+                int D, void* y, int64_t ldy, void* h, int64_t ldh, struct CUstream_st* stream) {
+  return pk::run_norm(pk::kNorm, dtype, x, ldx, residual, ldr, w, eps, T, D, y, ldy, nullptr, h, ldh, stream);
+}
+
+int pk_rms_norm_q8(int dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* w, float eps, int64_t T,
+                   int D, void* q, int64_t ldq, float* scale, void* h, int64_t ldh, struct CUstream_st* stream) {
+  return pk::run_norm(pk::kNormQ8, dtype, x, ldx, residual, ldr, w, eps, T, D, q, ldq, scale, h, ldh, stream);
+}
+
+int pk_quantize_rows(int dtype, const void* x, int64_t ldx, int64_t T, int D, void* q, int64_t ldq, float* scale,
+                     struct CUstream_st* stream) {
+  return pk::run_norm(pk::kQuantize, dtype, x, ldx, nullptr, 0, nullptr, 0.0f, T, D, q, ldq, scale, nullptr, 0, stream);
+}
+
+int pk_rms_norm_backward_workspace(int dtype, int64_t T, int D, int need_dw, int64_t* bytes) {
+  using namespace pk;
+  if (!bytes || !sizes_ok(dtype, T, D)) return PK_ERR_ARG;
+  *bytes = 0;
+  if (T == 0 || !need_dw) return PK_OK;
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  *bytes = back_blocks(dtype, T, D, d.sms) * D * 4;
+  return PK_OK;
+}
+
+int pk_rms_norm_backward(int dtype, const void* h, int64_t ldh, const void* w, const void* dy, int64_t lddy, const void* dh,
+                         int64_t lddh, float eps, int64_t T, int D, void* dx, int64_t lddx, void* dw, void* workspace,
+                         int64_t workspace_bytes, struct CUstream_st* stream) {
+  using namespace pk;
+  if (!sizes_ok(dtype, T, D) || !eps_ok(eps) || ldh < D || lddy < D || (dh && lddh < D) || (dx && lddx < D) || workspace_bytes < 0)
+    return PK_ERR_ARG;
+  if (T > 0 && (!h || !w || !dy)) return PK_ERR_ARG;
+  const int e = rows::elem_bytes(dtype);
+  if (!rows::aligned_to(h, e) || !rows::aligned_to(w, e) || !rows::aligned_to(dy, e) || !rows::aligned_to(dh, e) ||
+      !rows::aligned_to(dx, e) || !rows::aligned_to(dw, e) || !rows::aligned_to(workspace, 256))
+    return PK_ERR_ALIGN;
+  // no rows: the weights' gradient is zero
+  if (T == 0) return dw && cudaMemsetAsync(dw, 0, static_cast<size_t>(e) * D, stream) != cudaSuccess ? PK_ERR_CUDA : PK_OK;
+  if (!dx && !dw) return PK_OK;
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  const int64_t blocks = back_blocks(dtype, T, D, d.sms);
+  if (dw && (!workspace || workspace_bytes < blocks * D * 4)) return PK_ERR_NOMEM;
+  NormBackArgs a = {};
+  a.h = h;
+  a.w = w;
+  a.dy = dy;
+  a.dh = dh;
+  a.dx = dx;
+  a.part = dw ? static_cast<float*>(workspace) : nullptr;
+  a.ldh = ldh;
+  a.lddy = lddy;
+  a.lddh = lddh;
+  a.lddx = lddx;
+  a.T = T;
+  a.D = D;
+  a.eps = eps;
+  a.inv_d = 1.0f / static_cast<float>(D);
+  const bool vec = (D & 7) == 0 && rows16(h, ldh, e) && rows16(dy, lddy, e) && (!dh || rows16(dh, lddh, e)) &&
+                   (!dx || rows16(dx, lddx, e)) && rows::aligned_to(w, 16);
+  const cudaError_t r = dtype == PK_F32    ? back_launch<PK_F32>(a, vec, blocks, stream)
+                        : dtype == PK_BF16 ? back_launch<PK_BF16>(a, vec, blocks, stream)
+                                           : back_launch<PK_F16>(a, vec, blocks, stream);
+  if (r != cudaSuccess) return PK_ERR_CUDA;
+  if (dw && rows::sum_rows(dtype, a.part, blocks, nullptr, 1, D, D, nullptr, dw, stream) != cudaSuccess) return PK_ERR_CUDA;
+  return PK_OK;
+}
+
+}  // extern "C"
