@@ -468,6 +468,38 @@ int pk_rms_norm_backward(int dtype, const void *h, int64_t ldh, const void *w, c
 int pk_rms_norm_backward_workspace(int dtype, int64_t T, int D, int need_dw, int64_t *bytes);
 
 /*
+ * Gated feed-forward: [g | u] = x W^T + b, y = act(g) u.
+ *   x [T, K] (ldx), w [2 F, K]: F rows of the gate, then F of what it multiplies; bias [2 F] or NULL, y [T, F] (ldy),
+ *   pre [T, 2 F] or NULL: [g | u], which the backward pass needs. act as pk_linear's (PK_ACT_NONE: the two multiplied).
+ * Few rows run on the CUDA cores as pk_linear's do, without a workspace. F <= PK_ROWS_MAX_DIM / 2.
+ */
+int pk_gated_linear(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, int act, int64_t T, int F, int K, void *y,
+                    int64_t ldy, void *pre, void *workspace, int64_t workspace_bytes, int *status, struct CUstream_st *stream);
+int pk_gated_linear_workspace(int dtype, const void *x, int64_t ldx, const void *w, int64_t T, int F, int K, int64_t *bytes);
+/*
+ * Its gradients: dz = [dy u act'(g) | dy act(g)], dx = dz W [T, K], dw = dz^T x [2 F, K], db = column sums of dz [2 F]; each may be
+ * NULL. dy [T, F] (lddy), pre the forward's. dz is rounded to the element type before the products (db sums it
+ * unrounded), in fp16 times a power of two where its largest finite element is outside [2^-10, 65504].
+ */
+int pk_gated_linear_backward(int dtype, const void *x, int64_t ldx, const void *w, const void *dy, int64_t lddy, const void *pre,
+                             int act, int64_t T, int F, int K, void *dx, void *dw, void *db, void *workspace,
+                             int64_t workspace_bytes, int *status, struct CUstream_st *stream);
+int pk_gated_linear_backward_workspace(int dtype, const void *x, int64_t ldx, const void *w, int need_dx, int need_dw, int need_db,
+                                       int64_t T, int F, int K, int64_t *bytes);
+
+/*
+ * Projection of 8-bit rows: y = r + act(x_scale[t] w_scale[n] sum_k x[t, k] w[n, k] + b), for the rows of pk_rms_norm_q8 and
+ * pk_quantize_rows.
+ *   x [T, K] e4m3 (ldx, a multiple of 16), w [N, K] e4m3, K a multiple of 16, both 16-byte aligned; x_scale [T], w_scale [N]
+ *   fp32; bias [N], residual [T, N] (ldr) and y [T, N] (ldy) in `dtype`, the first two or NULL. y may be residual itself (ldy = ldr).
+ * Products are exact and sums fp32 (tensor cores; up to PK_LINEAR_FEW_T / 2 rows on the CUDA cores, without a workspace).
+ */
+int pk_linear_q8(int dtype, const void *x, int64_t ldx, const float *x_scale, const void *w, const float *w_scale, const void *bias,
+                 const void *residual, int64_t ldr, int act, int64_t T, int N, int K, void *y, int64_t ldy, void *workspace,
+                 int64_t workspace_bytes, int *status, struct CUstream_st *stream);
+int pk_linear_q8_workspace(int64_t T, int N, int K, int64_t *bytes);
+
+/*
  * Of rows of logits z [T, V] (ld): lse = ln sum_v exp z_v, logp[t] = z[t, labels[t]] - lse (0 for a negative label; NaN and
  * PK_ERR_BAD_LABEL for one at or past V), entropy = -sum_v p_v ln p_v with p = exp(z - lse), all fp32 [T]; and the `top`
  * likeliest words, the likeliest first and equal ones by their index: top_idx [T, top] int64 and top_logp [T, top]
@@ -486,6 +518,32 @@ int pk_token_logprobs(int dtype, const void *logits, int64_t ld, const int64_t *
 int pk_token_logprobs_backward(int dtype, const void *logits, int64_t ld, const int64_t *labels, const float *lse,
                                const float *entropy, const float *dlogp, const float *dentropy, int64_t T, int V, void *dlogits,
                                int64_t lddz, struct CUstream_st *stream);
+
+/*
+ * Distillation from a teacher's top logits (pk_token_logprobs' top_idx and top_logp, or logits themselves), the student's
+ * logits z = x W^T + b never stored: with q = softmax(values / temperature) over a row's `top` words and
+ * p = softmax(z / temperature) over the vocabulary,
+ *   loss[t] = sum_k q_k (ln q_k - ln p_idx(t, k)),  lse[t] = ln sum_v exp(z[t, v] / temperature).
+ *   x [T, D] (ldx), w [V, D], bias [V] or NULL, idx [T, top] int64, values [T, top] fp32 (any constant may be added to a row's);
+ *   loss, lse [T] fp32. 1 <= top <= PK_DISTILL_MAX_TOP; temperature in [1e-3, 1e3].
+ * An entry with a negative index or the value -inf is not there; a row without any has loss and lse 0 and costs no product. A
+ * word may stand more than once (its shares add up). An index >= V: loss NaN, lse 0, PK_ERR_BAD_LABEL, no gradient.
+ */
+#define PK_DISTILL_MAX_TOP 64
+int pk_distill(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, const int64_t *idx, const float *values, int top,
+               double temperature, int64_t T, int D, int V, float *loss, float *lse, void *workspace, int64_t workspace_bytes,
+               int *status, struct CUstream_st *stream);
+/*
+ * The gradient of sum_t dloss[t] loss[t] with respect to the student, for the forward's lse: dz = dloss / temperature (p - q at
+ * the words), dx = dz W [T, D], dw = dz^T x [V, D], db = column sums of dz [V]; each may be NULL. dz is rounded to the element
+ * type before the products (db sums it unrounded).
+ */
+int pk_distill_backward(int dtype, const void *x, int64_t ldx, const void *w, const void *bias, const int64_t *idx, const float *values,
+                        int top, double temperature, const float *lse, const float *dloss, int64_t T, int D, int V, void *dx, void *dw,
+                        void *db, void *workspace, int64_t workspace_bytes, int *status, struct CUstream_st *stream);
+/* backward: 0 or 1; need_db: whether the backward call has db. */
+int pk_distill_workspace(int dtype, const void *x, int64_t ldx, const void *w, int backward, int need_db, int64_t T, int D, int V, int top,
+                         int64_t *bytes);
 
 /* Text of a status code (static storage). */
 const char *pk_status_string(int status);

@@ -34,6 +34,7 @@ ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 NOALLOC_MAX_T = 1048576
 NORM_MAX_D = 16384
 LOGPROBS_MAX_TOP = 64
+DISTILL_MAX_TOP = 64
 LINEAR_FEW_T = 8  # include/pk.h: half as many rows of any type need no workspace in linear
 
 # names declared in include/pk.h
@@ -45,7 +46,9 @@ EXPORTS = ("pk_attend", "pk_attend_bf16", "pk_attend_f16", "pk_attend_f32", "pk_
            "pk_linear", "pk_linear_workspace", "pk_linear_backward", "pk_linear_backward_workspace", "pk_dropout",
            "pk_cross_entropy", "pk_cross_entropy_backward", "pk_cross_entropy_workspace",
            "pk_rms_norm", "pk_rms_norm_q8", "pk_quantize_rows", "pk_rms_norm_backward", "pk_rms_norm_backward_workspace",
-           "pk_token_logprobs", "pk_token_logprobs_backward")
+           "pk_token_logprobs", "pk_token_logprobs_backward",
+           "pk_gated_linear", "pk_gated_linear_workspace", "pk_gated_linear_backward", "pk_gated_linear_backward_workspace",
+           "pk_linear_q8", "pk_linear_q8_workspace", "pk_distill", "pk_distill_backward", "pk_distill_workspace")
 KERNELS = {0: "band", 1: "f32", 2: "tc", 3: "q4", 4: "tc_single", 5: "split"}
 
 _lib = None
@@ -129,6 +132,15 @@ def load(path: str | None = None):
         "pk_quantize_rows": [i32, vp, i64, i64, i32, vp, i64, vp, vp],
         "pk_rms_norm_backward": [i32, vp, i64, vp, vp, i64, vp, i64, f32, i64, i32, vp, i64, vp, vp, i64, vp],
         "pk_rms_norm_backward_workspace": [i32, i64, i32, i32, pi64],
+        "pk_gated_linear": [i32, vp, i64, vp, vp, i32, i64, i32, i32, vp, i64, vp] + tail,
+        "pk_gated_linear_workspace": [i32, vp, i64, vp, i64, i32, i32, pi64],
+        "pk_gated_linear_backward": [i32, vp, i64, vp, vp, i64, vp, i32, i64, i32, i32, vp, vp, vp] + tail,
+        "pk_gated_linear_backward_workspace": [i32, vp, i64, vp, i32, i32, i32, i64, i32, i32, pi64],
+        "pk_linear_q8": [i32, vp, i64, vp, vp, vp, vp, vp, i64, i32, i64, i32, i32, vp, i64] + tail,
+        "pk_linear_q8_workspace": [i64, i32, i32, pi64],
+        "pk_distill": [i32, vp, i64, vp, vp, vp, vp, i32, f64, i64, i32, i32, vp, vp] + tail,
+        "pk_distill_backward": [i32, vp, i64, vp, vp, vp, vp, i32, f64, vp, vp, i64, i32, i32, vp, vp, vp] + tail,
+        "pk_distill_workspace": [i32, vp, i64, vp, i32, i32, i64, i32, i32, i32, pi64],
         "pk_token_logprobs": [i32, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp],
         "pk_token_logprobs_backward": [i32, vp, i64, vp, vp, vp, vp, vp, i64, i32, vp, i64, vp],
     }.items():
@@ -897,6 +909,122 @@ def rms_norm_backward(h, w, dy, dh=None, eps: float = 1e-6, need_dx: bool = True
     return call(st) if st is not None else _on_stream(dev, stream, (h, w, dy, dh, out), call)
 
 
+def linear_q8(x, x_scale, w, w_scale, bias=None, residual=None, act: str = "none", out_dtype=None, out=None, status=None, stream=None):
+    """y [T, N] = residual + act(x_scale w_scale (x w^T) + bias) for rows in 8 bits: x [T, K] and w [N, K] float8_e4m3fn with a
+    float32 scale a row, as `rms_norm_q8` and `quantize_rows` give them; K a multiple of 16. y is of out_dtype (or out's, the
+    residual's or the bias's type; bfloat16 where none of them says), bias and residual too. x, residual and out may have
+    strided rows (of x: by multiples of 16); out may be residual itself."""
+    torch = _torch()
+    dev = x.device
+    ldx = _rows(x, None, "x", torch.float8_e4m3fn)
+    T, K = x.shape
+    N = w.shape[0] if w.dim() == 2 else 0
+    _dense(w, N, K, "w", torch.float8_e4m3fn, dev)
+    if N < 1 or K < 1 or K % 16:
+        raise ValueError("w must have at least one row, and x and w a multiple of 16 columns")
+    if ldx % 16 or x.data_ptr() % 16 or w.data_ptr() % 16:
+        raise ValueError("x and w must have rows on 16-byte boundaries")
+    _vector(x_scale, T, "x_scale", torch.float32, dev)
+    _vector(w_scale, N, "w_scale", torch.float32, dev)
+    dt = out_dtype
+    if dt is None:
+        dt = next((t.dtype for t in (out, residual, bias) if t is not None), torch.bfloat16)
+    code = {torch.float32: PK_F32, torch.bfloat16: PK_BF16, torch.float16: PK_F16}.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    if bias is not None:
+        _vector(bias, N, "bias", dt, dev)
+    ldr = _rows(residual, N, "residual", dt, dev, T) if residual is not None else N
+    a = _act_code(act)
+    _check_stream(stream, dev)
+    if status is not None:
+        _vector(status, 1, "status", torch.int32, dev)
+    ldy = N
+    if out is not None:
+        ldy = _rows(out, N, "out", dt, dev, T)
+        _disjoint(out, "out", x, x_scale, w, w_scale, bias, None if _same_place(out, residual) else residual)
+
+    def call(st):
+        y = torch.empty((T, N), dtype=dt, device=dev) if out is None else out
+        ws, wp, wb = (None, None, 0) if 2 * T <= LINEAR_FEW_T else _workspace("pk_linear_q8_workspace", dev, T, N, K)
+        _check(load().pk_linear_q8(code, x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), _ptr(bias),
+                                   _ptr(residual), ldr, a, T, N, K, y.data_ptr(), ldy, wp, wb, _ptr(status), st), "pk_linear_q8")
+        return y
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, x_scale, w, w_scale, bias, residual, out, status), call)
+
+
+# ------------------------------------------------------------------------------------------
+# the gated feed-forward
+
+
+def _gated_inputs(x, w, act, status, stream):
+    dt, dev = x.dtype, x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, K = x.shape
+    N = w.shape[0] if w.dim() == 2 else 0
+    _dense(w, N, K, "w", dt, dev)
+    if N < 2 or N % 2 or K < 1:
+        raise ValueError("w must have an even number of rows (the gate's, then the other's), x and w at least one column")
+    a = _act_code(act)
+    _check_stream(stream, dev)
+    if status is not None:
+        _vector(status, 1, "status", _torch().int32, dev)
+    return code, dt, dev, ldx, T, K, N // 2, a
+
+
+def gated_linear(x, w, bias=None, act: str = "gelu", out=None, return_pre: bool = False, status=None, stream=None):
+    """y [T, F] = act(g) u with [g | u] = x w^T + bias, for x [T, K] and w [2 F, K] (F rows of the gate, then F of what it
+    multiplies; float32, bfloat16 or float16, everything of one type) in one product; act "none", "relu", "gelu" or "silu".
+    return_pre: also [g | u] [T, 2 F], which gated_linear_backward needs. x and out may have strided rows. `status` as
+    for `linear`."""
+    torch = _torch()
+    code, dt, dev, ldx, T, K, F, a = _gated_inputs(x, w, act, status, stream)
+    if bias is not None:
+        _vector(bias, 2 * F, "bias", dt, dev)
+    ldy = F
+    if out is not None:
+        ldy = _rows(out, F, "out", dt, dev, T)
+        _disjoint(out, "out", x, w, bias)
+
+    def call(st):
+        y = torch.empty((T, F), dtype=dt, device=dev) if out is None else out
+        pre = torch.empty((T, 2 * F), dtype=dt, device=dev) if return_pre else None
+        ws, wp, wb = (None, None, 0) if 2 * T <= LINEAR_FEW_T else _workspace("pk_gated_linear_workspace", dev, code, x.data_ptr(), ldx,
+                                                                          w.data_ptr(), T, F, K)
+        _check(load().pk_gated_linear(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), a, T, F, K, y.data_ptr(), ldy, _ptr(pre), wp,
+                                      wb, _ptr(status), st), "pk_gated_linear")
+        return (y, pre) if return_pre else y
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, bias, out, status), call)
+
+
+def gated_linear_backward(x, w, dy, pre, act: str = "gelu", need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                          status=None, stream=None):
+    """(dx [T, K], dw [2 F, K], db [2 F]) of `gated_linear` for the gradient dy [T, F] of its output, each None where not
+    needed; pre [T, 2 F] is the forward's, act too."""
+    torch = _torch()
+    code, dt, dev, ldx, T, K, F, a = _gated_inputs(x, w, act, status, stream)
+    lddy = _rows(dy, F, "dy", dt, dev, T)
+    _dense(pre, T, 2 * F, "pre", dt, dev)
+
+    def call(st):
+        dx = torch.empty((T, K), dtype=dt, device=dev) if need_dx else None
+        dw = torch.empty((2 * F, K), dtype=dt, device=dev) if need_dw else None
+        db = torch.empty(2 * F, dtype=dt, device=dev) if need_db else None
+        ws, wp, wb = _workspace("pk_gated_linear_backward_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), bool(need_dx),
+                                bool(need_dw), bool(need_db), T, F, K)
+        _check(_lib.pk_gated_linear_backward(code, x.data_ptr(), ldx, w.data_ptr(), dy.data_ptr(), lddy, pre.data_ptr(), a, T, F, K,
+                                             _ptr(dx), _ptr(dw), _ptr(db), wp, wb, _ptr(status), st), "pk_gated_linear_backward")
+        return dx, dw, db
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, dy, pre, status), call)
+
+
 # ------------------------------------------------------------------------------------------
 # log probabilities of rows of logits
 
@@ -963,6 +1091,80 @@ def token_logprobs_backward(logits, labels, lse, entropy, dlogp, dentropy=None, 
 
     st = _here(dev, stream)
     return call(st) if st is not None else _on_stream(dev, stream, (logits, labels, lse, entropy, dlogp, dentropy, out), call)
+
+
+# ------------------------------------------------------------------------------------------
+# distillation
+
+
+def _distill_inputs(x, w, idx, values, bias, temperature, status, stream):
+    torch = _torch()
+    dt, dev = x.dtype, x.device
+    code = dtype_code(x)
+    ldx = _rows(x, None, "x")
+    T, D = x.shape
+    V = w.shape[0] if w.dim() == 2 else 0
+    _dense(w, V, D, "w", dt, dev)
+    if V < 1 or D < 1:
+        raise ValueError("x and w must have at least one column, w at least one row")
+    top = idx.shape[1] if idx.dim() == 2 else 0
+    if not 1 <= top <= DISTILL_MAX_TOP:
+        raise ValueError(f"idx must be [T, 1 to {DISTILL_MAX_TOP}], not {tuple(idx.shape)}")
+    _dense(idx, T, top, "idx", torch.int64, dev)
+    _dense(values, T, top, "values", torch.float32, dev)
+    if bias is not None:
+        _vector(bias, V, "bias", dt, dev)
+    if not 1e-3 <= temperature <= 1e3:
+        raise ValueError(f"temperature must be in [1e-3, 1e3], not {temperature}")
+    if status is not None:
+        _vector(status, 1, "status", torch.int32, dev)
+    _check_stream(stream, dev)
+    return code, dt, dev, ldx, T, D, V, top
+
+
+def distill(x, w, idx, values, bias=None, temperature: float = 1.0, status=None, stream=None):
+    """(loss [T], lse [T]), float32: how far a student's probabilities softmax((x w^T + bias) / temperature), x [T, D], w [V, D],
+    are from a teacher's q = softmax(values / temperature) over its top words idx [T, top] int64 (values [T, top] float32: its
+    logits or log probabilities there, as `token_logprobs` gives them; top up to 64): loss = sum_k q_k (ln q_k - ln p_k), without
+    storing the logits. An entry with a negative index or the value -inf is not there; a row without any has loss 0 and
+    costs no work; an index >= V gives a loss of NaN and PK_ERR_BAD_LABEL (in `status`, or last_status of the call's stream)."""
+    torch = _torch()
+    code, dt, dev, ldx, T, D, V, top = _distill_inputs(x, w, idx, values, bias, temperature, status, stream)
+
+    def call(st):
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        ws, wp, wb = _workspace("pk_distill_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), 0, 0, T, D, V, top)
+        _check(_lib.pk_distill(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), idx.data_ptr(), values.data_ptr(), top, temperature, T,
+                               D, V, loss.data_ptr(), lse.data_ptr(), wp, wb, _ptr(status), st), "pk_distill")
+        return loss, lse
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, idx, values, bias, status), call)
+
+
+def distill_backward(x, w, idx, values, lse, dloss, bias=None, temperature: float = 1.0, need_dx: bool = True, need_dw: bool = True,
+                     status=None, stream=None):
+    """(dx [T, D], dw [V, D], db [V] or None without a bias): the gradient of sum(dloss * loss) of `distill` with respect to the
+    student, for its lse [T]; dloss [T] float32 (temperature ** 2 / count for a mean that keeps the gradients' size at any
+    temperature). Rows without a target get a zero dx."""
+    torch = _torch()
+    code, dt, dev, ldx, T, D, V, top = _distill_inputs(x, w, idx, values, bias, temperature, status, stream)
+    _vector(lse, T, "lse", torch.float32, dev)
+    _vector(dloss, T, "dloss", torch.float32, dev)
+
+    def call(st):
+        dx = torch.empty((T, D), dtype=dt, device=dev) if need_dx else None
+        dw = torch.empty((V, D), dtype=dt, device=dev) if need_dw else None
+        db = torch.empty(V, dtype=dt, device=dev) if bias is not None else None
+        ws, wp, wb = _workspace("pk_distill_workspace", dev, code, x.data_ptr(), ldx, w.data_ptr(), 1, bias is not None, T, D, V, top)
+        _check(_lib.pk_distill_backward(code, x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), idx.data_ptr(), values.data_ptr(), top,
+                                        temperature, lse.data_ptr(), dloss.data_ptr(), T, D, V, _ptr(dx), _ptr(dw), _ptr(db), wp, wb,
+                                        _ptr(status), st), "pk_distill_backward")
+        return dx, dw, db
+
+    st = _here(dev, stream)
+    return call(st) if st is not None else _on_stream(dev, stream, (x, w, idx, values, lse, dloss, bias, status), call)
 
 
 def schedule(cu, T: int, window: int, stream=None):

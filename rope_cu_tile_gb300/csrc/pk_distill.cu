@@ -1,0 +1,363 @@
+// pk_distill.cu -- distillation from a teacher's top logits, without keeping the student's logits (pk_distill,
+// pk_distill_backward in include/pk.h).
+//
+//     q = softmax(values / tau) over a row's words,   z = x W^T + b,   p = softmax(z / tau) over the vocabulary
+//     loss = sum_k q_k (ln q_k - ln p_word(k)),   lse = ln sum_v exp(z_v / tau)
+//     dz_v = dloss / tau (p_v - sum of the q_k whose word is v),   dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+//
+// The cross entropy's passes (pk_xent.cu, pk_vocab.cuh) with a list of words in the place of a label: the epilogue that holds a
+// tile of logits in registers writes out those that the row's list names, or takes the q off there. So that it need not
+// search, a first kernel sorts each row's list by word; a tile's first word is found by counting the smaller ones before
+// the accumulators are ready, and most chunks of 32 columns hold none.
+#include "pk_vocab.cuh"
+
+namespace pk {
+
+namespace {
+
+template <int DT>
+using ListStat = StatEpi<DT, true>;
+template <int DT>
+using ListGrad = GradEpi<DT, true>;
+
+constexpr int kMaxTop = PK_DISTILL_MAX_TOP;
+
+struct ListArgs {
+  const long long* idx;  // [T, top]
+  const float* values;   // [T, top]
+  int64_t T;
+  int top, ld, V;
+  float inverse;         // 1 / temperature
+  int* word;             // [T, ld] sorted, then kNoWord
+  float* share;          // [T, ld]
+  long long* label;      // [T] 0 where the row has a word, -1 where it has none, V where it has one past the vocabulary
+};
+
+// A warp a row: the words that are there (an index of a word, a value above -inf), their probabilities and their order. Two
+// words of a lane at most.
+__global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_constant__ ListArgs a) {
+  const int lane = threadIdx.x & 31;
+  griddep_wait();
+  for (int64_t t = blockIdx.x * 8LL + (threadIdx.x >> 5); t < a.T; t += gridDim.x * 8LL) {
+    int word[2];
+    float v[2];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = lane + 32 * i;
+      long long x = -1;
+      v[i] = -INFINITY;
+      if (k < a.top) {
+        x = __ldcg(a.idx + t * a.top + k);
+        v[i] = __ldcg(a.values + t * a.top + k) * a.inverse;
+      }
+      if (v[i] == -INFINITY) x = -1;
+      bad = bad || x >= a.V;
+      word[i] = x < 0 ? kNoWord : x >= a.V ? kNoWord : static_cast<int>(x);
+      if (word[i] == kNoWord) v[i] = -INFINITY;
+    }
+    const bool any = __any_sync(0xffffffffu, word[0] != kNoWord || word[1] != kNoWord);
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) a.label[t] = bad ? a.V : any ? 0 : -1;
+    if (bad || !any) continue;
+    // (a NaN among the values, or an infinity, comes through the exponentials)
+    float m = fmaxf(v[0], v[1]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float e[2], sum;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) e[i] = word[i] == kNoWord ? 0.0f : expf(v[i] - m);
+    sum = e[0] + e[1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // the place of each word: how many are smaller, equal ones by their place in the list; those that are not there last
+    int at[2] = {0, 0};
+    for (int k = 0; k < a.top; ++k) {
+      const int other = __shfl_sync(0xffffffffu, k < 32 ? word[0] : word[1], k & 31);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) at[i] += other < word[i] || (other == word[i] && k < lane + 32 * i) ? 1 : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = lane + 32 * i;
+      if (k < a.ld) {
+        const int64_t to = t * a.ld + (k < a.top ? at[i] : k);
+        a.word[to] = word[i];
+        a.share[to] = e[i] / sum;
+      }
+    }
+  }
+}
+
+// The slices of each row joined, as pk_xent_join_kernel does, and the loss from the logits that the list names: 8 rows x 32
+// strided lanes of slices a block, then 32 lanes of words a row.
+__global__ void __launch_bounds__(256) pk_distill_join_kernel(const float2* part, int64_t cap, int slices, const float* picked,
+                                                              const int* word, const float* share, int ld, float inverse,
+                                                              const int* idx, const int* count, float* loss, float* lse) {
+  __shared__ float2 s[32][8];
+  const int r = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const float factor = inverse * kLog2e;
+  griddep_wait();
+  const int n = __ldcg(count);
+  const auto join = [&](float& m, float& l, float2 q) {
+    const float mn = fmaxf(m, q.x);
+    l = l * exp2f((m - mn) * factor) + q.y * exp2f((q.x - mn) * factor);
+    m = mn;
+  };
+  for (int64_t r0 = blockIdx.x * 8LL; r0 < n; r0 += gridDim.x * 8LL) {
+    float m = kFloor, l = 0.0f;
+    if (r0 + r < n) {
+#pragma unroll 4
+      for (int i = g; i < slices; i += 32) join(m, l, __ldcg(part + i * cap + r0 + r));
+    }
+    s[g][r] = make_float2(m, l);
+    __syncthreads();
+    const int64_t row = r0 + (threadIdx.x >> 5);  // a warp's
+    const int lane = threadIdx.x & 31;
+    if (row < n) {
+      float2 q = s[lane][threadIdx.x >> 5];
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const float2 u = make_float2(__shfl_xor_sync(0xffffffffu, q.x, o), __shfl_xor_sync(0xffffffffu, q.y, o));
+        // (the same order on both sides: the lower lane's first)
+        float2 a = lane & o ? u : q;
+        join(a.x, a.y, lane & o ? q : u);
+        q = a;
+      }
+      const float rest = logf(q.y);
+      const int64_t t = __ldcg(idx + row);
+      float v = 0.0f;
+      for (int k = lane; k < ld; k += 32) {
+        if (__ldcg(word + t * ld + k) == kNoWord) continue;
+        const float p = __ldcg(share + t * ld + k);
+        if (p != 0.0f) v += p * (logf(p) + ((q.x - __ldcg(picked + t * ld + k)) * inverse + rest));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) {
+        loss[t] = v;
+        lse[t] = q.x * inverse + rest;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// the scratch of a call: the lists, then what the cross entropy has
+struct Lists {
+  int ld;
+  int* word;
+  float* share;
+  long long* label;
+};
+Lists plan_lists(Carver& c, int64_t T, int top) {
+  Lists l;
+  l.ld = static_cast<int>(round_up(top, 4));
+  l.word = static_cast<int*>(c.take(T * l.ld * 4));
+  l.share = static_cast<float*>(c.take(T * l.ld * 4));
+  l.label = static_cast<long long*>(c.take(T * 8));
+  return l;
+}
+
+struct Fwd {
+  Lists lists;
+  Common m;
+  gemm::Shape shape;
+  float2* part;
+  float* picked;
+  int slices;
+  int64_t bytes;
+};
+Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T, int D, int V, int top, int sms, void* ws) {
+  Fwd f = {};
+  Carver c(ws);
+  f.lists = plan_lists(c, T, top);
+  plan_common(c, f.m, dtype, x, ldx, w, T, D, V);
+  f.shape = gemm::pick_shape(T, V, D, dtype == PK_F32 ? gemm::kTerms32 : 1, sms, false);
+  f.slices = (V + 64 * f.shape.cg - 1) / (64 * f.shape.cg);
+  f.part = static_cast<float2*>(c.take(f.slices * f.m.cap * 8));
+  f.picked = static_cast<float*>(c.take(T * f.lists.ld * 4));
+  f.bytes = c.used;
+  return f;
+}
+int64_t lists_bytes(int64_t T, int top) {
+  Carver c(nullptr);
+  plan_lists(c, T, top);
+  return c.used;
+}
+
+cudaError_t lists_launch(const Lists& l, const int64_t* idx, const float* values, int64_t T, int top, int V, float inverse, int sms,
+                         cudaStream_t stream) {
+  ListArgs a = {};
+  a.idx = reinterpret_cast<const long long*>(idx);
+  a.values = values;
+  a.T = T;
+  a.top = top;
+  a.ld = l.ld;
+  a.V = V;
+  a.inverse = inverse;
+  a.word = l.word;
+  a.share = l.share;
+  a.label = l.label;
+  const int64_t blocks = (T + 7) / 8, most = static_cast<int64_t>(sms) * 8;
+  Launch launch(blocks < most ? blocks : most, 256, stream);
+  return cudaLaunchKernelEx(&launch.cfg, pk_distill_list_kernel, a);
+}
+
+bool distill_ok(int dtype, int64_t T, int D, int V, int top, double temperature) {
+  return dtype_ok(dtype) && sizes_ok(T, D, V) && top >= 1 && top <= kMaxTop && temperature >= 1e-3 && temperature <= 1e3;
+}
+
+}  // namespace
+
+namespace rows {
+cudaError_t prepare_distill() {
+  cudaError_t e;
+  if ((e = gemm::prepare<ListStat<PK_F32>>()) != cudaSuccess) return e;
+  if ((e = gemm::prepare<ListStat<PK_BF16>>()) != cudaSuccess) return e;
+  if ((e = gemm::prepare<ListStat<PK_F16>>()) != cudaSuccess) return e;
+  if ((e = gemm::prepare<ListGrad<PK_F32>>()) != cudaSuccess) return e;
+  if ((e = gemm::prepare<ListGrad<PK_BF16>>()) != cudaSuccess) return e;
+  return gemm::prepare<ListGrad<PK_F16>>();
+}
+}  // namespace rows
+
+}  // namespace pk
+
+extern "C" {
+
+int pk_distill_workspace(int dtype, const void* x, int64_t ldx, const void* w, int backward, int need_db, int64_t T, int D, int V, int top,
+                         int64_t* bytes) {
+  using namespace pk;
+  if (!bytes || !distill_ok(dtype, T, D, V, top, 1.0) || ldx < D) return PK_ERR_ARG;
+  *bytes = 0;
+  if (T == 0) return PK_OK;
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  *bytes = backward ? lists_bytes(T, top) + plan_backward(dtype, x, ldx, w, need_db != 0, T, D, V, d.sms, nullptr).bytes
+                    : plan_forward(dtype, x, ldx, w, T, D, V, top, d.sms, nullptr).bytes;
+  return PK_OK;
+}
+
+int pk_distill(int dtype, const void* x, int64_t ldx, const void* w, const void* bias, const int64_t* idx, const float* values, int top,
+               double temperature, int64_t T, int D, int V, float* loss, float* lse, void* workspace, int64_t workspace_bytes,
+               int* status, struct CUstream_st* stream) {
+  using namespace pk;
+  if (!distill_ok(dtype, T, D, V, top, temperature) || ldx < D || workspace_bytes < 0) return PK_ERR_ARG;
+  if (T > 0 && (!x || !w || !idx || !values || !loss || !lse)) return PK_ERR_ARG;
+  const uintptr_t e = rows::elem_bytes(dtype);
+  if (!rows::aligned_to(x, e) || !rows::aligned_to(w, e) || !rows::aligned_to(bias, e) || !rows::aligned_to(idx, 8) ||
+      !rows::aligned_to(values, 4) || !rows::aligned_to(loss, 4) || !rows::aligned_to(lse, 4) || !rows::aligned_to(workspace, 256) ||
+      !rows::aligned_to(status, 4))
+    return PK_ERR_ALIGN;
+  if (T == 0) return status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess ? PK_ERR_CUDA : PK_OK;
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  const Fwd f = plan_forward(dtype, x, ldx, w, T, D, V, top, d.sms, workspace);
+  if (!workspace || workspace_bytes < f.bytes) return PK_ERR_NOMEM;
+  if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
+  const float inverse = static_cast<float>(1.0 / temperature);
+  if (lists_launch(f.lists, idx, values, T, top, V, inverse, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  RowArgs r = {};
+  r.labels = f.lists.label;
+  r.T = T;
+  r.V = V;
+  r.counts = f.m.counts;
+  r.maxima = f.m.maxima;
+  r.idx = f.m.idx;
+  r.lab = f.m.lab;
+  r.count = f.m.count;
+  r.loss = loss;
+  r.lse = lse;
+  r.status = status ? status : rows::stream_status(d, stream);
+  if (rows_launch(r, stream) != cudaSuccess) return PK_ERR_CUDA;
+  Inputs in;
+  if (lay_out(dtype, f.m, x, ldx, w, T, D, V, d.sms, stream, &in) != cudaSuccess) return PK_ERR_CUDA;
+  gemm::Args a = {};
+  a.M = static_cast<int>(T);
+  a.N = V;
+  a.K = D;
+  a.dyn = f.m.count;
+  a.dyn_axis = 0;
+  a.alt_count = static_cast<int>(T);
+  a.alt_operand = 0;
+  a.status = r.status;
+  a.timeout_ns = wait_limit_ns();
+  StatParams sp = {};
+  sp.bias = bias;
+  sp.bias_vec = bias && rows::aligned_to(bias, 16);
+  sp.part = f.part;
+  sp.picked = f.picked;
+  sp.cap = f.m.cap;
+  sp.lists = {f.lists.word, f.lists.share, f.m.idx, f.lists.ld};
+  sp.factor = inverse * kLog2e;
+  if (logits_product<ListStat>(dtype, in.xc, in.w, in.alt ? &in.xd : nullptr, a, sp, f.shape, d.sms, stream) != cudaSuccess)
+    return PK_ERR_CUDA;
+  const int64_t blocks = (T + 7) / 8, most = static_cast<int64_t>(d.sms) * 8;
+  rows::Launch l(blocks < most ? blocks : most, 256, stream);
+  const float2* part = f.part;
+  const float *picked = f.picked, *share = f.lists.share;
+  const int *word = f.lists.word, *at = f.m.idx, *count = f.m.count;
+  return cudaLaunchKernelEx(&l.cfg, pk_distill_join_kernel, part, f.m.cap, f.slices, picked, word, share, f.lists.ld, inverse, at, count,
+                            loss, lse) == cudaSuccess
+             ? PK_OK
+             : PK_ERR_CUDA;
+}
+
+int pk_distill_backward(int dtype, const void* x, int64_t ldx, const void* w, const void* bias, const int64_t* idx, const float* values,
+                        int top, double temperature, const float* lse, const float* dloss, int64_t T, int D, int V, void* dx, void* dw,
+                        void* db, void* workspace, int64_t workspace_bytes, int* status, struct CUstream_st* stream) {
+  using namespace pk;
+  if (!distill_ok(dtype, T, D, V, top, temperature) || ldx < D || workspace_bytes < 0) return PK_ERR_ARG;
+  if (T > 0 && (!x || !w || !idx || !values || !lse || !dloss)) return PK_ERR_ARG;
+  const uintptr_t e = rows::elem_bytes(dtype);
+  if (!rows::aligned_to(x, e) || !rows::aligned_to(w, e) || !rows::aligned_to(bias, e) || !rows::aligned_to(idx, 8) ||
+      !rows::aligned_to(values, 4) || !rows::aligned_to(lse, 4) || !rows::aligned_to(dloss, 4) || !rows::aligned_to(dx, e) ||
+      !rows::aligned_to(dw, e) || !rows::aligned_to(db, e) || !rows::aligned_to(workspace, 256) || !rows::aligned_to(status, 4))
+    return PK_ERR_ALIGN;
+  if (T == 0) {
+    if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (dw && cudaMemsetAsync(dw, 0, e * V * static_cast<size_t>(D), stream) != cudaSuccess) return PK_ERR_CUDA;
+    if (db && cudaMemsetAsync(db, 0, e * V, stream) != cudaSuccess) return PK_ERR_CUDA;
+    return PK_OK;
+  }
+  rows::Device d;
+  const int rc = rows::device(&d);
+  if (rc != PK_OK) return rc;
+  const int64_t before = lists_bytes(T, top);
+  const Bwd b = plan_backward(dtype, x, ldx, w, db != nullptr, T, D, V, d.sms, workspace ? static_cast<char*>(workspace) + before : nullptr);
+  if (!workspace || workspace_bytes < before + b.bytes) return PK_ERR_NOMEM;
+  Carver c(workspace);
+  const Lists lists = plan_lists(c, T, top);
+  if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
+  const float inverse = static_cast<float>(1.0 / temperature);
+  if (lists_launch(lists, idx, values, T, top, V, inverse, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
+  RowArgs r = {};
+  r.labels = lists.label;
+  r.T = T;
+  r.V = V;
+  r.counts = b.m.counts;
+  r.maxima = b.m.maxima;
+  r.idx = b.m.idx;
+  r.lab = b.m.lab;
+  r.count = b.m.count;
+  r.dloss = dloss;
+  r.lse_in = lse;
+  r.coef = b.coef;
+  r.lse_rows = b.lse;
+  r.unscale = b.unscale;
+  r.factor = inverse;
+  r.scaled = dtype == PK_F16;
+  r.status = status ? status : rows::stream_status(d, stream);
+  if (rows_launch(r, stream) != cudaSuccess) return PK_ERR_CUDA;
+  Inputs in;
+  if (lay_out(dtype, b.m, x, ldx, w, T, D, V, d.sms, stream, &in) != cudaSuccess) return PK_ERR_CUDA;
+  GradParams gp = {};
+  gp.lists = {lists.word, lists.share, b.m.idx, lists.ld};
+  gp.inverse = inverse;
+  return backward_pieces<ListGrad>(dtype, b, in, gp, bias, T, D, V, dx, dw, db, r.status, d.sms, stream);
+}
+
+}  // extern "C"

@@ -285,6 +285,57 @@ __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (
   }
 }
 
+// a[i] = act(z[i]) and s[i] = act'(z[i]), the exponentials shared; as exact as act_values and act_slopes
+template <int DT, int N>
+__device__ __forceinline__ void act_both(int act, const float (&z)[N], float (&a)[N], float (&s)[N]) {
+  if (act == PK_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 u = make_float2(fabsf(z[i]), fabsf(z[i + 1]));
+      float2 e, f = mul2(u, u);
+      if constexpr (DT == PK_F32) {
+        e = make_float2(0.5f * erfcf(u.x * 0.70710678118654752f), 0.5f * erfcf(u.y * 0.70710678118654752f));
+        f = make_float2(expf(-0.5f * f.x), expf(-0.5f * f.y));
+      } else {
+        e = tail2(u.x, u.y);
+        f = mul2(f, make_float2(-0.72134752044448170f, -0.72134752044448170f));
+        f = make_float2(attn::ex2(f.x), attn::ex2(f.y));
+      }
+      const float2 g = make_float2(-fminf(u.x, 3.0e38f), -fminf(u.y, 3.0e38f));
+      const float2 v = fma2(g, e, make_float2(fmaxf(z[i], 0.0f), fmaxf(z[i + 1], 0.0f)));
+      const float2 h = fma2(mul2(g, make_float2(0.39894228040143268f, 0.39894228040143268f)), f, e);
+      const float2 w = fma2(h, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+      a[i] = v.x;
+      a[i + 1] = v.y;
+      s[i] = z[i] < 0.0f ? h.x : w.x;
+      s[i + 1] = z[i + 1] < 0.0f ? h.y : w.y;
+    }
+  } else if (act == PK_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float h, rest;
+      if constexpr (DT == PK_F32) {
+        const float e = expf(-z[i]);
+        h = 1.0f / (1.0f + e);
+        rest = z[i] > 0.0f ? e * h : 1.0f - h;
+      } else {
+        h = rcp_fast(1.0f + attn::ex2(z[i] * -1.4426950408889634f));
+        rest = 1.0f - h;
+      }
+      const float low = fmaxf(z[i], -3.0e38f);
+      a[i] = low * h;
+      s[i] = h * fmaf(fminf(low, 3.0e38f), rest, 1.0f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool on = act == PK_ACT_NONE || z[i] > 0.0f || z[i] != z[i];
+      a[i] = on ? z[i] : 0.0f;
+      s[i] = z[i] != z[i] ? z[i] : on ? 1.0f : 0.0f;
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------------
 // the linear epilogue
 

@@ -18,10 +18,25 @@
 // Every wait is bounded: one that runs out records PK_ERR_TIMEOUT, raises the CTA's abort flag, and the roles leave.
 #pragma once
 
+#include <type_traits>
+
 #include "pk_attn_common.cuh"
 
 namespace pk {
 namespace gemm {
+
+// What an epilogue may ask of the product besides its own part:
+//   kPair   B's rows are two halves of N / 2 (a gate and what it multiplies). A tile then holds the same 64 or 128 columns of
+//           both, the first half's in the accumulator's first half, so that the epilogue finds the two side by side.
+//   kBytes  the operands are e4m3, two elements in the place of one: every size along k is counted in such pairs.
+template <class Epi, class = void>
+struct IsPair : std::false_type {};
+template <class Epi>
+struct IsPair<Epi, std::void_t<decltype(Epi::kPair)>> : std::bool_constant<Epi::kPair> {};
+template <class Epi, class = void>
+struct IsBytes : std::false_type {};
+template <class Epi>
+struct IsBytes<Epi, std::void_t<decltype(Epi::kBytes)>> : std::bool_constant<Epi::kBytes> {};
 
 constexpr int kStages = 6;
 constexpr int kBK = 64;                       // k step: 128 bytes, one swizzle row
@@ -57,6 +72,7 @@ struct Args {
   int M, N, K;      // K in elements of one plane
   int a_mn, b_mn;   // operand layouts (0: K-major, 1: MN-major)
   int bf16;
+  int phase;        // 0, or the most k steps that the tensor pipe may add up by itself
   int terms;        // 1, or kTerms32
   int splits;       // splits of k (with a device count of rows: the most that the device may choose)
   int part_rows;    // with a device count of rows: rows of the partial sums' memory
@@ -123,7 +139,7 @@ __device__ __forceinline__ Plan make_plan(const Args& a) {
   p.splits = choose_splits<CG>(a, p.M);
   p.kb_per = (p.kb_all + p.splits - 1) / p.splits;
   p.units = p.tiles_m * p.tiles_n * p.splits;
-  const int most = a.terms > 1 ? kPhase32 : kPhase16;
+  const int most = a.phase > 0 ? a.phase : a.terms > 1 ? kPhase32 : kPhase16;
   p.phased = p.kb_per > most;
   p.phase = p.phased ? most : p.kb_per;
   return p;
@@ -186,9 +202,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
-template <int CG>
+template <int CG, bool kBytes>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (CG == 2)
+  // (a step of 32 bytes along k either way: 16 elements or 32)
+  if constexpr (kBytes && CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else if constexpr (kBytes)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else if constexpr (CG == 2)
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
@@ -266,7 +295,7 @@ __device__ __forceinline__ bool wait_warp(Meta* m, const Args& a, uint64_t* bar,
 // ------------------------------------------------------------------------------------
 // roles
 
-template <int CG>
+template <int CG, bool kPair>
 __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap* mb, const Args& a, const Plan& p,
                                         uint8_t* smem, Meta* meta, uint32_t rank, int unit0, int unit_step) {
   uint32_t st = 0, ph = 0;
@@ -296,7 +325,16 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
           } else {
             tma_load_3d<CG>(sa, ma, bar, k, ra, pa);
           }
-          if (a.b_mn) {
+          if constexpr (kPair) {
+            // (the pair's second CTA holds the second half's rows, a lone CTA 64 of each)
+            const int f = t.n0 / 2, half = p.N / 2;
+            if constexpr (CG == 2) {
+              tma_load_3d<CG>(sb, mb, bar, k, f + static_cast<int>(rank) * half, pb);
+            } else {
+              tma_load_3d<CG>(sb, mb, bar, k, f, pb);
+              tma_load_3d<CG>(sb + kOpBytes / 2, mb, bar, k, f + half, pb);
+            }
+          } else if (a.b_mn) {
             tma_load_3d<CG>(sb, mb, bar, rb, k, pb);
             tma_load_3d<CG>(sb + kOpBytes / 2, mb, bar, rb + 64, k, pb);
           } else {
@@ -331,7 +369,7 @@ __device__ __forceinline__ void produce(const CUtensorMap* ma, const CUtensorMap
   }
 }
 
-template <int CG>
+template <int CG, bool kBytes>
 __device__ __forceinline__ void issue(const Args& a, const Plan& p, uint8_t* smem, Meta* meta, uint32_t tmem, int unit0,
                                       int unit_step) {
   const uint32_t idesc = idesc_f16(a.bf16 != 0, 128 * CG, 128 * CG, a.a_mn != 0, a.b_mn != 0);
@@ -357,7 +395,7 @@ __device__ __forceinline__ void issue(const Args& a, const Plan& p, uint8_t* sme
         const uint64_t xa = da + st * (kStageBytes >> 4), xb = db + st * (kStageBytes >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (uint32_t k = 0; k < kBK / 16; ++k) mma<CG>(d, xa + k * sa, xb + k * sb, idesc, (i | k) != 0 ? 1u : 0u);
+          for (uint32_t k = 0; k < kBK / 16; ++k) mma<CG, kBytes>(d, xa + k * sa, xb + k * sb, idesc, (i | k) != 0 ? 1u : 0u);
           commit<CG>(smem_u32(&meta->empty[st]));
           if (i + 1 == steps) commit<CG>(smem_u32(&meta->acc_full[buf]));
         }
@@ -397,10 +435,10 @@ __device__ __forceinline__ void add_phase(uint32_t acc, bool first) {
   tmem_wait_st();
 }
 
-// Epi: struct with kWarps and `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
+// Epi: struct with kWarps, perhaps kPair and kBytes, and `static __device__ bool run(const Params&, tmem address of the warp's lanes and first column, zero (there
 // are no accumulators: take zeros), first row, first column, columns, M, N, split, lane, staging, ready, done)`, called by
 // 32 lanes together; it calls ready() before it reads accumulators and done() once after the last of them, and
-// returns false when ready() did.
+// returns false when ready() did. With kPair: the addresses of both accumulators, and the columns of a half.
 template <int CG, class Epi>
 __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -442,12 +480,17 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
     const CUtensorMap* mb = alt && a.alt_operand == 1 ? &map_alt : &map_b;
     // operands that an earlier kernel wrote with ordinary stores, before TMA reads them
     asm volatile("fence.proxy.async.global;" ::: "memory");
-    produce<CG>(ma, mb, a, p, smem, meta, rank, unit0, unit_step);
+    produce<CG, IsPair<Epi>::value>(ma, mb, a, p, smem, meta, rank, unit0, unit_step);
   } else if (warp == 1) {
-    if (rank == 0) issue<CG>(a, p, smem, meta, tmem, unit0, unit_step);
+    if (rank == 0) issue<CG, IsBytes<Epi>::value>(a, p, smem, meta, tmem, unit0, unit_step);
   } else if (warp >= kEpiWarp0) {
     const int w = warp - kEpiWarp0, quarter = w & 3, part = w >> 2;
-    constexpr int kCols = 128 * CG / (Epi::kWarps / 4);  // columns a warp empties
+    // columns a warp empties: its share of the tile's; of a pair's two halves each, 32 at least, so that of a lone CTA's 64 two
+    // warps of a quarter have some
+    constexpr bool kPair = IsPair<Epi>::value;
+    constexpr int kEven = 128 * CG / (kPair ? 2 : 1) / (Epi::kWarps / 4), kCols = kEven < 32 ? 32 : kEven;
+    constexpr int kHalf = 64 * CG;  // columns between a pair's two accumulators
+    const bool idle = kPair && part * kCols >= kHalf;
     uint8_t* stage = smem + kOffEpi + w * (kEpiBytes / Epi::kWarps);
     uint32_t n = 0;
     uint32_t empty0 = smem_u32(&meta->acc_empty[0]);
@@ -477,7 +520,10 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
       if (p.phased) {
         // each phase's sums onto those of the phases before, in accumulator 1's place
         for (int k0 = 0; k0 < t.kbs && (ok = full()); k0 += p.phase) {
-          add_phase<kCols>(acc, k0 == 0);
+          if (!idle) {
+            add_phase<kCols>(acc, k0 == 0);
+            if constexpr (kPair) add_phase<kCols>(acc + kHalf, k0 == 0);
+          }
           empty();
           ++n;
         }
@@ -486,9 +532,19 @@ __global__ void __launch_bounds__(32 * (kEpiWarp0 + Epi::kWarps), 1)
       const auto done = [&]() {
         if (!zero && !p.phased) empty();
       };
-      if (!ok || !Epi::run(ep, acc + (p.phased ? 256 : buf * 256), zero, t.m0 + 128 * static_cast<int>(rank) + 32 * quarter,
-                           t.n0 + part * kCols, kCols, p.M, p.N, t.split, lane, stage, ready, done))
-        break;
+      if (kPair && idle) {
+        if (!ok || !ready()) break;
+        done();
+        if (!zero && !p.phased) ++n;
+        continue;
+      }
+      const uint32_t sums = acc + (p.phased ? 256 : buf * 256);
+      const int row = t.m0 + 128 * static_cast<int>(rank) + 32 * quarter, col = (kPair ? t.n0 / 2 : t.n0) + part * kCols;
+      if constexpr (kPair)
+        ok = ok && Epi::run(ep, sums, sums + kHalf, zero, row, col, kCols, p.M, p.N / 2, t.split, lane, stage, ready, done);
+      else
+        ok = ok && Epi::run(ep, sums, zero, row, col, kCols, p.M, p.N, t.split, lane, stage, ready, done);
+      if (!ok) break;
       if (!zero && !p.phased) ++n;
     }
     // copies in flight (a warp that gave up) land, and tiles stored by TMA are written, before the CTA leaves
@@ -521,6 +577,7 @@ struct Operand {
   int planes = 1;
   int bf16 = 1;
   int mn = 0;  // 0: rows are the product's m or n, cols its k; 1: rows are its k
+  int box = 128;  // rows of a tile, where they are not its k
 };
 inline bool operand_ok(const Operand& o) {
   return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && (o.ld & 7) == 0 && (o.plane & 7) == 0;
@@ -549,7 +606,9 @@ template <class Epi>
 cudaError_t launch(const Operand& A, const Operand& B, const Operand* alt, Args a, const typename Epi::Params& ep, Shape s,
                    int sms, cudaStream_t stream) {
   CUtensorMap ma, mb, mc;
-  if (!make_map(&ma, A) || !make_map(&mb, B)) return cudaErrorInvalidValue;
+  Operand second = B;
+  if (IsPair<Epi>::value && s.cg == 1) second.box = 64;
+  if (!make_map(&ma, A) || !make_map(&mb, second)) return cudaErrorInvalidValue;
   mc = ma;
   if (alt) {
     if (!make_map(&mc, *alt)) return cudaErrorInvalidValue;

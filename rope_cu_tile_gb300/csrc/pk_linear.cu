@@ -8,7 +8,8 @@
 // is an operand of both products, so it has to exist in memory in the operand's type) and sums its columns on the way.
 #include <cstring>
 
-#include "pk_rows.cuh"
+#include "pk_dz.cuh"
+#include "pk_few.cuh"
 
 namespace pk {
 
@@ -17,55 +18,7 @@ namespace {
 using namespace rows;
 
 // ------------------------------------------------------------------------------------
-// dz and its column sums
-
-constexpr int kDzThreads = 256;
-constexpr int kDzBlocks = 4;  // resident blocks of an SM
-constexpr int kDzLeast = 16;  // rows of a block
-// Rows of a block: one wave of resident blocks, all of the same length (fixed blocks of 128 rows left part of the SMs
-// idle at the end). Measured: 65536 x 2048 bf16, gelu and dropout, 159 us (0.75 of the copy rate; issue slots 63 % full).
-int dz_rows(int64_t T, int64_t ldz, int sms) {
-  const int64_t blocks = kDzBlocks * sms / ((ldz + 255) / 256);
-  const int64_t rows = blocks > 1 ? round_up((T + blocks - 1) / blocks, 8) : T;
-  return static_cast<int>(rows < kDzLeast ? kDzLeast : rows);
-}
-
-struct DzArgs {
-  const void* dy;
-  const void* pre;
-  int64_t lddy, ldpre;
-  int64_t T;
-  int N;
-  int act;
-  DropArgs drop;
-  uint16_t* dz;  // [T, ldz] operand (three planes for fp32), or null
-  int64_t ldz, plane;
-  float* part;  // [blocks of rows, ldz] column sums, or null
-  int dy_vec, pre_vec;
-  int rows;    // of a block
-  float* tops;     // [blocks] fp16: each block's largest finite |dz|, or null
-  float* unscale;  // the inverse of dz's scale
-};
-
-// The power of two that fp16's dz is multiplied by: 1 while the largest |dz| is within [2^-10, 65504], where it overflows
-// nothing and every element within 2^-4 of it keeps its 11 bits (half a step of the smallest numbers, 2^-25, is 2^-15 of it at
-// most); past either end the one that brings it to [2^14, 2^15).
-__device__ __forceinline__ int dz_exponent(float top) {
-  if (!(top > 0.0f) || (top >= 0.0009765625f && top <= 65504.0f)) return 0;
-  return max(-100, min(100, 14 - ilogbf(top)));
-}
-
-// The largest of a block's values, in every thread; `shared` holds a value a warp.
-__device__ __forceinline__ float block_top(float v, float* shared) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = shared[0];
-#pragma unroll
-  for (int i = 1; i < kDzThreads / 32; ++i) v = fmaxf(v, shared[i]);
-  return v;
-}
+// dz
 
 // A warp takes 256 columns of a row (8 a lane: one draw of the generator); a block eight rows at a time.
 // Moves dy, z and dz; bound by issue slots with dropout and gelu (64 % of them, 0.75 of the copy rate).
@@ -184,7 +137,6 @@ cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
 // k, so that most of W is on its way at once. One launch, no scratch. Past a few rows its arithmetic and the reads of x
 // outweigh the tensor cores' fixed costs: W [4096, 1024] in bf16 took 3.5 us at 1 row, 6.5 at 4, 11.9 at 8, and 7.3 there;
 // fp32 10.5 at 8 rows here and some 19 there, with its plane copies.
-constexpr int kFewThreads = 256;
 bool few_rows(int dtype, int64_t T) { return T <= (dtype == PK_F32 ? PK_LINEAR_FEW_T : PK_LINEAR_FEW_T / 2); }
 
 struct FewArgs {
@@ -197,58 +149,16 @@ struct FewArgs {
   LinParams ep;
 };
 
-// rows of W a warp, and steps of k asked for together: as many 16-byte loads in flight as the registers of 16 warps an SM hold
-__host__ __device__ constexpr int few_r(int dt, int tm) { return dt == PK_F32 && tm < 8 ? 2 : 4; }
-__host__ __device__ constexpr int few_steps(int dt) { return dt == PK_F32 ? 1 : 2; }
-
 template <int DT, int TM>
 __global__ void __launch_bounds__(kFewThreads) pk_linear_few_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int kR = few_r(DT, TM), kFewSteps = few_steps(DT);
+  constexpr int kR = few_r(DT, TM);
   __shared__ float part[8][kR * TM];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int group = w / a.share, sub = w % a.share, groups = 8 / a.share;
   const int n0 = (blockIdx.x * groups + group) * kR;
   float acc[kR][TM];
-#pragma unroll
-  for (int r = 0; r < kR; ++r)
-#pragma unroll
-    for (int t = 0; t < TM; ++t) acc[r][t] = 0.0f;
   griddep_wait();
-  if (n0 < a.N) {
-    const int step = a.share * 256;
-#pragma unroll 1
-    for (int k0 = sub * 256 + lane * 8; k0 < a.K; k0 += kFewSteps * step) {
-      Raw8<DT> q[kFewSteps][kR];
-#pragma unroll
-      for (int s = 0; s < kFewSteps; ++s)
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          const int k = k0 + s * step;
-          if (k < a.K) q[s][r].load(a.w, static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.K + k, a.vec, a.K - k);
-        }
-#pragma unroll
-      for (int s = 0; s < kFewSteps; ++s) {
-        const int k = k0 + s * step;
-        if (k >= a.K) break;
-        float v[kR][8];
-#pragma unroll
-        for (int r = 0; r < kR; ++r) q[s][r].get(v[r]);
-#pragma unroll
-        for (int t = 0; t < TM; ++t) {
-          float x[8];
-          const int64_t at = min(t, a.T - 1) * a.ldx + k;
-          if (a.vec && k + 8 <= a.K)
-            load8<DT, true>(a.x, at, x);
-          else
-            load8_any<DT>(a.x, at, a.K - k, x);
-#pragma unroll
-          for (int r = 0; r < kR; ++r)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(v[r][j], x[j], acc[r][t]);
-        }
-      }
-    }
-  }
+  few_dots<DT>(a.x, a.ldx, a.T, a.w, a.K, a.vec, n0 < a.N, sub, a.share, lane, [&](int r) { return min(n0 + r, a.N - 1); }, acc);
 #pragma unroll
   for (int r = 0; r < kR; ++r)
 #pragma unroll
@@ -270,8 +180,7 @@ __global__ void __launch_bounds__(kFewThreads) pk_linear_few_kernel(const __grid
 template <int DT, int TM>
 cudaError_t few_launch_rows(FewArgs a, int sms, cudaStream_t stream) {
   constexpr int kR = few_r(DT, TM);
-  a.share = 1;
-  while (a.share < 8 && static_cast<int64_t>(a.N) / kR * a.share < 16 * sms && a.K > 256 * a.share) a.share *= 2;
+  a.share = few_share(a.N / kR, a.K, sms);
   const int per_block = 8 / a.share * kR;
   Launch l((a.N + per_block - 1) / per_block, kFewThreads, stream);
   return cudaLaunchKernelEx(&l.cfg, pk_linear_few_kernel<DT, TM>, a);
@@ -306,47 +215,13 @@ Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T
   return f;
 }
 
-struct Bwd {
-  gemm::Shape dx, dw;
-  void *x, *w, *dz;
-  float *part, *partial;
-  float *tops, *unscale;  // of a dz that may need a scale
-  bool scaled;
-  int rows;  // of a block of dz
-  int64_t blocks, bytes;
-};
 Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, const void* dy, int64_t lddy, int act,
                   uint32_t cut, bool need_dx, bool need_dw, bool need_db, int64_t T, int N, int K, int sms, void* ws) {
-  Bwd b = {};
-  Carver c(ws);
-  const int terms = dtype == PK_F32 ? gemm::kTerms32 : 1;
-  if (need_dw && !in_place(dtype, x, ldx)) b.x = c.take(copy_bytes(dtype, T, K));
-  if (need_dx && !in_place(dtype, w, K)) b.w = c.take(copy_bytes(dtype, N, K));
   // dy itself is the operand when nothing changes it on the way
   const bool made = (need_dx || need_dw) && (act != PK_ACT_NONE || cut || !in_place(dtype, dy, lddy));
-  if (made) b.dz = c.take(copy_bytes(dtype, T, N));
-  b.rows = dz_rows(T, copy_ld(N), sms);
-  b.blocks = (T + b.rows - 1) / b.rows;
   // (without dropout dz of relu, or of no activation, is made of dy's elements and zeros: exact)
-  b.scaled = made && dtype == PK_F16 && (cut || act == PK_ACT_GELU || act == PK_ACT_SILU);
-  if (b.scaled) {
-    b.tops = static_cast<float*>(c.take(b.blocks * ((copy_ld(N) + 255) / 256) * 4));
-    b.unscale = static_cast<float*>(c.take(4));
-  }
-  if (need_db) b.part = static_cast<float*>(c.take(b.blocks * copy_ld(N) * 4));
-  int64_t partial = 0;
-  if (need_dx) {
-    b.dx = gemm::pick_shape(T, K, N, terms, sms, true);
-    partial = partial_bytes(b.dx, T, K);
-  }
-  if (need_dw) {
-    b.dw = gemm::pick_shape(N, K, T, terms, sms, true);
-    const int64_t m = partial_bytes(b.dw, N, K);
-    partial = m > partial ? m : partial;
-  }
-  b.partial = static_cast<float*>(c.take(partial));
-  b.bytes = c.used;
-  return b;
+  const bool scaled = made && dtype == PK_F16 && (cut || act == PK_ACT_GELU || act == PK_ACT_SILU);
+  return plan_products(dtype, x, ldx, w, made, scaled, N, need_dx, need_dw, need_db, T, N, K, sms, ws);
 }
 
 bool sizes_ok(int64_t T, int N, int K) {
@@ -484,38 +359,8 @@ int pk_linear_backward(int dtype, const void* x, int64_t ldx, const void* w, con
     if (dz_launch(dtype, z, stream) != cudaSuccess) return PK_ERR_CUDA;
     if (db && rows::sum_rows(dtype, b.part, b.blocks, nullptr, 1, N, z.ldz, nullptr, db, stream) != cudaSuccess) return PK_ERR_CUDA;
   }
-  rows::Copies copies(dtype);
-  if (b.w) copies.add(w, K, N, K, b.w);
-  if (b.x) copies.add(x, ldx, T, K, b.x);
-  if (copies.launch(d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
-  gemm::Args a = {};
-  a.status = status ? status : rows::stream_status(d, stream);
-  a.timeout_ns = wait_limit_ns();
-  if (dx) {
-    const gemm::Operand A = b.dz ? rows::operand_of_copy(dtype, b.dz, T, N, 0) : rows::operand(dtype, dy, lddy, T, N, 0);
-    const gemm::Operand B = b.w ? rows::operand_of_copy(dtype, b.w, N, K, 1) : rows::operand(dtype, w, K, N, K, 1);
-    a.M = static_cast<int>(T);
-    a.N = K;
-    a.K = N;
-    LinParams ep = {};
-    ep.y = dx;
-    ep.ldy = K;
-    ep.alpha = b.scaled ? b.unscale : nullptr;
-    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dx, b.partial, rows::partial_rows(b.dx, T), d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
-  }
-  if (dw) {
-    const gemm::Operand A = b.dz ? rows::operand_of_copy(dtype, b.dz, T, N, 1) : rows::operand(dtype, dy, lddy, T, N, 1);
-    const gemm::Operand B = b.x ? rows::operand_of_copy(dtype, b.x, T, K, 1) : rows::operand(dtype, x, ldx, T, K, 1);
-    a.M = N;
-    a.N = K;
-    a.K = static_cast<int>(T);
-    LinParams ep = {};
-    ep.y = dw;
-    ep.ldy = K;
-    ep.alpha = b.scaled ? b.unscale : nullptr;
-    if (rows::product(dtype, dtype, A, B, nullptr, a, ep, b.dw, b.partial, rows::partial_rows(b.dw, N), d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
-  }
-  return PK_OK;
+  return back_products(dtype, b, x, ldx, w, dy, lddy, T, N, K, dx, dw, status ? status : rows::stream_status(d, stream), d.sms,
+                       stream);
 }
 
 }  // extern "C"

@@ -39,7 +39,7 @@ bool make_map(CUtensorMap* map, const Operand& o) {
                               static_cast<cuuint64_t>(o.planes)};
   const cuuint64_t plane = o.planes > 1 ? o.plane : o.rows * o.ld;
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2, plane * 2};
-  const cuuint32_t box[3] = {64, o.mn ? 64u : 128u, 1};
+  const cuuint32_t box[3] = {64, o.mn ? 64u : static_cast<cuuint32_t>(o.box), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, o.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(o.p),
              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -110,6 +110,9 @@ std::mutex g_mu;
 
 cudaError_t prepare_products();
 cudaError_t prepare_xent();
+cudaError_t prepare_gated();
+cudaError_t prepare_q8();
+cudaError_t prepare_distill();
 
 int device(Device* out) {
   int dev = 0;
@@ -130,7 +133,8 @@ int device(Device* out) {
       } else {
         void* word = nullptr;
         if (cudaGetSymbolAddress(&word, g_rows_status) != cudaSuccess || prepare_products() != cudaSuccess ||
-            prepare_xent() != cudaSuccess) {
+            prepare_xent() != cudaSuccess || prepare_gated() != cudaSuccess ||
+            prepare_q8() != cudaSuccess || prepare_distill() != cudaSuccess) {
           cudaGetLastError();
           return PK_ERR_CUDA;
         }
@@ -351,6 +355,17 @@ cudaError_t prepare_products() {
   return gemm::prepare<LinEpi<PK_F16, PK_F32>>();
 }
 
+cudaError_t partial_sums(const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt, gemm::Args a, gemm::Shape s,
+                         float* partial, int64_t part_rows, int sms, cudaStream_t stream) {
+  LinTiles part = {};
+  part.y = partial;
+  part.ldy = round_up(a.N, 8);
+  part.tma_y = 1;
+  a.part_rows = static_cast<int>(part_rows);
+  if (!gemm::make_out_map(&part.map_y, PK_F32, partial, part_rows, a.N, part.ldy, 1, 0)) return cudaErrorInvalidValue;
+  return gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, part, s, sms, stream);
+}
+
 cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt,
                     gemm::Args a, LinParams ep, gemm::Shape s, float* partial, int64_t part_rows, int sms, cudaStream_t stream) {
   const int e = elem_bytes(dtype);
@@ -359,22 +374,17 @@ cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::O
   ep.pre_vec = ep.pre && rows16(ep.pre, ep.ldpre, e);
   ep.y_vec = rows16(ep.y, ep.ldy, e);
   if (s.splits > 1) {
-    LinTiles part = {};
-    part.y = partial;
-    part.ldy = round_up(a.N, 8);
-    part.tma_y = 1;
-    a.part_rows = static_cast<int>(part_rows);
-    if (!gemm::make_out_map(&part.map_y, PK_F32, partial, part_rows, a.N, part.ldy, 1, 0)) return cudaErrorInvalidValue;
-    cudaError_t r = gemm::launch<LinEpi<PK_F32, PK_F32>>(A, B, alt, a, part, s, sms, stream);
+    const cudaError_t r = partial_sums(A, B, alt, a, s, partial, part_rows, sms, stream);
     if (r != cudaSuccess) return r;
+    a.part_rows = static_cast<int>(part_rows);
     a.terms = A.planes == 3 ? gemm::kTerms32 : 1;  // what the launch above told the product
     a.splits = s.splits;
     a.slots = sms / s.cg;
-    const int64_t n = a.M * (part.ldy / 8), most = static_cast<int64_t>(sms) * 8;
+    const int64_t ldp = round_up(a.N, 8), n = a.M * (ldp / 8), most = static_cast<int64_t>(sms) * 8;
     Launch l(n / 256 + 1 < most ? n / 256 + 1 : most, 256, stream);
     const float* cp = partial;
-    const FastDiv groups(static_cast<uint32_t>(part.ldy / 8));
-    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, cp, s.cg, part.ldy, groups, a, ep); };
+    const FastDiv groups(static_cast<uint32_t>(ldp / 8));
+    auto run = [&](auto kernel) { return cudaLaunchKernelEx(&l.cfg, kernel, cp, s.cg, ldp, groups, a, ep); };
     if (dtype == PK_F32) return run(splits_kernel<PK_F32, PK_F32>);
     if (dtype == PK_BF16) return run(rdtype == PK_F32 ? splits_kernel<PK_BF16, PK_F32> : splits_kernel<PK_BF16, PK_BF16>);
     return run(rdtype == PK_F32 ? splits_kernel<PK_F16, PK_F32> : splits_kernel<PK_F16, PK_F16>);

@@ -91,6 +91,10 @@ cudaError_t product(int dtype, int rdtype, const gemm::Operand& A, const gemm::O
 inline int64_t partial_rows(const gemm::Shape& s, int64_t M) { return s.splits > 1 ? s.splits * round_up(M, 256) : 0; }
 inline int64_t partial_bytes(const gemm::Shape& s, int64_t M, int64_t N) { return partial_rows(s, M) * round_up(N, 8) * 4; }
 
+// The partial sums alone, fp32, `part_rows` rows of round_up(N, 8) floats (split s from row s x round_up(M, 256) on).
+cudaError_t partial_sums(const gemm::Operand& A, const gemm::Operand& B, const gemm::Operand* alt, gemm::Args a, gemm::Shape s,
+                         float* partial, int64_t part_rows, int sms, cudaStream_t stream);
+
 // out[c] = sum over rows of part[r][c], in a fixed order; with `count`, only the first ceil(*count / per) rows
 cudaError_t sum_rows(int dtype, const float* part, int64_t nrows, const int* count, int per, int cols, int64_t ld,
                      const float* alpha, void* out, cudaStream_t stream);

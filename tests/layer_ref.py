@@ -116,3 +116,120 @@ def token_logprobs_backward(z, labels, lse, entropy, dlogp, dentropy):
     err = p * mag * (2.0**-19 + 2.0**-21 * (l.abs() + Z.abs().clamp(max=1e4) + L.abs().clamp(max=1e4))) + one * 2.0**-23 * (g.abs() + d.abs())
     d = d + one * g
     return d, rounded(d, err, dt)
+
+
+# ------------------------------------------------------------------------------------------ the gated feed-forward
+
+
+def gated_linear(x, w, bias, kind):
+    """(y, pre), (their bounds) in float64. An activation is off by rows.ACT_ERR of its argument and no steeper than LIPSCHITZ."""
+    dt, K, F = x.dtype, x.shape[1], w.shape[0] // 2
+    z = x.double() @ w.double().T
+    mag = x.double().abs() @ w.double().abs().T
+    if bias is not None:
+        z, mag = z + bias.double(), mag + bias.double().abs()
+    ez = rows.sum_bound(K + 1, dt) * mag
+    g, u, eg, eu = z[:, :F], z[:, F:], ez[:, :F], ez[:, F:]
+    a = rows.act(g, kind)
+    ea = rows.LIPSCHITZ * eg + (rows.ACT_ERR * g.abs() if kind in ("gelu", "silu") else 0)
+    y = a * u
+    ey = ea * (u.abs() + eu) + a.abs() * eu + 2.0**-22 * y.abs()
+    return (y, z), (rounded(y, ey, dt), rounded(z, ez, dt))
+
+
+def gated_linear_backward(x, w, dy, pre, kind):
+    """(dx, dw, db), (their bounds) in float64; dz is an operand of the element type."""
+    dt, T, F = x.dtype, x.shape[0], dy.shape[1]
+    X, W, d = x.double(), w.double(), dy.double()
+    g, u = pre.double()[:, :F], pre.double()[:, F:]
+    a, s = rows.act(g, kind), rows.act_slope(g, kind)
+    smooth = rows.ACT_ERR if kind in ("gelu", "silu") else 0.0
+    dz = torch.cat([d * u * s, d * a], 1)
+    err = torch.cat([(d * u).abs() * 8 * smooth * (1 + g.abs()), d.abs() * smooth * g.abs()], 1) + 2.0**-21 * dz.abs()
+    once = err + (U[dt] if dt != torch.float32 else 0) * dz.abs() + TINY[dt]
+    dx, dw, db = dz @ W, dz.T @ X, dz.sum(0)
+    ex = once @ W.abs() + rows.sum_bound(2 * F, dt) * ((dz.abs() + once) @ W.abs())
+    ew = once.T @ X.abs() + rows.sum_bound(T, dt) * ((dz.abs() + once).T @ X.abs())
+    eb = err.sum(0) + T * 2.0**-23 * dz.abs().sum(0)
+    return (dx, dw, db), (rounded(dx, ex, dt), rounded(dw, ew, dt), rounded(db, eb, dt))
+
+
+# ------------------------------------------------------------------------------------------ 8-bit rows
+
+
+def linear_q8(x, xs, w, ws, bias, residual, kind, dt):
+    """y and its bound in float64: the products are exact, an fp32 sum of K of them is off by K 2^-23 of their magnitudes."""
+    K = x.shape[1]
+    X, W = x.float().double(), w.float().double()
+    scale = torch.outer(xs.double(), ws.double())
+    z, ez = (X @ W.T) * scale, (K * 2.0**-23 + 2.0**-22) * (X.abs() @ W.abs().T) * scale
+    if bias is not None:
+        z = z + bias.double()
+        ez = ez + 2.0**-23 * (z.abs() + bias.double().abs())
+    y = rows.act(z, kind)
+    ey = rows.LIPSCHITZ * ez + (rows.ACT_ERR * z.abs() if kind in ("gelu", "silu") else 0)
+    if residual is not None:
+        y = y + residual.double()
+        ey = ey + 2.0**-23 * (residual.double().abs() + y.abs())
+    return y, rounded(y, ey, dt)
+
+
+# ------------------------------------------------------------------------------------------ distillation
+
+
+def targets(idx, values, temperature, V):
+    """(Q [T, V] float64: the teacher's probabilities, its entropy's terms q ln q summed, rows with a target)."""
+    there = (idx >= 0) & ~torch.isneginf(values)
+    v = torch.where(there, values.double() / temperature, float("-inf"))
+    has = there.any(1)
+    q = torch.where(has[:, None] & there, torch.softmax(torch.where(has[:, None], v, 0.0), 1), 0.0)
+    Q = torch.zeros(idx.shape[0], V, dtype=torch.float64, device=idx.device).scatter_add_(1, idx.clamp(0, V - 1), q)
+    return q, Q, has
+
+
+def _share_error(idx, values, temperature):
+    """Of a q, relative: the exponential's, its argument's and the division's."""
+    there = (idx >= 0) & ~torch.isneginf(values)
+    return 2.0**-20 + 2.0**-21 * torch.where(there, values.double().abs() / temperature, 0.0).amax(1)
+
+
+def distill(x, w, idx, values, bias, temperature):
+    """(loss, lse), (their bounds) in float64; rows without a target zero."""
+    V = w.shape[0]
+    z, dz = rows.logits(x, w, bias)
+    z, dz = z / temperature, dz / temperature
+    q, _, has = targets(idx, values, temperature, V)
+    lse = torch.logsumexp(z, 1)
+    logp = (z - lse[:, None]).gather(1, idx.clamp(0, V - 1))
+    gap = torch.where(q > 0, torch.log(q.clamp(min=1e-300)) - logp, 0.0)
+    loss = (q * gap).sum(1)
+    el = dz.max(1).values * 2 + (z.abs().max(1).values + 1) * 2.0**-21 + (64 + V / 32) * 2.0**-23 + 2.0**-22 * lse.abs()
+    far = (z.abs().max(1).values + lse.abs())
+    eloss = el + dz.max(1).values + (q * (gap.abs() + 1)).sum(1) * (_share_error(idx, values, temperature) + 2.0**-20) + 2.0**-21 * far
+    return (loss * has, lse * has), (eloss * has, el * has)
+
+
+def distill_backward(x, w, idx, values, lse, dloss, bias, temperature):
+    """(dx, dw, db), (their bounds) in float64, for the lse that is given."""
+    dt, (T, D), V = x.dtype, x.shape, w.shape[0]
+    z, dz = rows.logits(x, w, bias)
+    z, dz = z / temperature, dz / temperature
+    _, Q, has = targets(idx, values, temperature, V)
+    p = torch.exp(z - lse.double()[:, None])
+    g = (dloss.double() / temperature)[:, None]
+    d = torch.where(has[:, None], (p - Q) * g, 0.0)
+    e = p * (dz + (z.abs() + lse.double().abs()[:, None] + 2) * 2.0**-21) + Q * _share_error(idx, values, temperature)[:, None]
+    # (an exponential below fp32's smallest normal number comes as 0: off by 2^-126 at most)
+    e = torch.where(has[:, None], (e + 2.0**-126) * g.abs() + 2.0**-22 * (p + Q) * g.abs(), 0.0)
+    free = e.clone()
+    if dt != torch.float32:
+        e = e + U[dt] * (d.abs() + e)
+    if dt == torch.float16 and bool(has.any()):
+        # dz is scaled by a power of two that brings the largest |dloss| / temperature to at least 2^14
+        e = e + has[:, None] * 2.0**-25 * g[has].abs().max() * 2.0**-14
+    X, W = x.double(), w.double()
+    dx, dw, db = d @ W, d.T @ X, d.sum(0)
+    ex = e @ W.abs() + 2 * rows.sum_bound(V, dt) * ((d.abs() + e) @ W.abs())
+    ew = e.T @ X.abs() + rows.sum_bound(T, dt) * ((d.abs() + e).T @ X.abs())
+    eb = free.sum(0) + T * 2.0**-23 * d.abs().sum(0)
+    return (dx, dw, db), (rounded(dx, ex, dt), rounded(dw, ew, dt), rounded(db, eb, dt))
