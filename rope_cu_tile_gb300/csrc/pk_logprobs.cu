@@ -25,7 +25,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxTop = PK_LOGPROBS_MAX_TOP;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kShort = 1024;  // words: up to here a row belongs to a warp and lies in its registers
 constexpr int kCap = 1024;    // candidates of a block
 constexpr int kAnywhere = 0x7ffffffe;  // of a maximum: some chunk of the thread's
 
@@ -128,14 +127,15 @@ __device__ __forceinline__ void raise(Stat& a, float m) {
   a.s *= c;
   a.m = m;
 }
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m);
-  raise(a, m);
-  raise(b, m);
-  return {m, a.s + b.s, a.u + b.u};
+// The largest of eight values as they were loaded: of 16-bit ones a pair at a time, the pair that holds it.
+template <int DT>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  if constexpr (DT == PK_BF16)
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  else
+    asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
 }
-
-// The largest of eight values as they were loaded: of 16-bit ones two at a time.
 template <int DT>
 __device__ __forceinline__ float top8(const Raw8<DT>& q) {
   if constexpr (DT == PK_F32) {
@@ -143,16 +143,8 @@ __device__ __forceinline__ float top8(const Raw8<DT>& q) {
     q.get(v);
     return fmaxf(attn::fmax3(v[0], v[1], v[2]), attn::fmax3(attn::fmax3(v[3], v[4], v[5]), v[6], v[7]));
   } else {
-    uint32_t m = q.q[0].x;
-    const uint32_t w[3] = {q.q[0].y, q.q[0].z, q.q[0].w};
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      if constexpr (DT == PK_BF16)
-        asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-      else
-        asm("max.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
-    }
-    const float2 f = Elem<DT == PK_BF16>::unpack(m);
+    const float2 f = Elem<DT == PK_BF16>::unpack(
+        max_pair<DT>(max_pair<DT>(q.q[0].x, q.q[0].y), max_pair<DT>(q.q[0].z, q.q[0].w)));
     return fmaxf(f.x, f.y);
   }
 }
@@ -175,11 +167,50 @@ __device__ __forceinline__ void accumulate(Stat& a, const Raw8<DT>& q) {
   a.u += u.x + u.y;
 }
 
+// The same for 16-bit values with fewer instructions: a value that is far below the maximum, -inf among them, is raised as a
+// pair to one that is still far enough below it, and the maximum taken off as the value is unpacked. That floor has to
+// lie apart from the maximum and above the type's lowest number: far_pair says whether it does (a maximum past -10^38, or
+// -50000 of fp16, is taken by `accumulate`).
+template <int DT>
+__device__ __forceinline__ bool far_pair(float m, uint32_t& pair) {
+  const float f = m - 300.0f - 0.125f * fabsf(m);
+  pair = Elem<DT == PK_BF16>::pack(f, f);
+  return m > (DT == PK_BF16 ? -1.0e38f : -5.0e4f);
+}
+template <int DT>
+__device__ __forceinline__ void accumulate_near(Stat& a, const Raw8<DT>& q, uint32_t far) {
+  using E = Elem<DT == PK_BF16>;
+  constexpr uint32_t kOnes = DT == PK_BF16 ? 0x3F803F80u : 0x3C003C00u;
+  const uint32_t w[4] = {q.q[0].x, q.q[0].y, q.q[0].z, q.q[0].w};
+  float2 s = make_float2(a.s, 0.0f), u = make_float2(a.u, 0.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t z = w[i];
+    if constexpr (DT == PK_BF16)
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(z) : "r"(far));
+    else
+      asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(z) : "r"(far));
+    const float2 d = make_float2(E::fma_lo(z, kOnes, -a.m), E::fma_hi(z, kOnes, -a.m));
+    const float2 p = mul2(d, make_float2(kLog2e, kLog2e));
+    const float2 e = make_float2(attn::ex2(p.x), attn::ex2(p.y));
+    add2(s.x, s.y, e);
+    u = fma2(e, d, u);
+  }
+  a.s = s.x + s.y;
+  a.u = u.x + u.y;
+}
+
+// The largest of a warp's values (none of them NaN).
+__device__ __forceinline__ float warp_max(float v) {
+  const int b = __float_as_int(v), k = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
 __device__ __forceinline__ Stat warp_join(Stat a) {
+  raise(a, warp_max(a.m));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.u, o)};
-    a = join(a, b);
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+    a.u += __shfl_xor_sync(0xffffffffu, a.u, o);
   }
   return a;
 }
@@ -203,76 +234,7 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
 }
 
 // ------------------------------------------------------------------------------------
-// short rows: a warp each, the elements in registers; the likeliest by repeated maxima
-
-template <int DT>
-__global__ void __launch_bounds__(kThreads) pk_logprobs_short_kernel(const __grid_constant__ LogprobArgs a) {
-  const int lane = threadIdx.x & 31;
-  griddep_wait();
-  for (int64_t row = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5); row < a.T;
-       row += static_cast<int64_t>(gridDim.x) * kWarps) {
-    constexpr int kC = kShort / 256 + 1;  // chunks of a lane: one more for a row that begins inside 16 bytes
-    const Row r = row_at<DT>(a.z, row * a.ld, a.V);
-    const long long label = __ldcg(a.labels + row);
-    float picked = 0.0f;
-    if (label >= 0 && label < a.V) picked = Ty<DT>::get(r.p, label);
-    Raw8<DT> q[kC];
-    float v[8];
-    Stat st = nothing();
-#pragma unroll
-    for (int i = 0; i < kC; ++i)
-      if (i * 32 + lane < r.chunks) fetch<DT>(q[i], r, i * 32 + lane, a.V);
-#pragma unroll
-    for (int i = 0; i < kC; ++i)
-      if (i * 32 + lane < r.chunks) {
-        raise(st, fmaxf(st.m, top8<DT>(q[i])));
-        accumulate<DT>(st, q[i]);
-      }
-    st = warp_join(st);
-    if (lane == 0) write_row<DT>(a, row, st, picked, label);
-    if (a.top == 0) continue;
-    // `best`: this lane's likeliest element that has not been taken, and its index; past the last one taken
-    const float rest = logf(st.s);
-    uint32_t last_key = 0xFFFFFFFFu;
-    int last_idx = -1;
-    const auto find = [&](uint32_t& key, int& idx) {
-      key = 0;
-      idx = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < kC; ++i)
-        if (i * 32 + lane < r.chunks) {
-          q[i].get(v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int c = (i * 32 + lane) * 8 - r.off + j;
-            const uint32_t k = key_of<DT>(v[j]);
-            const bool left = k < last_key || (k == last_key && c > last_idx);
-            if (c >= 0 && c < a.V && left && (k > key || idx == 0x7fffffff)) {
-              key = k;
-              idx = c;
-            }
-          }
-        }
-    };
-    uint32_t key;
-    int idx;
-    find(key, idx);
-    for (int n = 0; n < a.top; ++n) {
-      const uint32_t most = __reduce_max_sync(0xffffffffu, idx == 0x7fffffff ? 0u : key);
-      const int at = __reduce_min_sync(0xffffffffu, key == most ? idx : 0x7fffffff);
-      if (lane == 0) {
-        a.top_logp[row * a.top + n] = logp_of(st, rest, of_key<DT>(most));
-        a.top_idx[row * a.top + n] = at;
-      }
-      last_key = most;
-      last_idx = at;
-      if (idx == at) find(key, idx);
-    }
-  }
-}
-
-// ------------------------------------------------------------------------------------
-// longer rows: a block, or a cluster of blocks where there are few rows
+// short rows: a warp each, the row in shared memory, kC chunks a lane, which reads back what it asked for itself
 
 struct Candidate {
   uint32_t key;
@@ -282,124 +244,370 @@ __device__ __forceinline__ bool before(const Candidate& x, const Candidate& y) {
   return x.key > y.key || (x.key == y.key && x.idx < y.idx);
 }
 
+constexpr int kWarpCap = 128;  // candidates of a warp
+
+// A bound that `top` of a warp's keys, N a lane, reach, and as few more as can be: the top-th largest of them, or one below
+// it that no other reaches; found a bit at a time. 0 where there are not as many above 0.
+template <int DT, int N>
+__device__ __forceinline__ uint32_t warp_nth(const uint32_t (&k)[N], int top) {
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (int b = 31 - kKeyShift<DT>; b >= 0; --b) {
+    const uint32_t probe = bound | 1u << b;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += k[i] >= probe ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n >= top) bound = probe;
+    if (n == top) break;
+  }
+  return bound;
+}
+
+template <int DT, int kC>
+constexpr int kShortBytes = kWarps * kC * 32 * 8 * Ty<DT>::kBytes;
+
+template <int DT, int kC>
+__global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_kernel(const __grid_constant__ LogprobArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Candidate cand[kWarps][kWarpCap];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  constexpr int kPieces = Ty<DT>::kBytes / 2;  // of 16 bytes a chunk
+  uint4* const mine = reinterpret_cast<uint4*>(smem) + w * (kC * 32 * kPieces) + lane;
+  const auto chunk_at = [&](int i) {
+    Raw8<DT> q;
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) q.q[p] = mine[(i * kPieces + p) * 32];
+    return q;
+  };
+  griddep_wait();
+  for (int64_t row = blockIdx.x * static_cast<int64_t>(kWarps) + w; row < a.T; row += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const Row r = row_at<DT>(a.z, row * a.ld, a.V);
+    const int n_mine = (r.chunks - lane + 31) / 32;  // chunks of this lane
+#pragma unroll 4
+    for (int i = 0; i < n_mine; ++i) {
+      const int chunk = i * 32 + lane;
+      if (whole<DT>(r, chunk, a.V)) {
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(mine + (i * kPieces + p) * 32)),
+                       "l"(r.p + (static_cast<int64_t>(chunk) * 8 - r.off) * Ty<DT>::kBytes + 16 * p)
+                       : "memory");
+      } else {
+        Raw8<DT> q;
+        fetch<DT>(q, r, chunk, a.V);
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) mine[(i * kPieces + p) * 32] = q.q[p];
+      }
+    }
+    const long long label = __ldcg(a.labels + row);
+    float picked = 0.0f;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // the maxima of the chunks, or of pairs where the row has few chunks: each of another element
+    constexpr int kFine = kC <= 3 ? 4 : 1;
+    uint32_t key[kC * kFine];
+    Stat st = nothing();
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const bool here = i < n_mine;
+      Raw8<DT> q;
+      float m = -INFINITY;
+      if (here) {
+        q = chunk_at(i);
+        m = top8<DT>(q);
+        st.m = fmaxf(st.m, m);
+      }
+      if constexpr (kFine == 1) {
+        key[i] = here ? key_of<DT>(m) : 0u;
+      } else {
+        float v[8];
+        q.get(v);
+        const int c = (i * 32 + lane) * 8 - r.off;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool some = here && c + 2 * j + 1 >= 0 && c + 2 * j < a.V;
+          key[4 * i + j] = some ? key_of<DT>(fmaxf(v[2 * j], v[2 * j + 1])) : 0u;
+        }
+      }
+    }
+    raise(st, warp_max(st.m));
+    uint32_t far = 0;
+    bool near = false;
+    if constexpr (DT != PK_F32) near = far_pair<DT>(st.m, far);
+#pragma unroll 1
+    for (int i = 0; i < n_mine; ++i) {
+      if constexpr (DT != PK_F32) {
+        if (near) {
+          accumulate_near<DT>(st, chunk_at(i), far);
+          continue;
+        }
+      }
+      accumulate<DT>(st, chunk_at(i));
+    }
+    st = warp_join(st);
+    if (label >= 0 && label < a.V) picked = Ty<DT>::get(r.p, label);
+    if (lane == 0) write_row<DT>(a, row, st, picked, label);
+    if (a.top == 0) continue;
+
+    Candidate* out = cand[w];
+    const auto inside = [&](int e) { return e >= 0 && e < a.V; };
+    __syncwarp();  // (the row before has been written out)
+    int n = kWarpCap + 1;
+    if (st.s == st.s) {
+      // elements whose key reaches the bound: counted, then kept, perhaps not all of them
+      const uint32_t bound = warp_nth<DT>(key, a.top);
+      const auto each = [&](auto take) {
+#pragma unroll 1
+        for (int i = 0; i < n_mine; ++i) {
+          const Raw8<DT> q = chunk_at(i);
+          if (key_of<DT>(top8<DT>(q)) < bound) continue;
+          float v[8];
+          q.get(v);
+          const int c = (i * 32 + lane) * 8 - r.off;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t k = key_of<DT>(v[j]);
+            if (k >= bound && inside(c + j)) take(k, c + j);
+          }
+        }
+      };
+      int at = 0;
+      each([&](uint32_t, int) { ++at; });
+      int upto = at;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      n = __shfl_sync(0xffffffffu, upto, 31);
+      at = upto - at;
+      if (n <= kWarpCap) each([&](uint32_t k, int e) { out[at++] = {k, e}; });
+      __syncwarp();
+    }
+    if (n > kWarpCap) {
+      // many equal ones, or a NaN, which no maximum shows: the top-th largest of all elements, those above it, and of those
+      // equal to it the first
+      uint32_t bound = 0;
+#pragma unroll 1
+      for (int b = 31 - kKeyShift<DT>; b >= 0; --b) {
+        const uint32_t probe = bound | 1u << b;
+        int m = 0;
+#pragma unroll 1
+        for (int i = 0; i < n_mine; ++i) {
+          float v[8];
+          chunk_at(i).get(v);
+          const int c = (i * 32 + lane) * 8 - r.off;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m += key_of<DT>(v[j]) >= probe && inside(c + j) ? 1 : 0;
+        }
+        if (static_cast<int>(__reduce_add_sync(0xffffffffu, m)) >= a.top) bound = probe;
+      }
+      __syncwarp();
+      int taken = 0;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+        for (int i = 0; i * 32 < r.chunks; ++i) {
+          // this lane's elements of the kind, and where they stand among the warp's
+          const int c = (i * 32 + lane) * 8 - r.off;
+          float v[8];
+          uint32_t bits = 0;
+          if (i < n_mine) {
+            chunk_at(i).get(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t k = key_of<DT>(v[j]);
+              bits |= inside(c + j) && (pass == 0 ? k > bound : k == bound) ? 1u << j : 0u;
+            }
+          }
+          int upto = __popc(bits);
+#pragma unroll
+          for (int o = 1; o < 32; o *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+          }
+          int at = taken + upto - __popc(bits);
+          taken += __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (bits >> j & 1u) {
+              if (at < a.top) out[at] = {key_of<DT>(v[j]), c + j};
+              ++at;
+            }
+        }
+      __syncwarp();
+      n = a.top;
+    }
+    // ranked by how many stand before each
+    const float rest = logf(st.s);
+    for (int i = lane; i < n; i += 32) {
+      const Candidate x = out[i];
+      int at = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) at += before(out[j], x) ? 1 : 0;
+      if (at < a.top) {
+        a.top_logp[row * a.top + at] = logp_of(st, rest, of_key<DT>(x.key));
+        a.top_idx[row * a.top + at] = x.idx;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// longer rows: a block, or a cluster of blocks where there are few rows
+
+template <int kT>
 struct LogprobShared {
-  Stat stat[kWarps];
+  Stat stat[kT / 32];
   Stat mine;               // of the block's slice, read by the cluster's first block
-  uint32_t maxima[kThreads];
-  int chunk[kThreads];     // where each thread's maximum stands
-  int list[kThreads];      // threads whose elements are candidates
+  uint32_t maxima[kT];
+  int chunk[kT];           // where each thread's maximum stands
+  int list[kT];            // threads whose elements are candidates
   int listed, found;
   uint32_t bound;
   int bound_chunk;
   Candidate cand[kCap];
-  Candidate top[kMaxTop];  // the slice's likeliest, in order
-  Candidate pick[kWarps];
+  Candidate top[kMaxTop];  // of a slice: its likeliest, in order
+  Candidate pick[kT / 32];
 };
 
-// The candidates of the block's slice into sh.cand: elements whose key is above `bound`, or at it and in a chunk up to
-// `bound_chunk`. Their count (which may be past kCap) is returned in every thread.
+// Where the block's part of a row lies: chunks [c0, c1), of which those of [w0, w1) are whole. Thread t takes w0 + t, w0 + t + kT
+// and so on; a chunk that hangs over the row's first or last word is thread 0's or 1's besides.
+struct Slice {
+  Row r;
+  int c0, c1, w0, w1;
+};
 template <int DT>
-__device__ __forceinline__ int collect(LogprobShared& sh, const Row& r, int c0, int c1, int V, bool mine, uint32_t bound,
-                                       int bound_chunk) {
-  if (threadIdx.x == 0) sh.listed = sh.found = 0;
-  __syncthreads();
-  if (mine) sh.list[atomicAdd(&sh.listed, 1)] = threadIdx.x;
-  __syncthreads();
-  // the listed threads' chunks, shared out over all threads
-  const int each = (c1 - c0 + kThreads - 1) / kThreads, n = sh.listed * each;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int k = i / each, c = c0 + sh.list[k] + (i - k * each) * kThreads;
-    if (c >= c1 || *reinterpret_cast<volatile int*>(&sh.found) > kCap) continue;  // (too many already)
-    Raw8<DT> q;
-    fetch<DT>(q, r, c, V);
+__device__ __forceinline__ Slice slice_at(const LogprobArgs& a, int64_t row, int part, int parts) {
+  Slice s;
+  s.r = row_at<DT>(a.z, row * a.ld, a.V);
+  const int per = (s.r.chunks + parts - 1) / parts;
+  s.c0 = part * per;
+  s.c1 = min(s.c0 + per, s.r.chunks);
+  s.w0 = s.c0 + (s.c0 == 0 && s.r.off > 0 ? 1 : 0);
+  s.w1 = s.c1 - (s.c1 == s.r.chunks && !whole<DT>(s.r, s.c1 - 1, a.V) ? 1 : 0);
+  return s;
+}
+// the chunk that hangs over which thread t has, or -1
+__device__ __forceinline__ int edge_of(const Slice& s, int t) {
+  return t == 0 ? (s.w0 > s.c0 ? s.c0 : -1) : t == 1 ? (s.w1 < s.c1 ? s.w1 : -1) : -1;
+}
+
+// The candidates of the listed threads' chunks into sh.cand: elements whose key is above `bound`, or at it and in a chunk up to
+// `last`. Their count (which may be past kCap) is returned in every thread.
+template <int DT, int kT>
+__device__ __forceinline__ int collect(LogprobShared<kT>& sh, const Slice& s, int V, uint32_t bound, int last) {
+  const auto look = [&](const Raw8<DT>& q, int c) {
     float v[8];
     q.get(v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t x = key_of<DT>(v[j]);
-      const int e = c * 8 - r.off + j;
-      if ((x > bound || (x == bound && c <= bound_chunk)) && e >= 0 && e < V) {
+      const int e = c * 8 - s.r.off + j;
+      if ((x > bound || (x == bound && c <= last)) && e >= 0 && e < V) {
         const int at = atomicAdd(&sh.found, 1);
         if (at < kCap) sh.cand[at] = {x, e};
       }
     }
+  };
+  const int each = (s.w1 - s.w0 + kT - 1) / kT, n = sh.listed * each;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kT) {
+    const int k = i / each, c = s.w0 + sh.list[k] + (i - k * each) * kT;
+    if (c >= s.w1 || *reinterpret_cast<volatile int*>(&sh.found) > kCap) continue;  // (too many already)
+    Raw8<DT> q;
+    q.load(s.r.p, c * 8 - s.r.off, true, 8);
+    look(q, c);
+  }
+  const int edge = edge_of(s, threadIdx.x);
+  if (edge >= 0) {
+    Raw8<DT> q;
+    fetch<DT>(q, s.r, edge, V);
+    look(q, edge);
   }
   __syncthreads();
   return sh.found;
 }
 
-// The first `top` of sh.cand[0 .. n) in order, by counting for each how many stand before it.
-__device__ __forceinline__ void rank(const Candidate* cand, int n, Candidate* out, int top) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+// The likeliest of sh.cand[0 .. n) handed to `emit` with their places: a warp counts what stands before a candidate.
+template <int kT, class Emit>
+__device__ __forceinline__ void rank(const Candidate* cand, int n, int top, const Emit& emit) {
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < n; i += kT / 32) {
     const Candidate x = cand[i];
     int at = 0;
-    for (int j = 0; j < n; ++j) at += before(cand[j], x) ? 1 : 0;
-    if (at < top) out[at] = x;
+    for (int j = lane; j < n; j += 32) at += before(cand[j], x) ? 1 : 0;
+    at = __reduce_add_sync(0xffffffffu, at);
+    if (lane == 0 && at < top) emit(at, x);
   }
 }
 
-// The slice's `top` likeliest words into sh.top; how many there are (fewer in a slice with fewer words).
-template <int DT>
-__device__ __forceinline__ int slice_top(LogprobShared& sh, const Row& r, int c0, int c1, int V, int top, uint32_t key, int chunk,
-                                         bool any) {
-  constexpr int kBits = 32 - kKeyShift<DT>;
+// The slice's `top` likeliest words to `emit`. Every thread has a chunk of the slice; sh.maxima, sh.chunk are written, and the
+// block synchronized.
+template <int DT, int kT, class Emit>
+__device__ __forceinline__ void slice_top(LogprobShared<kT>& sh, const Slice& s, int V, int top, const Emit& emit) {
   const int lane = threadIdx.x & 31;
-  sh.maxima[threadIdx.x] = any ? key : 0u;
-  sh.chunk[threadIdx.x] = any ? chunk : 0x7fffffff;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    // the top-th largest of the threads' maxima, a bit at a time (0 where there are not as many)
-    uint32_t k[kThreads / 32], bound = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) k[i] = sh.maxima[i * 32 + lane];
-#pragma unroll 1
-    for (int b = kBits - 1; b >= 0; --b) {
-      const uint32_t probe = bound | 1u << b;
-      int n = 0;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) n += k[i] >= probe ? 1 : 0;
-      if (__reduce_add_sync(0xffffffffu, n) >= top) bound = probe;
+  // warp 0 names the threads whose elements may be among them: of those whose maximum is the bound only the ones that stand no
+  // later than `last`
+  const auto name = [&](uint32_t bound, int last) {
+    int n = 0;
+    for (int i = 0; i < kT / 32; ++i) {
+      const uint32_t k = sh.maxima[i * 32 + lane];
+      const int c = sh.chunk[i * 32 + lane];
+      const bool is = k > bound || (k == bound && (c <= last || c == kAnywhere));
+      const uint32_t votes = __ballot_sync(0xffffffffu, is);
+      if (is) sh.list[n + __popc(votes & ((1u << lane) - 1u))] = i * 32 + lane;
+      n += __popc(votes);
     }
-    if (lane == 0) sh.bound = bound;
+    if (lane == 0) {
+      sh.listed = n;
+      sh.found = 0;
+      sh.bound = bound;
+      sh.bound_chunk = last;
+    }
+  };
+  if (threadIdx.x < 32) {
+    uint32_t k[kT / 32];
+#pragma unroll
+    for (int i = 0; i < kT / 32; ++i) k[i] = sh.maxima[i * 32 + lane];
+    name(warp_nth<DT>(k, top), 0x7fffffff);
   }
   __syncthreads();
   const uint32_t bound = sh.bound;
-  int n = collect<DT>(sh, r, c0, c1, V, any && key >= bound, bound, 0x7fffffff);
+  int n = collect<DT, kT>(sh, s, V, bound, 0x7fffffff);
   if (n > kCap) {
     // many equal ones (a masked vocabulary): of those at the bound only the first chunks', up to the one that completes `top`
+    __syncthreads();
     if (threadIdx.x < 32) {
       int at = 0;
 #pragma unroll 1
-      for (int b = 17; b >= 0; --b) {  // the largest chunk at which there are still fewer than `top`
+      for (int b = 17; b >= 0; --b) {  // the largest chunk before which there are still fewer than `top`
         const int probe = at | 1 << b;
         int m = 0;
-        for (int i = lane; i < kThreads; i += 32) m += sh.maxima[i] > bound || (sh.maxima[i] == bound && sh.chunk[i] < probe) ? 1 : 0;
+        for (int i = lane; i < kT; i += 32) m += sh.maxima[i] > bound || (sh.maxima[i] == bound && sh.chunk[i] < probe) ? 1 : 0;
         if (__reduce_add_sync(0xffffffffu, m) < top) at = probe;
       }
-      if (lane == 0) sh.bound_chunk = at;
+      name(bound, at);
     }
     __syncthreads();
-    const int last = sh.bound_chunk;
-    n = collect<DT>(sh, r, c0, c1, V, any && (key > bound || (key == bound && (chunk <= last || chunk == kAnywhere))), bound, last);
+    n = collect<DT, kT>(sh, s, V, bound, sh.bound_chunk);
   }
   if (n <= kCap) {
-    rank(sh.cand, n, sh.top, top);
-    __syncthreads();
-    return min(n, top);
+    rank<kT>(sh.cand, n, top, emit);
+    return;
   }
   // many large ones in few threads: one maximum after another
   Candidate done = {0xFFFFFFFFu, -1};
   for (int i = 0; i < top; ++i) {
     Candidate best = {0u, 0x7fffffff};
-    for (int c = c0 + threadIdx.x; c < c1; c += kThreads) {
+    for (int c = s.c0 + threadIdx.x; c < s.c1; c += kT) {
       Raw8<DT> q;
-      fetch<DT>(q, r, c, V);
+      fetch<DT>(q, s.r, c, V);
       float v[8];
       q.get(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const Candidate x = {key_of<DT>(v[j]), c * 8 - r.off + j};
+        const Candidate x = {key_of<DT>(v[j]), c * 8 - s.r.off + j};
         if (x.idx >= 0 && x.idx < V && before(done, x) && before(x, best)) best = x;
       }
     }
@@ -408,12 +616,11 @@ __device__ __forceinline__ int slice_top(LogprobShared& sh, const Row& r, int c0
     if (lane == 0) sh.pick[threadIdx.x >> 5] = {most, at};
     __syncthreads();
     done = sh.pick[0];
-    for (int k = 1; k < kWarps; ++k)
+    for (int k = 1; k < kT / 32; ++k)
       if (before(sh.pick[k], done)) done = sh.pick[k];
-    if (threadIdx.x == 0) sh.top[i] = done;
+    if (threadIdx.x == 0) emit(i, done);
     __syncthreads();
   }
-  return top;
 }
 
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) { return gemm::mapa(smem_u32(p), rank); }
@@ -423,107 +630,122 @@ __device__ __forceinline__ uint32_t ld_remote(uint32_t addr) {
   return v;
 }
 
-constexpr int kBatch = 2;  // chunks that a thread takes together, with as many on their way
+constexpr int kBatch = 4;  // chunks that a thread has in flight
 
-template <int DT, bool kCluster>
-__global__ void __launch_bounds__(kThreads, DT == PK_F32 ? 4 : 5) pk_logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
-  __shared__ LogprobShared sh;
+// Bound by the bytes of z where rows are long, with 1280 threads an SM (1024 of fp32) and four loads each in flight, as far as
+// instructions go (some 50 for eight 16-bit values); by the way from a row's last load to its last output where they are not.
+template <int DT, int kT, bool kCluster>
+__global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : 1280) / kT) pk_logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
+  __shared__ LogprobShared<kT> sh;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int part = kCluster ? static_cast<int>(gemm::cluster_rank()) : 0;
   const int64_t row = kCluster ? blockIdx.x / parts : blockIdx.x;
   griddep_wait();
-  const Row r = row_at<DT>(a.z, row * a.ld, a.V);
-  const int per = kCluster ? (r.chunks + parts - 1) / parts : r.chunks;
-  const int c0 = part * per, c1 = min(c0 + per, r.chunks);
+  const Slice sl = slice_at<DT>(a, row, part, kCluster ? parts : 1);
   long long label = -1;
   float picked = 0.0f;
-  if (threadIdx.x == 0 && part == 0) {
-    label = __ldcg(a.labels + row);
-    if (label >= 0 && label < a.V) picked = Ty<DT>::get(r.p, label);
-  }
+  if (threadIdx.x == 0 && part == 0) label = __ldcg(a.labels + row);
   Stat st = nothing();
-  int at = c0 + threadIdx.x;  // the chunk of the maximum
-  const bool any = at < c1;
-  // the next chunks are asked for before these are used
-  Raw8<DT> q[kBatch], ahead[kBatch];
-  const auto load = [&](Raw8<DT>(&r8)[kBatch], int c) {
+  int at = sl.w0 + threadIdx.x;  // the chunk of the maximum
+  // `kN` chunks from c on, kT apart
+  const auto take = [&](const auto& q, int c) {
+    constexpr int kN = sizeof(q) / sizeof(Raw8<DT>);
+    float top[kN], m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (c + i * kThreads < c1) fetch<DT>(r8[i], r, c + i * kThreads, a.V);
+    for (int i = 0; i < kN; ++i) {
+      top[i] = top8<DT>(q[i]);
+      m = fmaxf(m, top[i]);
+    }
+    // (no sum so far: the lowest number, where the maximum starts, is then news too)
+    if (m > st.m || (st.s == 0.0f && m == st.m)) {
+#pragma unroll
+      for (int i = kN - 1; i >= 0; --i) at = top[i] == m ? c + i * kT : at;
+    }
+    raise(st, fmaxf(st.m, m));
+    if constexpr (DT != PK_F32) {
+      uint32_t far;
+      if (far_pair<DT>(st.m, far)) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) accumulate_near<DT>(st, q[i], far);
+        return;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) accumulate<DT>(st, q[i]);
   };
-  load(q, c0 + threadIdx.x);
+  int c = sl.w0 + threadIdx.x;
 #pragma unroll 1
-  for (int c = c0 + threadIdx.x; c < c1; c += kBatch * kThreads) {
-    load(ahead, c + kBatch * kThreads);
-    float m = st.m;
-    bool none = st.s == 0.0f;  // (so far: the lowest number is then larger than what there was, though not than m)
+  for (; c + (kBatch - 1) * kT < sl.w1; c += kBatch * kT) {
+    Raw8<DT> q[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float top = c + i * kThreads < c1 ? top8<DT>(q[i]) : -INFINITY;
-      const bool larger = top > m || (none && top == m);
-      at = larger ? c + i * kThreads : at;
-      none = none && !larger;
-      m = fmaxf(m, top);
-    }
-    raise(st, m);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (c + i * kThreads < c1) accumulate<DT>(st, q[i]);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) q[i] = ahead[i];
+    for (int i = 0; i < kBatch; ++i) q[i].load(sl.r.p, (c + i * kT) * 8 - sl.r.off, true, 8);
+    take(q, c);
   }
-  // (a sum without a value: one of the thread's elements is infinite or NaN, so at least infinity, in a chunk unknown. No sum at
-  // all: every element is -inf, the first of them in its first chunk)
-  const bool nan = st.s != st.s;
-  const uint32_t key = key_of<DT>(nan ? INFINITY : st.s == 0.0f ? -INFINITY : st.m);
-  if (nan) at = kAnywhere;
-  const Stat ws = warp_join(st);
-  if (lane == 0) sh.stat[w] = ws;
-  int n = 0;
+#pragma unroll 1
+  for (; c < sl.w1; c += kT) {
+    Raw8<DT> q[1];
+    q[0].load(sl.r.p, c * 8 - sl.r.off, true, 8);
+    take(q, c);
+  }
+  const int edge = edge_of(sl, threadIdx.x);
+  if (edge >= 0) {
+    Raw8<DT> q[1];
+    fetch<DT>(q[0], sl.r, edge, a.V);
+    take(q, edge);
+  }
+  if (label >= 0 && label < a.V) picked = Ty<DT>::get(sl.r.p, label);  // (asked for here, used below)
+  if (a.top > 0) {
+    // (a sum without a value: one of the thread's elements is infinite or NaN, so at least infinity, in a chunk unknown. No sum
+    // at all: every element is -inf, the first of them in its first chunk)
+    const bool nan = st.s != st.s;
+    sh.maxima[threadIdx.x] = key_of<DT>(nan ? INFINITY : st.s == 0.0f ? -INFINITY : st.m);
+    sh.chunk[threadIdx.x] = nan ? kAnywhere : at;
+  }
+  st = warp_join(st);
+  if (lane == 0) sh.stat[w] = st;
   __syncthreads();
-  if (a.top > 0) n = slice_top<DT>(sh, r, c0, c1, a.V, min(a.top, max(0, min(a.V, c1 * 8 - r.off) - max(0, c0 * 8 - r.off))), key, at, any);
-  st = sh.stat[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) st = join(st, sh.stat[i]);
-  const Candidate* top = sh.top;
-  if constexpr (kCluster) {
-    if (threadIdx.x == 0) {
-      sh.mine = st;
-      sh.found = n;
-    }
+  st = nothing();
+  if (lane < kT / 32) st = sh.stat[lane];
+  st = warp_join(st);
+  if constexpr (!kCluster) {
+    if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
+    if (a.top == 0) return;
+    const float rest = logf(st.s);
+    slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, const Candidate& x) {
+      a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(x.key));
+      a.top_idx[row * a.top + i] = x.idx;
+    });
+  } else {
+    if (a.top > 0) slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, const Candidate& x) { sh.top[i] = x; });
+    if (threadIdx.x == 0) sh.mine = st;
     gemm::cluster_sync();
     if (part == 0) {
-      // the slices' sums and likeliest words, in the order of the slices
-      int have = n;
-      for (int p = 1; p < parts; ++p) {
-        const uint32_t s = remote(&sh.mine, p);
-        const Stat b = {__uint_as_float(ld_remote(s)), __uint_as_float(ld_remote(s + 4)), __uint_as_float(ld_remote(s + 8))};
-        st = join(st, b);
-        if (a.top > 0) {
-          const int k = static_cast<int>(ld_remote(remote(&sh.found, p)));
-          const uint32_t t = remote(&sh.top[0], p);
-          for (int i = threadIdx.x; i < k; i += kThreads)
-            sh.cand[have + i] = {ld_remote(t + 8 * i), static_cast<int>(ld_remote(t + 8 * i + 4))};
-          have += k;
-        }
+      // the slices' sums and likeliest words, a warp a slice
+      st = nothing();
+      if (lane < parts) {
+        const uint32_t from = remote(&sh.mine, lane);
+        st = {__uint_as_float(ld_remote(from)), __uint_as_float(ld_remote(from + 4)), __uint_as_float(ld_remote(from + 8))};
       }
-      if (a.top > 0) {
-        for (int i = threadIdx.x; i < n; i += kThreads) sh.cand[i] = sh.top[i];
-        __syncthreads();
-        rank(sh.cand, have, sh.top, a.top);
-        __syncthreads();
+      for (int p = w; p < parts && a.top > 0; p += kT / 32) {
+        const uint32_t from = remote(&sh.top[0], p);
+        for (int i = lane; i < a.top; i += 32)
+          sh.cand[p * a.top + i] = {ld_remote(from + 8 * i), static_cast<int>(ld_remote(from + 8 * i + 4))};
       }
+      st = warp_join(st);
+      if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
+      __syncthreads();
+      const float rest = logf(st.s);
+      if (a.top > 0)
+        rank<kT>(sh.cand, parts * a.top, a.top, [&](int i, const Candidate& x) {
+          a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(x.key));
+          a.top_idx[row * a.top + i] = x.idx;
+        });
     }
     gemm::cluster_sync();  // (no block leaves while its memory is read)
-    if (part != 0) return;
-  }
-  if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
-  const float rest = logf(st.s);
-  for (int i = threadIdx.x; i < a.top; i += kThreads) {
-    a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(top[i].key));
-    a.top_idx[row * a.top + i] = top[i].idx;
   }
 }
+
+constexpr int kMiddle = 16384;  // words of a row of a block of 128 threads
 
 // Blocks a row: one where the rows fill the SMs, up to eight where they do not, none with fewer than 4096 words.
 int parts_of(int64_t T, int V, int sms) {
@@ -532,23 +754,43 @@ int parts_of(int64_t T, int V, int sms) {
   return parts;
 }
 
+// chunks of a lane of the longest row that belongs to a warp: 4345 words in 16 bits, 2301 in fp32, three blocks an SM
+template <int DT>
+constexpr int kMostChunks = DT == PK_F32 ? 9 : 17;
+
+template <int DT, int kC>
+cudaError_t short_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
+  const int64_t blocks = (a.T + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 8;
+  Launch l(blocks < most ? blocks : most, kThreads, stream);
+  l.cfg.dynamicSmemBytes = kShortBytes<DT, kC>;
+  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_short_kernel<DT, kC>, a);
+}
+
 template <int DT>
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
-  if (a.V <= kShort) {
-    const int64_t blocks = (a.T + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 8;
-    Launch l(blocks < most ? blocks : most, kThreads, stream);
-    return cudaLaunchKernelEx(&l.cfg, pk_logprobs_short_kernel<DT>, a);
-  }
+  // chunks of a row wherever it begins
+  const int chunks = static_cast<int>((static_cast<int64_t>(a.V) + 16 / Ty<DT>::kBytes - 1 + 7) / 8);
+  if (chunks <= 32 * 3) return short_launch<DT, 3>(a, sms, stream);
+  if (chunks <= 32 * 5) return short_launch<DT, 5>(a, sms, stream);
+  if (chunks <= 32 * kMostChunks<DT>) return short_launch<DT, kMostChunks<DT>>(a, sms, stream);
   const int parts = parts_of(a.T, a.V, sms);
-  Launch l(a.T * parts, kThreads, stream);
-  if (parts == 1) return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, false>, a, parts);
+  if (parts == 1) {
+    // (shorter rows take as long from their last load to their last output: twice the blocks then)
+    if (a.V <= kMiddle) {
+      Launch l(a.T, 128, stream);
+      return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 128, false>, a, 1);
+    }
+    Launch l(a.T, 256, stream);
+    return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 256, false>, a, 1);
+  }
+  Launch l(a.T * parts, 256, stream);
   cudaLaunchAttribute at[2] = {l.at[0], {}};
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim.x = parts;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   l.cfg.attrs = at;
   l.cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, true>, a, parts);
+  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 256, true>, a, parts);
 }
 
 // ------------------------------------------------------------------------------------
@@ -633,7 +875,24 @@ bool sizes_ok(int dtype, int64_t T, int V, int64_t ld) {
   return dtype_ok(dtype) && T >= 0 && T <= PK_ROWS_MAX_T && V >= 1 && V <= PK_ROWS_MAX_DIM && ld >= V;
 }
 
+template <int DT>
+cudaError_t prepare_short() {
+  constexpr int kC = kMostChunks<DT>;
+  const cudaError_t e = cudaFuncSetAttribute(pk_logprobs_short_kernel<DT, 5>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShortBytes<DT, 5>);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(pk_logprobs_short_kernel<DT, kC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShortBytes<DT, kC>);
+}
+
 }  // namespace
+
+namespace rows {
+cudaError_t prepare_logprobs() {
+  cudaError_t e;
+  if ((e = prepare_short<PK_F32>()) != cudaSuccess) return e;
+  if ((e = prepare_short<PK_BF16>()) != cudaSuccess) return e;
+  return prepare_short<PK_F16>();
+}
+}  // namespace rows
 
 }  // namespace pk
 
