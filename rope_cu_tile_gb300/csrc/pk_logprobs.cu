@@ -25,7 +25,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxTop = PK_LOGPROBS_MAX_TOP;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCap = 1024;    // candidates of a block
 constexpr int kAnywhere = 0x7ffffffe;  // of a maximum: some chunk of the thread's
 
 struct LogprobArgs {
@@ -236,14 +235,6 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
 // ------------------------------------------------------------------------------------
 // short rows: a warp each, the row in shared memory, kC chunks a lane, which reads back what it asked for itself
 
-struct Candidate {
-  uint32_t key;
-  int idx;
-};
-__device__ __forceinline__ bool before(const Candidate& x, const Candidate& y) {
-  return x.key > y.key || (x.key == y.key && x.idx < y.idx);
-}
-
 constexpr int kWarpCap = 128;  // candidates of a warp
 
 // A bound that `top` of a warp's keys, N a lane, reach, and as few more as can be: the top-th largest of them, or one below
@@ -264,13 +255,77 @@ __device__ __forceinline__ uint32_t warp_nth(const uint32_t (&k)[N], int top) {
   return bound;
 }
 
+// A candidate as one number, larger for one that stands before: the key, then the index downwards.
+__device__ __forceinline__ uint64_t packed(uint32_t key, int idx) { return static_cast<uint64_t>(key) << 32 | (0xFFFFFFFFu - idx); }
+
+// 32 kR numbers of a warp in descending order, number r 32 + lane in v[r]: a bitonic network, through shuffles within 32.
+template <int kR>
+__device__ __forceinline__ void warp_sort(uint64_t (&v)[kR], int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32 * kR; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j > 0; j /= 2) {
+      if (j >= 32) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+          if (!(r & (j / 32))) {
+            const int o = r | (j / 32);
+            const bool down = !((r * 32) & k);
+            const uint64_t hi = v[r] > v[o] ? v[r] : v[o], lo = v[r] > v[o] ? v[o] : v[r];
+            v[r] = down ? hi : lo;
+            v[o] = down ? lo : hi;
+          }
+      } else {
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const uint64_t u = __shfl_xor_sync(0xffffffffu, v[r], j);
+          const bool larger = !((r * 32 + lane) & k) == !(lane & j);
+          v[r] = (v[r] > u) == larger ? v[r] : u;
+        }
+      }
+    }
+}
+template <int kR, class Emit>
+__device__ __forceinline__ void sort_emit(const uint64_t* cand, int n, int top, int lane, const Emit& emit) {
+  uint64_t v[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) v[r] = r * 32 + lane < n ? cand[r * 32 + lane] : 0;
+  warp_sort<kR>(v, lane);
+#pragma unroll
+  for (int r = 0; r < kR; ++r)
+    if (r * 32 + lane < top) emit(r * 32 + lane, static_cast<uint32_t>(v[r] >> 32), static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(v[r])));
+}
+// The first `top` <= 64 of n <= 128 candidates handed to `emit` (place, key, index), by a warp.
+template <class Emit>
+__device__ __forceinline__ void first_of(const uint64_t* cand, int n, int top, int lane, const Emit& emit) {
+  if (n <= 32)
+    sort_emit<1>(cand, n, top, lane, emit);
+  else if (n <= 64)
+    sort_emit<2>(cand, n, top, lane, emit);
+  else
+    sort_emit<4>(cand, n, top, lane, emit);
+}
+
+// Eight values against a bound: bit j where v[j] is above it, or at it too where `at` says so. NaN is above.
+__device__ __forceinline__ uint32_t reach(const float (&v)[8], float bound, bool at) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bits |= (at ? !(v[j] < bound) : !(v[j] <= bound)) ? 1u << j : 0u;
+  return bits;
+}
+// the bits of the elements from `first` on that are of the row
+__device__ __forceinline__ uint32_t row_bits(int first, int V) {
+  const int lo = first < 0 ? -first : 0, hi = V - first < 8 ? V - first : 8;
+  return hi <= lo ? 0u : (0xFFu >> (8 - hi)) & (0xFFu << lo);
+}
+
 template <int DT, int kC>
 constexpr int kShortBytes = kWarps * kC * 32 * 8 * Ty<DT>::kBytes;
 
 template <int DT, int kC>
 __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_kernel(const __grid_constant__ LogprobArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ Candidate cand[kWarps][kWarpCap];
+  __shared__ uint64_t cand[kWarps][kWarpCap];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   constexpr int kPieces = Ty<DT>::kBytes / 2;  // of 16 bytes a chunk
   uint4* const mine = reinterpret_cast<uint4*>(smem) + w * (kC * 32 * kPieces) + lane;
@@ -349,30 +404,26 @@ __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_ke
     if (lane == 0) write_row<DT>(a, row, st, picked, label);
     if (a.top == 0) continue;
 
-    Candidate* out = cand[w];
+    uint64_t* out = cand[w];
     const auto inside = [&](int e) { return e >= 0 && e < a.V; };
     __syncwarp();  // (the row before has been written out)
     int n = kWarpCap + 1;
     if (st.s == st.s) {
       // elements whose key reaches the bound: counted, then kept, perhaps not all of them
-      const uint32_t bound = warp_nth<DT>(key, a.top);
-      const auto each = [&](auto take) {
+      const float bound = of_key<DT>(warp_nth<DT>(key, a.top));
+      const auto each = [&](const auto& take) {
 #pragma unroll 1
         for (int i = 0; i < n_mine; ++i) {
           const Raw8<DT> q = chunk_at(i);
-          if (key_of<DT>(top8<DT>(q)) < bound) continue;
+          if (top8<DT>(q) < bound) continue;
           float v[8];
           q.get(v);
           const int c = (i * 32 + lane) * 8 - r.off;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t k = key_of<DT>(v[j]);
-            if (k >= bound && inside(c + j)) take(k, c + j);
-          }
+          take(v, c, reach(v, bound, true) & row_bits(c, a.V));
         }
       };
       int at = 0;
-      each([&](uint32_t, int) { ++at; });
+      each([&](const float(&)[8], int, uint32_t bits) { at += __popc(bits); });
       int upto = at;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
@@ -381,7 +432,12 @@ __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_ke
       }
       n = __shfl_sync(0xffffffffu, upto, 31);
       at = upto - at;
-      if (n <= kWarpCap) each([&](uint32_t k, int e) { out[at++] = {k, e}; });
+      if (n <= kWarpCap)
+        each([&](const float(&v)[8], int c, uint32_t bits) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (bits >> j & 1u) out[at++] = packed(key_of<DT>(v[j]), c + j);
+        });
       __syncwarp();
     }
     if (n > kWarpCap) {
@@ -431,30 +487,27 @@ __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_ke
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (bits >> j & 1u) {
-              if (at < a.top) out[at] = {key_of<DT>(v[j]), c + j};
+              if (at < a.top) out[at] = packed(key_of<DT>(v[j]), c + j);
               ++at;
             }
         }
       __syncwarp();
       n = a.top;
     }
-    // ranked by how many stand before each
     const float rest = logf(st.s);
-    for (int i = lane; i < n; i += 32) {
-      const Candidate x = out[i];
-      int at = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) at += before(out[j], x) ? 1 : 0;
-      if (at < a.top) {
-        a.top_logp[row * a.top + at] = logp_of(st, rest, of_key<DT>(x.key));
-        a.top_idx[row * a.top + at] = x.idx;
-      }
-    }
+    first_of(out, n, a.top, lane, [&](int i, uint32_t k, int e) {
+      a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(k));
+      a.top_idx[row * a.top + i] = e;
+    });
   }
 }
 
 // ------------------------------------------------------------------------------------
 // longer rows: a block, or a cluster of blocks where there are few rows
+
+// candidates that a block keeps
+template <int kT>
+constexpr int kCap = kT >= 256 ? 1024 : 512;
 
 template <int kT>
 struct LogprobShared {
@@ -466,9 +519,9 @@ struct LogprobShared {
   int listed, found;
   uint32_t bound;
   int bound_chunk;
-  Candidate cand[kCap];
-  Candidate top[kMaxTop];  // of a slice: its likeliest, in order
-  Candidate pick[kT / 32];
+  uint64_t cand[kCap<kT>];
+  uint64_t few[128];       // of them those that may be among the likeliest; of a slice: its likeliest
+  uint64_t pick[kT / 32];
 };
 
 // Where the block's part of a row lies: chunks [c0, c1), of which those of [w0, w1) are whole. Thread t takes w0 + t, w0 + t + kT
@@ -493,28 +546,29 @@ __device__ __forceinline__ int edge_of(const Slice& s, int t) {
   return t == 0 ? (s.w0 > s.c0 ? s.c0 : -1) : t == 1 ? (s.w1 < s.c1 ? s.w1 : -1) : -1;
 }
 
-// The candidates of the listed threads' chunks into sh.cand: elements whose key is above `bound`, or at it and in a chunk up to
-// `last`. Their count (which may be past kCap) is returned in every thread.
+// The candidates of the listed threads' chunks into sh.cand: elements above `bound`, or at it and in a chunk up to `last`.
+// Their count (which may be past what is kept) is returned in every thread.
 template <int DT, int kT>
-__device__ __forceinline__ int collect(LogprobShared<kT>& sh, const Slice& s, int V, uint32_t bound, int last) {
+__device__ __forceinline__ int collect(LogprobShared<kT>& sh, const Slice& s, int V, float bound, int last) {
   const auto look = [&](const Raw8<DT>& q, int c) {
     float v[8];
     q.get(v);
+    const int first = c * 8 - s.r.off;
+    const uint32_t bits = reach(v, bound, c <= last) & row_bits(first, V);
+    if (bits == 0) return;
+    int at = atomicAdd(&sh.found, __popc(bits));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t x = key_of<DT>(v[j]);
-      const int e = c * 8 - s.r.off + j;
-      if ((x > bound || (x == bound && c <= last)) && e >= 0 && e < V) {
-        const int at = atomicAdd(&sh.found, 1);
-        if (at < kCap) sh.cand[at] = {x, e};
+    for (int j = 0; j < 8; ++j)
+      if (bits >> j & 1u) {
+        if (at < kCap<kT>) sh.cand[at] = packed(key_of<DT>(v[j]), first + j);
+        ++at;
       }
-    }
   };
   const int each = (s.w1 - s.w0 + kT - 1) / kT, n = sh.listed * each;
-#pragma unroll 4
+#pragma unroll 2
   for (int i = threadIdx.x; i < n; i += kT) {
     const int k = i / each, c = s.w0 + sh.list[k] + (i - k * each) * kT;
-    if (c >= s.w1 || *reinterpret_cast<volatile int*>(&sh.found) > kCap) continue;  // (too many already)
+    if (c >= s.w1 || *reinterpret_cast<volatile int*>(&sh.found) > kCap<kT>) continue;  // (too many already)
     Raw8<DT> q;
     q.load(s.r.p, c * 8 - s.r.off, true, 8);
     look(q, c);
@@ -529,17 +583,35 @@ __device__ __forceinline__ int collect(LogprobShared<kT>& sh, const Slice& s, in
   return sh.found;
 }
 
-// The likeliest of sh.cand[0 .. n) handed to `emit` with their places: a warp counts what stands before a candidate.
+// The first `top` of sh.cand[0 .. n) to `emit`, by warp 0. Of many, first the top-th: no two are equal, so exactly `top` reach it.
 template <int kT, class Emit>
-__device__ __forceinline__ void rank(const Candidate* cand, int n, int top, const Emit& emit) {
+__device__ __forceinline__ void finish(LogprobShared<kT>& sh, int n, int top, const Emit& emit) {
   const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < n; i += kT / 32) {
-    const Candidate x = cand[i];
-    int at = 0;
-    for (int j = lane; j < n; j += 32) at += before(cand[j], x) ? 1 : 0;
-    at = __reduce_add_sync(0xffffffffu, at);
-    if (lane == 0 && at < top) emit(at, x);
+  if (threadIdx.x >= 32) return;
+  if (n <= 128) {
+    first_of(sh.cand, n, top, lane, emit);
+    return;
   }
+  uint64_t bound = 0;
+#pragma unroll 1
+  for (int b = 63; b >= 0; --b) {
+    const uint64_t probe = bound | uint64_t(1) << b;
+    int m = 0;
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) m += sh.cand[i] >= probe ? 1 : 0;
+    m = __reduce_add_sync(0xffffffffu, m);
+    if (m >= top) bound = probe;
+    if (m == top) break;
+  }
+  int have = 0;
+  for (int i = 0; i < n; i += 32) {
+    const bool is = i + lane < n && sh.cand[i + lane] >= bound;
+    const uint32_t votes = __ballot_sync(0xffffffffu, is);
+    if (is) sh.few[have + __popc(votes & ((1u << lane) - 1u))] = sh.cand[i + lane];
+    have += __popc(votes);
+  }
+  __syncwarp();
+  first_of(sh.few, have, top, lane, emit);
 }
 
 // The slice's `top` likeliest words to `emit`. Every thread has a chunk of the slice; sh.maxima, sh.chunk are written, and the
@@ -574,8 +646,8 @@ __device__ __forceinline__ void slice_top(LogprobShared<kT>& sh, const Slice& s,
   }
   __syncthreads();
   const uint32_t bound = sh.bound;
-  int n = collect<DT, kT>(sh, s, V, bound, 0x7fffffff);
-  if (n > kCap) {
+  int n = collect<DT, kT>(sh, s, V, of_key<DT>(bound), 0x7fffffff);
+  if (n > kCap<kT>) {
     // many equal ones (a masked vocabulary): of those at the bound only the first chunks', up to the one that completes `top`
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -590,35 +662,38 @@ __device__ __forceinline__ void slice_top(LogprobShared<kT>& sh, const Slice& s,
       name(bound, at);
     }
     __syncthreads();
-    n = collect<DT, kT>(sh, s, V, bound, sh.bound_chunk);
+    n = collect<DT, kT>(sh, s, V, of_key<DT>(bound), sh.bound_chunk);
   }
-  if (n <= kCap) {
-    rank<kT>(sh.cand, n, top, emit);
+  if (n <= kCap<kT>) {
+    finish<kT>(sh, n, top, emit);
     return;
   }
   // many large ones in few threads: one maximum after another
-  Candidate done = {0xFFFFFFFFu, -1};
+  uint64_t done = ~uint64_t(0);
   for (int i = 0; i < top; ++i) {
-    Candidate best = {0u, 0x7fffffff};
+    uint64_t best = 0;
     for (int c = s.c0 + threadIdx.x; c < s.c1; c += kT) {
       Raw8<DT> q;
       fetch<DT>(q, s.r, c, V);
       float v[8];
       q.get(v);
+      const uint32_t bits = row_bits(c * 8 - s.r.off, V);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const Candidate x = {key_of<DT>(v[j]), c * 8 - s.r.off + j};
-        if (x.idx >= 0 && x.idx < V && before(done, x) && before(x, best)) best = x;
+        const uint64_t x = packed(key_of<DT>(v[j]), c * 8 - s.r.off + j);
+        if ((bits >> j & 1u) && x < done && x > best) best = x;
       }
     }
-    const uint32_t most = __reduce_max_sync(0xffffffffu, best.key);
-    const int at = __reduce_min_sync(0xffffffffu, best.key == most ? best.idx : 0x7fffffff);
-    if (lane == 0) sh.pick[threadIdx.x >> 5] = {most, at};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t u = __shfl_xor_sync(0xffffffffu, best, o);
+      best = u > best ? u : best;
+    }
+    if (lane == 0) sh.pick[threadIdx.x >> 5] = best;
     __syncthreads();
     done = sh.pick[0];
-    for (int k = 1; k < kT / 32; ++k)
-      if (before(sh.pick[k], done)) done = sh.pick[k];
-    if (threadIdx.x == 0) emit(i, done);
+    for (int k = 1; k < kT / 32; ++k) done = sh.pick[k] > done ? sh.pick[k] : done;
+    if (threadIdx.x == 0) emit(i, static_cast<uint32_t>(done >> 32), static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(done)));
     __syncthreads();
   }
 }
@@ -711,12 +786,12 @@ __global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : 1280) / kT) pk_logp
     if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
     if (a.top == 0) return;
     const float rest = logf(st.s);
-    slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, const Candidate& x) {
-      a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(x.key));
-      a.top_idx[row * a.top + i] = x.idx;
+    slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, uint32_t k, int e) {
+      a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(k));
+      a.top_idx[row * a.top + i] = e;
     });
   } else {
-    if (a.top > 0) slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, const Candidate& x) { sh.top[i] = x; });
+    if (a.top > 0) slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, uint32_t k, int e) { sh.few[i] = packed(k, e); });
     if (threadIdx.x == 0) sh.mine = st;
     gemm::cluster_sync();
     if (part == 0) {
@@ -727,25 +802,26 @@ __global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : 1280) / kT) pk_logp
         st = {__uint_as_float(ld_remote(from)), __uint_as_float(ld_remote(from + 4)), __uint_as_float(ld_remote(from + 8))};
       }
       for (int p = w; p < parts && a.top > 0; p += kT / 32) {
-        const uint32_t from = remote(&sh.top[0], p);
+        const uint32_t from = remote(&sh.few[0], p);
         for (int i = lane; i < a.top; i += 32)
-          sh.cand[p * a.top + i] = {ld_remote(from + 8 * i), static_cast<int>(ld_remote(from + 8 * i + 4))};
+          sh.cand[p * a.top + i] = ld_remote(from + 8 * i) | static_cast<uint64_t>(ld_remote(from + 8 * i + 4)) << 32;
       }
       st = warp_join(st);
       if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
       __syncthreads();
       const float rest = logf(st.s);
       if (a.top > 0)
-        rank<kT>(sh.cand, parts * a.top, a.top, [&](int i, const Candidate& x) {
-          a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(x.key));
-          a.top_idx[row * a.top + i] = x.idx;
+        finish<kT>(sh, parts * a.top, a.top, [&](int i, uint32_t k, int e) {
+          a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(k));
+          a.top_idx[row * a.top + i] = e;
         });
     }
     gemm::cluster_sync();  // (no block leaves while its memory is read)
   }
 }
 
-constexpr int kMiddle = 16384;  // words of a row of a block of 128 threads
+constexpr int kShort = 704;     // words of a row of a warp
+constexpr int kMiddle = 16384;  // words of a row of a block of 128 threads, and four times those of 64
 
 // Blocks a row: one where the rows fill the SMs, up to eight where they do not, none with fewer than 4096 words.
 int parts_of(int64_t T, int V, int sms) {
@@ -753,10 +829,6 @@ int parts_of(int64_t T, int V, int sms) {
   while (parts < 8 && T * parts * 2 <= 2 * sms && V / (parts * 2) >= 4096) parts *= 2;
   return parts;
 }
-
-// chunks of a lane of the longest row that belongs to a warp: 4345 words in 16 bits, 2301 in fp32, three blocks an SM
-template <int DT>
-constexpr int kMostChunks = DT == PK_F32 ? 9 : 17;
 
 template <int DT, int kC>
 cudaError_t short_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
@@ -768,14 +840,17 @@ cudaError_t short_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
 
 template <int DT>
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
-  // chunks of a row wherever it begins
-  const int chunks = static_cast<int>((static_cast<int64_t>(a.V) + 16 / Ty<DT>::kBytes - 1 + 7) / 8);
-  if (chunks <= 32 * 3) return short_launch<DT, 3>(a, sms, stream);
-  if (chunks <= 32 * 5) return short_launch<DT, 5>(a, sms, stream);
-  if (chunks <= 32 * kMostChunks<DT>) return short_launch<DT, kMostChunks<DT>>(a, sms, stream);
+  // a warp's row: up to three chunks a lane. (Longer ones took a warp longer than a block of 64: 65536 rows of 1500 words with 16
+  // likeliest 305 us.)
+  if (a.V <= kShort) return short_launch<DT, 3>(a, sms, stream);
   const int parts = parts_of(a.T, a.V, sms);
   if (parts == 1) {
-    // (shorter rows take as long from their last load to their last output: twice the blocks then)
+    // what a row takes from its last load to its last output hardly depends on its length: more and smaller blocks for
+    // shorter ones
+    if (a.V <= kMiddle / 4) {
+      Launch l(a.T, 64, stream);
+      return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 64, false>, a, 1);
+    }
     if (a.V <= kMiddle) {
       Launch l(a.T, 128, stream);
       return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 128, false>, a, 1);
@@ -875,24 +950,7 @@ bool sizes_ok(int dtype, int64_t T, int V, int64_t ld) {
   return dtype_ok(dtype) && T >= 0 && T <= PK_ROWS_MAX_T && V >= 1 && V <= PK_ROWS_MAX_DIM && ld >= V;
 }
 
-template <int DT>
-cudaError_t prepare_short() {
-  constexpr int kC = kMostChunks<DT>;
-  const cudaError_t e = cudaFuncSetAttribute(pk_logprobs_short_kernel<DT, 5>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShortBytes<DT, 5>);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(pk_logprobs_short_kernel<DT, kC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShortBytes<DT, kC>);
-}
-
 }  // namespace
-
-namespace rows {
-cudaError_t prepare_logprobs() {
-  cudaError_t e;
-  if ((e = prepare_short<PK_F32>()) != cudaSuccess) return e;
-  if ((e = prepare_short<PK_BF16>()) != cudaSuccess) return e;
-  return prepare_short<PK_F16>();
-}
-}  // namespace rows
 
 }  // namespace pk
 

@@ -114,7 +114,6 @@ cudaError_t prepare_gated();
 cudaError_t prepare_q8();
 cudaError_t prepare_distill();
 cudaError_t prepare_norm();
-cudaError_t prepare_logprobs();
 
 int device(Device* out) {
   int dev = 0;
@@ -137,7 +136,7 @@ int device(Device* out) {
         if (cudaGetSymbolAddress(&word, g_rows_status) != cudaSuccess || prepare_products() != cudaSuccess ||
             prepare_xent() != cudaSuccess || prepare_gated() != cudaSuccess ||
             prepare_q8() != cudaSuccess || prepare_distill() != cudaSuccess ||
-            prepare_norm() != cudaSuccess || prepare_logprobs() != cudaSuccess) {
+            prepare_norm() != cudaSuccess) {
           cudaGetLastError();
           return PK_ERR_CUDA;
         }
