@@ -34,27 +34,28 @@ struct NormArgs {
   float eps, inv_d;
 };
 
-// A row belongs to kTpr threads, each with kNv groups of eight elements kTpr groups apart: 8 threads for the shortest rows,
-// so that a warp's lanes all have something to load, up to a block of 512 for the longest; four groups a thread in flight
+// A row belongs to kTpr threads, each with kNg groups of 16 bytes, kTpr groups apart: 8 threads for the shortest rows,
+// so that a warp's lanes all have something to load, up to a block of 512 for the longest; 32 elements a thread in flight
 // wherever the row has as many.
 template <int kTpr>
 constexpr int kBlock = kTpr <= 32 ? 256 : kTpr;
 
-// The eight elements of a group: 16 bytes of a row where every row of every matrix begins and ends on such a boundary (kVec),
-// else eight columns kTpr apart, so that a warp's scalar accesses are of neighbours. `n`: columns of the row from the first.
+// A group of elements: the 16 bytes of a row where every row of every matrix begins and ends on such a boundary (kVec), else as
+// many columns kTpr apart, so that a warp's scalar accesses are of neighbours. `n`: columns of the row from the first.
+template <int DT>
+constexpr int kE = 16 / Ty<DT>::kBytes;
 template <int DT, int kTpr, bool kVec>
 struct Group {
-  uint4 q[DT == PK_F32 ? 2 : 1];
-  static __device__ __forceinline__ int column(int i, int t) { return kVec ? (i * kTpr + t) * 8 : i * 8 * kTpr + t; }
+  static constexpr int E = kE<DT>;
+  uint4 q;
+  static __device__ __forceinline__ int column(int i, int t) { return kVec ? (i * kTpr + t) * E : i * E * kTpr + t; }
   __device__ __forceinline__ void load(const void* p, int64_t at, int n) {
     if constexpr (kVec) {
-      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes);
-      q[0] = __ldcg(s);
-      if constexpr (DT == PK_F32) q[1] = __ldcg(s + 1);
+      q = __ldcg(reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes));
     } else {
-      uint32_t w[DT == PK_F32 ? 8 : 4];
+      uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < E; ++j) {
         if constexpr (DT == PK_F32) {
           w[j] = j * kTpr < n ? __ldcg(static_cast<const unsigned int*>(p) + at + j * kTpr) : 0u;
         } else {
@@ -62,36 +63,44 @@ struct Group {
           w[j >> 1] = j & 1 ? w[j >> 1] | x << 16 : x;
         }
       }
-      q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      if constexpr (DT == PK_F32) q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      q = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   // the weights, which every row reads again: through L1
   __device__ __forceinline__ void load_shared(const void* p, int at, int n) {
-    if constexpr (kVec) {
-      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes);
-      q[0] = *s;
-      if constexpr (DT == PK_F32) q[1] = s[1];
-    } else {
+    if constexpr (kVec)
+      q = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes);
+    else
       load(p, at, n);
+  }
+  __device__ __forceinline__ void get(float (&v)[E]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == PK_F32) {
+        v[j] = __uint_as_float(w[j]);
+      } else {
+        const float2 f = Elem<DT == PK_BF16>::unpack(w[j]);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
     }
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    Raw8<DT> r;
-    r.q[0] = q[0];
-    if constexpr (DT == PK_F32) r.q[1] = q[1];
-    r.get(v);
-  }
-  // the eight as they were loaded from here on: what was unpacked of them before is not kept in registers
-  __device__ __forceinline__ void forget() {
-    asm volatile("" : "+r"(q[0].x), "+r"(q[0].y), "+r"(q[0].z), "+r"(q[0].w));
-  }
-  static __device__ __forceinline__ void store(void* p, int64_t at, int n, const float (&v)[8]) {
+  // the elements as they were loaded from here on: what was unpacked of them before is not kept in registers
+  __device__ __forceinline__ void forget() { asm volatile("" : "+r"(q.x), "+r"(q.y), "+r"(q.z), "+r"(q.w)); }
+  static __device__ __forceinline__ void store(void* p, int64_t at, int n, const float (&v)[E]) {
     if constexpr (kVec) {
-      store8<DT>(p, at, v);
+      uint4 u;
+      if constexpr (DT == PK_F32) {
+        u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      } else {
+        using P = Elem<DT == PK_BF16>;
+        u = make_uint4(P::pack(v[0], v[1]), P::pack(v[2], v[3]), P::pack(v[4], v[5]), P::pack(v[6], v[7]));
+      }
+      *reinterpret_cast<uint4*>(static_cast<char*>(p) + at * Ty<DT>::kBytes) = u;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < E; ++j)
         if (j * kTpr < n) Ty<DT>::put(p, at + j * kTpr, v[j]);
     }
   }
@@ -126,22 +135,27 @@ __device__ __forceinline__ void row_reduce(float (&v)[N], float* red, int& turn)
   }
 }
 
-__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8]) {
-  uint16_t p[4];
+// N values (4 or 8) as e4m3, four a word
+template <int N>
+__device__ __forceinline__ void to_e4m3(const float (&v)[N], uint32_t (&q)[N / 4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
-  return make_uint2(p[0] | static_cast<uint32_t>(p[1]) << 16, p[2] | static_cast<uint32_t>(p[3]) << 16);
+  for (int i = 0; i < N / 4; ++i) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * i + 1]), "f"(v[4 * i]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * i + 3]), "f"(v[4 * i + 2]));
+    q[i] = lo | static_cast<uint32_t>(hi) << 16;
+  }
 }
 
 // blocks of an SM: 85 registers a thread, 128 of fp32
 template <int DT, int kTpr>
 constexpr int kResident = kTpr > 256 ? 1 : (DT == PK_F32 ? 512 : 768) / kBlock<kTpr>;
 
-template <int DT, int kMode, int kTpr, int kNv, bool kVec>
+template <int DT, int kMode, int kTpr, int kNg, bool kVec>
 __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
     pk_norm_kernel(const __grid_constant__ NormArgs a) {
   using G = Group<DT, kTpr, kVec>;
+  constexpr int E = G::E;
   __shared__ float red[kTpr > 32 ? 2 * 16 * 2 : 1];
   constexpr int kRows = kBlock<kTpr> / kTpr;
   const int t = threadIdx.x % kTpr;
@@ -151,11 +165,11 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.T; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
     const int64_t row = r0 + threadIdx.x / kTpr;
     const int D = row < a.T ? a.D : 0;  // (no columns of a row that is not there)
-    float h[kNv][8];
+    float h[kNg][E];
     {
-      G x[kNv], res[kNv];
+      G x[kNg], res[kNg];
 #pragma unroll
-      for (int i = 0; i < kNv; ++i) {
+      for (int i = 0; i < kNg; ++i) {
         const int c = G::column(i, t);
         if (c < D) {
           x[i].load(a.x, row * a.ldx + c, D - c);
@@ -163,17 +177,17 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
         }
       }
 #pragma unroll
-      for (int i = 0; i < kNv; ++i) {
+      for (int i = 0; i < kNg; ++i) {
         const int c = G::column(i, t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
+        for (int j = 0; j < E; ++j) h[i][j] = 0.0f;
         if (c < D) {
           x[i].get(h[i]);
           if (kMode != kQuantize && a.res) {
-            float b[8];
+            float b[E];
             res[i].get(b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] += b[j];
+            for (int j = 0; j < E; ++j) h[i][j] += b[j];
           }
           if (kMode != kQuantize && a.h) G::store(a.h, row * a.ldh + c, D - c, h[i]);
         }
@@ -184,9 +198,9 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
       const auto squares = [&]() {
         s[0] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kNv; ++i)
+        for (int i = 0; i < kNg; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);
+          for (int j = 0; j < E; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);
         row_reduce<kTpr, 1, 0>(s, red, turn);
       };
       squares();
@@ -197,22 +211,22 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
         const float down = past ? 0x1p-80f : 1.0f;
         eps = past ? 0.0f : eps;
 #pragma unroll
-        for (int i = 0; i < kNv; ++i)
+        for (int i = 0; i < kNg; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] *= down;
+          for (int j = 0; j < E; ++j) h[i][j] *= down;
         squares();
       }
       const float f = rsqrtf(fmaf(s[0], a.inv_d, eps));
 #pragma unroll
-      for (int i = 0; i < kNv; ++i) {
+      for (int i = 0; i < kNg; ++i) {
         const int c = G::column(i, t);
         if (c < D) {
           G w;
           w.load_shared(a.w, c, D - c);
-          float b[8];
+          float b[E];
           w.get(b);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * f * b[j];
+          for (int j = 0; j < E; ++j) h[i][j] = h[i][j] * f * b[j];
           if constexpr (kMode == kNorm) G::store(a.y, row * a.ldy + c, D - c, h[i]);
         }
       }
@@ -221,9 +235,9 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
       // (a maximum passes over NaN: a row that holds one gets a NaN scale, so that nobody takes the others for its values)
       float m[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < kNv; ++i)
+      for (int i = 0; i < kNg; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < E; ++j) {
           m[0] = fmaxf(m[0], fabsf(h[i][j]));
           m[1] = h[i][j] != h[i][j] ? 1.0f : m[1];
         }
@@ -233,19 +247,23 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
       const float up = scale < 0x1p-100f ? 0x1p60f : 1.0f;
       const float inv = scale > 0.0f ? 1.0f / (scale * up) : (scale == 0.0f ? 0.0f : scale);
 #pragma unroll
-      for (int i = 0; i < kNv; ++i) {
+      for (int i = 0; i < kNg; ++i) {
         const int c = G::column(i, t);
         if (c < D) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * up * inv;
-          const uint2 q = to_e4m3(h[i]);
+          for (int j = 0; j < E; ++j) h[i][j] = h[i][j] * up * inv;
+          uint32_t q[E / 4];
+          to_e4m3(h[i], q);
           uint8_t* d = static_cast<uint8_t*>(a.y) + row * a.ldy + c;
           if constexpr (kVec) {
-            *reinterpret_cast<uint2*>(d) = q;
+if constexpr (E == 8)
+              *reinterpret_cast<uint2*>(d) = make_uint2(q[0], q[1]);
+            else
+              *reinterpret_cast<uint32_t*>(d) = q[0];
           } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (j * kTpr < D - c) d[j * kTpr] = static_cast<uint8_t>((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+            for (int j = 0; j < E; ++j)
+              if (j * kTpr < D - c) d[j * kTpr] = static_cast<uint8_t>(q[j / 4] >> (8 * (j & 3)));
           }
         }
       }
@@ -253,6 +271,13 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
     }
   }
 }
+
+// values as pairs, for arithmetic on two at a time
+template <int N>
+__device__ __forceinline__ float2 pair(const float (&v)[N], int i) {
+  return make_float2(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
 struct NormBackArgs {
   const void* h;
@@ -272,162 +297,191 @@ struct NormBackArgs {
 // shared memory (kVec; a thread reads back what it asked for itself, so nothing is synchronized).
 // 16931 x 768 bf16 with dh: 23.8 us without that, on 16 warps an SM with a row in flight each.
 template <int DT, int kTpr>
-constexpr int kBackThreads = kTpr > 256 ? kTpr : DT == PK_F32 ? 256 : 512;  // of an SM: 128 registers, 255 of fp32
+constexpr int kBackThreads = kTpr > 256 ? kTpr : 512;  // of an SM: 128 registers
 template <int DT, int kTpr>
 constexpr int kBackResident = kBackThreads<DT, kTpr> / kBlock<kTpr>;
-template <int DT, int kTpr, int kNv>
-constexpr int kRowBytes = kBlock<kTpr> * kNv * 8 * Ty<DT>::kBytes;  // a block's groups of one input
+template <int DT, int kTpr, int kNg>
+constexpr int kRowBytes = kBlock<kTpr> * kNg * 16;  // a block's groups of one input
 // stages of the three inputs: two, or one fewer where they do not fit
-template <int DT, int kTpr, int kNv>
-constexpr int kStages = 6 * kRowBytes<DT, kTpr, kNv> * kBackResident<DT, kTpr> <= 200 * 1024 ? 2 : 1;
-template <int DT, int kTpr, int kNv, bool kVec>
+template <int DT, int kTpr, int kNg>
+constexpr int kStages = 6 * kRowBytes<DT, kTpr, kNg> * kBackResident<DT, kTpr> <= 200 * 1024 ? 2 : 1;
+template <int DT, int kTpr, int kNg, bool kVec>
 constexpr int back_smem() {
-  const int ring = kVec ? 3 * kStages<DT, kTpr, kNv> * kRowBytes<DT, kTpr, kNv> : 0, cols = kTpr <= 32 ? kBlock<kTpr> * kNv * 32 : 0;
+  const int ring = kVec ? 3 * kStages<DT, kTpr, kNg> * kRowBytes<DT, kTpr, kNg> : 0, cols = kTpr <= 32 ? kBlock<kTpr> * kNg * kE<DT> * 4 : 0;
   return ring > cols ? ring : cols;
 }
 
-template <int DT, int kTpr, int kNv, bool kVec>
+template <int DT, int kTpr, int kNg, bool kVec>
 __global__ void __launch_bounds__(kBlock<kTpr>, (kBackResident<DT, kTpr>)) pk_norm_backward_kernel(const __grid_constant__ NormBackArgs a) {
   using G = Group<DT, kTpr, kVec>;
+  constexpr int E = G::E;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[kTpr > 32 ? 2 * 16 * 2 : 1];
-  constexpr int kRows = kBlock<kTpr> / kTpr, kCols = kTpr * kNv * 8, kS = kStages<DT, kTpr, kNv>;
+  constexpr int kRows = kBlock<kTpr> / kTpr, kCols = kTpr * kNg * E, kS = kStages<DT, kTpr, kNg>;
   const int t = threadIdx.x % kTpr;
   int turn = 0;
-  float sum[kNv][8];
-  G w[kNv];
+  float2 sum[kNg][E / 2];
+  G held[DT == PK_F32 ? 1 : kNg];  // the weights, where the registers hold them
   griddep_wait();
 #pragma unroll
-  for (int i = 0; i < kNv; ++i) {
+  for (int i = 0; i < kNg; ++i) {
     const int c = G::column(i, t);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[i][j] = 0.0f;
-    if (c < a.D) w[i].load(a.w, c, a.D - c);
+    for (int j = 0; j < E / 2; ++j) sum[i][j] = twice(0.0f);
+    if (DT != PK_F32 && c < a.D) held[DT == PK_F32 ? 0 : i].load(a.w, c, a.D - c);
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  // this thread's 16 bytes (32 of fp32) of group i of input k in a stage
-  const auto slot = [&](int stage, int k, int i) {
-    return smem + ((stage * 3 + k) * kNv + i) * kBlock<kTpr> * 8 * Ty<DT>::kBytes + threadIdx.x * 16;
+  const auto weights = [&](int i, int c, float(&g)[E]) {
+    if constexpr (DT == PK_F32) {
+      G w;
+      w.load_shared(a.w, c, a.D - c);
+      w.get(g);
+    } else {
+      held[i].get(g);
+    }
   };
-  const auto ask = [&](int stage, int64_t r0) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  // this thread's 16 bytes of group i of input k in a stage
+  const auto slot = [&](int stage, int k, int i) {
+    return smem + (((stage * 3 + k) * kNg + i) * kBlock<kTpr> + threadIdx.x) * 16;
+  };
+  // inputs [k0, k1) of a row into a stage; every call makes one group of copies
+  const auto ask = [&](int stage, int64_t r0, auto k0, auto k1) {
     const int64_t row = r0 + threadIdx.x / kTpr;
     if (row < a.T) {
 #pragma unroll
-      for (int i = 0; i < kNv; ++i) {
+      for (int i = 0; i < kNg; ++i) {
         const int c = G::column(i, t);
         if (c < a.D) {
-          const void* src[3] = {static_cast<const char*>(a.h) + (row * a.ldh + c) * Ty<DT>::kBytes,
-                                static_cast<const char*>(a.dy) + (row * a.lddy + c) * Ty<DT>::kBytes,
-                                static_cast<const char*>(a.dh) + (row * a.lddh + c) * Ty<DT>::kBytes};
+          const void* const base[3] = {a.h, a.dy, a.dh};
+          const int64_t ld[3] = {a.ldh, a.lddy, a.lddh};
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
+          for (int k = decltype(k0)::value; k < decltype(k1)::value; ++k)
             if (k < 2 || a.dh) {
-#pragma unroll
-              for (int p = 0; p < Ty<DT>::kBytes / 2; ++p)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, k, i) + p * kBlock<kTpr> * 16)),
-                             "l"(static_cast<const char*>(src[k]) + 16 * p)
-                             : "memory");
+              const char* src = static_cast<const char*>(base[k]) + (row * ld[k] + c) * Ty<DT>::kBytes;
+asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, k, i))), "l"(src) : "memory");
             }
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  using K0 = std::integral_constant<int, 0>;
+  using K2 = std::integral_constant<int, 2>;
+  using K3 = std::integral_constant<int, 3>;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
   if constexpr (kVec) {
 #pragma unroll
-    for (int k = 0; k < kS; ++k) ask(k, first + k * step);
+    for (int k = 0; k < kS; ++k) {
+      ask(k, first + k * step, K0(), K2());
+      ask(k, first + k * step, K2(), K3());
+    }
   }
   int stage = 0;
   for (int64_t r0 = first; r0 < a.T; r0 += step) {
     const int64_t row = r0 + threadIdx.x / kTpr;
     const int D = row < a.T ? a.D : 0;
-    G xh[kNv], xd[kNv], xr[kNv];
-    if constexpr (kVec) asm volatile("cp.async.wait_group %0;" ::"n"(kS - 1) : "memory");
+    G xh[kNg], xd[kNg];
+    if constexpr (kVec) asm volatile("cp.async.wait_group %0;" ::"n"(2 * (kS - 1)) : "memory");
+    const auto read = [&](G& x, int k, int i) { x.q = *reinterpret_cast<const uint4*>(slot(stage, k, i)); };
 #pragma unroll
-    for (int i = 0; i < kNv; ++i) {
+    for (int i = 0; i < kNg; ++i) {
       const int c = G::column(i, t);
       if (c < D) {
         if constexpr (kVec) {
-#pragma unroll
-          for (int p = 0; p < Ty<DT>::kBytes / 2; ++p) {
-            const int at = p * kBlock<kTpr> * 16;
-            xh[i].q[p] = *reinterpret_cast<const uint4*>(slot(stage, 0, i) + at);
-            xd[i].q[p] = *reinterpret_cast<const uint4*>(slot(stage, 1, i) + at);
-            if (a.dh) xr[i].q[p] = *reinterpret_cast<const uint4*>(slot(stage, 2, i) + at);
-          }
+          read(xh[i], 0, i);
+          read(xd[i], 1, i);
         } else {
           xh[i].load(a.h, row * a.ldh + c, D - c);
           xd[i].load(a.dy, row * a.lddy + c, D - c);
-          if (a.dh) xr[i].load(a.dh, row * a.lddh + c, D - c);
         }
       }
     }
-    float s[2], down = 1.0f, eps = a.eps;
-    const auto sums = [&]() {
-      s[0] = s[1] = 0.0f;
+    float s[2];
+    const auto sums = [&](auto scaled) {
+      float2 hh = twice(0.0f), hg = twice(0.0f);
 #pragma unroll
-      for (int i = 0; i < kNv; ++i)
-        if (G::column(i, t) < D) {
-          float h[8], d[8], g[8];
+      for (int i = 0; i < kNg; ++i) {
+        const int c = G::column(i, t);
+        if (c < D) {
+          float h[E], d[E], g[E];
           xh[i].get(h);
           xd[i].get(d);
-          w[i].get(g);
+          weights(i, c, g);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            h[j] *= down;
-            s[0] = fmaf(h[j], h[j], s[0]);
-            s[1] = fmaf(h[j], d[j] * g[j], s[1]);
+          for (int j = 0; j < E / 2; ++j) {
+            float2 x = pair(h, j);
+            if constexpr (decltype(scaled)::value) x = mul2(x, twice(0x1p-80f));
+            hh = fma2(x, x, hh);
+            hg = fma2(x, mul2(pair(d, j), pair(g, j)), hg);
           }
         }
+      }
+      s[0] = hh.x + hh.y;
+      s[1] = hg.x + hg.y;
       row_reduce<kTpr, 2, 0>(s, red, turn);
     };
-    sums();
+    sums(std::false_type());
+    float down = 1.0f, eps = a.eps;
     // (as forwards: squares past fp32's range)
     const bool past = s[0] > FLT_MAX;
     if (kTpr > 32 ? past : __any_sync(0xffffffffu, past)) {
-      down = past ? 0x1p-80f : 1.0f;
-      eps = past ? 0.0f : eps;
-      sums();
-    }
-    if constexpr (kVec) {
-      // (this stage has been read: the sums are made of it)
-      ask(stage, r0 + kS * step);
-      stage = stage + 1 == kS ? 0 : stage + 1;
-    }
-    if constexpr (DT != PK_F32) {
-#pragma unroll
-      for (int i = 0; i < kNv; ++i) {
-        xh[i].forget();
-        xd[i].forget();
-        w[i].forget();
+      const float whole[2] = {s[0], s[1]};
+      sums(std::true_type());
+      if (past) {
+        down = 0x1p-80f;
+        eps = 0.0f;
+      } else {
+        s[0] = whole[0];
+        s[1] = whole[1];
       }
     }
+    // (h and dy have been read: the sums are made of them)
+    if constexpr (kVec) ask(stage, r0 + kS * step, K0(), K2());
     const float f = rsqrtf(fmaf(s[0], a.inv_d, eps));  // of h times `down`
     const float mean = s[1] * a.inv_d * f;             // of g n
+    const float2 rate = twice(f * down), mean2 = twice(-mean);
+    if constexpr (DT != PK_F32) {
 #pragma unroll
-    for (int i = 0; i < kNv; ++i) {
+      for (int i = 0; i < kNg; ++i) {
+        xh[i].forget();
+        xd[i].forget();
+        held[i].forget();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kNg; ++i) {
       const int c = G::column(i, t);
       if (c < D) {
-        float n[8], d[8], g[8];
+        float n[E], d[E], g[E];
         xh[i].get(n);
         xd[i].get(d);
-        w[i].get(g);
+        weights(i, c, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          n[j] = n[j] * down * f;
-          sum[i][j] = fmaf(d[j], n[j], sum[i][j]);
-          d[j] = (d[j] * g[j] - n[j] * mean) * f * down;
+        for (int j = 0; j < E / 2; ++j) {
+          const float2 x = mul2(pair(n, j), rate), y = pair(d, j);
+          sum[i][j] = fma2(y, x, sum[i][j]);
+          const float2 v = mul2(fma2(x, mean2, mul2(y, pair(g, j))), rate);
+          d[2 * j] = v.x;
+          d[2 * j + 1] = v.y;
         }
         if (a.dx) {
           if (a.dh) {
-            xr[i].get(n);
+            G xr;
+            if constexpr (kVec)
+              read(xr, 2, i);
+            else
+              xr.load(a.dh, row * a.lddh + c, D - c);
+            xr.get(n);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] += n[j];
+            for (int j = 0; j < E; j += 2) add2(d[j], d[j + 1], make_float2(n[j], n[j + 1]));
           }
           G::store(a.dx, row * a.lddx + c, D - c, d);
         }
       }
+    }
+    if constexpr (kVec) {
+      ask(stage, r0 + kS * step, K2(), K3());  // (and dh: what was written is made of it)
+      stage = stage + 1 == kS ? 0 : stage + 1;
     }
   }
   if constexpr (kVec) asm volatile("cp.async.wait_all;" ::: "memory");
@@ -436,14 +490,15 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kBackResident<DT, kTpr>)) pk_no
   float* cols = reinterpret_cast<float*>(smem);
   if constexpr (kTpr <= 32) __syncthreads();  // (the stages have been read)
 #pragma unroll
-  for (int i = 0; i < kNv; ++i)
+  for (int i = 0; i < kNg; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < E; ++j) {
       const int c = G::column(i, t) + (kVec ? j : j * kTpr);
+      const float v = j & 1 ? sum[i][j >> 1].y : sum[i][j >> 1].x;
       if constexpr (kTpr > 32) {
-        if (c < a.D) part[c] = sum[i][j];
+        if (c < a.D) part[c] = v;
       } else {
-        cols[threadIdx.x / kTpr * kCols + c] = sum[i][j];
+        cols[threadIdx.x / kTpr * kCols + c] = v;
       }
     }
   if constexpr (kTpr <= 32) {
@@ -476,31 +531,31 @@ __global__ void __launch_bounds__(1024) pk_norm_weight_kernel(const float* part,
   }
 }
 
-// How a row of D elements is shared out: calls f(threads a row, groups of eight a thread).
+// How a row of D elements is shared out.
 template <int A, int B>
 struct Cut {
-  static constexpr int kTpr = A, kNv = B;
+  static constexpr int kTpr = A, kElems = B;  // threads a row, elements a thread
 };
 template <class F>
 cudaError_t by_length(int D, const F& f) {
-  if (D <= 64) return f(Cut<8, 1>());
-  if (D <= 256) return f(Cut<8, 4>());
-  if (D <= 1024) return f(Cut<32, 4>());
-  if (D <= 2048) return f(Cut<64, 4>());
-  if (D <= 4096) return f(Cut<128, 4>());
-  if (D <= 8192) return f(Cut<256, 4>());
-  return f(Cut<512, 4>());
+  if (D <= 64) return f(Cut<8, 8>());
+  if (D <= 256) return f(Cut<8, 32>());
+  if (D <= 1024) return f(Cut<32, 32>());
+  if (D <= 2048) return f(Cut<64, 32>());
+  if (D <= 4096) return f(Cut<128, 32>());
+  if (D <= 8192) return f(Cut<256, 32>());
+  return f(Cut<512, 32>());
 }
-static_assert(512 * 4 * 8 == kMaxD, "the longest row");
+static_assert(512 * 32 == kMaxD, "the longest row");
 
 template <int DT, int kMode>
 cudaError_t norm_launch(const NormArgs& a, bool vec, int sms, cudaStream_t stream) {
   return by_length(a.D, [&](auto cut) {
-    constexpr int kTpr = decltype(cut)::kTpr, kNv = decltype(cut)::kNv, kRows = kBlock<kTpr> / kTpr;
+    constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>, kRows = kBlock<kTpr> / kTpr;
     const int64_t blocks = (a.T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * (2048 / kBlock<kTpr>);
     Launch l(blocks < most ? blocks : most, kBlock<kTpr>, stream);
-    return vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNv, true>, a)
-               : cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNv, false>, a);
+    return vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNg, true>, a)
+               : cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNg, false>, a);
   });
 }
 
@@ -523,11 +578,11 @@ int64_t back_blocks(int dtype, int64_t T, int D, int sms) {
 template <int DT>
 cudaError_t back_launch(const NormBackArgs& a, bool vec, int64_t blocks, void* dw, cudaStream_t stream) {
   return by_length(a.D, [&](auto cut) {
-    constexpr int kTpr = decltype(cut)::kTpr, kNv = decltype(cut)::kNv;
+    constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>;
     Launch l(blocks, kBlock<kTpr>, stream);
-    l.cfg.dynamicSmemBytes = vec ? back_smem<DT, kTpr, kNv, true>() : back_smem<DT, kTpr, kNv, false>();
-    const cudaError_t e = vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNv, true>, a)
-                              : cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNv, false>, a);
+    l.cfg.dynamicSmemBytes = vec ? back_smem<DT, kTpr, kNg, true>() : back_smem<DT, kTpr, kNg, false>();
+    const cudaError_t e = vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNg, true>, a)
+                              : cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNg, false>, a);
     if (e != cudaSuccess || !dw) return e;
     Launch lw((a.D + 31) / 32, 1024, stream);
     const float* part = a.part;
@@ -541,9 +596,9 @@ cudaError_t prepare_back() {
   cudaError_t e = cudaSuccess;
   for (const int D : {64, 256, 1024, 2048, 4096, 8192, kMaxD}) {
     e = by_length(D, [&](auto cut) {
-      constexpr int kTpr = decltype(cut)::kTpr, kNv = decltype(cut)::kNv;
-      return cudaFuncSetAttribute(pk_norm_backward_kernel<DT, kTpr, kNv, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  back_smem<DT, kTpr, kNv, true>());
+      constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>;
+      return cudaFuncSetAttribute(pk_norm_backward_kernel<DT, kTpr, kNg, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  back_smem<DT, kTpr, kNg, true>());
     });
     if (e != cudaSuccess) return e;
   }
@@ -581,8 +636,8 @@ int run_norm(int mode, int dtype, const void* x, int64_t ldx, const void* residu
   a.D = D;
   a.eps = eps;
   a.inv_d = 1.0f / static_cast<float>(D);
-  const bool vec = (D & 7) == 0 && rows16(x, ldx, e) && (!residual || rows16(residual, ldr, e)) && (!h || rows16(h, ldh, e)) &&
-                   aligned_to(w, 16) && (mode == kNorm ? rows16(y, ldy, e) : aligned_to(y, 8) && (ldy & 7) == 0);
+  const bool vec = (D * e & 15) == 0 && rows16(x, ldx, e) && (!residual || rows16(residual, ldr, e)) && (!h || rows16(h, ldh, e)) &&
+                   aligned_to(w, 16) && (mode == kNorm ? rows16(y, ldy, e) : aligned_to(y, 16 / e) && (ldy & (16 / e - 1)) == 0);
   const auto run = [&](auto type) {
     constexpr int DT = decltype(type)::value;
     if (mode == kNorm) return norm_launch<DT, kNorm>(a, vec, d.sms, stream);
@@ -671,7 +726,7 @@ int pk_rms_norm_backward(int dtype, const void* h, int64_t ldh, const void* w, c
   a.D = D;
   a.eps = eps;
   a.inv_d = 1.0f / static_cast<float>(D);
-  const bool vec = (D & 7) == 0 && rows16(h, ldh, e) && rows16(dy, lddy, e) && (!dh || rows16(dh, lddh, e)) &&
+  const bool vec = (D * e & 15) == 0 && rows16(h, ldh, e) && rows16(dy, lddy, e) && (!dh || rows16(dh, lddh, e)) &&
                    (!dx || rows16(dx, lddx, e)) && rows::aligned_to(w, 16);
   const cudaError_t r = dtype == PK_F32    ? back_launch<PK_F32>(a, vec, blocks, dw, stream)
                         : dtype == PK_BF16 ? back_launch<PK_BF16>(a, vec, blocks, dw, stream)

@@ -48,35 +48,39 @@ struct Q8Epi {
 #pragma unroll 1
     for (int cc = 0; cc < end; cc += 32) {
       const int c = c0 + cc;
-      stored(lane);
-      if (p.res) S::fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
+      if (p.res) {
+        stored(lane);  // the previous chunk's tile has left the staging memory
+        S::fetch(stage, lane, p.res, p.ldres, p.res_vec, r0, c, M, N);
+      }
       float v[32];
       {
         Bias<PK_F32, 32> ws;
+        Bias<DT, 32> b;
         ws.fetch(p.ws, p.ws_vec, c, N);
+        if (p.bias) b.fetch(p.bias, p.bias_vec, c, N);
         if (cc == 0 && !ready()) return false;
         read_acc(tacc + cc, zero, v);
         if (cc + 32 >= end) done();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 lo = mul2(make_float2(__uint_as_float(ws.q[i].x), __uint_as_float(ws.q[i].y)), make_float2(xs, xs));
-          const float2 hi = mul2(make_float2(__uint_as_float(ws.q[i].z), __uint_as_float(ws.q[i].w)), make_float2(xs, xs));
-          v[4 * i] *= lo.x;
-          v[4 * i + 1] *= lo.y;
-          v[4 * i + 2] *= hi.x;
-          v[4 * i + 3] *= hi.y;
+          const uint32_t u[4] = {ws.q[i].x, ws.q[i].y, ws.q[i].z, ws.q[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const float2 f = mul2(mul2(make_float2(v[4 * i + j], v[4 * i + j + 1]), make_float2(xs, xs)),
+                                  make_float2(__uint_as_float(u[j]), __uint_as_float(u[j + 1])));
+            v[4 * i + j] = f.x;
+            v[4 * i + j + 1] = f.y;
+          }
         }
-      }
-      if (p.bias) {
-        Bias<DT, 32> b;
-        b.fetch(p.bias, p.bias_vec, c, N);
-        b.add(v);
+        if (p.bias) b.add(v);
       }
       act_values<DT>(p.act, v);
       if (p.res) {
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
         S::add(stage, lane, v, 0);
+      } else {
+        stored(lane);  // (as late as can be: all of the above runs under the copy)
       }
       S::put(stage, lane, v);
       if (p.tma_y) {
