@@ -7,8 +7,7 @@
 //
 // The cross entropy's passes (pk_xent.cu, pk_vocab.cuh) with a list of words in the place of a label: the epilogue that holds a
 // tile of logits in registers writes out those that the row's list names, or takes the q off there. So that it need not
-// search, a first kernel sorts each row's list by word; a tile's first word is found by counting the smaller ones before
-// the accumulators are ready, and most chunks of 32 columns hold none.
+// search, the lists are sorted by word first, and a table says which word of a row is the first in each slice of the vocabulary.
 #include "pk_vocab.cuh"
 
 namespace pk {
@@ -28,20 +27,48 @@ struct ListArgs {
   int64_t T;
   int top, ld, V;
   float inverse;         // 1 / temperature
-  int* word;             // [T, ld] sorted, then kNoWord
-  float* share;          // [T, ld]
   long long* label;      // [T] 0 where the row has a word, -1 where it has none, V where it has one past the vocabulary
+  uint32_t* first;       // [slices][cap]
+  int64_t cap, entries;  // of first
+  int width;             // of a slice
+  const int* rows;       // [count] the rows with a word
+  const int* count;
+  int* word;             // [count, ld] sorted, then kNoWord
+  float* share;          // [count, ld]
 };
 
-// A warp a row: the words that are there (an index of a word, a value above -inf), their probabilities and their order. Two
-// words of a lane at most.
+// whether an entry is there: an index of a word, a value above -inf
+__device__ __forceinline__ bool there(long long x, float v) { return x >= 0 && v != -INFINITY; }
+
+// Which rows have words, a warp a row; and the table of first words emptied.
+__global__ void __launch_bounds__(256) pk_distill_rows_kernel(const __grid_constant__ ListArgs a) {
+  const int lane = threadIdx.x & 31;
+  griddep_wait();
+  for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < a.entries / 4; i += gridDim.x * 256LL)
+    reinterpret_cast<uint4*>(a.first)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t t = blockIdx.x * 8LL + (threadIdx.x >> 5); t < a.T; t += gridDim.x * 8LL) {
+    bool any = false, bad = false;
+    for (int k = lane; k < a.top; k += 32) {
+      const long long x = __ldcg(a.idx + t * a.top + k);
+      const bool is = there(x, __ldcg(a.values + t * a.top + k));
+      any = any || is;
+      bad = bad || (is && x >= a.V);
+    }
+    any = __any_sync(0xffffffffu, any);
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) a.label[t] = bad ? a.V : any ? 0 : -1;
+  }
+}
+
+// A warp a row that has words: their probabilities, their order, and the first of each slice. Two words of a lane at most.
 __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_constant__ ListArgs a) {
   const int lane = threadIdx.x & 31;
   griddep_wait();
-  for (int64_t t = blockIdx.x * 8LL + (threadIdx.x >> 5); t < a.T; t += gridDim.x * 8LL) {
+  const int n = __ldcg(a.count);
+  for (int64_t row = blockIdx.x * 8LL + (threadIdx.x >> 5); row < n; row += gridDim.x * 8LL) {
+    const int64_t t = __ldcg(a.rows + row);
     int word[2];
     float v[2];
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = lane + 32 * i;
@@ -49,17 +76,11 @@ __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_const
       v[i] = -INFINITY;
       if (k < a.top) {
         x = __ldcg(a.idx + t * a.top + k);
-        v[i] = __ldcg(a.values + t * a.top + k) * a.inverse;
+        v[i] = __ldcg(a.values + t * a.top + k);
       }
-      if (v[i] == -INFINITY) x = -1;
-      bad = bad || x >= a.V;
-      word[i] = x < 0 ? kNoWord : x >= a.V ? kNoWord : static_cast<int>(x);
-      if (word[i] == kNoWord) v[i] = -INFINITY;
+      word[i] = there(x, v[i]) ? static_cast<int>(x) : kNoWord;
+      v[i] = word[i] == kNoWord ? -INFINITY : v[i] * a.inverse;
     }
-    const bool any = __any_sync(0xffffffffu, word[0] != kNoWord || word[1] != kNoWord);
-    bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) a.label[t] = bad ? a.V : any ? 0 : -1;
-    if (bad || !any) continue;
     // (a NaN among the values, or an infinity, comes through the exponentials)
     float m = fmaxf(v[0], v[1]);
 #pragma unroll
@@ -70,21 +91,29 @@ __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_const
     sum = e[0] + e[1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    // the place of each word: how many are smaller, equal ones by their place in the list; those that are not there last
+    // the place of each word: how many are smaller, equal ones by their place in the list; those that are not there last. The
+    // first of a slice has no smaller one in it.
     int at[2] = {0, 0};
+    bool lead[2] = {word[0] != kNoWord, word[1] != kNoWord};
+    const int slice[2] = {word[0] / a.width, word[1] / a.width};
     for (int k = 0; k < a.top; ++k) {
-      const int other = __shfl_sync(0xffffffffu, k < 32 ? word[0] : word[1], k & 31);
+      const int other = __shfl_sync(0xffffffffu, k < 32 ? word[0] : word[1], k & 31), theirs = other / a.width;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) at[i] += other < word[i] || (other == word[i] && k < lane + 32 * i) ? 1 : 0;
+      for (int i = 0; i < 2; ++i) {
+        const bool smaller = other < word[i] || (other == word[i] && k < lane + 32 * i);
+        at[i] += smaller ? 1 : 0;
+        lead[i] = lead[i] && !(smaller && theirs == slice[i]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int k = lane + 32 * i;
       if (k < a.ld) {
-        const int64_t to = t * a.ld + (k < a.top ? at[i] : k);
+        const int64_t to = row * a.ld + (k < a.top ? at[i] : k);
         a.word[to] = word[i];
         a.share[to] = e[i] / sum;
       }
+      if (lead[i]) a.first[slice[i] * a.cap + row] = static_cast<uint32_t>(at[i]) << 8 | (word[i] - slice[i] * a.width + 1);
     }
   }
 }
@@ -128,9 +157,9 @@ __global__ void __launch_bounds__(256) pk_distill_join_kernel(const float2* part
       const int64_t t = __ldcg(idx + row);
       float v = 0.0f;
       for (int k = lane; k < ld; k += 32) {
-        if (__ldcg(word + t * ld + k) == kNoWord) continue;
-        const float p = __ldcg(share + t * ld + k);
-        if (p != 0.0f) v += p * (logf(p) + ((q.x - __ldcg(picked + t * ld + k)) * inverse + rest));
+        if (__ldcg(word + row * ld + k) == kNoWord) continue;
+        const float p = __ldcg(share + row * ld + k);
+        if (p != 0.0f) v += p * (logf(p) + ((q.x - __ldcg(picked + row * ld + k)) * inverse + rest));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -143,18 +172,24 @@ __global__ void __launch_bounds__(256) pk_distill_join_kernel(const float2* part
   }
 }
 
-// the scratch of a call: the lists, then what the cross entropy has
+// the scratch of the lists, beside what the cross entropy has
 struct Lists {
-  int ld;
+  int ld, width;
+  int64_t cap, entries;
   int* word;
   float* share;
+  uint32_t* first;
   long long* label;
 };
-Lists plan_lists(Carver& c, int64_t T, int top) {
+Lists plan_lists(Carver& c, int64_t T, int V, int top, int width) {
   Lists l;
   l.ld = static_cast<int>(round_up(top, 4));
+  l.width = width;
+  l.cap = round_up(T, 256);
+  l.entries = (V + width - 1) / width * l.cap;
   l.word = static_cast<int*>(c.take(T * l.ld * 4));
   l.share = static_cast<float*>(c.take(T * l.ld * 4));
+  l.first = static_cast<uint32_t*>(c.take(l.entries * 4));
   l.label = static_cast<long long*>(c.take(T * 8));
   return l;
 }
@@ -171,23 +206,33 @@ struct Fwd {
 Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T, int D, int V, int top, int sms, void* ws) {
   Fwd f = {};
   Carver c(ws);
-  f.lists = plan_lists(c, T, top);
-  plan_common(c, f.m, dtype, x, ldx, w, T, D, V);
   f.shape = gemm::pick_shape(T, V, D, dtype == PK_F32 ? gemm::kTerms32 : 1, sms, false);
-  f.slices = (V + 64 * f.shape.cg - 1) / (64 * f.shape.cg);
+  const int width = 64 * f.shape.cg;  // of an epilogue's warp (eight of them)
+  f.lists = plan_lists(c, T, V, top, width);
+  plan_common(c, f.m, dtype, x, ldx, w, T, D, V);
+  f.slices = (V + width - 1) / width;
   f.part = static_cast<float2*>(c.take(f.slices * f.m.cap * 8));
   f.picked = static_cast<float*>(c.take(T * f.lists.ld * 4));
   f.bytes = c.used;
   return f;
 }
-int64_t lists_bytes(int64_t T, int top) {
-  Carver c(nullptr);
-  plan_lists(c, T, top);
-  return c.used;
+struct Back {
+  Lists lists;
+  Bwd b;
+  int64_t bytes;
+};
+Back plan_back(int dtype, const void* x, int64_t ldx, const void* w, bool need_db, int64_t T, int D, int V, int top, int sms, void* ws) {
+  Back p;
+  // (the tile of dz, and with it the slices, is the plan's to say: once for that, once for its place behind the lists)
+  const int width = 32 * plan_backward(dtype, x, ldx, w, need_db, T, D, V, sms, nullptr).dz_shape.cg;  // (sixteen warps)
+  Carver c(ws);
+  p.lists = plan_lists(c, T, V, top, width);
+  p.b = plan_backward(dtype, x, ldx, w, need_db, T, D, V, sms, ws ? static_cast<char*>(ws) + c.used : nullptr);
+  p.bytes = c.used + p.b.bytes;
+  return p;
 }
 
-cudaError_t lists_launch(const Lists& l, const int64_t* idx, const float* values, int64_t T, int top, int V, float inverse, int sms,
-                         cudaStream_t stream) {
+ListArgs list_args(const Lists& l, const Common& m, const int64_t* idx, const float* values, int64_t T, int top, int V, float inverse) {
   ListArgs a = {};
   a.idx = reinterpret_cast<const long long*>(idx);
   a.values = values;
@@ -196,12 +241,24 @@ cudaError_t lists_launch(const Lists& l, const int64_t* idx, const float* values
   a.ld = l.ld;
   a.V = V;
   a.inverse = inverse;
+  a.label = l.label;
+  a.first = l.first;
+  a.cap = l.cap;
+  a.entries = l.entries;
+  a.width = l.width;
+  a.rows = m.idx;
+  a.count = m.count;
   a.word = l.word;
   a.share = l.share;
-  a.label = l.label;
-  const int64_t blocks = (T + 7) / 8, most = static_cast<int64_t>(sms) * 8;
-  Launch launch(blocks < most ? blocks : most, 256, stream);
-  return cudaLaunchKernelEx(&launch.cfg, pk_distill_list_kernel, a);
+  return a;
+}
+// The rows with words, listed as the cross entropy lists its labelled ones, and their lists.
+cudaError_t lists_launch(const ListArgs& a, const RowArgs& r, int sms, cudaStream_t stream) {
+  const int64_t blocks = (a.T + 7) / 8, most = static_cast<int64_t>(sms) * 8;
+  Launch l(blocks < most ? blocks : most, 256, stream);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, pk_distill_rows_kernel, a);
+  if (e != cudaSuccess || (e = rows_launch(r, stream)) != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&l.cfg, pk_distill_list_kernel, a);
 }
 
 bool distill_ok(int dtype, int64_t T, int D, int V, int top, double temperature) {
@@ -235,7 +292,7 @@ int pk_distill_workspace(int dtype, const void* x, int64_t ldx, const void* w, i
   rows::Device d;
   const int rc = rows::device(&d);
   if (rc != PK_OK) return rc;
-  *bytes = backward ? lists_bytes(T, top) + plan_backward(dtype, x, ldx, w, need_db != 0, T, D, V, d.sms, nullptr).bytes
+  *bytes = backward ? plan_back(dtype, x, ldx, w, need_db != 0, T, D, V, top, d.sms, nullptr).bytes
                     : plan_forward(dtype, x, ldx, w, T, D, V, top, d.sms, nullptr).bytes;
   return PK_OK;
 }
@@ -259,7 +316,6 @@ int pk_distill(int dtype, const void* x, int64_t ldx, const void* w, const void*
   if (!workspace || workspace_bytes < f.bytes) return PK_ERR_NOMEM;
   if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
   const float inverse = static_cast<float>(1.0 / temperature);
-  if (lists_launch(f.lists, idx, values, T, top, V, inverse, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   RowArgs r = {};
   r.labels = f.lists.label;
   r.T = T;
@@ -272,7 +328,7 @@ int pk_distill(int dtype, const void* x, int64_t ldx, const void* w, const void*
   r.loss = loss;
   r.lse = lse;
   r.status = status ? status : rows::stream_status(d, stream);
-  if (rows_launch(r, stream) != cudaSuccess) return PK_ERR_CUDA;
+  if (lists_launch(list_args(f.lists, f.m, idx, values, T, top, V, inverse), r, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   Inputs in;
   if (lay_out(dtype, f.m, x, ldx, w, T, D, V, d.sms, stream, &in) != cudaSuccess) return PK_ERR_CUDA;
   gemm::Args a = {};
@@ -291,7 +347,7 @@ int pk_distill(int dtype, const void* x, int64_t ldx, const void* w, const void*
   sp.part = f.part;
   sp.picked = f.picked;
   sp.cap = f.m.cap;
-  sp.lists = {f.lists.word, f.lists.share, f.m.idx, f.lists.ld};
+  sp.lists = {f.lists.word, f.lists.share, f.lists.first, f.lists.ld};
   sp.factor = inverse * kLog2e;
   if (logits_product<ListStat>(dtype, in.xc, in.w, in.alt ? &in.xd : nullptr, a, sp, f.shape, d.sms, stream) != cudaSuccess)
     return PK_ERR_CUDA;
@@ -326,14 +382,12 @@ int pk_distill_backward(int dtype, const void* x, int64_t ldx, const void* w, co
   rows::Device d;
   const int rc = rows::device(&d);
   if (rc != PK_OK) return rc;
-  const int64_t before = lists_bytes(T, top);
-  const Bwd b = plan_backward(dtype, x, ldx, w, db != nullptr, T, D, V, d.sms, workspace ? static_cast<char*>(workspace) + before : nullptr);
-  if (!workspace || workspace_bytes < before + b.bytes) return PK_ERR_NOMEM;
-  Carver c(workspace);
-  const Lists lists = plan_lists(c, T, top);
+  const Back plan = plan_back(dtype, x, ldx, w, db != nullptr, T, D, V, top, d.sms, workspace);
+  if (!workspace || workspace_bytes < plan.bytes) return PK_ERR_NOMEM;
+  const Bwd& b = plan.b;
+  const Lists& lists = plan.lists;
   if (status && cudaMemsetAsync(status, 0, sizeof(int), stream) != cudaSuccess) return PK_ERR_CUDA;
   const float inverse = static_cast<float>(1.0 / temperature);
-  if (lists_launch(lists, idx, values, T, top, V, inverse, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   RowArgs r = {};
   r.labels = lists.label;
   r.T = T;
@@ -351,11 +405,11 @@ int pk_distill_backward(int dtype, const void* x, int64_t ldx, const void* w, co
   r.factor = inverse;
   r.scaled = dtype == PK_F16;
   r.status = status ? status : rows::stream_status(d, stream);
-  if (rows_launch(r, stream) != cudaSuccess) return PK_ERR_CUDA;
+  if (lists_launch(list_args(lists, b.m, idx, values, T, top, V, inverse), r, d.sms, stream) != cudaSuccess) return PK_ERR_CUDA;
   Inputs in;
   if (lay_out(dtype, b.m, x, ldx, w, T, D, V, d.sms, stream, &in) != cudaSuccess) return PK_ERR_CUDA;
   GradParams gp = {};
-  gp.lists = {lists.word, lists.share, b.m.idx, lists.ld};
+  gp.lists = {lists.word, lists.share, lists.first, lists.ld};
   gp.inverse = inverse;
   return backward_pieces<ListGrad>(dtype, b, in, gp, bias, T, D, V, dx, dw, db, r.status, d.sms, stream);
 }

@@ -155,38 +155,34 @@ cudaError_t rows_launch(const RowArgs& a, cudaStream_t stream) {
 // change of base: a fused z log2(e) - m' would be off by up to 2^-24 |m'| in the exponent and overflow for logits past 2^31.
 
 // The words that a row's loss names: one label, or a list of them in ascending order with the probabilities that the
-// gradient takes off there, `ld` a row (a multiple of 4; the list ends with kNoWord). Lists lie at the rows of the batch.
+// gradient takes off there, `ld` a row of the product (the list ends with kNoWord). Of each slice of the vocabulary that a
+// warp of an epilogue empties a table holds, by row, which of the row's words is the first inside: 0 for none, else its place in
+// the list << 8 | its column in the slice + 1. So a warp without words in its slice, most of them, pays one load.
 constexpr int kNoWord = 0x7fffffff;
 struct WordLists {
   const int* word;
   const float* share;
-  const int* rows;  // of the batch, by row of the product
+  const uint32_t* first;  // [slices of the vocabulary][cap]
   int ld;
 };
-// A thread's place in its row's list: the next word not yet met, and the one after it on its way.
+// A thread's place in its row's list: the next word, and the one after it on its way.
 struct WordCursor {
   const int* list;
   int64_t base;  // of the list
   int pos, ld, next, after;
   __device__ __forceinline__ int at(int i) const { return i < ld ? __ldcg(list + i) : kNoWord; }
-  // from the first word at or past `from`
-  __device__ __forceinline__ void start(const WordLists& w, int row, bool live, int from) {
+  // at the first word of slice `slice`, which begins at column `from` of the vocabulary
+  __device__ __forceinline__ void start(const WordLists& w, int64_t cap, int row, bool live, int slice, int from) {
+    const uint32_t e = live ? __ldcg(w.first + slice * cap + row) : 0u;
     ld = w.ld;
-    pos = 0;
-    next = after = kNoWord;
-    base = 0;
-    list = w.word;
-    if (!live) return;
-    base = static_cast<int64_t>(__ldcg(w.rows + row)) * ld;
+    base = static_cast<int64_t>(row) * ld;
     list = w.word + base;
-    const int4* l = reinterpret_cast<const int4*>(list);
-#pragma unroll 4
-    for (int i = 0; i < ld / 4; ++i) {
-      const int4 q = __ldcg(l + i);
-      pos += (q.x < from) + (q.y < from) + (q.z < from) + (q.w < from);
+    pos = static_cast<int>(e >> 8);
+    next = after = kNoWord;
+    if (e) {
+      next = from + static_cast<int>(e & 255u) - 1;
+      after = at(pos + 1);
     }
-    next = at(pos);
-    after = at(pos + 1);
   }
   __device__ __forceinline__ void step() {
     ++pos;
@@ -237,7 +233,7 @@ struct StatEpi {
     const int label = !kList && row < M ? __ldcg(p.lab + row) : -1;
     const float factor = kList ? p.factor : kLog2e;
     WordCursor words;
-    if constexpr (kList) words.start(p.lists, row, row < M, c0);
+    if constexpr (kList) words.start(p.lists, p.cap, row, row < M, c0 / cols, c0);
     const int end = min(cols, N - c0);
     float m = kFloor, l = 0.0f;
 #pragma unroll 1
@@ -345,7 +341,7 @@ struct GradEpi {
     const float g = live ? __ldcg(p.coef + row) : 0.0f, lse = live ? __ldcg(p.lse + row) : 0.0f;
     const int label = !kList && live ? __ldcg(p.lab + row) - p.v0 : -1;
     WordCursor words;
-    if constexpr (kList) words.start(p.lists, row, live, p.v0 + c0);
+    if constexpr (kList) words.start(p.lists, p.cap, row, live, (p.v0 + c0) / cols, p.v0 + c0);
     const int end = min(cols, N - c0);
 #pragma unroll 1
     for (int cc = 0; cc < end; cc += 32) {
