@@ -9,12 +9,11 @@ namespace pk {
 namespace rows {
 
 constexpr int kDzThreads = 256;
-constexpr int kDzBlocks = 4;  // resident blocks of an SM
 constexpr int kDzLeast = 16;  // rows of a block
 // Rows of a block: one wave of resident blocks, all of the same length (fixed blocks of 128 rows left part of the SMs
 // idle at the end). Measured: 65536 x 2048 bf16, gelu and dropout, 159 us (0.75 of the copy rate; issue slots 63 % full).
-inline int dz_rows(int64_t T, int64_t ldz, int sms) {
-  const int64_t blocks = kDzBlocks * sms / ((ldz + 255) / 256);
+inline int dz_rows(int64_t T, int64_t ldz, int sms, int resident) {
+  const int64_t blocks = resident * sms / ((ldz + 255) / 256);
   const int64_t rows = blocks > 1 ? round_up((T + blocks - 1) / blocks, 8) : T;
   return static_cast<int>(rows < kDzLeast ? kDzLeast : rows);
 }
@@ -66,16 +65,16 @@ struct Bwd {
   int64_t blocks, bytes;
 };
 // `made`: dz is not dy itself; `scaled`: fp16's dz may need a scale; `wide`: columns that the kernel which makes dz walks (dz
-// itself has N).
-inline Bwd plan_products(int dtype, const void* x, int64_t ldx, const void* w, bool made, bool scaled, int wide, bool need_dx,
-                         bool need_dw, bool need_db, int64_t T, int N, int K, int sms, void* ws) {
+// itself has N), with `resident` blocks an SM.
+inline Bwd plan_products(int dtype, const void* x, int64_t ldx, const void* w, bool made, bool scaled, int wide, int resident,
+                         bool need_dx, bool need_dw, bool need_db, int64_t T, int N, int K, int sms, void* ws) {
   Bwd b = {};
   Carver c(ws);
   const int terms = dtype == PK_F32 ? gemm::kTerms32 : 1;
   if (need_dw && !in_place(dtype, x, ldx)) b.x = c.take(copy_bytes(dtype, T, K));
   if (need_dx && !in_place(dtype, w, K)) b.w = c.take(copy_bytes(dtype, N, K));
   if (made) b.dz = c.take(copy_bytes(dtype, T, N));
-  b.rows = dz_rows(T, copy_ld(wide), sms);
+  b.rows = dz_rows(T, copy_ld(wide), sms, resident);
   b.blocks = (T + b.rows - 1) / b.rows;
   b.scaled = scaled;
   if (b.scaled) {

@@ -456,8 +456,22 @@ struct Stage {
       }
       return;
     }
+    if constexpr (kE == 2) {
+      // 16-bit columns in pairs, two rows at a time, where the rows begin and end on such
+      if (((reinterpret_cast<uintptr_t>(out) & 3) | (ld & 1) | (N & 1)) == 0) {
+        const int c = 2 * (lane & 15);
+        if (c0 + c >= N) return;
+#pragma unroll 8
+        for (int r = lane >> 4; r < rows; r += 2) {
+          const int64_t row = rowmap ? __ldcg(rowmap + r0 + r) : r0 + r;
+          *reinterpret_cast<uint32_t*>(static_cast<char*>(out) + (row * ld + c0 + c) * kE) =
+              *reinterpret_cast<const uint32_t*>(element(stage, r, c));
+        }
+        return;
+      }
+    }
     if (c0 + lane >= N) return;
-#pragma unroll 4
+#pragma unroll 8
     for (int r = 0; r < rows; ++r) {
       const int64_t row = rowmap ? __ldcg(rowmap + r0 + r) : r0 + r;
       char* d = static_cast<char*>(out) + (row * ld + c0 + lane) * kE;
@@ -486,16 +500,25 @@ struct Stage {
     }
     fetch_ragged(stage, lane, in, ld, r0, c0, rows, N);
   }
+  // (a column a lane: fp32 elements by asynchronous copies too, 16-bit ones sixteen rows at a time)
   static __device__ __noinline__ void fetch_ragged(uint8_t* stage, int lane, const void* in, int64_t ld, int r0, int c0,
                                                    int rows, int N) {
     if (c0 + lane >= N) return;
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const char* s = static_cast<const char*>(in) + ((static_cast<int64_t>(r0) + r) * ld + c0 + lane) * kE;
-      if constexpr (kE == 4)
-        *reinterpret_cast<uint32_t*>(element(stage, r, lane)) = __ldcg(reinterpret_cast<const uint32_t*>(s));
-      else
-        *reinterpret_cast<uint16_t*>(element(stage, r, lane)) = __ldcg(reinterpret_cast<const unsigned short*>(s));
+    const char* s = static_cast<const char*>(in) + (static_cast<int64_t>(r0) * ld + c0 + lane) * kE;
+    if constexpr (kE == 4) {
+      for (int r = 0; r < rows; ++r)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(element(stage, r, lane))), "l"(s + r * ld * kE)
+                     : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      for (int r = 0; r < rows; r += 16) {
+        unsigned short v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = r + i < rows ? __ldcg(reinterpret_cast<const unsigned short*>(s + (r + i) * ld * kE)) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (r + i < rows) *reinterpret_cast<uint16_t*>(element(stage, r + i, lane)) = v[i];
+      }
     }
   }
 };

@@ -263,8 +263,10 @@ cudaError_t few_launch(const FewArgs& a, int sms, cudaStream_t stream) {
 // read and both halves of dz written, their columns summed on the way. The activation and its slope share their
 // exponentials. In fp16 always with the second launch that applies a scale where the largest element asks for one: a
 // product of three factors is no element of dy.
+constexpr int dz_resident(int dtype) { return dtype == PK_F32 ? 2 : 3; }  // blocks of an SM
+
 template <int DT, bool kScale>
-__global__ void __launch_bounds__(kDzThreads, DT == PK_F32 ? 2 : 3) pk_gated_dz_kernel(const __grid_constant__ DzArgs a, int F) {
+__global__ void __launch_bounds__(kDzThreads, (DT == PK_F32 ? 2 : 3)) pk_gated_dz_kernel(const __grid_constant__ DzArgs a, int F) {
   __shared__ float sums[2][8][256];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.y * 256 + lane * 8;
@@ -282,36 +284,53 @@ __global__ void __launch_bounds__(kDzThreads, DT == PK_F32 ? 2 : 3) pk_gated_dz_
     if (e == 0) return;
     scale = scalbnf(1.0f, e);
   }
-  const bool pairs = (F & 7) == 0;  // both halves of dz on 16-byte boundaries
+  // (dz's rows begin on 16-byte boundaries, and so does every eighth column of the gate's half; the other's where F allows)
+  const auto put16 = [&](uint16_t* d, const uint32_t(&q)[4], bool whole) {
+    if (whole) {
+      *reinterpret_cast<uint4*>(d) = make_uint4(q[0], q[1], q[2], q[3]);
+    } else if ((F & 1) == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (2 * j < n) reinterpret_cast<uint32_t*>(d)[j] = q[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) d[j] = static_cast<uint16_t>(q[j >> 1] >> (16 * (j & 1)));
+    }
+  };
   const auto put = [&](int64_t r, int col, float(&v)[8]) {
+    const bool whole = n >= 8 && (col == c || (F & 7) == 0);
+    uint16_t* d = a.dz + r * a.ldz + col;
     if constexpr (DT == PK_F32) {
       uint32_t h[3][4];
       planes8(v, h);
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        uint16_t* d = a.dz + k * a.plane + r * a.ldz + col;
-        if (pairs) {
-          *reinterpret_cast<uint4*>(d) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n) d[j] = static_cast<uint16_t>(h[k][j >> 1] >> (16 * (j & 1)));
-        }
-      }
-    } else if (pairs) {
-      store8<DT>(a.dz, r * a.ldz + col, v);
+      for (int k = 0; k < 3; ++k) put16(d + k * a.plane, h[k], whole);
     } else {
-      store8_any<DT>(a.dz, r * a.ldz + col, n, v);
+      using E = Elem<DT == PK_BF16>;
+      const uint32_t q[4] = {E::pack(v[0], v[1]), E::pack(v[2], v[3]), E::pack(v[4], v[5]), E::pack(v[6], v[7])};
+      put16(d, q, whole);
     }
   };
   if (c < F) {
     const int64_t end = min(r0 + a.rows, a.T);
     Raw8<DT> xd, xg, xu;
+    // vec 1: 16 bytes at a time, 2: 16-bit elements in pairs, 0: one by one
+    const auto read = [&](Raw8<DT>& x, const void* p, int64_t at, int vec) {
+      if constexpr (DT != PK_F32) {
+        if (vec == 2) {
+          const uint32_t* s = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + at);
+          x.q[0] = make_uint4(__ldcg(s), n > 2 ? __ldcg(s + 1) : 0u, n > 4 ? __ldcg(s + 2) : 0u, n > 6 ? __ldcg(s + 3) : 0u);
+          return;
+        }
+      }
+      x.load(p, at, vec == 1, n);
+    };
     const auto load = [&](int64_t r) {
       if (r >= end) return;
-      xd.load(a.dy, r * a.lddy + c, a.dy_vec, n);
-      xg.load(a.pre, r * a.ldpre + c, a.pre_vec, n);
-      xu.load(a.pre, r * a.ldpre + F + c, a.pre_vec, n);
+      read(xd, a.dy, r * a.lddy + c, a.dy_vec);
+      read(xg, a.pre, r * a.ldpre + c, a.pre_vec);
+      read(xu, a.pre, r * a.ldpre + F + c, a.pre_vec);
     };
     load(r0 + w);
 #pragma unroll 1
@@ -378,8 +397,9 @@ __global__ void __launch_bounds__(kDzThreads, DT == PK_F32 ? 2 : 3) pk_gated_dz_
 
 cudaError_t dz_launch(int dtype, DzArgs a, int F, cudaStream_t stream) {
   const int e = elem_bytes(dtype);
-  a.dy_vec = rows16(a.dy, a.lddy, e);
-  a.pre_vec = rows16(a.pre, a.ldpre, e) && (F * e & 15) == 0;
+  const bool even = e == 2 && (F & 1) == 0;  // (an even number of columns left wherever a group of eight begins)
+  a.dy_vec = rows16(a.dy, a.lddy, e) ? 1 : even && aligned_to(a.dy, 4) && (a.lddy & 1) == 0 ? 2 : 0;
+  a.pre_vec = rows16(a.pre, a.ldpre, e) && (F * e & 15) == 0 ? 1 : even && aligned_to(a.pre, 4) ? 2 : 0;
   Launch l(1, kDzThreads, stream);
   l.cfg.gridDim = dim3(static_cast<unsigned int>((a.T + a.rows - 1) / a.rows), static_cast<unsigned int>((F + 255) / 256));
   if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pk_gated_dz_kernel<PK_F32, false>, a, F);
@@ -412,7 +432,7 @@ Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T
 Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, bool need_dx, bool need_dw, bool need_db, int64_t T, int F,
                   int K, int sms, void* ws) {
   const bool made = need_dx || need_dw;
-  return plan_products(dtype, x, ldx, w, made, made && dtype == PK_F16, F, need_dx, need_dw, need_db, T, 2 * F, K, sms, ws);
+  return plan_products(dtype, x, ldx, w, made, made && dtype == PK_F16, F, dz_resident(dtype), need_dx, need_dw, need_db, T, 2 * F, K, sms, ws);
 }
 
 template <int DT>

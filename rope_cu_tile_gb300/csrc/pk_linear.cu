@@ -20,6 +20,8 @@ using namespace rows;
 // ------------------------------------------------------------------------------------
 // dz
 
+constexpr int kDzBlocks = 4;  // resident blocks of an SM
+
 // A warp takes 256 columns of a row (8 a lane: one draw of the generator); a block eight rows at a time.
 // Moves dy, z and dz; bound by issue slots with dropout and gelu (64 % of them, 0.75 of the copy rate).
 // dz is rounded to the element type once: it is an operand of tensor-core products of that type, as x and W are. bf16
@@ -221,7 +223,7 @@ Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, const vo
   const bool made = (need_dx || need_dw) && (act != PK_ACT_NONE || cut || !in_place(dtype, dy, lddy));
   // (without dropout dz of relu, or of no activation, is made of dy's elements and zeros: exact)
   const bool scaled = made && dtype == PK_F16 && (cut || act == PK_ACT_GELU || act == PK_ACT_SILU);
-  return plan_products(dtype, x, ldx, w, made, scaled, N, need_dx, need_dw, need_db, T, N, K, sms, ws);
+  return plan_products(dtype, x, ldx, w, made, scaled, N, kDzBlocks, need_dx, need_dw, need_db, T, N, K, sms, ws);
 }
 
 bool sizes_ok(int64_t T, int N, int K) {
