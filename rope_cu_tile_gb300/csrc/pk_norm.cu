@@ -40,18 +40,33 @@ struct NormArgs {
 template <int kTpr>
 constexpr int kBlock = kTpr <= 32 ? 256 : kTpr;
 
-// A group of elements: the 16 bytes of a row where every row of every matrix begins and ends on such a boundary (kVec), else as
-// many columns kTpr apart, so that a warp's scalar accesses are of neighbours. `n`: columns of the row from the first.
+// A group of elements, 16 bytes of them: neighbours where every row of every matrix begins and ends on a 16-byte boundary
+// (kWhole), pairs of 16-bit elements where on a 4-byte one (kPairs; a warp then reads 128 bytes at once, not 64), else single
+// columns, 2 kTpr or kTpr apart so that a warp's accesses are of neighbours. `n`: columns of the row from the first.
+enum Unit { kSingle, kPairs, kWhole };
 template <int DT>
 constexpr int kE = 16 / Ty<DT>::kBytes;
-template <int DT, int kTpr, bool kVec>
+template <int DT, int kTpr, int kUnit>
 struct Group {
   static constexpr int E = kE<DT>;
+  static constexpr bool kVec = kUnit == kWhole;
   uint4 q;
-  static __device__ __forceinline__ int column(int i, int t) { return kVec ? (i * kTpr + t) * E : i * E * kTpr + t; }
+  // the first column of group i, and how far element j's is from it
+  static __device__ __forceinline__ int column(int i, int t) {
+    return kVec ? (i * kTpr + t) * E : i * E * kTpr + (kUnit == kPairs ? 2 * t : t);
+  }
+  static __device__ __forceinline__ constexpr int offset(int j) {
+    return kVec ? j : kUnit == kPairs ? (j >> 1) * 2 * kTpr + (j & 1) : j * kTpr;
+  }
   __device__ __forceinline__ void load(const void* p, int64_t at, int n) {
     if constexpr (kVec) {
       q = __ldcg(reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes));
+    } else if constexpr (kUnit == kPairs) {
+      const uint16_t* s = static_cast<const uint16_t*>(p) + at;
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = offset(2 * j) < n ? __ldcg(reinterpret_cast<const unsigned int*>(s + offset(2 * j))) : 0u;
+      q = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
       uint32_t w[4];
 #pragma unroll
@@ -89,19 +104,23 @@ struct Group {
   // the elements as they were loaded from here on: what was unpacked of them before is not kept in registers
   __device__ __forceinline__ void forget() { asm volatile("" : "+r"(q.x), "+r"(q.y), "+r"(q.z), "+r"(q.w)); }
   static __device__ __forceinline__ void store(void* p, int64_t at, int n, const float (&v)[E]) {
-    if constexpr (kVec) {
-      uint4 u;
-      if constexpr (DT == PK_F32) {
-        u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    if constexpr (DT != PK_F32 && kUnit != kSingle) {
+      using P = Elem<DT == PK_BF16>;
+      const uint32_t w[4] = {P::pack(v[0], v[1]), P::pack(v[2], v[3]), P::pack(v[4], v[5]), P::pack(v[6], v[7])};
+      uint16_t* d = static_cast<uint16_t*>(p) + at;
+      if constexpr (kVec) {
+        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
-        using P = Elem<DT == PK_BF16>;
-        u = make_uint4(P::pack(v[0], v[1]), P::pack(v[2], v[3]), P::pack(v[4], v[5]), P::pack(v[6], v[7]));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (offset(2 * j) < n) *reinterpret_cast<uint32_t*>(d + offset(2 * j)) = w[j];
       }
-      *reinterpret_cast<uint4*>(static_cast<char*>(p) + at * Ty<DT>::kBytes) = u;
+    } else if constexpr (kVec) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < E; ++j)
-        if (j * kTpr < n) Ty<DT>::put(p, at + j * kTpr, v[j]);
+        if (offset(j) < n) Ty<DT>::put(p, at + offset(j), v[j]);
     }
   }
 };
@@ -151,11 +170,12 @@ __device__ __forceinline__ void to_e4m3(const float (&v)[N], uint32_t (&q)[N / 4
 template <int DT, int kTpr>
 constexpr int kResident = kTpr > 256 ? 1 : (DT == PK_F32 ? 512 : 768) / kBlock<kTpr>;
 
-template <int DT, int kMode, int kTpr, int kNg, bool kVec>
+template <int DT, int kMode, int kTpr, int kNg, int kUnit>
 __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
     pk_norm_kernel(const __grid_constant__ NormArgs a) {
-  using G = Group<DT, kTpr, kVec>;
+  using G = Group<DT, kTpr, kUnit>;
   constexpr int E = G::E;
+  constexpr bool kVec = G::kVec;
   __shared__ float red[kTpr > 32 ? 2 * 16 * 2 : 1];
   constexpr int kRows = kBlock<kTpr> / kTpr;
   const int t = threadIdx.x % kTpr;
@@ -263,7 +283,7 @@ if constexpr (E == 8)
           } else {
 #pragma unroll
             for (int j = 0; j < E; ++j)
-              if (j * kTpr < D - c) d[j * kTpr] = static_cast<uint8_t>(q[j / 4] >> (8 * (j & 3)));
+              if (G::offset(j) < D - c) d[G::offset(j)] = static_cast<uint8_t>(q[j / 4] >> (8 * (j & 3)));
           }
         }
       }
@@ -305,16 +325,17 @@ constexpr int kRowBytes = kBlock<kTpr> * kNg * 16;  // a block's groups of one i
 // stages of the three inputs: two, or one fewer where they do not fit
 template <int DT, int kTpr, int kNg>
 constexpr int kStages = 6 * kRowBytes<DT, kTpr, kNg> * kBackResident<DT, kTpr> <= 200 * 1024 ? 2 : 1;
-template <int DT, int kTpr, int kNg, bool kVec>
+template <int DT, int kTpr, int kNg, int kUnit>
 constexpr int back_smem() {
-  const int ring = kVec ? 3 * kStages<DT, kTpr, kNg> * kRowBytes<DT, kTpr, kNg> : 0, cols = kTpr <= 32 ? kBlock<kTpr> * kNg * kE<DT> * 4 : 0;
+  const int ring = kUnit == kWhole ? 3 * kStages<DT, kTpr, kNg> * kRowBytes<DT, kTpr, kNg> : 0, cols = kTpr <= 32 ? kBlock<kTpr> * kNg * kE<DT> * 4 : 0;
   return ring > cols ? ring : cols;
 }
 
-template <int DT, int kTpr, int kNg, bool kVec>
+template <int DT, int kTpr, int kNg, int kUnit>
 __global__ void __launch_bounds__(kBlock<kTpr>, (kBackResident<DT, kTpr>)) pk_norm_backward_kernel(const __grid_constant__ NormBackArgs a) {
-  using G = Group<DT, kTpr, kVec>;
+  using G = Group<DT, kTpr, kUnit>;
   constexpr int E = G::E;
+  constexpr bool kVec = G::kVec;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[kTpr > 32 ? 2 * 16 * 2 : 1];
   constexpr int kRows = kBlock<kTpr> / kTpr, kCols = kTpr * kNg * E, kS = kStages<DT, kTpr, kNg>;
@@ -493,7 +514,7 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
   for (int i = 0; i < kNg; ++i)
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const int c = G::column(i, t) + (kVec ? j : j * kTpr);
+      const int c = G::column(i, t) + G::offset(j);
       const float v = j & 1 ? sum[i][j >> 1].y : sum[i][j >> 1].x;
       if constexpr (kTpr > 32) {
         if (c < a.D) part[c] = v;
@@ -546,24 +567,51 @@ cudaError_t by_length(int D, const F& f) {
   if (D <= 8192) return f(Cut<256, 32>());
   return f(Cut<512, 32>());
 }
+// (ragged rows are bound by their narrow accesses: fewer lengths)
+template <class F>
+cudaError_t by_ragged_length(int D, const F& f) {
+  if (D <= 256) return f(Cut<8, 32>());
+  if (D <= 1024) return f(Cut<32, 32>());
+  if (D <= 4096) return f(Cut<128, 32>());
+  if (D <= 8192) return f(Cut<256, 32>());
+  return f(Cut<512, 32>());
+}
 static_assert(512 * 32 == kMaxD, "the longest row");
 
-template <int DT, int kMode>
-cudaError_t norm_launch(const NormArgs& a, bool vec, int sms, cudaStream_t stream) {
-  return by_length(a.D, [&](auto cut) {
-    constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>, kRows = kBlock<kTpr> / kTpr;
-    const int64_t blocks = (a.T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * (2048 / kBlock<kTpr>);
-    Launch l(blocks < most ? blocks : most, kBlock<kTpr>, stream);
-    return vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNg, true>, a)
-               : cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNg, false>, a);
+// What every row of a matrix begins and ends on, and of several together.
+Unit unit_of(const void* p, int64_t ld, int D, int e) {
+  if (rows16(p, ld, e) && (D * e & 15) == 0) return kWhole;
+  return e == 2 && aligned_to(p, 4) && ((ld | D) & 1) == 0 ? kPairs : kSingle;
+}
+Unit least(Unit a, Unit b) { return a < b ? a : b; }
+
+// f(Cut, Unit) for a row length and an alignment
+template <int DT, class F>
+cudaError_t by_shape(int D, Unit unit, const F& f) {
+  if (unit == kWhole) return by_length(D, [&](auto cut) { return f(cut, std::integral_constant<int, kWhole>()); });
+  return by_ragged_length(D, [&](auto cut) {
+    if constexpr (DT != PK_F32)
+      if (unit == kPairs) return f(cut, std::integral_constant<int, kPairs>());
+    return f(cut, std::integral_constant<int, kSingle>());
   });
 }
 
-// Blocks of the backward pass: as many as are resident at once, each with its own partial column sums.
+template <int DT, int kMode>
+cudaError_t norm_launch(const NormArgs& a, Unit unit, int sms, cudaStream_t stream) {
+  return by_shape<DT>(a.D, unit, [&](auto cut, auto u) {
+    constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>, kRows = kBlock<kTpr> / kTpr;
+    const int64_t blocks = (a.T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * (2048 / kBlock<kTpr>);
+    Launch l(blocks < most ? blocks : most, kBlock<kTpr>, stream);
+    return cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNg, decltype(u)::value>, a);
+  });
+}
+
+// Blocks of the backward pass: as many as are resident at once, each with its own partial column sums. The workspace is for the
+// most of any alignment.
 template <int DT>
-int64_t back_blocks_of(int64_t T, int D, int sms) {
+int64_t back_blocks_of(int64_t T, int D, Unit unit, int sms) {
   int64_t n = 0;
-  by_length(D, [&](auto cut) {
+  by_shape<DT>(D, unit, [&](auto cut, auto) {
     constexpr int kTpr = decltype(cut)::kTpr, kRows = kBlock<kTpr> / kTpr;
     const int64_t blocks = (T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * kBackResident<DT, kTpr>;
     n = blocks < most ? blocks : most;
@@ -571,18 +619,23 @@ int64_t back_blocks_of(int64_t T, int D, int sms) {
   });
   return n;
 }
-int64_t back_blocks(int dtype, int64_t T, int D, int sms) {
-  return dtype == PK_F32 ? back_blocks_of<PK_F32>(T, D, sms) : back_blocks_of<PK_BF16>(T, D, sms);
+int64_t back_bytes(int dtype, int64_t T, int D, int sms) {
+  const auto most = [&](auto type) {
+    constexpr int DT = decltype(type)::value;
+    const int64_t a = back_blocks_of<DT>(T, D, kWhole, sms), b = back_blocks_of<DT>(T, D, kSingle, sms);
+    return (a > b ? a : b) * D * 4;
+  };
+  return dtype == PK_F32 ? most(std::integral_constant<int, PK_F32>()) : most(std::integral_constant<int, PK_BF16>());
 }
 
 template <int DT>
-cudaError_t back_launch(const NormBackArgs& a, bool vec, int64_t blocks, void* dw, cudaStream_t stream) {
-  return by_length(a.D, [&](auto cut) {
-    constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>;
+cudaError_t back_launch(const NormBackArgs& a, Unit unit, int sms, void* dw, cudaStream_t stream) {
+  const int64_t blocks = back_blocks_of<DT>(a.T, a.D, unit, sms);
+  return by_shape<DT>(a.D, unit, [&](auto cut, auto u) {
+    constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>, kUnit = decltype(u)::value;
     Launch l(blocks, kBlock<kTpr>, stream);
-    l.cfg.dynamicSmemBytes = vec ? back_smem<DT, kTpr, kNg, true>() : back_smem<DT, kTpr, kNg, false>();
-    const cudaError_t e = vec ? cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNg, true>, a)
-                              : cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNg, false>, a);
+    l.cfg.dynamicSmemBytes = back_smem<DT, kTpr, kNg, kUnit>();
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, pk_norm_backward_kernel<DT, kTpr, kNg, kUnit>, a);
     if (e != cudaSuccess || !dw) return e;
     Launch lw((a.D + 31) / 32, 1024, stream);
     const float* part = a.part;
@@ -597,8 +650,8 @@ cudaError_t prepare_back() {
   for (const int D : {64, 256, 1024, 2048, 4096, 8192, kMaxD}) {
     e = by_length(D, [&](auto cut) {
       constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>;
-      return cudaFuncSetAttribute(pk_norm_backward_kernel<DT, kTpr, kNg, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  back_smem<DT, kTpr, kNg, true>());
+      return cudaFuncSetAttribute(pk_norm_backward_kernel<DT, kTpr, kNg, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  back_smem<DT, kTpr, kNg, kWhole>());
     });
     if (e != cudaSuccess) return e;
   }
@@ -636,13 +689,18 @@ int run_norm(int mode, int dtype, const void* x, int64_t ldx, const void* residu
   a.D = D;
   a.eps = eps;
   a.inv_d = 1.0f / static_cast<float>(D);
-  const bool vec = (D * e & 15) == 0 && rows16(x, ldx, e) && (!residual || rows16(residual, ldr, e)) && (!h || rows16(h, ldh, e)) &&
-                   aligned_to(w, 16) && (mode == kNorm ? rows16(y, ldy, e) : aligned_to(y, 16 / e) && (ldy & (16 / e - 1)) == 0);
+  Unit unit = least(unit_of(x, ldx, D, e), unit_of(w, D, D, e));  // (a null w is aligned)
+  if (residual) unit = least(unit, unit_of(residual, ldr, D, e));
+  if (h) unit = least(unit, unit_of(h, ldh, D, e));
+  if (mode == kNorm)
+    unit = least(unit, unit_of(y, ldy, D, e));
+  else if (unit == kWhole && !(aligned_to(y, 16 / e) && (ldy & (16 / e - 1)) == 0))
+    unit = kSingle;
   const auto run = [&](auto type) {
     constexpr int DT = decltype(type)::value;
-    if (mode == kNorm) return norm_launch<DT, kNorm>(a, vec, d.sms, stream);
-    if (mode == kNormQ8) return norm_launch<DT, kNormQ8>(a, vec, d.sms, stream);
-    return norm_launch<DT, kQuantize>(a, vec, d.sms, stream);
+    if (mode == kNorm) return norm_launch<DT, kNorm>(a, unit, d.sms, stream);
+    if (mode == kNormQ8) return norm_launch<DT, kNormQ8>(a, unit, d.sms, stream);
+    return norm_launch<DT, kQuantize>(a, unit, d.sms, stream);
   };
   const cudaError_t r = dtype == PK_F32    ? run(std::integral_constant<int, PK_F32>())
                         : dtype == PK_BF16 ? run(std::integral_constant<int, PK_BF16>())
@@ -688,7 +746,7 @@ int pk_rms_norm_backward_workspace(int dtype, int64_t T, int D, int need_dw, int
   rows::Device d;
   const int rc = rows::device(&d);
   if (rc != PK_OK) return rc;
-  *bytes = back_blocks(dtype, T, D, d.sms) * D * 4;
+  *bytes = back_bytes(dtype, T, D, d.sms);
   return PK_OK;
 }
 
@@ -709,8 +767,7 @@ int pk_rms_norm_backward(int dtype, const void* h, int64_t ldh, const void* w, c
   rows::Device d;
   const int rc = rows::device(&d);
   if (rc != PK_OK) return rc;
-  const int64_t blocks = back_blocks(dtype, T, D, d.sms);
-  if (dw && (!workspace || workspace_bytes < blocks * D * 4)) return PK_ERR_NOMEM;
+  if (dw && (!workspace || workspace_bytes < back_bytes(dtype, T, D, d.sms))) return PK_ERR_NOMEM;
   NormBackArgs a = {};
   a.h = h;
   a.w = w;
@@ -726,11 +783,12 @@ int pk_rms_norm_backward(int dtype, const void* h, int64_t ldh, const void* w, c
   a.D = D;
   a.eps = eps;
   a.inv_d = 1.0f / static_cast<float>(D);
-  const bool vec = (D * e & 15) == 0 && rows16(h, ldh, e) && rows16(dy, lddy, e) && (!dh || rows16(dh, lddh, e)) &&
-                   (!dx || rows16(dx, lddx, e)) && rows::aligned_to(w, 16);
-  const cudaError_t r = dtype == PK_F32    ? back_launch<PK_F32>(a, vec, blocks, dw, stream)
-                        : dtype == PK_BF16 ? back_launch<PK_BF16>(a, vec, blocks, dw, stream)
-                                           : back_launch<PK_F16>(a, vec, blocks, dw, stream);
+  Unit unit = least(least(unit_of(h, ldh, D, e), unit_of(dy, lddy, D, e)), unit_of(w, D, D, e));
+  if (dh) unit = least(unit, unit_of(dh, lddh, D, e));
+  if (dx) unit = least(unit, unit_of(dx, lddx, D, e));
+  const cudaError_t r = dtype == PK_F32    ? back_launch<PK_F32>(a, unit, d.sms, dw, stream)
+                        : dtype == PK_BF16 ? back_launch<PK_BF16>(a, unit, d.sms, dw, stream)
+                                           : back_launch<PK_F16>(a, unit, d.sms, dw, stream);
   return r == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
