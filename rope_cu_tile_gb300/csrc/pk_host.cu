@@ -803,7 +803,7 @@ const char* pk_status_string(int status) {
     case PK_ERR_INTERNAL: return "schedule capacity exceeded (library bug)";
     case PK_ERR_TOO_LARGE: return "T exceeds PK_NOALLOC_MAX_T, the static scratch capacity of pk_attend_noalloc";
     case PK_ERR_CAPTURE: return "stream capture would have to allocate the workspace: make one uncaptured call first";
-    case PK_ERR_BAD_LABEL: return "a label past the vocabulary";
+    case PK_ERR_BAD_LABEL: return "a label, or a target word, past the vocabulary";
     default: return "unknown status";
   }
 }

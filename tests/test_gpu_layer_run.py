@@ -1,7 +1,11 @@
 """The operators as they are used together: a teacher's batch scored and its likeliest words kept, a pre-norm encoder layer with a
 gated feed-forward distilled from them, forwards and backwards against 64-bit autograd; and the layer's 8-bit form."""
 
+import json
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -127,3 +131,86 @@ def test_layer_in_8_bits(pk):
         off = float((y.double() - H64 - want).norm()) / float(want.norm())
         assert off <= 2 * 2.0**-4 * math.sqrt(2 / 3) + 2.0**-6
     assert pk.last_status() == 0
+
+
+_STALL_SCRIPT = """
+import json, os, sys
+sys.path.insert(0, os.getcwd())
+import torch
+import rope_cu_tile_gb300 as pk
+
+torch.manual_seed(0)
+r = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+got = []
+for T in (40, 3000):
+    x, w = r(T, 256), r(512, 256)
+    xq, xs = pk.quantize_rows(x)
+    wq, ws = pk.quantize_rows(w)
+    idx = torch.randint(0, 512, (T, 3), device="cuda")
+    v = torch.randn(T, 3, device="cuda")
+    for call in (lambda: pk.gated_linear(x, w), lambda: pk.linear_q8(xq, xs, wq, ws), lambda: pk.distill(x, w, idx, v)[0]):
+        want = call()
+        torch.cuda.synchronize()
+        os.environ["PK_DEBUG_SKIP_ARRIVE"] = "1"
+        call()
+        torch.cuda.synchronize()
+        del os.environ["PK_DEBUG_SKIP_ARRIVE"]
+        word = pk.last_status()
+        after = call()
+        torch.cuda.synchronize()
+        got.append([word, pk.last_status(), bool(torch.equal(after, want))])
+print(json.dumps(got))
+"""
+
+
+def test_withheld_stage_times_out_and_the_context_stays_usable():
+    env = {k: v for k, v in os.environ.items() if k != "PK_DEBUG_SKIP_ARRIVE"}
+    env["PK_TIMEOUT_MS"] = "100"
+    p = subprocess.run([sys.executable, "-c", _STALL_SCRIPT], env=env, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-3000:]
+    assert json.loads(p.stdout.strip().splitlines()[-1]) == [[6, 0, True]] * 6
+
+
+def test_two_calls_at_once(pk):
+    """The same operators on two streams at the same time, and two captured graphs replayed side by side: no scratch is shared."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(10)
+    dt = torch.bfloat16
+
+    def inputs():
+        T = 700
+        idx = torch.randint(0, V, (T, 5), generator=gen, device="cuda")
+        return dict(x=rand(gen, T, D, dtype=dt), w=rand(gen, D, dtype=dt), up=rand(gen, 2 * F, D, std=D**-0.5, dtype=dt), dy=rand(gen, T, F, dtype=dt),
+                    head=rand(gen, V, D, std=D**-0.5, dtype=dt), idx=idx, values=rand(gen, T, 5), g=rand(gen, T))
+
+    def run(i):
+        y = pk.rms_norm(i["x"], i["w"])
+        a, pre = pk.gated_linear(y, i["up"], return_pre=True)
+        dx, dw, _ = pk.gated_linear_backward(y, i["up"], i["dy"], pre)
+        dn = pk.rms_norm_backward(i["x"], i["w"], dx)
+        loss, lse = pk.distill(y, i["head"], i["idx"], i["values"])
+        dd = pk.distill_backward(y, i["head"], i["idx"], i["values"], lse, i["g"])
+        return (a, dw, *dn, loss, dd[0], dd[1])
+
+    ins = [inputs(), inputs()]
+    want = [[t.clone() for t in run(i)] for i in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    got = []
+    for s, i in zip(streams, ins):
+        with torch.cuda.stream(s):
+            got.append(run(i))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    graphs, outs = [], []
+    for i in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(i))
+        graphs.append(g)
+    for _ in range(3):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(outs, want) for a, b in zip(g, w))
