@@ -19,6 +19,7 @@ and, on the token rows of the same packed batch:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -271,18 +272,30 @@ def pk_last_status(stream) -> int:
 # torch-tensor front (torch only allocates and supplies the stream)
 
 
-def _torch():
-    import torch
+_torch_module = None
+_codes = None  # enum pk_dtype of a torch type
 
-    return torch
+
+def _torch():
+    global _torch_module, _codes
+    if _torch_module is None:
+        import torch
+
+        _codes = {torch.float32: PK_F32, torch.bfloat16: PK_BF16, torch.float16: PK_F16}
+        _torch_module = torch
+    return _torch_module
+
+
+def _code(dtype) -> int:
+    _torch()
+    code = _codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: PK_F32, torch.bfloat16: PK_BF16, torch.float16: PK_F16}
-    if t.dtype not in m:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return _code(t.dtype)
 
 
 def _need(t, shape, dtype, what):
@@ -496,14 +509,23 @@ def _on_stream(dev, stream, tensors, call):
 
 def _here(dev, stream):
     """The raw current stream when the call runs on it and on the current device (the usual case), else None."""
-    cuda = _torch().cuda
-    if stream is None and cuda.current_device() == dev.index:
-        return _torch()._C._cuda_getCurrentRawStream(dev.index)
+    if stream is not None:
+        return None
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
     return None
 
 
 def _rows(t, cols, what, dtype=None, dev=None, rows=None):
     """The row stride of a [T, cols] CUDA matrix whose rows are contiguous (strided rows allowed, none overlapping)."""
+    # (the usual cases in few steps: these checks are part of what a small call takes)
+    shape = t.shape
+    if len(shape) == 2 and t.is_cuda and t.is_contiguous():
+        if cols is None and dtype is None and rows is None:
+            return max(shape[1], 1)
+        if shape[1] == cols and shape[0] == rows and t.dtype == dtype and t.device == dev:
+            return max(cols, 1)
     if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
         raise ValueError(f"{what} must be [{'T' if rows is None else rows}, {'K' if cols is None else cols}], "
                          f"not {tuple(t.shape)}")
@@ -874,6 +896,14 @@ def quantize_rows(x, stream=None):
     return call(st) if st is not None else _on_stream(dev, stream, (x,), call)
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(dev, code, T, D) -> int:
+    """Bytes that pk_rms_norm_backward needs (its sizes alone decide; asked for with the device current)."""
+    n = ctypes.c_int64(0)
+    _check(load().pk_rms_norm_backward_workspace(code, T, D, 1, ctypes.byref(n)), "pk_rms_norm_backward_workspace")
+    return n.value
+
+
 def rms_norm_backward(h, w, dy, dh=None, eps: float = 1e-6, need_dx: bool = True, need_dw: bool = True, out=None, stream=None):
     """(dx [T, D], dw [D]) of `rms_norm` for the gradient dy of its output, each None where not needed; h is the forward's sum
     (x where there was no residual), dh the gradient that arrives on h itself. dx is the gradient of x and of the residual
@@ -900,7 +930,9 @@ def rms_norm_backward(h, w, dy, dh=None, eps: float = 1e-6, need_dx: bool = True
     def call(st):
         dx = out if out is not None or not need_dx else torch.empty((T, D), dtype=dt, device=dev)
         dw = torch.empty(D, dtype=dt, device=dev) if need_dw else None
-        ws, wp, wb = _workspace("pk_rms_norm_backward_workspace", dev, code, T, D, bool(need_dw))
+        wb = _norm_workspace(dev, code, T, D) if need_dw else 0
+        ws = torch.empty(wb, dtype=torch.uint8, device=dev) if wb else None
+        wp = _ptr(ws)
         _check(load().pk_rms_norm_backward(code, h.data_ptr(), ldh, w.data_ptr(), dy.data_ptr(), lddy, _ptr(dh), lddh, eps, T, D,
                                            _ptr(dx), lddx, _ptr(dw), wp, wb, st), "pk_rms_norm_backward")
         return dx, dw
@@ -929,9 +961,7 @@ def linear_q8(x, x_scale, w, w_scale, bias=None, residual=None, act: str = "none
     dt = out_dtype
     if dt is None:
         dt = next((t.dtype for t in (out, residual, bias) if t is not None), torch.bfloat16)
-    code = {torch.float32: PK_F32, torch.bfloat16: PK_BF16, torch.float16: PK_F16}.get(dt)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dt}")
+    code = _code(dt)
     if bias is not None:
         _vector(bias, N, "bias", dt, dev)
     ldr = _rows(residual, N, "residual", dt, dev, T) if residual is not None else N

@@ -237,8 +237,7 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
 
 constexpr int kWarpCap = 128;  // candidates of a warp
 
-// A bound that `top` of a warp's keys, N a lane, reach, and as few more as can be: the top-th largest of them, or one below
-// it that no other reaches; found a bit at a time. 0 where there are not as many above 0.
+// The top-th largest of a warp's keys, N a lane, a bit at a time until that many are left; 0 where there are not as many above 0.
 template <int DT, int N>
 __device__ __forceinline__ uint32_t warp_nth(const uint32_t (&k)[N], int top) {
   uint32_t bound = 0;
@@ -250,7 +249,13 @@ __device__ __forceinline__ uint32_t warp_nth(const uint32_t (&k)[N], int top) {
     for (int i = 0; i < N; ++i) n += k[i] >= probe ? 1 : 0;
     n = __reduce_add_sync(0xffffffffu, n);
     if (n >= top) bound = probe;
-    if (n == top) break;
+    if (n == top) {
+      // (the smallest of them: elements between it and the probe would only be more candidates)
+      uint32_t least = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < N; ++i) least = k[i] >= probe && k[i] < least ? k[i] : least;
+      return __reduce_min_sync(0xffffffffu, least);
+    }
   }
   return bound;
 }
@@ -707,10 +712,10 @@ __device__ __forceinline__ uint32_t ld_remote(uint32_t addr) {
 
 constexpr int kBatch = 4;  // chunks that a thread has in flight
 
-// Bound by the bytes of z where rows are long, with 1280 threads an SM (1024 of fp32) and four loads each in flight, as far as
+// Bound by the bytes of z where rows are long, with 1280 threads an SM (1536 in smaller blocks, 1024 of fp32) and four loads each in flight, as far as
 // instructions go (some 50 for eight 16-bit values); by the way from a row's last load to its last output where they are not.
 template <int DT, int kT, bool kCluster>
-__global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : 1280) / kT) pk_logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
+__global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : kT == 256 ? 1280 : 1536) / kT) pk_logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
   __shared__ LogprobShared<kT> sh;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int part = kCluster ? static_cast<int>(gemm::cluster_rank()) : 0;
@@ -846,8 +851,10 @@ cudaError_t logprobs_launch(const LogprobArgs& a, int sms, cudaStream_t stream) 
   const int parts = parts_of(a.T, a.V, sms);
   if (parts == 1) {
     // what a row takes from its last load to its last output hardly depends on its length: more and smaller blocks for
-    // shorter ones
-    if (a.V <= kMiddle / 4) {
+    // shorter ones, where that leaves at least twice as many maxima as are asked for (64 of 64 bound little: 63880 rows of
+    // 4588 words took a block of 64 1425 us, one of 128 444) and every thread a chunk. 16 likeliest of 65536 x 4300 bf16: 279 us in
+    // either, of 16384 x 16384 153 and 124 (64 and 128 threads), of 8192 x 50000 204 and 168 (128 and 256).
+    if (a.V <= kMiddle / 4 && (a.top <= 32 || a.V < 1040)) {
       Launch l(a.T, 64, stream);
       return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 64, false>, a, 1);
     }
