@@ -30,7 +30,7 @@ struct ListArgs {
   long long* label;      // [T] 0 where the row has a word, -1 where it has none, V where it has one past the vocabulary
   uint32_t* first;       // [slices][cap]
   int64_t cap, entries;  // of first
-  int width;             // of a slice
+  int shift;             // of a slice: 2^shift words
   const int* rows;       // [count] the rows with a word
   const int* count;
   int* word;             // [count, ld] sorted, then kNoWord
@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_const
     // first of a slice has no smaller one in it.
     int at[2] = {0, 0};
     bool lead[2] = {word[0] != kNoWord, word[1] != kNoWord};
-    const int slice[2] = {word[0] / a.width, word[1] / a.width};
+    const int slice[2] = {word[0] >> a.shift, word[1] >> a.shift};
     for (int k = 0; k < a.top; ++k) {
-      const int other = __shfl_sync(0xffffffffu, k < 32 ? word[0] : word[1], k & 31), theirs = other / a.width;
+      const int other = __shfl_sync(0xffffffffu, k < 32 ? word[0] : word[1], k & 31), theirs = other >> a.shift;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const bool smaller = other < word[i] || (other == word[i] && k < lane + 32 * i);
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_const
         a.word[to] = word[i];
         a.share[to] = e[i] / sum;
       }
-      if (lead[i]) a.first[slice[i] * a.cap + row] = static_cast<uint32_t>(at[i]) << 8 | (word[i] - slice[i] * a.width + 1);
+      if (lead[i]) a.first[slice[i] * a.cap + row] = static_cast<uint32_t>(at[i]) << 8 | (word[i] - (slice[i] << a.shift) + 1);
     }
   }
 }
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(256) pk_distill_join_kernel(const float2* part
 
 // the scratch of the lists, beside what the cross entropy has
 struct Lists {
-  int ld, width;
+  int ld, shift;
   int64_t cap, entries;
   int* word;
   float* share;
@@ -184,7 +184,8 @@ struct Lists {
 Lists plan_lists(Carver& c, int64_t T, int V, int top, int width) {
   Lists l;
   l.ld = static_cast<int>(round_up(top, 4));
-  l.width = width;
+  l.shift = 0;
+  while (1 << l.shift < width) ++l.shift;  // (slices are 32, 64 or 128 words)
   l.cap = round_up(T, 256);
   l.entries = (V + width - 1) / width * l.cap;
   l.word = static_cast<int*>(c.take(T * l.ld * 4));
@@ -245,7 +246,7 @@ ListArgs list_args(const Lists& l, const Common& m, const int64_t* idx, const fl
   a.first = l.first;
   a.cap = l.cap;
   a.entries = l.entries;
-  a.width = l.width;
+  a.shift = l.shift;
   a.rows = m.idx;
   a.count = m.count;
   a.word = l.word;
