@@ -3,7 +3,10 @@
  * and its typed forms, pk_attend_noalloc, pk_attend_mixed), its backward pass
  * (pk_attend_backward), the tile schedule (pk_schedule) and the standalone rotation (pk_rope);
  * and what an encoder needs around it on the same token rows: the projection (pk_linear), dropout
- * (pk_dropout) and the cross entropy over a vocabulary (pk_cross_entropy), with their gradients.
+ * (pk_dropout), the cross entropy over a vocabulary (pk_cross_entropy), the root-mean-square norm
+ * (pk_rms_norm), the gated feed-forward (pk_gated_linear), log probabilities and likeliest words
+ * (pk_token_logprobs) and distillation from a teacher's (pk_distill), with their gradients; and
+ * the norm and the projection with rows in 8 bits (pk_rms_norm_q8, pk_linear_q8).
  *
  * The operation (hanzo-kernel 0.2.42 packed.rs, module doc and fn attend / fn attend_ref):
  * attention over packed variable-length sequences straight from a packed QKV projection,
@@ -341,8 +344,9 @@ int pk_rope(int dtype, const void *x, void *y, const void *cos, const void *sin,
 
 /*
  * Token-row operators: what stands around the attention in an encoder, on the rows of the same
- * packed batch -- the projection with its epilogue, dropout, and the cross entropy over a
- * vocabulary, each with its gradient.
+ * packed batch -- the projection with its epilogue, dropout, the norm, the gated feed-forward, the
+ * losses over a vocabulary (labels, a teacher's words) and the log probabilities of given logits,
+ * each with its gradient; and the norm and the projection of rows in 8 bits, for serving.
  *
  * Conventions of these entry points:
  *   - Matrices are row-major in one element type (`dtype`, enum pk_dtype). `ld*` arguments are

@@ -14,6 +14,11 @@ and, on the token rows of the same packed batch:
     linear(x, w, bias, residual, act, p, seed, offset)          linear_backward(x, w, dy, pre, act, p, seed, offset)
     dropout(x, p, seed, offset, residual)                       dropout_backward(dy, p, seed, offset)
     cross_entropy(x, w, labels, bias) -> loss, lse              cross_entropy_backward(x, w, labels, lse, dloss, bias)
+    rms_norm(x, w, residual, eps) -> y, h                       rms_norm_backward(h, w, dy, dh, eps)
+    gated_linear(x, w, bias, act)                               gated_linear_backward(x, w, dy, pre, act)
+    token_logprobs(logits, labels, top)                         token_logprobs_backward(logits, labels, lse, entropy, dlogp, dentropy)
+    distill(x, w, idx, values, bias, temperature)               distill_backward(x, w, idx, values, lse, dloss, bias, temperature)
+    rms_norm_q8, quantize_rows -> rows in e4m3, scales          linear_q8(xq, xs, wq, ws, bias, residual, act, out_dtype)
 """
 
 from __future__ import annotations

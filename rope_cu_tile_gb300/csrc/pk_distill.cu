@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(256) pk_distill_rows_kernel(const __grid_const
   }
 }
 
+// (A chain of latencies: 8 us for 2540 rows of 32 words, 10 with divisions in the place of shifts.)
 // A warp a row that has words: their probabilities, their order, and the first of each slice. Two words of a lane at most.
 __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_constant__ ListArgs a) {
   const int lane = threadIdx.x & 31;

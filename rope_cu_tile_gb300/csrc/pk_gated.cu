@@ -36,6 +36,8 @@ __device__ __forceinline__ const void* up_half(const void* p, int F) {
 
 // A chunk of 32 columns: each half with its bias to `pre` where that is kept, then both again, 16 columns at a time, for y.
 // One staging tile a warp serves the three; an accumulator read twice costs less than the registers to hold both halves.
+// 16384 x 1024 -> 2 x 2624 bf16: 109 us with gelu (a plain product of that size 104; bound by its operands' way through L2 as
+// that is), 121 with both halves kept.
 template <int DT>
 struct GluEpi {
   using Params = GluTiles;
@@ -263,6 +265,7 @@ cudaError_t few_launch(const FewArgs& a, int sms, cudaStream_t stream) {
 // read and both halves of dz written, their columns summed on the way. The activation and its slope share their
 // exponentials. In fp16 always with the second launch that applies a scale where the largest element asks for one: a
 // product of three factors is no element of dy.
+// 65536 x 2624 bf16 272 us (0.95 of the copy rate); 16931 x 1152 f16 37.
 constexpr int dz_resident(int dtype) { return dtype == PK_F32 ? 2 : 3; }  // blocks of an SM
 
 template <int DT, bool kScale>

@@ -714,6 +714,8 @@ constexpr int kBatch = 4;  // chunks that a thread has in flight
 
 // Bound by the bytes of z where rows are long, with 1280 threads an SM (1536 in smaller blocks, 1024 of fp32) and four loads each in flight, as far as
 // instructions go (some 50 for eight 16-bit values); by the way from a row's last load to its last output where they are not.
+// 8192 x 50000 bf16: 127 us without likeliest words (0.97 of the copy rate), 167 with 16. One row of 128000 words, 16 likeliest: 8.0.
+// Four loads ahead in shared memory instead of registers took 210 us: the copies' own instructions cost more than they hide.
 template <int DT, int kT, bool kCluster>
 __global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : kT == 256 ? 1280 : 1536) / kT) pk_logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
   __shared__ LogprobShared<kT> sh;

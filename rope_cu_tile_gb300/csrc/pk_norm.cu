@@ -166,6 +166,8 @@ __device__ __forceinline__ void to_e4m3(const float (&v)[N], uint32_t (&q)[N / 4
   }
 }
 
+// Bound by bytes: 131072 x 1024 bf16 with a residual 161 us, 1.0 of the copy rate; 100000 x 1024 to 8 bits 114 us (issue slots
+// half full); rows off the 16-byte grid pay for narrower accesses (100000 x 1002 bf16 167 us by pairs, x 1003 305 one by one, 120 of bytes).
 // blocks of an SM: 85 registers a thread, 128 of fp32
 template <int DT, int kTpr>
 constexpr int kResident = kTpr > 256 ? 1 : (DT == PK_F32 ? 512 : 768) / kBlock<kTpr>;
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
           to_e4m3(h[i], q);
           uint8_t* d = static_cast<uint8_t*>(a.y) + row * a.ldy + c;
           if constexpr (kVec) {
-if constexpr (E == 8)
+            if constexpr (E == 8)
               *reinterpret_cast<uint2*>(d) = make_uint2(q[0], q[1]);
             else
               *reinterpret_cast<uint32_t*>(d) = q[0];
@@ -315,7 +317,8 @@ struct NormBackArgs {
 // A block keeps its columns' sums of dy n in registers over all of its rows, so there are only as many blocks as are resident
 // at once, and few threads: what covers the latency is that each thread's groups of the next rows are on their way into
 // shared memory (kVec; a thread reads back what it asked for itself, so nothing is synchronized).
-// 16931 x 768 bf16 with dh: 23.8 us without that, on 16 warps an SM with a row in flight each.
+// 16931 x 768 bf16 with dh: 19.4 us (23.8 without that, on 16 warps an SM with a row in flight each), and 2.7 to add the
+// blocks' sums; 131072 x 768 124 us, 0.98 of the copy rate.
 template <int DT, int kTpr>
 constexpr int kBackThreads = kTpr > 256 ? kTpr : 512;  // of an SM: 128 registers
 template <int DT, int kTpr>

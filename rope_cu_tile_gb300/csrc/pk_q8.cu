@@ -28,6 +28,9 @@ struct Q8Tiles : Q8Params {
   int tma_y;
 };
 
+// 16384 x 1024 -> 4096, bf16 results: 50 us (the tensor cores' floor 35: at this K the operands and the 134 MB of results share
+// the way through L2), 68 with bias and gelu, 89 with a residual besides. Stored from registers, 16 or 32 bytes a lane, it took
+// 62 to 80 us; in tiles of 64 columns on eight warps 50 and 76 with gelu.
 template <int DT>
 struct Q8Epi {
   using Params = Q8Tiles;
