@@ -204,10 +204,19 @@ __device__ __forceinline__ float warp_max(float v) {
   const int b = __float_as_int(v), k = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
   return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
+// the sums of kN neighbouring lanes, in each of them
+template <int kN = 32>
 __device__ __forceinline__ Stat warp_join(Stat a) {
-  raise(a, warp_max(a.m));
+  if constexpr (kN == 32) {
+    raise(a, warp_max(a.m));
+  } else {
+    float m = a.m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+    for (int o = kN / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    raise(a, m);
+  }
+#pragma unroll
+  for (int o = kN / 2; o > 0; o >>= 1) {
     a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
     a.u += __shfl_xor_sync(0xffffffffu, a.u, o);
   }
@@ -237,12 +246,24 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
 
 constexpr int kWarpCap = 128;  // candidates of a warp
 
-// The top-th largest of a warp's keys, N a lane, a bit at a time until that many are left; 0 where there are not as many above 0.
-template <int DT, int N>
+// The top-th largest of a warp's keys, N a lane and more than `top` in all: from the highest bit in which any two differ, a bit at a
+// time until that many are left.
+template <int N>
 __device__ __forceinline__ uint32_t warp_nth(const uint32_t (&k)[N], int top) {
-  uint32_t bound = 0;
+  static_assert(32 * N >= kMaxTop, "fewer keys than may be asked for");
+  uint32_t hi = k[0], lo = k[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) {
+    hi = max(hi, k[i]);
+    lo = min(lo, k[i]);
+  }
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (hi == lo) return hi;
+  int b = 31 - __clz(hi ^ lo);
+  uint32_t bound = hi >> b >> 1 << b << 1;
 #pragma unroll 1
-  for (int b = 31 - kKeyShift<DT>; b >= 0; --b) {
+  for (; b >= 0; --b) {
     const uint32_t probe = bound | 1u << b;
     int n = 0;
 #pragma unroll
@@ -415,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_ke
     int n = kWarpCap + 1;
     if (st.s == st.s) {
       // elements whose key reaches the bound: counted, then kept, perhaps not all of them
-      const float bound = of_key<DT>(warp_nth<DT>(key, a.top));
+      const float bound = of_key<DT>(warp_nth(key, a.top));
       const auto each = [&](const auto& take) {
 #pragma unroll 1
         for (int i = 0; i < n_mine; ++i) {
@@ -510,22 +531,27 @@ __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_ke
 // ------------------------------------------------------------------------------------
 // longer rows: a block, or a cluster of blocks where there are few rows
 
-// candidates that a block keeps
+// candidates that are kept
 template <int kT>
 constexpr int kCap = kT >= 256 ? 1024 : 512;
 
+// what the threads find as they go over a slice
 template <int kT>
-struct LogprobShared {
+struct Found {
   Stat stat[kT / 32];
-  Stat mine;               // of the block's slice, read by the cluster's first block
   uint32_t maxima[kT];
-  int chunk[kT];           // where each thread's maximum stands
-  int list[kT];            // threads whose elements are candidates
+  int chunk[kT];  // where each thread's maximum stands
+};
+constexpr int kLook = 2;  // chunks that a thread has in flight in the search
+template <int kT>
+struct Search {
+  int list[kT];           // threads whose elements are candidates
+  int hits[kT / 32][32 + 32 * kLook];  // chunks that hold some, a warp's own
   int listed, found;
   uint32_t bound;
   int bound_chunk;
   uint64_t cand[kCap<kT>];
-  uint64_t few[128];       // of them those that may be among the likeliest; of a slice: its likeliest
+  uint64_t few[128];  // of them those that may be among the likeliest; of a slice: its likeliest
   uint64_t pick[kT / 32];
 };
 
@@ -552,47 +578,87 @@ __device__ __forceinline__ int edge_of(const Slice& s, int t) {
 }
 
 // The candidates of the listed threads' chunks into sh.cand: elements above `bound`, or at it and in a chunk up to `last`.
-// Their count (which may be past what is kept) is returned in every thread.
+// Their count (which may be past what is kept) is returned in every thread. `clean`: there is no NaN, which a maximum passes over.
+// Few chunks hold one: those are noted first and then looked into a lane each, not wherever one of 32 lanes has one.
 template <int DT, int kT>
-__device__ __forceinline__ int collect(LogprobShared<kT>& sh, const Slice& s, int V, float bound, int last) {
-  const auto look = [&](const Raw8<DT>& q, int c) {
-    float v[8];
-    q.get(v);
-    const int first = c * 8 - s.r.off;
-    const uint32_t bits = reach(v, bound, c <= last) & row_bits(first, V);
-    if (bits == 0) return;
-    int at = atomicAdd(&sh.found, __popc(bits));
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (bits >> j & 1u) {
-        if (at < kCap<kT>) sh.cand[at] = packed(key_of<DT>(v[j]), first + j);
-        ++at;
-      }
+__device__ __forceinline__ int collect(Search<kT>& sh, const Slice& s, int V, float bound, int last, bool clean) {
+  const int lane = threadIdx.x & 31;
+  int* const hits = sh.hits[threadIdx.x >> 5];
+  int have = 0;  // chunks in `hits`
+  const auto keep = [&](bool is, int c) {
+    const uint32_t votes = __ballot_sync(0xffffffffu, is);
+    if (is) hits[have + __popc(votes & ((1u << lane) - 1u))] = c;
+    have += __popc(votes);
   };
-  const int each = (s.w1 - s.w0 + kT - 1) / kT, n = sh.listed * each;
-#pragma unroll 2
-  for (int i = threadIdx.x; i < n; i += kT) {
-    const int k = i / each, c = s.w0 + sh.list[k] + (i - k * each) * kT;
-    if (c >= s.w1 || *reinterpret_cast<volatile int*>(&sh.found) > kCap<kT>) continue;  // (too many already)
-    Raw8<DT> q;
-    q.load(s.r.p, c * 8 - s.r.off, true, 8);
-    look(q, c);
+  // the elements of the first n <= 32 of them, a chunk a lane
+  const auto drain = [&](int n) {
+    __syncwarp();
+    if (lane < n) {
+      const int c = hits[lane], first = c * 8 - s.r.off;
+      Raw8<DT> q;
+      fetch<DT>(q, s.r, c, V);
+      float v[8];
+      q.get(v);
+      const uint32_t bits = reach(v, bound, c <= last) & row_bits(first, V);
+      if (bits != 0) {
+        int at = atomicAdd(&sh.found, __popc(bits));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (bits >> j & 1u) {
+            if (at < kCap<kT>) sh.cand[at] = packed(key_of<DT>(v[j]), first + j);
+            ++at;
+          }
+      }
+    }
+    have -= n;
+    __syncwarp();
+    for (int i = 0; i < have; i += 32) {  // (those behind, to the front)
+      const int more = i + lane < have ? hits[n + i + lane] : 0;
+      __syncwarp();
+      if (i + lane < have) hits[i + lane] = more;
+      __syncwarp();
+    }
+  };
+  if (threadIdx.x < 32) {
+    const int edge = edge_of(s, lane);
+    keep(edge >= 0, edge);
   }
-  const int edge = edge_of(s, threadIdx.x);
-  if (edge >= 0) {
-    Raw8<DT> q;
-    fetch<DT>(q, s.r, edge, V);
-    look(q, edge);
+  // chunk j of listed thread k is w0 + list[k] + j kT; this thread's are kT apart in the list of (k, j)
+  const int each = (s.w1 - s.w0 + kT - 1) / kT, dk = kT / each, dj = kT - dk * each, n = sh.listed;
+  int k = threadIdx.x / each, j = threadIdx.x - k * each;
+#pragma unroll 1
+  for (int i0 = threadIdx.x & ~31; i0 < n * each; i0 += kLook * kT) {
+    Raw8<DT> q[kLook];
+    int at[kLook];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      at[i] = k < n ? s.w0 + sh.list[k] + j * kT : s.w1;
+      if (at[i] < s.w1) q[i].load(s.r.p, at[i] * 8 - s.r.off, true, 8);
+      k += dk;
+      j += dj;
+      if (j >= each) {
+        j -= each;
+        ++k;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+      bool is = at[i] < s.w1;
+      if (is && clean) is = top8<DT>(q[i]) >= bound;
+      keep(is, at[i]);
+    }
+#pragma unroll 1
+    while (have >= 32 || (have > 0 && i0 + kLook * kT >= n * each)) drain(min(have, 32));
+    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&sh.found) > kCap<kT>)) break;  // (more than are kept: enough seen)
   }
   __syncthreads();
   return sh.found;
 }
 
-// The first `top` of sh.cand[0 .. n) to `emit`, by warp 0. Of many, first the top-th: no two are equal, so exactly `top` reach it.
+// The first `top` of sh.cand[0 .. n) to `emit`, by a warp. Of many, first the top-th: no two are equal, so exactly `top` reach it.
 template <int kT, class Emit>
-__device__ __forceinline__ void finish(LogprobShared<kT>& sh, int n, int top, const Emit& emit) {
+__device__ __forceinline__ void finish(Search<kT>& sh, int n, int top, const Emit& emit) {
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x >= 32) return;
   if (n <= 128) {
     first_of(sh.cand, n, top, lane, emit);
     return;
@@ -619,19 +685,16 @@ __device__ __forceinline__ void finish(LogprobShared<kT>& sh, int n, int top, co
   first_of(sh.few, have, top, lane, emit);
 }
 
-// The slice's `top` likeliest words to `emit`. Every thread has a chunk of the slice; sh.maxima, sh.chunk are written, and the
-// block synchronized.
+// The slice's `top` likeliest words to `emit`. Each thread has a chunk of the slice and its maximum in `fd`; the block is synchronized.
 template <int DT, int kT, class Emit>
-__device__ __forceinline__ void slice_top(LogprobShared<kT>& sh, const Slice& s, int V, int top, const Emit& emit) {
+__device__ __forceinline__ void slice_top(Search<kT>& sh, const Found<kT>& fd, const Slice& s, int V, int top, bool clean, const Emit& emit) {
   const int lane = threadIdx.x & 31;
-  // warp 0 names the threads whose elements may be among them: of those whose maximum is the bound only the ones that stand no
-  // later than `last`
-  const auto name = [&](uint32_t bound, int last) {
+  // a warp names the threads whose elements may be among them
+  const auto name = [&](uint32_t bound, int last, const auto& may) {
     int n = 0;
+#pragma unroll
     for (int i = 0; i < kT / 32; ++i) {
-      const uint32_t k = sh.maxima[i * 32 + lane];
-      const int c = sh.chunk[i * 32 + lane];
-      const bool is = k > bound || (k == bound && (c <= last || c == kAnywhere));
+      const bool is = may(i);
       const uint32_t votes = __ballot_sync(0xffffffffu, is);
       if (is) sh.list[n + __popc(votes & ((1u << lane) - 1u))] = i * 32 + lane;
       n += __popc(votes);
@@ -646,12 +709,13 @@ __device__ __forceinline__ void slice_top(LogprobShared<kT>& sh, const Slice& s,
   if (threadIdx.x < 32) {
     uint32_t k[kT / 32];
 #pragma unroll
-    for (int i = 0; i < kT / 32; ++i) k[i] = sh.maxima[i * 32 + lane];
-    name(warp_nth<DT>(k, top), 0x7fffffff);
+    for (int i = 0; i < kT / 32; ++i) k[i] = fd.maxima[i * 32 + lane];
+    const uint32_t nth = warp_nth(k, top);
+    name(nth, 0x7fffffff, [&](int i) { return k[i] >= nth; });
   }
   __syncthreads();
   const uint32_t bound = sh.bound;
-  int n = collect<DT, kT>(sh, s, V, of_key<DT>(bound), 0x7fffffff);
+  int n = collect<DT, kT>(sh, s, V, of_key<DT>(bound), 0x7fffffff, clean);
   if (n > kCap<kT>) {
     // many equal ones (a masked vocabulary): of those at the bound only the first chunks', up to the one that completes `top`
     __syncthreads();
@@ -661,16 +725,21 @@ __device__ __forceinline__ void slice_top(LogprobShared<kT>& sh, const Slice& s,
       for (int b = 17; b >= 0; --b) {  // the largest chunk before which there are still fewer than `top`
         const int probe = at | 1 << b;
         int m = 0;
-        for (int i = lane; i < kT; i += 32) m += sh.maxima[i] > bound || (sh.maxima[i] == bound && sh.chunk[i] < probe) ? 1 : 0;
+        for (int i = lane; i < kT; i += 32) m += fd.maxima[i] > bound || (fd.maxima[i] == bound && fd.chunk[i] < probe) ? 1 : 0;
         if (__reduce_add_sync(0xffffffffu, m) < top) at = probe;
       }
-      name(bound, at);
+      // (of those whose maximum is the bound only the ones that stand no later)
+      name(bound, at, [&](int i) {
+        const uint32_t k = fd.maxima[i * 32 + lane];
+        const int c = fd.chunk[i * 32 + lane];
+        return k > bound || (k == bound && (c <= at || c == kAnywhere));
+      });
     }
     __syncthreads();
-    n = collect<DT, kT>(sh, s, V, of_key<DT>(bound), sh.bound_chunk);
+    n = collect<DT, kT>(sh, s, V, of_key<DT>(bound), sh.bound_chunk, clean);
   }
   if (n <= kCap<kT>) {
-    finish<kT>(sh, n, top, emit);
+    if (threadIdx.x < 32) finish<kT>(sh, n, top, emit);
     return;
   }
   // many large ones in few threads: one maximum after another
@@ -712,23 +781,12 @@ __device__ __forceinline__ uint32_t ld_remote(uint32_t addr) {
 
 constexpr int kBatch = 4;  // chunks that a thread has in flight
 
-// Bound by the bytes of z where rows are long, with 1280 threads an SM (1536 in smaller blocks, 1024 of fp32) and four loads each in flight, as far as
-// instructions go (some 50 for eight 16-bit values); by the way from a row's last load to its last output where they are not.
-// 8192 x 50000 bf16: 127 us without likeliest words (0.97 of the copy rate), 167 with 16. One row of 128000 words, 16 likeliest: 8.0.
-// Four loads ahead in shared memory instead of registers took 210 us: the copies' own instructions cost more than they hide.
-template <int DT, int kT, bool kCluster>
-__global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : kT == 256 ? 1280 : 1536) / kT) pk_logprobs_kernel(const __grid_constant__ LogprobArgs a, int parts) {
-  __shared__ LogprobShared<kT> sh;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int part = kCluster ? static_cast<int>(gemm::cluster_rank()) : 0;
-  const int64_t row = kCluster ? blockIdx.x / parts : blockIdx.x;
-  griddep_wait();
-  const Slice sl = slice_at<DT>(a, row, part, kCluster ? parts : 1);
-  long long label = -1;
-  float picked = 0.0f;
-  if (threadIdx.x == 0 && part == 0) label = __ldcg(a.labels + row);
+// One of kT threads over its chunks of a slice: its sums, and the chunk `at` where its maximum stands.
+template <int DT, int kT>
+__device__ __forceinline__ Stat go_over(const Slice& sl, int V, int& at) {
+  const int t = threadIdx.x;
   Stat st = nothing();
-  int at = sl.w0 + threadIdx.x;  // the chunk of the maximum
+  at = sl.w0 + t;
   // `kN` chunks from c on, kT apart
   const auto take = [&](const auto& q, int c) {
     constexpr int kN = sizeof(q) / sizeof(Raw8<DT>);
@@ -755,7 +813,7 @@ __global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : kT == 256 ? 1280 : 
 #pragma unroll
     for (int i = 0; i < kN; ++i) accumulate<DT>(st, q[i]);
   };
-  int c = sl.w0 + threadIdx.x;
+  int c = sl.w0 + t;
 #pragma unroll 1
   for (; c + (kBatch - 1) * kT < sl.w1; c += kBatch * kT) {
     Raw8<DT> q[kBatch];
@@ -769,66 +827,111 @@ __global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : kT == 256 ? 1280 : 
     q[0].load(sl.r.p, c * 8 - sl.r.off, true, 8);
     take(q, c);
   }
-  const int edge = edge_of(sl, threadIdx.x);
+  const int edge = edge_of(sl, t);
   if (edge >= 0) {
     Raw8<DT> q[1];
-    fetch<DT>(q[0], sl.r, edge, a.V);
+    fetch<DT>(q[0], sl.r, edge, V);
     take(q, edge);
   }
+  return st;
+}
+template <int DT, int kT>
+__device__ __forceinline__ void leave(Found<kT>& fd, const Stat& mine, const Stat& warps, int at) {
+  // (a sum without a value: one of the thread's elements is infinite or NaN, so at least infinity, in a chunk unknown. No sum
+  // at all: every element is -inf, the first of them in its first chunk)
+  const bool nan = mine.s != mine.s;
+  fd.maxima[threadIdx.x] = key_of<DT>(nan ? INFINITY : mine.s == 0.0f ? -INFINITY : mine.m);
+  fd.chunk[threadIdx.x] = nan ? kAnywhere : at;
+  if ((threadIdx.x & 31) == 0) fd.stat[threadIdx.x >> 5] = warps;
+}
+template <int kT>
+__device__ __forceinline__ Stat joined(const Found<kT>& fd) {
+  return warp_join<kT / 32>(fd.stat[threadIdx.x % (kT / 32)]);
+}
+
+// Bound by the bytes of z where rows are long, with 1280 threads an SM (1536 in smaller blocks, 1024 of fp32) and four loads each in flight, as far as
+// instructions go (some 50 for eight 16-bit values); by the way from a row's last load to its last output where they are not.
+// 8192 x 50000 bf16: 126 us without likeliest words (0.97 of the copy rate), 163 with 16. One row of 128000 words, 16 likeliest: 8.0.
+// Not kept: four loads ahead in shared memory instead of registers (210 us: the copies' own instructions cost more than they hide)
+// or in registers, with fewer blocks (166); the next row's words fetched into L2 during the search (171, when the search took
+// longer); one or two warps more a block that search while the others go over the next row (273 and 197: a few hundred instructions
+// in one chain, among 32 warps that ask for the same issue slots).
+template <int DT, int kT>
+__global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : kT == 256 ? 1280 : 1536) / kT) pk_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+  __shared__ Found<kT> found;
+  __shared__ Search<kT> search;
+  const int64_t row = blockIdx.x;
+  griddep_wait();
+  const Slice sl = slice_at<DT>(a, row, 0, 1);
+  long long label = -1;
+  float picked = 0.0f;
+  if (threadIdx.x == 0) label = __ldcg(a.labels + row);
+  int at;
+  const Stat mine = go_over<DT, kT>(sl, a.V, at);
   if (label >= 0 && label < a.V) picked = Ty<DT>::get(sl.r.p, label);  // (asked for here, used below)
-  if (a.top > 0) {
-    // (a sum without a value: one of the thread's elements is infinite or NaN, so at least infinity, in a chunk unknown. No sum
-    // at all: every element is -inf, the first of them in its first chunk)
-    const bool nan = st.s != st.s;
-    sh.maxima[threadIdx.x] = key_of<DT>(nan ? INFINITY : st.s == 0.0f ? -INFINITY : st.m);
-    sh.chunk[threadIdx.x] = nan ? kAnywhere : at;
-  }
-  st = warp_join(st);
-  if (lane == 0) sh.stat[w] = st;
+  leave<DT, kT>(found, mine, warp_join(mine), at);
   __syncthreads();
-  st = nothing();
-  if (lane < kT / 32) st = sh.stat[lane];
-  st = warp_join(st);
-  if constexpr (!kCluster) {
-    if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
-    if (a.top == 0) return;
-    const float rest = logf(st.s);
-    slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, uint32_t k, int e) {
-      a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(k));
-      a.top_idx[row * a.top + i] = e;
-    });
-  } else {
-    if (a.top > 0) slice_top<DT, kT>(sh, sl, a.V, a.top, [&](int i, uint32_t k, int e) { sh.few[i] = packed(k, e); });
-    if (threadIdx.x == 0) sh.mine = st;
-    gemm::cluster_sync();
-    if (part == 0) {
-      // the slices' sums and likeliest words, a warp a slice
-      st = nothing();
-      if (lane < parts) {
-        const uint32_t from = remote(&sh.mine, lane);
-        st = {__uint_as_float(ld_remote(from)), __uint_as_float(ld_remote(from + 4)), __uint_as_float(ld_remote(from + 8))};
-      }
-      for (int p = w; p < parts && a.top > 0; p += kT / 32) {
-        const uint32_t from = remote(&sh.few[0], p);
-        for (int i = lane; i < a.top; i += 32)
-          sh.cand[p * a.top + i] = ld_remote(from + 8 * i) | static_cast<uint64_t>(ld_remote(from + 8 * i + 4)) << 32;
-      }
-      st = warp_join(st);
-      if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
-      __syncthreads();
-      const float rest = logf(st.s);
-      if (a.top > 0)
-        finish<kT>(sh, parts * a.top, a.top, [&](int i, uint32_t k, int e) {
-          a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(k));
-          a.top_idx[row * a.top + i] = e;
-        });
+  const Stat st = joined(found);
+  if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
+  if (a.top == 0) return;
+  const float rest = logf(st.s);
+  slice_top<DT, kT>(search, found, sl, a.V, a.top, st.s == st.s, [&](int i, uint32_t k, int e) {
+    a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(k));
+    a.top_idx[row * a.top + i] = e;
+  });
+}
+
+// few rows: a cluster of blocks a row, each its part of it, and the first joins what they find
+template <int DT, int kT>
+__global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : 1280) / kT) pk_logprobs_cluster_kernel(const __grid_constant__ LogprobArgs a, int parts) {
+  __shared__ Found<kT> found;
+  __shared__ Search<kT> search;
+  __shared__ Stat whole;  // the slice's
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int part = static_cast<int>(gemm::cluster_rank());
+  const int64_t row = blockIdx.x / parts;
+  griddep_wait();
+  const Slice sl = slice_at<DT>(a, row, part, parts);
+  long long label = -1;
+  float picked = 0.0f;
+  if (threadIdx.x == 0 && part == 0) label = __ldcg(a.labels + row);
+  int at;
+  const Stat mine = go_over<DT, kT>(sl, a.V, at);
+  if (label >= 0 && label < a.V) picked = Ty<DT>::get(sl.r.p, label);  // (asked for here, used below)
+  leave<DT, kT>(found, mine, warp_join(mine), at);
+  __syncthreads();
+  Stat st = joined(found);
+  if (a.top > 0)
+    slice_top<DT, kT>(search, found, sl, a.V, a.top, st.s == st.s, [&](int i, uint32_t k, int e) { search.few[i] = packed(k, e); });
+  if (threadIdx.x == 0) whole = st;
+  gemm::cluster_sync();
+  if (part == 0) {
+    // the slices' sums and likeliest words, a warp a slice
+    st = nothing();
+    if (lane < parts) {
+      const uint32_t from = remote(&whole, lane);
+      st = {__uint_as_float(ld_remote(from)), __uint_as_float(ld_remote(from + 4)), __uint_as_float(ld_remote(from + 8))};
     }
-    gemm::cluster_sync();  // (no block leaves while its memory is read)
+    for (int p = w; p < parts && a.top > 0; p += kT / 32) {
+      const uint32_t from = remote(&search.few[0], p);
+      for (int i = lane; i < a.top; i += 32)
+        search.cand[p * a.top + i] = ld_remote(from + 8 * i) | static_cast<uint64_t>(ld_remote(from + 8 * i + 4)) << 32;
+    }
+    st = warp_join(st);
+    if (threadIdx.x == 0) write_row<DT>(a, row, st, picked, label);
+    __syncthreads();
+    const float rest = logf(st.s);
+    if (a.top > 0 && w == 0)
+      finish<kT>(search, parts * a.top, a.top, [&](int i, uint32_t k, int e) {
+        a.top_logp[row * a.top + i] = logp_of(st, rest, of_key<DT>(k));
+        a.top_idx[row * a.top + i] = e;
+      });
   }
+  gemm::cluster_sync();  // (no block leaves while its memory is read)
 }
 
 constexpr int kShort = 704;     // words of a row of a warp
-constexpr int kMiddle = 16384;  // words of a row of a block of 128 threads, and four times those of 64
+constexpr int kMiddle = 32768;  // words of a row of a block of 128 threads, and four times those of 64
 
 // Blocks a row: one where the rows fill the SMs, up to eight where they do not, none with fewer than 4096 words.
 int parts_of(int64_t T, int V, int sms) {
@@ -845,6 +948,12 @@ cudaError_t short_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&l.cfg, pk_logprobs_short_kernel<DT, kC>, a);
 }
 
+template <int DT, int kT>
+cudaError_t rows_launch(const LogprobArgs& a, cudaStream_t stream) {
+  Launch l(a.T, kT, stream);
+  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, kT>, a);
+}
+
 template <int DT>
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
   // a warp's row: up to three chunks a lane. (Longer ones took a warp longer than a block of 64: 65536 rows of 1500 words with 16
@@ -854,18 +963,11 @@ cudaError_t logprobs_launch(const LogprobArgs& a, int sms, cudaStream_t stream) 
   if (parts == 1) {
     // what a row takes from its last load to its last output hardly depends on its length: more and smaller blocks for
     // shorter ones, where that leaves at least twice as many maxima as are asked for (64 of 64 bound little: 63880 rows of
-    // 4588 words took a block of 64 1425 us, one of 128 444) and every thread a chunk. 16 likeliest of 65536 x 4300 bf16: 279 us in
-    // either, of 16384 x 16384 153 and 124 (64 and 128 threads), of 8192 x 50000 204 and 168 (128 and 256).
-    if (a.V <= kMiddle / 4 && (a.top <= 32 || a.V < 1040)) {
-      Launch l(a.T, 64, stream);
-      return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 64, false>, a, 1);
-    }
-    if (a.V <= kMiddle) {
-      Launch l(a.T, 128, stream);
-      return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 128, false>, a, 1);
-    }
-    Launch l(a.T, 256, stream);
-    return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 256, false>, a, 1);
+    // 4588 words took a block of 64 1425 us, one of 128 389) and every thread a chunk. 16 likeliest in bf16: of 65536 x 4300 233 us
+    // and 278 (blocks of 64 and 128), 16384 x 16384 151 and 115, 16384 x 30000 198 and 244 (128 and 256), 8192 x 50000 185 and 163.
+    if (a.V <= kMiddle / 4 && (a.top <= 32 || a.V < 1040)) return rows_launch<DT, 64>(a, stream);
+    if (a.V <= kMiddle) return rows_launch<DT, 128>(a, stream);
+    return rows_launch<DT, 256>(a, stream);
   }
   Launch l(a.T * parts, 256, stream);
   cudaLaunchAttribute at[2] = {l.at[0], {}};
@@ -874,7 +976,7 @@ cudaError_t logprobs_launch(const LogprobArgs& a, int sms, cudaStream_t stream) 
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   l.cfg.attrs = at;
   l.cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_kernel<DT, 256, true>, a, parts);
+  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_cluster_kernel<DT, 256>, a, parts);
 }
 
 // ------------------------------------------------------------------------------------
