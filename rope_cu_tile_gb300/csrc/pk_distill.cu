@@ -60,61 +60,82 @@ __global__ void __launch_bounds__(256) pk_distill_rows_kernel(const __grid_const
   }
 }
 
-// (A chain of latencies: 8 us for 2540 rows of 32 words, 10 with divisions in the place of shifts.)
-// A warp a row that has words: their probabilities, their order, and the first of each slice. Two words of a lane at most.
+// 32 kR numbers of a warp in ascending order, number r 32 + lane in v[r]: a bitonic network, through shuffles within 32.
+template <int kR>
+__device__ __forceinline__ void ascend(uint32_t (&v)[kR], int lane) {
+  static_assert(kR <= 2, "");
+#pragma unroll
+  for (int k = 2; k <= 32 * kR; k *= 2) {
+    if (k == 64) {
+      const uint32_t lo = min(v[0], v[kR - 1]);
+      v[kR - 1] = max(v[0], v[kR - 1]);
+      v[0] = lo;
+    }
+#pragma unroll
+    for (int j = k < 64 ? k / 2 : 16; j > 0; j /= 2)
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const uint32_t u = __shfl_xor_sync(0xffffffffu, v[r], j);
+        v[r] = !((r * 32 + lane) & k) == !(lane & j) ? min(v[r], u) : max(v[r], u);
+      }
+  }
+}
+
+// A warp a row that has words: their probabilities, their order (by word, equal ones by their place in the list; those that are
+// not there last), and the first of each slice. One word a lane, or two. A chain of latencies.
+constexpr int kGone = PK_ROWS_MAX_DIM;  // a word that is not there, among 26 bits with the place
+template <int kR>
 __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_constant__ ListArgs a) {
   const int lane = threadIdx.x & 31;
   griddep_wait();
   const int n = __ldcg(a.count);
   for (int64_t row = blockIdx.x * 8LL + (threadIdx.x >> 5); row < n; row += gridDim.x * 8LL) {
     const int64_t t = __ldcg(a.rows + row);
-    int word[2];
-    float v[2];
+    uint32_t key[kR];
+    float e[kR], m = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kR; ++i) {
       const int k = lane + 32 * i;
       long long x = -1;
-      v[i] = -INFINITY;
+      float v = -INFINITY;
       if (k < a.top) {
         x = __ldcg(a.idx + t * a.top + k);
-        v[i] = __ldcg(a.values + t * a.top + k);
+        v = __ldcg(a.values + t * a.top + k);
       }
-      word[i] = there(x, v[i]) ? static_cast<int>(x) : kNoWord;
-      v[i] = word[i] == kNoWord ? -INFINITY : v[i] * a.inverse;
+      const bool is = there(x, v);
+      key[i] = static_cast<uint32_t>(is ? static_cast<int>(x) : kGone) << 6 | static_cast<uint32_t>(k);
+      e[i] = is ? v * a.inverse : -INFINITY;
+      m = fmaxf(m, e[i]);
     }
     // (a NaN among the values, or an infinity, comes through the exponentials)
-    float m = fmaxf(v[0], v[1]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float e[2], sum;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) e[i] = word[i] == kNoWord ? 0.0f : expf(v[i] - m);
-    sum = e[0] + e[1];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    // the place of each word: how many are smaller, equal ones by their place in the list; those that are not there last. The
-    // first of a slice has no smaller one in it.
-    int at[2] = {0, 0};
-    bool lead[2] = {word[0] != kNoWord, word[1] != kNoWord};
-    const int slice[2] = {word[0] >> a.shift, word[1] >> a.shift};
-    for (int k = 0; k < a.top; ++k) {
-      const int other = __shfl_sync(0xffffffffu, k < 32 ? word[0] : word[1], k & 31), theirs = other >> a.shift;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool smaller = other < word[i] || (other == word[i] && k < lane + 32 * i);
-        at[i] += smaller ? 1 : 0;
-        lead[i] = lead[i] && !(smaller && theirs == slice[i]);
-      }
+    for (int i = 0; i < kR; ++i) {
+      e[i] = key[i] >> 6 == kGone ? 0.0f : expf(e[i] - m);
+      sum += e[i];
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = lane + 32 * i;
-      if (k < a.ld) {
-        const int64_t to = row * a.ld + (k < a.top ? at[i] : k);
-        a.word[to] = word[i];
-        a.share[to] = e[i] / sum;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    ascend<kR>(key, lane);
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      const int word = static_cast<int>(key[i] >> 6), place = static_cast<int>(key[i] & 63u), at = lane + 32 * i;
+      float mine = __shfl_sync(0xffffffffu, e[0], place & 31);
+      if (kR > 1) {
+        const float second = __shfl_sync(0xffffffffu, e[kR - 1], place & 31);
+        mine = place >= 32 ? second : mine;
       }
-      if (lead[i]) a.first[slice[i] * a.cap + row] = static_cast<uint32_t>(at[i]) << 8 | (word[i] - (slice[i] << a.shift) + 1);
+      int before = __shfl_up_sync(0xffffffffu, word, 1);
+      const int end = __shfl_sync(0xffffffffu, static_cast<int>(key[0] >> 6), 31);
+      if (lane == 0) before = i > 0 ? end : -1;
+      if (at < a.ld) {
+        a.word[row * a.ld + at] = word == kGone ? kNoWord : word;
+        a.share[row * a.ld + at] = mine / sum;
+      }
+      const int slice = word >> a.shift;
+      if (word != kGone && (before < 0 || before >> a.shift != slice))
+        a.first[slice * a.cap + row] = static_cast<uint32_t>(at) << 8 | (word - (slice << a.shift) + 1);
     }
   }
 }
@@ -260,7 +281,7 @@ cudaError_t lists_launch(const ListArgs& a, const RowArgs& r, int sms, cudaStrea
   Launch l(blocks < most ? blocks : most, 256, stream);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, pk_distill_rows_kernel, a);
   if (e != cudaSuccess || (e = rows_launch(r, stream)) != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&l.cfg, pk_distill_list_kernel, a);
+  return a.top <= 32 ? cudaLaunchKernelEx(&l.cfg, pk_distill_list_kernel<1>, a) : cudaLaunchKernelEx(&l.cfg, pk_distill_list_kernel<2>, a);
 }
 
 bool distill_ok(int dtype, int64_t T, int D, int V, int top, double temperature) {
