@@ -140,12 +140,13 @@ __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_const
   }
 }
 
-// The slices of each row joined, as pk_xent_join_kernel does, and the loss from the logits that the list names: 8 rows x 32
+// The slices of each row joined, as pk_xent_join_kernel does, and the loss from the logits that the list names: 8 rows x kLanes
 // strided lanes of slices a block, then 32 lanes of words a row.
-__global__ void __launch_bounds__(256) pk_distill_join_kernel(const float2* part, int64_t cap, int slices, const float* picked,
-                                                              const int* word, const float* share, int ld, float inverse,
-                                                              const int* idx, const int* count, float* loss, float* lse) {
-  __shared__ float2 s[32][8];
+template <int kLanes>
+__global__ void __launch_bounds__(8 * kLanes) pk_distill_join_kernel(const float2* part, int64_t cap, int slices, const float* picked,
+                                                                     const int* word, const float* share, int ld, float inverse,
+                                                                     const int* idx, const int* count, float* loss, float* lse) {
+  __shared__ float2 s[kLanes][8];
   const int r = threadIdx.x & 7, g = threadIdx.x >> 3;
   const float factor = inverse * kLog2e;
   griddep_wait();
@@ -159,14 +160,16 @@ __global__ void __launch_bounds__(256) pk_distill_join_kernel(const float2* part
     float m = kFloor, l = 0.0f;
     if (r0 + r < n) {
 #pragma unroll 4
-      for (int i = g; i < slices; i += 32) join(m, l, __ldcg(part + i * cap + r0 + r));
+      for (int i = g; i < slices; i += kLanes) join(m, l, __ldcg(part + i * cap + r0 + r));
     }
     s[g][r] = make_float2(m, l);
     __syncthreads();
     const int64_t row = r0 + (threadIdx.x >> 5);  // a warp's
     const int lane = threadIdx.x & 31;
-    if (row < n) {
+    if (threadIdx.x < 256 && row < n) {
       float2 q = s[lane][threadIdx.x >> 5];
+#pragma unroll
+      for (int i = 32; i < kLanes; i += 32) join(q.x, q.y, s[i + lane][threadIdx.x >> 5]);
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
         const float2 u = make_float2(__shfl_xor_sync(0xffffffffu, q.x, o), __shfl_xor_sync(0xffffffffu, q.y, o));
@@ -374,13 +377,16 @@ int pk_distill(int dtype, const void* x, int64_t ldx, const void* w, const void*
   sp.factor = inverse * kLog2e;
   if (logits_product<ListStat>(dtype, in.xc, in.w, in.alt ? &in.xd : nullptr, a, sp, f.shape, d.sms, stream) != cudaSuccess)
     return PK_ERR_CUDA;
-  const int64_t blocks = (T + 7) / 8, most = static_cast<int64_t>(d.sms) * 8;
-  rows::Launch l(blocks < most ? blocks : most, 256, stream);
+  // more lanes a row where there are many slices and few rows (284 rows over 105909 words 84 us with 32 lanes a row in all, 72 with
+  // 128; 16384 over 32768 383 and 408)
+  const bool wide = f.slices > 64 && T <= static_cast<int64_t>(d.sms) * 16;
+  const int64_t blocks = (T + 7) / 8, most = static_cast<int64_t>(d.sms) * (wide ? 2 : 8);
+  rows::Launch l(blocks < most ? blocks : most, wide ? 1024 : 256, stream);
   const float2* part = f.part;
   const float *picked = f.picked, *share = f.lists.share;
   const int *word = f.lists.word, *at = f.m.idx, *count = f.m.count;
-  return cudaLaunchKernelEx(&l.cfg, pk_distill_join_kernel, part, f.m.cap, f.slices, picked, word, share, f.lists.ld, inverse, at, count,
-                            loss, lse) == cudaSuccess
+  return cudaLaunchKernelEx(&l.cfg, wide ? pk_distill_join_kernel<128> : pk_distill_join_kernel<32>, part, f.m.cap, f.slices, picked, word,
+                            share, f.lists.ld, inverse, at, count, loss, lse) == cudaSuccess
              ? PK_OK
              : PK_ERR_CUDA;
 }

@@ -165,31 +165,60 @@ struct WordLists {
   const uint32_t* first;  // [slices of the vocabulary][cap]
   int ld;
 };
-// A thread's place in its row's list: the next word, and the one after it on its way.
+// A thread's place in its row's list: the next word, and the one after it on its way (of the gradient's, with their shares).
+template <bool kShares>
 struct WordCursor {
   const int* list;
   int64_t base;  // of the list
   int pos, ld, next, after;
-  __device__ __forceinline__ int at(int i) const { return i < ld ? __ldcg(list + i) : kNoWord; }
-  // at the first word of slice `slice`, which begins at column `from` of the vocabulary
-  __device__ __forceinline__ void start(const WordLists& w, int64_t cap, int row, bool live, int slice, int from) {
-    const uint32_t e = live ? __ldcg(w.first + slice * cap + row) : 0u;
+  uint32_t first;
+  const float* shares;
+  float share, share_after;
+  __device__ __forceinline__ void ahead(int i) {
+    after = kNoWord;
+    share_after = 0.0f;
+    if (i < ld) {
+      after = __ldcg(list + i);
+      if (kShares) share_after = __ldcg(shares + i);
+    }
+  }
+  // asks where slice `slice` begins in the row's list
+  __device__ __forceinline__ void ask(const WordLists& w, int64_t cap, int row, bool live, int slice) {
+    first = live ? __ldcg(w.first + slice * cap + row) : 0u;
     ld = w.ld;
     base = static_cast<int64_t>(row) * ld;
     list = w.word + base;
-    pos = static_cast<int>(e >> 8);
+    shares = w.share + base;
+  }
+  // at the first word of the slice, which begins at column `from` of the vocabulary. (Called when the tile's logits have been
+  // asked for too: the answer's way costs nothing then.)
+  __device__ __forceinline__ void begin(int from) {
+    pos = static_cast<int>(first >> 8);
     next = after = kNoWord;
-    if (e) {
-      next = from + static_cast<int>(e & 255u) - 1;
-      after = at(pos + 1);
+    if (first) {
+      next = from + static_cast<int>(first & 255u) - 1;
+      if (kShares) share = __ldcg(shares + pos);
+      ahead(pos + 1);
     }
   }
   __device__ __forceinline__ void step() {
     ++pos;
     next = after;
-    after = at(pos + 1);
+    share = share_after;
+    ahead(pos + 1);
   }
 };
+// v[at] of 32 registers
+__device__ __forceinline__ float element(const float (&v)[32], int at) {
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t[i] = at & 16 ? v[i + 16] : v[i];
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) t[i] = at & o ? t[i + o] : t[i];
+  return t[0];
+}
 
 struct StatParams {
   const void* bias;
@@ -232,8 +261,8 @@ struct StatEpi {
     const int row = r0 + lane;
     const int label = !kList && row < M ? __ldcg(p.lab + row) : -1;
     const float factor = kList ? p.factor : kLog2e;
-    WordCursor words;
-    if constexpr (kList) words.start(p.lists, p.cap, row, row < M, c0 / cols, c0);
+    WordCursor<false> words;
+    if constexpr (kList) words.ask(p.lists, p.cap, row, row < M, c0 / cols);
     const int end = min(cols, N - c0);
     float m = kFloor, l = 0.0f;
 #pragma unroll 1
@@ -260,11 +289,9 @@ struct StatEpi {
         p.picked[row] = z;
       }
       if constexpr (kList) {
+        if (cc == 0) words.begin(c0);
         while (words.next < c + 32) {
-          float z = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) z = words.next == c + i ? v[i] : z;
-          p.picked[words.base + words.pos] = z;
+          p.picked[words.base + words.pos] = element(v, words.next - c);
           words.step();
         }
       }
@@ -340,8 +367,8 @@ struct GradEpi {
     // (rows past the count feed dW and db: set to zero below)
     const float g = live ? __ldcg(p.coef + row) : 0.0f, lse = live ? __ldcg(p.lse + row) : 0.0f;
     const int label = !kList && live ? __ldcg(p.lab + row) - p.v0 : -1;
-    WordCursor words;
-    if constexpr (kList) words.start(p.lists, p.cap, row, live, (p.v0 + c0) / cols, p.v0 + c0);
+    WordCursor<true> words;
+    if constexpr (kList) words.ask(p.lists, p.cap, row, live, (p.v0 + c0) / cols);
     const int end = min(cols, N - c0);
 #pragma unroll 1
     for (int cc = 0; cc < end; cc += 32) {
@@ -356,6 +383,7 @@ struct GradEpi {
         if (p.bias) b.add(v);
       }
       if constexpr (kList) {
+        if (cc == 0) words.begin(p.v0 + c0);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= p.inverse;
       }
@@ -366,9 +394,8 @@ struct GradEpi {
       }
       if constexpr (kList) {
         while (words.next < p.v0 + c + 32) {
-          const float q = __ldcg(p.lists.share + words.base + words.pos);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = words.next == p.v0 + c + i ? v[i] - q : v[i];
+          for (int i = 0; i < 32; ++i) v[i] = words.next == p.v0 + c + i ? v[i] - words.share : v[i];
           words.step();
         }
       }
