@@ -32,6 +32,7 @@ struct NormArgs {
   int64_t T;
   int D;
   float eps, inv_d;
+  int period, shift, slide;  // kSlide: rows until the same shift, the first row's, and from a row to the next
 };
 
 // A row belongs to kTpr threads, each with kNg groups of 16 bytes, kTpr groups apart: 8 threads for the shortest rows,
@@ -41,52 +42,75 @@ template <int kTpr>
 constexpr int kBlock = kTpr <= 32 ? 256 : kTpr;
 
 // A group of elements, 16 bytes of them: neighbours where every row of every matrix begins and ends on a 16-byte boundary
-// (kWhole), pairs of 16-bit elements where on a 4-byte one (kPairs; a warp then reads 128 bytes at once, not 64), else single
-// columns, 2 kTpr or kTpr apart so that a warp's accesses are of neighbours. `n`: columns of the row from the first.
-enum Unit { kSingle, kPairs, kWhole };
+// (kWhole) or where, in 16 bits, a row begins equally far past one in all of them (kSlide), else single columns kTpr apart, so
+// that a warp's accesses are of neighbours (kSingle; of fp32 that is no slower: 50000 x 1003 145 us, 332 in groups).
+//
+// kSlide: a block takes only rows that begin `shift` elements past a boundary, every period-th one, so a thread has the same
+// columns of each. Groups that hang over a row's first or last column are read with what stands beside them in the matrix, which
+// is then cleared (of the matrix's first and last row, where nothing need stand there, by elements), and written in part.
+enum Unit { kSingle, kSlide, kWhole };
 template <int DT>
 constexpr int kE = 16 / Ty<DT>::kBytes;
 template <int DT, int kTpr, int kUnit>
 struct Group {
   static constexpr int E = kE<DT>;
-  static constexpr bool kVec = kUnit == kWhole;
+  static constexpr bool kVec = kUnit != kSingle;
   uint4 q;
-  // the first column of group i, and how far element j's is from it
-  static __device__ __forceinline__ int column(int i, int t) {
-    return kVec ? (i * kTpr + t) * E : i * E * kTpr + (kUnit == kPairs ? 2 * t : t);
+  // the first column of group i (below 0 where it hangs over), and how far element j's is from it
+  static __device__ __forceinline__ int column(int i, int t, int shift) {
+    return kVec ? (i * kTpr + t) * E - (kUnit == kSlide ? shift : 0) : i * E * kTpr + t;
   }
-  static __device__ __forceinline__ constexpr int offset(int j) {
-    return kVec ? j : kUnit == kPairs ? (j >> 1) * 2 * kTpr + (j & 1) : j * kTpr;
-  }
-  __device__ __forceinline__ void load(const void* p, int64_t at, int n) {
-    if constexpr (kVec) {
-      q = __ldcg(reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes));
-    } else if constexpr (kUnit == kPairs) {
-      const uint16_t* s = static_cast<const uint16_t*>(p) + at;
-      uint32_t w[4];
+  static __device__ __forceinline__ constexpr int offset(int j) { return kVec ? j : j * kTpr; }
+  // whether 16 bytes are read: there is something on both sides of the row, or the group lies within it
+  static __device__ __forceinline__ bool at_once(int c, int D, bool inner) { return kUnit == kWhole || inner || (c >= 0 && c + E <= D); }
+  // of a group that hangs over: what is not of the row
+  __device__ __forceinline__ void clear(int c, int D) {
+    if constexpr (kUnit == kSlide) {
+      uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const auto from = [](int bit) { return __funnelshift_lc(0u, 0xFFFFFFFFu, max(bit, 0)); };  // bits `bit` and above
+      if (c < 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = offset(2 * j) < n ? __ldcg(reinterpret_cast<const unsigned int*>(s + offset(2 * j))) : 0u;
-      q = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      uint32_t w[4];
+        for (int k = 0; k < 4; ++k) w[k] &= from(-16 * c - 32 * k);
+      }
+      if (c + E > D) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        if constexpr (DT == PK_F32) {
-          w[j] = j * kTpr < n ? __ldcg(static_cast<const unsigned int*>(p) + at + j * kTpr) : 0u;
-        } else {
-          const uint32_t x = j * kTpr < n ? __ldcg(static_cast<const unsigned short*>(p) + at + j * kTpr) : 0u;
-          w[j >> 1] = j & 1 ? w[j >> 1] | x << 16 : x;
-        }
+        for (int k = 0; k < 4; ++k) w[k] &= ~from(16 * (D - c) - 32 * k);
       }
       q = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // the weights, which every row reads again: through L1
-  __device__ __forceinline__ void load_shared(const void* p, int at, int n) {
-    if constexpr (kVec)
-      q = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * Ty<DT>::kBytes);
+  // columns c, c + offset(1) .. of a row of D that begins at element `at` of p
+  __device__ __forceinline__ void load(const void* p, int64_t at, int c, int D, bool inner = false) {
+    if (kVec && at_once(c, D, inner)) {
+      q = __ldcg(reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (at + c) * Ty<DT>::kBytes));
+      clear(c, D);
+      return;
+    }
+    if constexpr (kUnit != kWhole) load_each(p, at, c, D);
+  }
+  // the same by elements, wherever the row begins
+  __device__ __forceinline__ void load_each(const void* p, int64_t at, int c, int D) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const char* s = static_cast<const char*>(p) + (at + c) * Ty<DT>::kBytes;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      if (offset(j) >= D - c || (kVec && c + offset(j) < 0)) continue;
+      const char* d = s + offset(j) * Ty<DT>::kBytes;
+      if constexpr (DT == PK_F32)
+        w[j] = __ldcg(reinterpret_cast<const unsigned int*>(d));
+      else
+        w[j >> 1] |= static_cast<uint32_t>(__ldcg(reinterpret_cast<const unsigned short*>(d))) << (16 * (j & 1));
+    }
+    q = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // the weights, which every row reads again: through L1, or from their copy in shared memory
+  __device__ __forceinline__ void load_shared(const void* p, int c, int D, const uint8_t* copy = nullptr, int i = 0, int t = 0) {
+    if constexpr (kUnit == kWhole)
+      q = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + c * Ty<DT>::kBytes);
+    else if (kUnit == kSlide && copy)
+      q = *reinterpret_cast<const uint4*>(copy + (i * kTpr + t) * 16);
     else
-      load(p, at, n);
+      load_each(p, 0, c, D);  // (they need not begin where the rows do)
   }
   __device__ __forceinline__ void get(float (&v)[E]) const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -103,27 +127,67 @@ struct Group {
   }
   // the elements as they were loaded from here on: what was unpacked of them before is not kept in registers
   __device__ __forceinline__ void forget() { asm volatile("" : "+r"(q.x), "+r"(q.y), "+r"(q.z), "+r"(q.w)); }
-  static __device__ __forceinline__ void store(void* p, int64_t at, int n, const float (&v)[E]) {
-    if constexpr (DT != PK_F32 && kUnit != kSingle) {
-      using P = Elem<DT == PK_BF16>;
-      const uint32_t w[4] = {P::pack(v[0], v[1]), P::pack(v[2], v[3]), P::pack(v[4], v[5]), P::pack(v[6], v[7])};
-      uint16_t* d = static_cast<uint16_t*>(p) + at;
-      if constexpr (kVec) {
-        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
+  static __device__ __forceinline__ void store(void* p, int64_t at, int c, int D, const float (&v)[E]) {
+    if constexpr (kVec) {
+      uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (offset(2 * j) < n) *reinterpret_cast<uint32_t*>(d + offset(2 * j)) = w[j];
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == PK_F32)
+          w[j] = __float_as_uint(v[j]);
+        else
+          w[j] = Elem<DT == PK_BF16>::pack(v[2 * j], v[2 * j + 1]);
       }
-    } else if constexpr (kVec) {
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
+      char* d = static_cast<char*>(p) + (at + c) * Ty<DT>::kBytes;
+      if (kUnit == kWhole || (c >= 0 && c + E <= D)) {
+        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+      }
+      if constexpr (kUnit == kSlide) {
+        // what hangs over on one side: in pieces of 2, 4 and 8 bytes
+        const auto word = [&](int k) { return k & 2 ? (k & 1 ? w[3] : w[2]) : k & 1 ? w[1] : w[0]; };
+        if (c + E <= D) {
+          const int s = -c, f = s + (s & 1), g = f + (f & 2);
+          if (s & 1) *reinterpret_cast<uint16_t*>(d + 2 * s) = static_cast<uint16_t>(word(s >> 1) >> 16);
+          if (f & 2) *reinterpret_cast<uint32_t*>(d + 2 * f) = word(f >> 1);
+          if (g == 4) *reinterpret_cast<uint2*>(d + 8) = make_uint2(w[2], w[3]);
+          return;
+        }
+        if (c >= 0) {
+          const int n = D - c;
+          if (n & 4) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+          if (n & 2) *reinterpret_cast<uint32_t*>(d + 2 * (n & 4)) = word((n & 4) >> 1);
+          if (n & 1) *reinterpret_cast<uint16_t*>(d + 2 * (n & 6)) = static_cast<uint16_t>(word((n & 6) >> 1));
+          return;
+        }
+      }
+    }
+    if constexpr (kUnit != kWhole) {
 #pragma unroll
       for (int j = 0; j < E; ++j)
-        if (offset(j) < n) Ty<DT>::put(p, at + offset(j), v[j]);
+        if (offset(j) < D - c && (!kVec || c + offset(j) >= 0)) Ty<DT>::put(p, at + c + offset(j), v[j]);
     }
   }
 };
+
+// The rows of a block, and of its row of threads: all that are there, or every period-th from `first`.
+struct Walk {
+  int64_t first, rows, start, step;  // row first + k period, k < rows, from k = start (of the block's first) on
+  int period, shift;
+};
+template <int kUnit, int kRows>
+__device__ __forceinline__ Walk walk(int64_t T, int period, int shift0, int slide, int E) {
+  Walk w = {0, T, static_cast<int64_t>(blockIdx.x) * kRows, static_cast<int64_t>(gridDim.x) * kRows, 1, 0};
+  if constexpr (kUnit == kSlide) {
+    const int residue = blockIdx.x % period;
+    w.first = residue;
+    w.period = period;
+    w.rows = T > residue ? (T - residue + period - 1) / period : 0;
+    w.start = static_cast<int64_t>(blockIdx.x / period) * kRows;
+    w.step = static_cast<int64_t>(gridDim.x / period) * kRows;
+    w.shift = (shift0 + residue * slide) & (E - 1);
+  }
+  return w;
+}
 
 // N sums (or maxima, where bit i of kMax is set) over a row's threads, in every one of them. `red`: 2 x 16 x N floats, used
 // alternately so that one barrier a row is enough.
@@ -167,7 +231,7 @@ __device__ __forceinline__ void to_e4m3(const float (&v)[N], uint32_t (&q)[N / 4
 }
 
 // Bound by bytes: 131072 x 1024 bf16 with a residual 161 us, 1.0 of the copy rate; 100000 x 1024 to 8 bits 114 us (issue slots
-// half full); rows off the 16-byte grid pay for narrower accesses (100000 x 1002 bf16 167 us by pairs, x 1003 305 one by one, 120 of bytes).
+// half full); rows off the 16-byte grid 100000 x 1003 bf16 178 (120 of bytes; 313 in single columns).
 // blocks of an SM: 85 registers a thread, 128 of fp32
 template <int DT, int kTpr>
 constexpr int kResident = kTpr > 256 ? 1 : (DT == PK_F32 ? 512 : 768) / kBlock<kTpr>;
@@ -182,25 +246,36 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
   constexpr int kRows = kBlock<kTpr> / kTpr;
   const int t = threadIdx.x % kTpr;
   int turn = 0;
+  const Walk rows = walk<kUnit, kRows>(a.T, a.period, a.shift, a.slide, E);
+  const int shift = rows.shift;
   griddep_wait();
+  // (16 bits: weights as the block's rows need them)
+  constexpr bool kCopy = kUnit == kSlide && kMode != kQuantize;
+  __shared__ __align__(16) uint8_t copy[kCopy ? kTpr * kNg * 16 : 16];
+  if constexpr (kCopy) {
+    for (int c = threadIdx.x; c < kTpr * kNg * E; c += kBlock<kTpr>)
+      reinterpret_cast<uint16_t*>(copy)[c] = c >= shift && c - shift < a.D ? __ldcg(static_cast<const unsigned short*>(a.w) + c - shift) : 0;
+    __syncthreads();
+  }
   // (the rows of one warp go round together: the shuffles are warp-wide)
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.T; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t row = r0 + threadIdx.x / kTpr;
-    const int D = row < a.T ? a.D : 0;  // (no columns of a row that is not there)
+  for (int64_t k0 = rows.start; k0 < rows.rows; k0 += rows.step) {
+    const int64_t k = k0 + threadIdx.x / kTpr, row = rows.first + k * rows.period;
+    const int D = k < rows.rows ? a.D : 0;  // (no columns of a row that is not there)
+    const bool inner = row > 0 && row + 1 < a.T;
     float h[kNg][E];
     {
       G x[kNg], res[kNg];
 #pragma unroll
       for (int i = 0; i < kNg; ++i) {
-        const int c = G::column(i, t);
+        const int c = G::column(i, t, shift);
         if (c < D) {
-          x[i].load(a.x, row * a.ldx + c, D - c);
-          if (kMode != kQuantize && a.res) res[i].load(a.res, row * a.ldr + c, D - c);
+          x[i].load(a.x, row * a.ldx, c, D, inner);
+          if (kMode != kQuantize && a.res) res[i].load(a.res, row * a.ldr, c, D, inner);
         }
       }
 #pragma unroll
       for (int i = 0; i < kNg; ++i) {
-        const int c = G::column(i, t);
+        const int c = G::column(i, t, shift);
 #pragma unroll
         for (int j = 0; j < E; ++j) h[i][j] = 0.0f;
         if (c < D) {
@@ -211,7 +286,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
 #pragma unroll
             for (int j = 0; j < E; ++j) h[i][j] += b[j];
           }
-          if (kMode != kQuantize && a.h) G::store(a.h, row * a.ldh + c, D - c, h[i]);
+          if (kMode != kQuantize && a.h) G::store(a.h, row * a.ldh, c, D, h[i]);
         }
       }
     }
@@ -241,15 +316,15 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
       const float f = rsqrtf(fmaf(s[0], a.inv_d, eps));
 #pragma unroll
       for (int i = 0; i < kNg; ++i) {
-        const int c = G::column(i, t);
+        const int c = G::column(i, t, shift);
         if (c < D) {
           G w;
-          w.load_shared(a.w, c, D - c);
+          w.load_shared(a.w, c, D, kCopy ? copy : nullptr, i, t);
           float b[E];
           w.get(b);
 #pragma unroll
           for (int j = 0; j < E; ++j) h[i][j] = h[i][j] * f * b[j];
-          if constexpr (kMode == kNorm) G::store(a.y, row * a.ldy + c, D - c, h[i]);
+          if constexpr (kMode == kNorm) G::store(a.y, row * a.ldy, c, D, h[i]);
         }
       }
     }
@@ -270,22 +345,24 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
       const float inv = scale > 0.0f ? 1.0f / (scale * up) : (scale == 0.0f ? 0.0f : scale);
 #pragma unroll
       for (int i = 0; i < kNg; ++i) {
-        const int c = G::column(i, t);
+        const int c = G::column(i, t, shift);
         if (c < D) {
 #pragma unroll
           for (int j = 0; j < E; ++j) h[i][j] = h[i][j] * up * inv;
           uint32_t q[E / 4];
           to_e4m3(h[i], q);
           uint8_t* d = static_cast<uint8_t*>(a.y) + row * a.ldy + c;
-          if constexpr (kVec) {
+          if (kVec && G::at_once(c, D, false)) {
             if constexpr (E == 8)
               *reinterpret_cast<uint2*>(d) = make_uint2(q[0], q[1]);
             else
               *reinterpret_cast<uint32_t*>(d) = q[0];
           } else {
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-              if (G::offset(j) < D - c) d[G::offset(j)] = static_cast<uint8_t>(q[j / 4] >> (8 * (j & 3)));
+            for (int j = 0; j < E; ++j) {
+              const int e = c + G::offset(j);
+              if (e < D && (!kVec || e >= 0)) d[G::offset(j)] = static_cast<uint8_t>(q[j / 4] >> (8 * (j & 3)));
+            }
           }
         }
       }
@@ -312,13 +389,14 @@ struct NormBackArgs {
   int64_t T;
   int D;
   float eps, inv_d;
+  int period, shift, slide;  // as of the norm
 };
 
 // A block keeps its columns' sums of dy n in registers over all of its rows, so there are only as many blocks as are resident
 // at once, and few threads: what covers the latency is that each thread's groups of the next rows are on their way into
-// shared memory (kVec; a thread reads back what it asked for itself, so nothing is synchronized).
-// 16931 x 768 bf16 with dh: 19.4 us (23.8 without that, on 16 warps an SM with a row in flight each), and 2.7 to add the
-// blocks' sums; 131072 x 768 124 us, 0.98 of the copy rate.
+// shared memory (not kSingle; a thread reads back what it asked for itself, so nothing is synchronized).
+// 16931 x 768 bf16 with dh: 18.0 us (23.8 without that, on 16 warps an SM with a row in flight each), and 2.7 to add the
+// blocks' sums; 131072 x 768 124 us, 0.98 of the copy rate. Rows off the grid: 100000 x 763 146 us (249 in single columns).
 template <int DT, int kTpr>
 constexpr int kBackThreads = kTpr > 256 ? kTpr : 512;  // of an SM: 128 registers
 template <int DT, int kTpr>
@@ -330,7 +408,7 @@ template <int DT, int kTpr, int kNg>
 constexpr int kStages = 6 * kRowBytes<DT, kTpr, kNg> * kBackResident<DT, kTpr> <= 200 * 1024 ? 2 : 1;
 template <int DT, int kTpr, int kNg, int kUnit>
 constexpr int back_smem() {
-  const int ring = kUnit == kWhole ? 3 * kStages<DT, kTpr, kNg> * kRowBytes<DT, kTpr, kNg> : 0, cols = kTpr <= 32 ? kBlock<kTpr> * kNg * kE<DT> * 4 : 0;
+  const int ring = kUnit != kSingle ? 3 * kStages<DT, kTpr, kNg> * kRowBytes<DT, kTpr, kNg> : 0, cols = kTpr <= 32 ? kBlock<kTpr> * kNg * kE<DT> * 4 : 0;
   return ring > cols ? ring : cols;
 }
 
@@ -344,45 +422,53 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kBackResident<DT, kTpr>)) pk_no
   constexpr int kRows = kBlock<kTpr> / kTpr, kCols = kTpr * kNg * E, kS = kStages<DT, kTpr, kNg>;
   const int t = threadIdx.x % kTpr;
   int turn = 0;
+  const Walk rows = walk<kUnit, kRows>(a.T, a.period, a.shift, a.slide, E);
+  const int shift = rows.shift;
   float2 sum[kNg][E / 2];
   G held[DT == PK_F32 ? 1 : kNg];  // the weights, where the registers hold them
   griddep_wait();
 #pragma unroll
   for (int i = 0; i < kNg; ++i) {
-    const int c = G::column(i, t);
+    const int c = G::column(i, t, shift);
 #pragma unroll
     for (int j = 0; j < E / 2; ++j) sum[i][j] = twice(0.0f);
-    if (DT != PK_F32 && c < a.D) held[DT == PK_F32 ? 0 : i].load(a.w, c, a.D - c);
+    if (DT != PK_F32 && c < a.D) held[DT == PK_F32 ? 0 : i].load_shared(a.w, c, a.D);
   }
   const auto weights = [&](int i, int c, float(&g)[E]) {
     if constexpr (DT == PK_F32) {
       G w;
-      w.load_shared(a.w, c, a.D - c);
+      w.load_shared(a.w, c, a.D);
       w.get(g);
     } else {
       held[i].get(g);
     }
   };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   // this thread's 16 bytes of group i of input k in a stage
   const auto slot = [&](int stage, int k, int i) {
     return smem + (((stage * 3 + k) * kNg + i) * kBlock<kTpr> + threadIdx.x) * 16;
   };
   // inputs [k0, k1) of a row into a stage; every call makes one group of copies
-  const auto ask = [&](int stage, int64_t r0, auto k0, auto k1) {
-    const int64_t row = r0 + threadIdx.x / kTpr;
-    if (row < a.T) {
+  const auto ask = [&](int stage, int64_t k0, auto i0, auto i1) {
+    const int64_t n = k0 + threadIdx.x / kTpr, row = rows.first + n * rows.period;
+    if (n < rows.rows) {
+      const bool inner = row > 0 && row + 1 < a.T;
 #pragma unroll
       for (int i = 0; i < kNg; ++i) {
-        const int c = G::column(i, t);
+        const int c = G::column(i, t, shift);
         if (c < a.D) {
           const void* const base[3] = {a.h, a.dy, a.dh};
           const int64_t ld[3] = {a.ldh, a.lddy, a.lddh};
 #pragma unroll
-          for (int k = decltype(k0)::value; k < decltype(k1)::value; ++k)
+          for (int k = decltype(i0)::value; k < decltype(i1)::value; ++k)
             if (k < 2 || a.dh) {
-              const char* src = static_cast<const char*>(base[k]) + (row * ld[k] + c) * Ty<DT>::kBytes;
-asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, k, i))), "l"(src) : "memory");
+              if (G::at_once(c, a.D, inner)) {
+                const char* src = static_cast<const char*>(base[k]) + (row * ld[k] + c) * Ty<DT>::kBytes;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, k, i))), "l"(src) : "memory");
+              } else {
+                G x;
+                x.load(base[k], row * ld[k], c, a.D);
+                *reinterpret_cast<uint4*>(slot(stage, k, i)) = x.q;
+              }
             }
         }
       }
@@ -392,31 +478,33 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
   using K0 = std::integral_constant<int, 0>;
   using K2 = std::integral_constant<int, 2>;
   using K3 = std::integral_constant<int, 3>;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
   if constexpr (kVec) {
 #pragma unroll
     for (int k = 0; k < kS; ++k) {
-      ask(k, first + k * step, K0(), K2());
-      ask(k, first + k * step, K2(), K3());
+      ask(k, rows.start + k * rows.step, K0(), K2());
+      ask(k, rows.start + k * rows.step, K2(), K3());
     }
   }
   int stage = 0;
-  for (int64_t r0 = first; r0 < a.T; r0 += step) {
-    const int64_t row = r0 + threadIdx.x / kTpr;
-    const int D = row < a.T ? a.D : 0;
+  for (int64_t k0 = rows.start; k0 < rows.rows; k0 += rows.step) {
+    const int64_t k = k0 + threadIdx.x / kTpr, row = rows.first + k * rows.period;
+    const int D = k < rows.rows ? a.D : 0;
     G xh[kNg], xd[kNg];
     if constexpr (kVec) asm volatile("cp.async.wait_group %0;" ::"n"(2 * (kS - 1)) : "memory");
-    const auto read = [&](G& x, int k, int i) { x.q = *reinterpret_cast<const uint4*>(slot(stage, k, i)); };
+    const auto read = [&](G& x, int k, int i, int c) {
+      x.q = *reinterpret_cast<const uint4*>(slot(stage, k, i));
+      x.clear(c, D);
+    };
 #pragma unroll
     for (int i = 0; i < kNg; ++i) {
-      const int c = G::column(i, t);
+      const int c = G::column(i, t, shift);
       if (c < D) {
         if constexpr (kVec) {
-          read(xh[i], 0, i);
-          read(xd[i], 1, i);
+          read(xh[i], 0, i, c);
+          read(xd[i], 1, i, c);
         } else {
-          xh[i].load(a.h, row * a.ldh + c, D - c);
-          xd[i].load(a.dy, row * a.lddy + c, D - c);
+          xh[i].load(a.h, row * a.ldh, c, D);
+          xd[i].load(a.dy, row * a.lddy, c, D);
         }
       }
     }
@@ -425,7 +513,7 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
       float2 hh = twice(0.0f), hg = twice(0.0f);
 #pragma unroll
       for (int i = 0; i < kNg; ++i) {
-        const int c = G::column(i, t);
+        const int c = G::column(i, t, shift);
         if (c < D) {
           float h[E], d[E], g[E];
           xh[i].get(h);
@@ -460,7 +548,7 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
       }
     }
     // (h and dy have been read: the sums are made of them)
-    if constexpr (kVec) ask(stage, r0 + kS * step, K0(), K2());
+    if constexpr (kVec) ask(stage, k0 + kS * rows.step, K0(), K2());
     const float f = rsqrtf(fmaf(s[0], a.inv_d, eps));  // of h times `down`
     const float mean = s[1] * a.inv_d * f;             // of g n
     const float2 rate = twice(f * down), mean2 = twice(-mean);
@@ -474,7 +562,7 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
     }
 #pragma unroll
     for (int i = 0; i < kNg; ++i) {
-      const int c = G::column(i, t);
+      const int c = G::column(i, t, shift);
       if (c < D) {
         float n[E], d[E], g[E];
         xh[i].get(n);
@@ -492,19 +580,19 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
           if (a.dh) {
             G xr;
             if constexpr (kVec)
-              read(xr, 2, i);
+              read(xr, 2, i, c);
             else
-              xr.load(a.dh, row * a.lddh + c, D - c);
+              xr.load(a.dh, row * a.lddh, c, D);
             xr.get(n);
 #pragma unroll
             for (int j = 0; j < E; j += 2) add2(d[j], d[j + 1], make_float2(n[j], n[j + 1]));
           }
-          G::store(a.dx, row * a.lddx + c, D - c, d);
+          G::store(a.dx, row * a.lddx, c, D, d);
         }
       }
     }
     if constexpr (kVec) {
-      ask(stage, r0 + kS * step, K2(), K3());  // (and dh: what was written is made of it)
+      ask(stage, k0 + kS * rows.step, K2(), K3());  // (and dh: what was written is made of it)
       stage = stage + 1 == kS ? 0 : stage + 1;
     }
   }
@@ -517,12 +605,12 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
   for (int i = 0; i < kNg; ++i)
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      const int c = G::column(i, t) + G::offset(j);
+      const int c = G::column(i, t, shift) + G::offset(j);
       const float v = j & 1 ? sum[i][j >> 1].y : sum[i][j >> 1].x;
       if constexpr (kTpr > 32) {
-        if (c < a.D) part[c] = v;
+        if (c < a.D && c >= 0) part[c] = v;
       } else {
-        cols[threadIdx.x / kTpr * kCols + c] = v;
+        cols[threadIdx.x / kTpr * kCols + c + shift] = v;
       }
     }
   if constexpr (kTpr <= 32) {
@@ -530,7 +618,7 @@ asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(sta
     for (int c = threadIdx.x; c < a.D; c += kBlock<kTpr>) {
       float v = 0.0f;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) v += cols[r * kCols + c];
+      for (int r = 0; r < kRows; ++r) v += cols[r * kCols + c + shift];
       part[c] = v;
     }
   }
@@ -581,30 +669,49 @@ cudaError_t by_ragged_length(int D, const F& f) {
 }
 static_assert(512 * 32 == kMaxD, "the longest row");
 
-// What every row of a matrix begins and ends on, and of several together.
-Unit unit_of(const void* p, int64_t ld, int D, int e) {
-  if (rows16(p, ld, e) && (D * e & 15) == 0) return kWhole;
-  return e == 2 && aligned_to(p, 4) && ((ld | D) & 1) == 0 ? kPairs : kSingle;
-}
-Unit least(Unit a, Unit b) { return a < b ? a : b; }
+// How far past a 16-byte boundary (of the element type) the rows of several matrices begin: whether they do so equally.
+struct Shifts {
+  int e, D;
+  bool whole = true, alike = true, any = false;
+  int first = 0, slide = 0;  // elements: of the first row, and from a row to the next
+  // `unit`: bytes of an element of this matrix
+  void add(const void* p, int64_t ld, int unit) {
+    const int E = 16 / e, f = static_cast<int>(reinterpret_cast<uintptr_t>(p) / unit) & (E - 1), s = static_cast<int>(ld & (E - 1));
+    alike = alike && ld >= E && (!any || (f == first && s == slide));
+    if (!any) {
+      first = f;
+      slide = s;
+    }
+    any = true;
+    whole = whole && f == 0 && s == 0;
+  }
+  int period() const { return slide == 0 ? 1 : 16 / e / (slide & -slide); }
+  Unit unit(const void* w) const {
+    if (whole && aligned_to(w, 16) && (D * e & 15) == 0) return kWhole;
+    return e == 2 && alike && D + 16 / e - 1 <= kMaxD ? kSlide : kSingle;
+  }
+};
 
 // f(Cut, Unit) for a row length and an alignment
 template <int DT, class F>
 cudaError_t by_shape(int D, Unit unit, const F& f) {
   if (unit == kWhole) return by_length(D, [&](auto cut) { return f(cut, std::integral_constant<int, kWhole>()); });
-  return by_ragged_length(D, [&](auto cut) {
-    if constexpr (DT != PK_F32)
-      if (unit == kPairs) return f(cut, std::integral_constant<int, kPairs>());
-    return f(cut, std::integral_constant<int, kSingle>());
-  });
+  if constexpr (DT != PK_F32)
+    if (unit == kSlide)
+      return by_ragged_length(D + kE<DT> - 1, [&](auto cut) { return f(cut, std::integral_constant<int, kSlide>()); });
+  return by_ragged_length(D, [&](auto cut) { return f(cut, std::integral_constant<int, kSingle>()); });
+}
+// Blocks of kRows rows each, `most` at once: of every shift as many.
+int64_t blocks_for(int64_t T, int rows, int64_t most, int period) {
+  const int64_t each = ((T + period - 1) / period + rows - 1) / rows, room = most / period > 1 ? most / period : 1;
+  return (each < room ? each : room) * period;
 }
 
 template <int DT, int kMode>
 cudaError_t norm_launch(const NormArgs& a, Unit unit, int sms, cudaStream_t stream) {
   return by_shape<DT>(a.D, unit, [&](auto cut, auto u) {
     constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>, kRows = kBlock<kTpr> / kTpr;
-    const int64_t blocks = (a.T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * (2048 / kBlock<kTpr>);
-    Launch l(blocks < most ? blocks : most, kBlock<kTpr>, stream);
+    Launch l(blocks_for(a.T, kRows, static_cast<int64_t>(sms) * (2048 / kBlock<kTpr>), a.period), kBlock<kTpr>, stream);
     return cudaLaunchKernelEx(&l.cfg, pk_norm_kernel<DT, kMode, kTpr, kNg, decltype(u)::value>, a);
   });
 }
@@ -612,12 +719,11 @@ cudaError_t norm_launch(const NormArgs& a, Unit unit, int sms, cudaStream_t stre
 // Blocks of the backward pass: as many as are resident at once, each with its own partial column sums. The workspace is for the
 // most of any alignment.
 template <int DT>
-int64_t back_blocks_of(int64_t T, int D, Unit unit, int sms) {
+int64_t back_blocks_of(int64_t T, int D, Unit unit, int period, int sms) {
   int64_t n = 0;
   by_shape<DT>(D, unit, [&](auto cut, auto) {
-    constexpr int kTpr = decltype(cut)::kTpr, kRows = kBlock<kTpr> / kTpr;
-    const int64_t blocks = (T + kRows - 1) / kRows, most = static_cast<int64_t>(sms) * kBackResident<DT, kTpr>;
-    n = blocks < most ? blocks : most;
+    constexpr int kTpr = decltype(cut)::kTpr;
+    n = blocks_for(T, kBlock<kTpr> / kTpr, static_cast<int64_t>(sms) * kBackResident<DT, kTpr>, period);
     return cudaSuccess;
   });
   return n;
@@ -625,15 +731,19 @@ int64_t back_blocks_of(int64_t T, int D, Unit unit, int sms) {
 int64_t back_bytes(int dtype, int64_t T, int D, int sms) {
   const auto most = [&](auto type) {
     constexpr int DT = decltype(type)::value;
-    const int64_t a = back_blocks_of<DT>(T, D, kWhole, sms), b = back_blocks_of<DT>(T, D, kSingle, sms);
-    return (a > b ? a : b) * D * 4;
+    int64_t n = back_blocks_of<DT>(T, D, kWhole, 1, sms);
+    const auto or_else = [&](int64_t m) { n = m > n ? m : n; };
+    or_else(back_blocks_of<DT>(T, D, kSingle, 1, sms));
+    if (DT != PK_F32 && D + kE<DT> - 1 <= kMaxD)
+      for (int period = 1; period <= kE<DT>; period *= 2) or_else(back_blocks_of<DT>(T, D, kSlide, period, sms));
+    return n * D * 4;
   };
   return dtype == PK_F32 ? most(std::integral_constant<int, PK_F32>()) : most(std::integral_constant<int, PK_BF16>());
 }
 
 template <int DT>
 cudaError_t back_launch(const NormBackArgs& a, Unit unit, int sms, void* dw, cudaStream_t stream) {
-  const int64_t blocks = back_blocks_of<DT>(a.T, a.D, unit, sms);
+  const int64_t blocks = back_blocks_of<DT>(a.T, a.D, unit, a.period, sms);
   return by_shape<DT>(a.D, unit, [&](auto cut, auto u) {
     constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>, kUnit = decltype(u)::value;
     Launch l(blocks, kBlock<kTpr>, stream);
@@ -651,12 +761,13 @@ template <int DT>
 cudaError_t prepare_back() {
   cudaError_t e = cudaSuccess;
   for (const int D : {64, 256, 1024, 2048, 4096, 8192, kMaxD}) {
-    e = by_length(D, [&](auto cut) {
-      constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>;
-      return cudaFuncSetAttribute(pk_norm_backward_kernel<DT, kTpr, kNg, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  back_smem<DT, kTpr, kNg, kWhole>());
-    });
-    if (e != cudaSuccess) return e;
+    const auto allow = [&](auto cut, auto u) {
+      constexpr int kTpr = decltype(cut)::kTpr, kNg = decltype(cut)::kElems / kE<DT>, kUnit = decltype(u)::value;
+      return cudaFuncSetAttribute(pk_norm_backward_kernel<DT, kTpr, kNg, kUnit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  back_smem<DT, kTpr, kNg, kUnit>());
+    };
+    if ((e = by_shape<DT>(D, kWhole, allow)) != cudaSuccess) return e;
+    if (DT != PK_F32 && (e = by_shape<DT>(D - kE<DT> + 1, kSlide, allow)) != cudaSuccess) return e;
   }
   return e;
 }
@@ -692,13 +803,15 @@ int run_norm(int mode, int dtype, const void* x, int64_t ldx, const void* residu
   a.D = D;
   a.eps = eps;
   a.inv_d = 1.0f / static_cast<float>(D);
-  Unit unit = least(unit_of(x, ldx, D, e), unit_of(w, D, D, e));  // (a null w is aligned)
-  if (residual) unit = least(unit, unit_of(residual, ldr, D, e));
-  if (h) unit = least(unit, unit_of(h, ldh, D, e));
-  if (mode == kNorm)
-    unit = least(unit, unit_of(y, ldy, D, e));
-  else if (unit == kWhole && !(aligned_to(y, 16 / e) && (ldy & (16 / e - 1)) == 0))
-    unit = kSingle;
+  Shifts shifts = {e, D};
+  shifts.add(x, ldx, e);
+  if (residual) shifts.add(residual, ldr, e);
+  if (h) shifts.add(h, ldh, e);
+  shifts.add(y, ldy, mode == kNorm ? e : 1);
+  const Unit unit = shifts.unit(w);  // (a null w is aligned)
+  a.period = unit == kSlide ? shifts.period() : 1;
+  a.shift = shifts.first;
+  a.slide = shifts.slide;
   const auto run = [&](auto type) {
     constexpr int DT = decltype(type)::value;
     if (mode == kNorm) return norm_launch<DT, kNorm>(a, unit, d.sms, stream);
@@ -786,9 +899,15 @@ int pk_rms_norm_backward(int dtype, const void* h, int64_t ldh, const void* w, c
   a.D = D;
   a.eps = eps;
   a.inv_d = 1.0f / static_cast<float>(D);
-  Unit unit = least(least(unit_of(h, ldh, D, e), unit_of(dy, lddy, D, e)), unit_of(w, D, D, e));
-  if (dh) unit = least(unit, unit_of(dh, lddh, D, e));
-  if (dx) unit = least(unit, unit_of(dx, lddx, D, e));
+  Shifts shifts = {e, D};
+  shifts.add(h, ldh, e);
+  shifts.add(dy, lddy, e);
+  if (dh) shifts.add(dh, lddh, e);
+  if (dx) shifts.add(dx, lddx, e);
+  const Unit unit = shifts.unit(w);
+  a.period = unit == kSlide ? shifts.period() : 1;
+  a.shift = shifts.first;
+  a.slide = shifts.slide;
   const cudaError_t r = dtype == PK_F32    ? back_launch<PK_F32>(a, unit, d.sms, dw, stream)
                         : dtype == PK_BF16 ? back_launch<PK_BF16>(a, unit, d.sms, dw, stream)
                                            : back_launch<PK_F16>(a, unit, d.sms, dw, stream);

@@ -164,6 +164,46 @@ def test_strided_rows_and_in_place(pk, gen, dtype, D):
             assert torch.equal(got, dx)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,D,ld,first", [(40, 131, 131, 3), (17, 1003, 1011, 0), (2, 77, 77, 5), (1, 30, 33, 1), (29, 9, 9, 7), (50, 5, 8, 2),
+                                          (64, 3, 5, 1), (33, 260, 262, 2), (300, 4099, 4100, 4), (19, 16383, 16385, 1)])
+def test_rows_that_begin_past_a_boundary(pk, gen, dtype, T, D, ld, first):
+    """Rows `first` elements into an allocation and ld apart, equally in every matrix: what stands between and beside them (NaN here)
+    is neither taken for theirs nor written."""
+
+    def within(values=None, fill=float("nan")):
+        whole = torch.full((first + T * ld + 8,), fill, device="cuda", dtype=dtype)
+        view = whole[first : first + T * ld].view(T, ld)[:, :D] if ld > D else whole[first : first + T * D].view(T, D)
+        if values is not None:
+            view.copy_(values)
+        return whole, view
+
+    def beside(whole, view):
+        rest = whole.clone()
+        rest[first : first + T * ld].view(T, ld)[:, :D] = float("nan")
+        assert bool(rest.isnan().all())
+        return view
+
+    x, r, w = rand(gen, T, D, std=1.5, dtype=dtype), rand(gen, T, D, dtype=dtype), rand(gen, D, dtype=dtype)
+    out, h = within(), within()
+    pk.rms_norm(within(x)[1], w, residual=within(r)[1], out=out[1], h_out=h[1])
+    (wy, wh), (by, bh), ey = ref.rms_norm(x, w, r, 1e-6)
+    assert ref.worst(beside(*out), wy, by) <= 1 and ref.worst(beside(*h), wh, bh) <= 1
+    at = within(x)  # (the sum in the place of x)
+    q, scale, _ = pk.rms_norm_q8(at[1], w, residual=within(r)[1], h_out=at[1])
+    ws = wy.abs().amax(1) / 448
+    assert ref.worst(beside(*at), wh, bh) <= 1
+    assert ref.worst(q.double() * scale.double()[:, None], wy, ref.e4m3_bound(wy, ey, ws)) <= 1
+    q, scale = pk.quantize_rows(within(x)[1])
+    ws = x.double().abs().amax(1) / 448
+    assert ref.worst(q.double() * scale.double()[:, None], x.double(), ref.e4m3_bound(x.double(), 2.0**-21 * x.double().abs(), ws)) <= 1
+    dy, dh = rand(gen, T, D, std=0.1, dtype=dtype), rand(gen, T, D, std=0.1, dtype=dtype)
+    at = within(dh)  # (the gradient in the place of dh)
+    _, dw = pk.rms_norm_backward(within(x)[1], w, within(dy)[1], dh=at[1], out=at[1])
+    (wx, ww), (bx, bw) = ref.rms_norm_backward(x, w, dy, dh, 1e-6)
+    assert ref.worst(beside(*at), wx, bx) <= 1 and ref.worst(dw, ww, bw) <= 1
+
+
 def test_no_rows(pk, gen):
     x, w = rand(gen, 0, 100), rand(gen, 100)
     y, h = pk.rms_norm(x, w, residual=x)
