@@ -199,12 +199,20 @@ __device__ __forceinline__ float2 tail2(float u0, float u1) {
   return make_float2(attn::ex2(q.x), attn::ex2(q.y));
 }
 
+// max(z, 0), NaN for NaN (written as comparisons it became a branch an element: 82 us where gelu takes 67, 16384 x 1024 -> 4096
+// of 8-bit rows; 52 so)
+__device__ __forceinline__ float relu(float z) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(z));
+  return y;
+}
+
 // act(v) of a row's columns; DT: the type of the result, which says how exact it has to be
 template <int DT, int N>
 __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
   if (act == PK_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] > 0.0f ? v[i] : (v[i] != v[i] ? v[i] : 0.0f);
+    for (int i = 0; i < N; ++i) v[i] = relu(v[i]);
   } else if (act == PK_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
@@ -238,7 +246,10 @@ template <int DT, int N>
 __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (&d)[N]) {
   if (act == PK_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) d[i] = z[i] > 0.0f ? d[i] : (z[i] != z[i] ? z[i] : 0.0f);
+    for (int i = 0; i < N; ++i) {
+      const float on = z[i] > 0.0f ? d[i] : 0.0f;
+      d[i] = z[i] != z[i] ? z[i] : on;
+    }
   } else if (act == PK_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
@@ -327,11 +338,12 @@ __device__ __forceinline__ void act_both(int act, const float (&z)[N], float (&a
       s[i] = h * fmaf(fminf(low, 3.0e38f), rest, 1.0f);
     }
   } else {
+    const float off = act == PK_ACT_NONE ? 1.0f : 0.0f;  // the slope below 0
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool on = act == PK_ACT_NONE || z[i] > 0.0f || z[i] != z[i];
-      a[i] = on ? z[i] : 0.0f;
-      s[i] = z[i] != z[i] ? z[i] : on ? 1.0f : 0.0f;
+      const float on = z[i] > 0.0f ? 1.0f : off, y = relu(z[i]);
+      a[i] = act == PK_ACT_NONE ? z[i] : y;
+      s[i] = z[i] == z[i] ? on : z[i];
     }
   }
 }
