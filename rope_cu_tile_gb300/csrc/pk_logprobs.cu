@@ -242,23 +242,24 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
 }
 
 // ------------------------------------------------------------------------------------
-// short rows: a warp each, the row in shared memory, kC chunks a lane, which reads back what it asked for itself
+// short rows: a warp each, the row in shared memory, kC chunks a lane
 
 constexpr int kWarpCap = 128;  // candidates of a warp
 
 // The top-th largest of a warp's keys, N a lane and more than `top` in all: from the highest bit in which any two differ, a bit at a
-// time until that many are left.
-template <int N>
+// time until that many are left. kAbsent: keys of 0 are none, and `top` others are there.
+template <bool kAbsent, int N>
 __device__ __forceinline__ uint32_t warp_nth(const uint32_t (&k)[N], int top) {
   static_assert(32 * N >= kMaxTop, "fewer keys than may be asked for");
-  uint32_t hi = k[0], lo = k[0];
+  constexpr uint32_t kOne = kAbsent ? 1u : 0u;  // (0 less 1 is no minimum)
+  uint32_t hi = k[0], lo = k[0] - kOne;
 #pragma unroll
   for (int i = 1; i < N; ++i) {
     hi = max(hi, k[i]);
-    lo = min(lo, k[i]);
+    lo = min(lo, k[i] - kOne);
   }
   hi = __reduce_max_sync(0xffffffffu, hi);
-  lo = __reduce_min_sync(0xffffffffu, lo);
+  lo = __reduce_min_sync(0xffffffffu, lo) + kOne;
   if (hi == lo) return hi;
   int b = 31 - __clz(hi ^ lo);
   uint32_t bound = hi >> b >> 1 << b << 1;
@@ -348,19 +349,23 @@ __device__ __forceinline__ uint32_t row_bits(int first, int V) {
 template <int DT, int kC>
 constexpr int kShortBytes = kWarps * kC * 32 * 8 * Ty<DT>::kBytes;
 
-template <int DT, int kC>
-__global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_kernel(const __grid_constant__ LogprobArgs a) {
+// kFine: maxima that a chunk has, of all its elements or of pairs of them, where the row has few chunks.
+template <int DT, int kC, int kFine>
+__global__ void __launch_bounds__(kThreads, 5) pk_logprobs_short_kernel(const __grid_constant__ LogprobArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t cand[kWarps][kWarpCap];
+  __shared__ uint16_t noted[kWarps][kC * 32];  // chunks that hold candidates
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   constexpr int kPieces = Ty<DT>::kBytes / 2;  // of 16 bytes a chunk
-  uint4* const mine = reinterpret_cast<uint4*>(smem) + w * (kC * 32 * kPieces) + lane;
-  const auto chunk_at = [&](int i) {
+  uint4* const rows = reinterpret_cast<uint4*>(smem) + w * (kC * 32 * kPieces);
+  uint4* const mine = rows + lane;
+  const auto chunk_of = [&](int i, int owner) {
     Raw8<DT> q;
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) q.q[p] = mine[(i * kPieces + p) * 32];
+    for (int p = 0; p < kPieces; ++p) q.q[p] = rows[(i * kPieces + p) * 32 + owner];
     return q;
   };
+  const auto chunk_at = [&](int i) { return chunk_of(i, lane); };
   griddep_wait();
   for (int64_t row = blockIdx.x * static_cast<int64_t>(kWarps) + w; row < a.T; row += static_cast<int64_t>(gridDim.x) * kWarps) {
     const Row r = row_at<DT>(a.z, row * a.ld, a.V);
@@ -384,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_ke
     const long long label = __ldcg(a.labels + row);
     float picked = 0.0f;
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // the maxima of the chunks, or of pairs where the row has few chunks: each of another element
-    constexpr int kFine = kC <= 3 ? 4 : 1;
+    // the maxima, each of another element
     uint32_t key[kC * kFine];
     Stat st = nothing();
 #pragma unroll
@@ -435,35 +439,44 @@ __global__ void __launch_bounds__(kThreads, kC > 5 ? 3 : 5) pk_logprobs_short_ke
     __syncwarp();  // (the row before has been written out)
     int n = kWarpCap + 1;
     if (st.s == st.s) {
-      // elements whose key reaches the bound: counted, then kept, perhaps not all of them
-      const float bound = of_key<DT>(warp_nth(key, a.top));
-      const auto each = [&](const auto& take) {
-#pragma unroll 1
-        for (int i = 0; i < n_mine; ++i) {
-          const Raw8<DT> q = chunk_at(i);
-          if (top8<DT>(q) < bound) continue;
-          float v[8];
-          q.get(v);
-          const int c = (i * 32 + lane) * 8 - r.off;
-          take(v, c, reach(v, bound, true) & row_bits(c, a.V));
-        }
-      };
-      int at = 0;
-      each([&](const float(&)[8], int, uint32_t bits) { at += __popc(bits); });
-      int upto = at;
+      // chunks whose maximum reaches the bound are noted, then looked into a lane each
+      const float bound = of_key<DT>(warp_nth<kFine == 1>(key, a.top));
+      int have = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int u = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += u;
+      for (int i = 0; i < kC; ++i) {
+        const bool is = i < n_mine && !(top8<DT>(chunk_at(i)) < bound);  // (no bound: NaN)
+        const uint32_t votes = __ballot_sync(0xffffffffu, is);
+        if (is) noted[w][have + __popc(votes & ((1u << lane) - 1u))] = static_cast<uint16_t>(i * 32 + lane);
+        have += __popc(votes);
       }
-      n = __shfl_sync(0xffffffffu, upto, 31);
-      at = upto - at;
-      if (n <= kWarpCap)
-        each([&](const float(&v)[8], int c, uint32_t bits) {
+      __syncwarp();
+      n = 0;
+#pragma unroll 1
+      for (int k = 0; k < have && n <= kWarpCap; k += 32) {
+        float v[8];
+        uint32_t bits = 0;
+        int c = 0;
+        if (k + lane < have) {
+          const int chunk = noted[w][k + lane];
+          chunk_of(chunk >> 5, chunk & 31).get(v);
+          c = chunk * 8 - r.off;
+          bits = reach(v, bound, true) & row_bits(c, a.V);
+        }
+        int upto = __popc(bits);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (bits >> j & 1u) out[at++] = packed(key_of<DT>(v[j]), c + j);
-        });
+        for (int o = 1; o < 32; o *= 2) {
+          const int u = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += u;
+        }
+        int at = n + upto - __popc(bits);
+        n += __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (bits >> j & 1u) {
+            if (at < kWarpCap) out[at] = packed(key_of<DT>(v[j]), c + j);
+            ++at;
+          }
+      }
       __syncwarp();
     }
     if (n > kWarpCap) {
@@ -644,7 +657,7 @@ __device__ __forceinline__ int collect(Search<kT>& sh, const Slice& s, int V, fl
 #pragma unroll
     for (int i = 0; i < kLook; ++i) {
       bool is = at[i] < s.w1;
-      if (is && clean) is = top8<DT>(q[i]) >= bound;
+      if (is && clean) is = !(top8<DT>(q[i]) < bound);
       keep(is, at[i]);
     }
 #pragma unroll 1
@@ -710,7 +723,7 @@ __device__ __forceinline__ void slice_top(Search<kT>& sh, const Found<kT>& fd, c
     uint32_t k[kT / 32];
 #pragma unroll
     for (int i = 0; i < kT / 32; ++i) k[i] = fd.maxima[i * 32 + lane];
-    const uint32_t nth = warp_nth(k, top);
+    const uint32_t nth = warp_nth<false>(k, top);
     name(nth, 0x7fffffff, [&](int i) { return k[i] >= nth; });
   }
   __syncthreads();
@@ -931,6 +944,7 @@ __global__ void __launch_bounds__(kT, (DT == PK_F32 ? 1024 : 1280) / kT) pk_logp
 }
 
 constexpr int kShort = 704;     // words of a row of a warp
+constexpr int kMedium = 2032;   // where there are many: eight chunks a lane, less one that hangs over
 constexpr int kMiddle = 32768;  // words of a row of a block of 128 threads, and four times those of 64
 
 // Blocks a row: one where the rows fill the SMs, up to eight where they do not, none with fewer than 4096 words.
@@ -940,12 +954,12 @@ int parts_of(int64_t T, int V, int sms) {
   return parts;
 }
 
-template <int DT, int kC>
+template <int DT, int kC, int kFine>
 cudaError_t short_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
   const int64_t blocks = (a.T + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 8;
   Launch l(blocks < most ? blocks : most, kThreads, stream);
   l.cfg.dynamicSmemBytes = kShortBytes<DT, kC>;
-  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_short_kernel<DT, kC>, a);
+  return cudaLaunchKernelEx(&l.cfg, pk_logprobs_short_kernel<DT, kC, kFine>, a);
 }
 
 template <int DT, int kT>
@@ -956,9 +970,13 @@ cudaError_t rows_launch(const LogprobArgs& a, cudaStream_t stream) {
 
 template <int DT>
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, cudaStream_t stream) {
-  // a warp's row: up to three chunks a lane. (Longer ones took a warp longer than a block of 64: 65536 rows of 1500 words with 16
-  // likeliest 305 us.)
-  if (a.V <= kShort) return short_launch<DT, 3>(a, sms, stream);
+  // a warp's row: up to three chunks a lane, with at least two maxima for each word that is asked for; in 16 bits, where there are rows
+  // for every warp, up to eight. (16 likeliest of 65536 rows: of 700 words 97 us, 142 with the maxima of pairs; of 1500 136, 189 a
+  // block of 64 a row; of 2500 x 2000 10.6 and 10.2, of 300 x 2000 7.6 and 5.8. Of 3000 words, 16 chunks a lane, 250 and 189.)
+  const bool enough = a.V / 8 >= 2 * a.top;
+  if (a.V <= kShort) return enough ? short_launch<DT, 3, 1>(a, sms, stream) : short_launch<DT, 3, 4>(a, sms, stream);
+  if constexpr (DT != PK_F32)
+    if (a.V <= kMedium && a.T > 16 * sms) return short_launch<DT, 8, 1>(a, sms, stream);
   const int parts = parts_of(a.T, a.V, sms);
   if (parts == 1) {
     // what a row takes from its last load to its last output hardly depends on its length: more and smaller blocks for

@@ -156,6 +156,36 @@ def test_large_words_side_by_side(pk, gen, dtype, T, V):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V,top", [(705, 64), (1000, 16), (1500, 33), (2027, 64), (2032, 5), (2033, 16)])
+def test_many_rows_of_middle_length(pk, gen, dtype, V, top):
+    """More rows than there are warps, off the 16-byte grid too: random ones, masked ones, equal ones, one large word in a chunk."""
+    T = 2700
+    z = rand(gen, T, V + 3, std=2.5, dtype=dtype)[:, 3:]
+    z[0] = float("-inf")
+    z[0, V - 1], z[0, 3] = 1.0, 2.0
+    z[1] = torch.finfo(dtype).min
+    z[2] = 1.25
+    z[3, : V - 2] = float("-inf")
+    z[4] = (torch.arange(V, device="cuda") % 3).to(dtype)
+    z[5, : V // 2] += 30
+    z[6] = torch.arange(V, device="cuda").to(dtype) / V
+    z[7, ::8] = 20.0
+    z[T - 1, 100:300] = 25.0
+    labels = torch.randint(-1, V, (T,), generator=gen, device="cuda")
+    labels[0] = 3
+    check(pk, z, labels, top)
+    check(pk, z.contiguous(), labels, top)
+    check(pk, z.contiguous(), labels, 0)  # (not the same bits: how a row is shared out, and so its sums' order, goes by top too)
+    z[9, 7] = float("nan")
+    z[2600, 9], z[2600, 30] = float("inf"), float("nan")
+    _, lse, _, _, top_idx = pk.token_logprobs(z, labels, top=top)
+    key = torch.where(z.isnan(), float("inf"), z.double())
+    key[2600, 9] = 1e299  # NaN above all numbers
+    assert torch.equal(top_idx, torch.sort(key, dim=1, descending=True, stable=True).indices[:, :top])
+    assert bool(lse[9].isnan()) and bool(lse[2600].isnan()) and bool(lse[10:2600].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("V", [77, 4000, 33001])
 def test_strided_rows(pk, gen, dtype, V):
     wide, out = rand(gen, 6, V + 13, std=2.0, dtype=dtype), rand(gen, 6, V + 13, dtype=dtype)
