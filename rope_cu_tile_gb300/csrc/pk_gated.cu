@@ -261,18 +261,20 @@ cudaError_t few_launch(const FewArgs& a, int sms, cudaStream_t stream) {
 // ------------------------------------------------------------------------------------
 // dz
 
-// As pk_dz_kernel (pk_linear.cu): a warp takes 256 columns of a row, 8 a lane, a block eight rows at a time; dy, g and u are
+// As pk_dz_kernel (pk_linear.cu), but for a half warp to 128 columns of a row, a block sixteen rows at a time (dz_rows is asked for
+// blocks of 256, so for twice the columns): widths such as 1152 leave fewer lanes without any. dy, g and u are
 // read and both halves of dz written, their columns summed on the way. The activation and its slope share their
 // exponentials. In fp16 always with the second launch that applies a scale where the largest element asks for one: a
 // product of three factors is no element of dy.
-// 65536 x 2624 bf16 214 us with gelu, 16931 x 1152 f16 31: what the caches hold of 1.7 GB and 0.2 GB helps.
+// 65536 x 2624 bf16 272 us (0.95 of the copy rate), 16384 x 2624 74 (0.87), 16931 x 1152 f16 38 (0.77; 40 with whole
+// warps to 256 columns).
 constexpr int dz_resident(int dtype) { return dtype == PK_F32 ? 2 : 3; }  // blocks of an SM
 
 template <int DT, bool kScale>
 __global__ void __launch_bounds__(kDzThreads, (DT == PK_F32 ? 2 : 3)) pk_gated_dz_kernel(const __grid_constant__ DzArgs a, int F) {
-  __shared__ float sums[2][8][256];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c = blockIdx.y * 256 + lane * 8;
+  __shared__ float sums[2][16][128];
+  const int lane = threadIdx.x & 15, w = threadIdx.x >> 4;  // of a half warp
+  const int c = blockIdx.y * 128 + lane * 8;
   const int n = F - c;
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   griddep_wait();
@@ -337,12 +339,12 @@ __global__ void __launch_bounds__(kDzThreads, (DT == PK_F32 ? 2 : 3)) pk_gated_d
     };
     load(r0 + w);
 #pragma unroll 1
-    for (int64_t r = r0 + w; r < end; r += 8) {
+    for (int64_t r = r0 + w; r < end; r += 16) {
       float d[8], g[8], u[8], v[8], s[8];
       xd.get(d);
       xg.get(g);
       xu.get(u);
-      load(r + 8);
+      load(r + 16);
       act_both<DT>(a.act, g, v, s);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -386,15 +388,12 @@ __global__ void __launch_bounds__(kDzThreads, (DT == PK_F32 ? 2 : 3)) pk_gated_d
     sums[1][w][lane * 8 + j] = su[j];
   }
   __syncthreads();
-  const int col = blockIdx.y * 256 + threadIdx.x;
+  const int h = threadIdx.x >> 7, col = blockIdx.y * 128 + (threadIdx.x & 127);
   if (col < F) {
+    float v = 0.0f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v += sums[h][i][threadIdx.x];
-      a.part[static_cast<int64_t>(blockIdx.x) * a.ldz + h * F + col] = v;
-    }
+    for (int i = 0; i < 16; ++i) v += sums[h][i][threadIdx.x & 127];
+    a.part[static_cast<int64_t>(blockIdx.x) * a.ldz + h * F + col] = v;
   }
 }
 
@@ -404,7 +403,7 @@ cudaError_t dz_launch(int dtype, DzArgs a, int F, cudaStream_t stream) {
   a.dy_vec = rows16(a.dy, a.lddy, e) ? 1 : even && aligned_to(a.dy, 4) && (a.lddy & 1) == 0 ? 2 : 0;
   a.pre_vec = rows16(a.pre, a.ldpre, e) && (F * e & 15) == 0 ? 1 : even && aligned_to(a.pre, 4) ? 2 : 0;
   Launch l(1, kDzThreads, stream);
-  l.cfg.gridDim = dim3(static_cast<unsigned int>((a.T + a.rows - 1) / a.rows), static_cast<unsigned int>((F + 255) / 256));
+  l.cfg.gridDim = dim3(static_cast<unsigned int>((a.T + a.rows - 1) / a.rows), static_cast<unsigned int>((F + 127) / 128));
   if (dtype == PK_F32) return cudaLaunchKernelEx(&l.cfg, pk_gated_dz_kernel<PK_F32, false>, a, F);
   if (dtype == PK_BF16) return cudaLaunchKernelEx(&l.cfg, pk_gated_dz_kernel<PK_BF16, false>, a, F);
   const cudaError_t r = cudaLaunchKernelEx(&l.cfg, pk_gated_dz_kernel<PK_F16, false>, a, F);
@@ -435,7 +434,7 @@ Fwd plan_forward(int dtype, const void* x, int64_t ldx, const void* w, int64_t T
 Bwd plan_backward(int dtype, const void* x, int64_t ldx, const void* w, bool need_dx, bool need_dw, bool need_db, int64_t T, int F,
                   int K, int sms, void* ws) {
   const bool made = need_dx || need_dw;
-  return plan_products(dtype, x, ldx, w, made, made && dtype == PK_F16, F, dz_resident(dtype), need_dx, need_dw, need_db, T, 2 * F, K, sms, ws);
+  return plan_products(dtype, x, ldx, w, made, made && dtype == PK_F16, 2 * static_cast<int>(round_up(F, 128)), dz_resident(dtype), need_dx, need_dw, need_db, T, 2 * F, K, sms, ws);
 }
 
 template <int DT>
