@@ -13,7 +13,6 @@ constexpr int kFewThreads = 256;
 __host__ __device__ constexpr int few_r(int dt, int tm) { return dt == PK_F32 && tm < 8 ? 2 : 4; }
 __host__ __device__ constexpr int few_steps(int dt) { return dt == PK_F32 ? 1 : 2; }
 
-
 // Warps that split k among them, where the `dots` groups of rows alone give too few warps: 1, 2, 4 or 8.
 inline int few_share(int64_t dots, int K, int sms) {
   int share = 1;
@@ -46,21 +45,42 @@ __device__ __forceinline__ void few_dots(const void* x, int64_t ldx, int T, cons
     for (int s = 0; s < kFewSteps; ++s) {
       const int k = k0 + s * step;
       if (k >= K) break;
-      float v[kR][8];
+      if constexpr (DT != PK_F32) {
+        // (a product of two 16-bit numbers is exact in fp32, and one instruction adds it)
+        using E = Elem<DT == PK_BF16>;
 #pragma unroll
-      for (int r = 0; r < kR; ++r) q[s][r].get(v[r]);
+        for (int t = 0; t < TM; ++t) {
+          Raw8<DT> b;
+          const int64_t at = min(t, T - 1) * ldx + k;
+          if (vec && k + 8 <= K)
+            b.q[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+          else
+            b.load(x, at, false, K - k);
+          const uint32_t p[4] = {b.q[0].x, b.q[0].y, b.q[0].z, b.q[0].w};
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        float b[8];
-        const int64_t at = min(t, T - 1) * ldx + k;
-        if (vec && k + 8 <= K)
-          load8<DT, true>(x, at, b);
-        else
-          load8_any<DT>(x, at, K - k, b);
+          for (int r = 0; r < kR; ++r) {
+            const uint32_t u[4] = {q[s][r].q[0].x, q[s][r].q[0].y, q[s][r].q[0].z, q[s][r].q[0].w};
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
+            for (int j = 0; j < 4; ++j) acc[r][t] = E::fma_hi(u[j], p[j], E::fma_lo(u[j], p[j], acc[r][t]));
+          }
+        }
+      } else {
+        float v[kR][8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(v[r][j], b[j], acc[r][t]);
+        for (int r = 0; r < kR; ++r) q[s][r].get(v[r]);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+          float b[8];
+          const int64_t at = min(t, T - 1) * ldx + k;
+          if (vec && k + 8 <= K)
+            load8<DT, true>(x, at, b);
+          else
+            load8_any<DT>(x, at, K - k, b);
+#pragma unroll
+          for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(v[r][j], b[j], acc[r][t]);
+        }
       }
     }
   }

@@ -196,8 +196,11 @@ struct FewArgs {
   GluParams ep;
 };
 
+// Bound by the bytes of W from 10 MB on, by its launch below: one row bf16 or f16, 2 x 4096 x 4096 12.2 us (0.82 of the copy rate; 16.4
+// while both operands were unpacked first), 2 x 2624 x 1024 3.8. Up to two rows on 64 registers, for four blocks an SM: two rows 15 us, 17
+// to 18.6 without. Four rows 23 and 7.2.
 template <int DT, int TM>
-__global__ void __launch_bounds__(kFewThreads) pk_gated_few_kernel(const __grid_constant__ FewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, TM > 2 ? 1 : 4) pk_gated_few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kR = few_r(DT, TM), kCols = kR / 2;
   __shared__ float part[8][kR * TM];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;

@@ -225,6 +225,19 @@ def test_past_32_bits(pk, gen):
         assert ref.worst(y[part], wy, by) <= 1
 
 
+def test_odd_rows_past_32_bits(pk, gen):
+    """The same of rows off the 16-byte grid, and their gradient."""
+    T, D = (1 << 31) // 1023 + 300, 1023
+    x, w = torch.ones(T, D, dtype=torch.bfloat16, device="cuda"), rand(gen, D, dtype=torch.bfloat16)
+    x[:300], x[-300:] = rand(gen, 300, D), rand(gen, 300, D)
+    y = pk.rms_norm(x, w)
+    dx, _ = pk.rms_norm_backward(x, w, y, dh=x, need_dw=False)
+    for part in (slice(0, 300), slice(T - 300, T)):
+        (wy, _), (by, _), _ = ref.rms_norm(x[part], w, None, 1e-6)
+        (wx, _), (bx, _) = ref.rms_norm_backward(x[part], w, y[part], x[part], 1e-6)
+        assert ref.worst(y[part], wy, by) <= 1 and ref.worst(dx[part], wx, bx) <= 1
+
+
 def test_streams_and_graphs(pk, gen):
     """Another stream than the tensors' own; a captured step replayed on new inputs."""
     T, D = 300, 768
