@@ -137,7 +137,8 @@ cudaError_t dz_launch(int dtype, DzArgs a, cudaStream_t stream) {
 // Bound by W's bytes, read once; x stays in L1. A warp dots kR rows of W with every row of x, 8 elements a lane and step, in
 // fp32 on the CUDA cores (fp32 inputs need no planes); where N alone gives too few warps, several share the rows and split
 // k, so that most of W is on its way at once. One launch, no scratch. Past a few rows its arithmetic and the reads of x
-// outweigh the tensor cores' fixed costs: W [4096, 1024] in bf16 took 3.5 us at 1 row, 6.5 at 4, 11.9 at 8, and 7.3 there;
+// outweigh the tensor cores' fixed costs: W [4096, 1024] in bf16 takes 3.3 us at 1 row, 6.1 at 4 (11.9 at 8, when both operands were
+// unpacked first), and 7.3 there;
 // fp32 10.5 at 8 rows here and some 19 there, with its plane copies.
 bool few_rows(int dtype, int64_t T) { return T <= (dtype == PK_F32 ? PK_LINEAR_FEW_T : PK_LINEAR_FEW_T / 2); }
 
