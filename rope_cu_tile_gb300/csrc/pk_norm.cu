@@ -189,8 +189,11 @@ __device__ __forceinline__ Walk walk(int64_t T, int period, int shift0, int slid
   return w;
 }
 
-// N sums (or maxima, where bit i of kMax is set) over a row's threads, in every one of them. `red`: 2 x 16 x N floats, used
-// alternately so that one barrier a row is enough.
+// N sums (or maxima, where bit i of kMax is set) over a row's threads, in every one of them. `red`: two halves of kRedHalf floats,
+// taken alternately, so that one barrier a call is enough: who writes a half has passed the barrier of the call between, and
+// with it everyone has read what that half held before. The halves lie equally far apart whatever N is, as calls of
+// different N follow one another in any number (a row whose squares are summed again makes one more).
+constexpr int kRedHalf = 16 * 2;  // warps of the longest row x the most values
 template <int kTpr, int N, int kMax>
 __device__ __forceinline__ void row_reduce(float (&v)[N], float* red, int& turn) {
 #pragma unroll
@@ -202,7 +205,8 @@ __device__ __forceinline__ void row_reduce(float (&v)[N], float* red, int& turn)
     }
   if constexpr (kTpr > 32) {
     constexpr int kWarps = kTpr / 32;
-    float* r = red + turn * 16 * N;
+    static_assert(kWarps * N <= kRedHalf, "a half holds a call's values");
+    float* r = red + turn * kRedHalf;
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kResident<DT, kTpr>))
   using G = Group<DT, kTpr, kUnit>;
   constexpr int E = G::E;
   constexpr bool kVec = G::kVec;
-  __shared__ float red[kTpr > 32 ? 2 * 16 * 2 : 1];
+  __shared__ float red[kTpr > 32 ? 2 * kRedHalf : 1];
   constexpr int kRows = kBlock<kTpr> / kTpr;
   const int t = threadIdx.x % kTpr;
   int turn = 0;
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, (kBackResident<DT, kTpr>)) pk_no
   constexpr int E = G::E;
   constexpr bool kVec = G::kVec;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float red[kTpr > 32 ? 2 * 16 * 2 : 1];
+  __shared__ float red[kTpr > 32 ? 2 * kRedHalf : 1];
   constexpr int kRows = kBlock<kTpr> / kTpr, kCols = kTpr * kNg * E, kS = kStages<DT, kTpr, kNg>;
   const int t = threadIdx.x % kTpr;
   int turn = 0;

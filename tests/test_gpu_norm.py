@@ -131,6 +131,33 @@ def test_special_rows(pk, gen, dtype, D):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [8192, 8189, 9000, 16384, 16377, 16383])
+def test_rows_after_special_ones(pk, gen, dtype, D):
+    """More long rows than there are blocks, after rows whose squares pass fp32's range (which are summed once more): every other row
+    comes out as it does without them, bit for bit, and as in 64 bits."""
+    T = 2500
+    x, r, w = rand(gen, T, D, std=1.5, dtype=dtype), rand(gen, T, D, dtype=dtype), rand(gen, D, dtype=dtype)
+    special = torch.zeros(T, dtype=torch.bool, device="cuda")
+    special[3:140:7] = True
+    special[700:760:3] = True
+    odd = x.clone()
+    odd[special] = torch.finfo(dtype).max / 4  # (past 2^64 but in fp16)
+    odd[special.nonzero()[::2, 0], D // 3] = float("inf")
+    want, got = pk.rms_norm_q8(x, w, residual=r), pk.rms_norm_q8(odd, w, residual=r)
+    for a, b in zip(want, got):
+        assert torch.equal(a[~special].view(torch.uint8), b[~special].view(torch.uint8))
+    (wy, _), _, ey = ref.rms_norm(x, w, r, 1e-6)
+    ws = wy.abs().amax(1) / 448
+    ok = ~special
+    assert ref.worst(got[1][ok], ws[ok], 2.0**-16 * ws[ok]) <= 1
+    assert ref.worst(got[0][ok].double() * got[1][ok].double()[:, None], wy[ok], ref.e4m3_bound(wy[ok], ey[ok], ws[ok])) <= 1
+    assert torch.equal(pk.rms_norm(odd, w)[ok], pk.rms_norm(x, w)[ok])
+    assert torch.equal(pk.quantize_rows(odd)[1][ok], pk.quantize_rows(x)[1][ok])
+    dx, _ = pk.rms_norm_backward(odd, w, r)
+    assert torch.equal(dx[ok], pk.rms_norm_backward(x, w, r)[0][ok])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("D", [64, 96, 1024, 2000])
 def test_strided_rows_and_in_place(pk, gen, dtype, D):
     T = 37
