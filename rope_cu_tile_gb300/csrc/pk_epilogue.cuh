@@ -570,7 +570,10 @@ struct Bias {
   }
 };
 
+// 32 columns of this warp's accumulators. The load is of 32 lanes together; what stands before it (a list of words, an
+// activation's slow path, one lane's store) need not leave them so.
 __device__ __forceinline__ void read_acc(uint32_t t, bool zero, float (&v)[32]) {
+  __syncwarp();
   if (zero) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = 0.0f;

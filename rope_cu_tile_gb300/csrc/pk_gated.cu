@@ -87,6 +87,7 @@ struct GluEpi {
 #pragma unroll
           for (int i = 0; i < 16; ++i) g[i] = u[i] = 0.0f;
         } else {
+          __syncwarp();  // (as in read_acc)
           tmem_ld16(gate + cc + q, g);
           tmem_ld16(up + cc + q, u);
         }

@@ -125,6 +125,26 @@ def test_gradient_against_differences(pk, gen):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [90, 700, 20000])
+def test_words_close_together(pk, gen, dtype, V):
+    """Neighbouring rows with none to 64 of their words in the same 32 of the vocabulary, some more than once, the rest anywhere."""
+    T, D, top = 200, 72, 64
+    x, w, bias, idx, values = case(gen, dtype, T, D, V, top, holes=False)
+    close = torch.arange(top, device="cuda")[None] < (torch.arange(T, device="cuda")[:, None] * 37) % 65
+    near = 32 * (torch.arange(T, device="cuda") // 32 % 2)[:, None] + torch.randint(0, 32, (T, top), generator=gen, device="cuda")
+    idx = torch.where(close, near, idx)
+    idx[::9, ::2] = -1
+    loss, lse = pk.distill(x, w, idx, values, bias=bias)
+    (wl, ws), (bl, bs) = ref.distill(x, w, idx, values, bias, 1.0)
+    assert ref.worst(lse, ws, bs) <= 1 and ref.worst(loss, wl, bl) <= 1
+    dloss = rand(gen, T) / T
+    got = pk.distill_backward(x, w, idx, values, lse, dloss, bias=bias)
+    want, bound = ref.distill_backward(x, w, idx, values, lse, dloss, bias, 1.0)
+    for g, v, e in zip(got, want, bound):
+        assert ref.worst(g, v, e) <= 1
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tau", [1e-3, 0.05, 1e3])
 def test_temperatures_at_the_ends(pk, gen, dtype, tau):
     """The coldest and the hottest: probabilities all but one-hot, and all but equal; fp16's dz stays in range."""
