@@ -180,6 +180,7 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // (a warp arrives as one, and what stands before may have been one lane's)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {

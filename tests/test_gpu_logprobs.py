@@ -186,6 +186,23 @@ def test_many_rows_of_middle_length(pk, gen, dtype, V, top):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", [(5, 8192), (36, 33000), (70, 17000), (18, 70001)])
+def test_rows_over_several_blocks(pk, gen, dtype, T, V):
+    """Two, four and eight blocks a row: their likeliest words all in the first block's part, in the last's, one in each, equal ones."""
+    z = rand(gen, T, V, std=2.0, dtype=dtype)
+    z[0, :100] += 20
+    z[1, -100:] += 20
+    z[2, :: V // 50] += 20
+    z[3] = 0.75
+    z[4] = float("-inf")
+    z[4, V // 2] = 0.0
+    labels = torch.randint(-1, V, (T,), generator=gen, device="cuda")
+    labels[4] = V // 2
+    for top in (64, 1, 33, 0):
+        check(pk, z, labels, top)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("V", [77, 4000, 33001])
 def test_strided_rows(pk, gen, dtype, V):
     wide, out = rand(gen, 6, V + 13, std=2.0, dtype=dtype), rand(gen, 6, V + 13, dtype=dtype)
