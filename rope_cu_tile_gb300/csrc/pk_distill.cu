@@ -104,15 +104,16 @@ __global__ void __launch_bounds__(256) pk_distill_list_kernel(const __grid_const
       }
       const bool is = there(x, v);
       key[i] = static_cast<uint32_t>(is ? static_cast<int>(x) : kGone) << 6 | static_cast<uint32_t>(k);
-      e[i] = is ? v * a.inverse : -INFINITY;
+      e[i] = is ? v : -INFINITY;
       m = fmaxf(m, e[i]);
     }
-    // (a NaN among the values, or an infinity, comes through the exponentials)
+    // the maximum is taken off before the temperature: what is left is exact where it counts, whatever the values have in common
+    // (a NaN among them, or an infinity, comes through the exponentials)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      e[i] = key[i] >> 6 == kGone ? 0.0f : expf(e[i] - m);
+      e[i] = key[i] >> 6 == kGone ? 0.0f : expf((e[i] - m) * a.inverse);
       sum += e[i];
     }
 #pragma unroll

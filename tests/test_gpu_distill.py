@@ -124,6 +124,62 @@ def test_gradient_against_differences(pk, gen):
         assert abs(slope - want) <= 2e-3 * float((g.double().abs() * d.double().abs()).sum())
 
 
+@pytest.mark.parametrize("top", [5, 40])
+@pytest.mark.parametrize("tau", [1e-3, 0.3, 1.0, 30.0])
+def test_a_constant_on_the_teachers_values(pk, gen, tau, top):
+    """Values that all have the same constant added, exactly (steps of 2^-4 beside 2^18): the same loss and gradients, bit for bit."""
+    T, D, V = 70, 40, 300
+    x, w, bias, idx, _ = case(gen, torch.float32, T, D, V, top)
+    values = torch.randint(-128, 128, (T, top), generator=gen, device="cuda").float() / 16
+    values[torch.rand(T, top, generator=gen, device="cuda") < 0.1] = float("-inf")
+    dloss = rand(gen, T) / T
+
+    def run(values):
+        loss, lse = pk.distill(x, w, idx, values, bias=bias, temperature=tau)
+        return loss, lse, *pk.distill_backward(x, w, idx, values, lse, dloss, bias=bias, temperature=tau)
+
+    want = run(values)
+    for c in (2.0**18, -(2.0**18)):
+        assert all(torch.equal(a, b) for a, b in zip(run(values + c), want))
+
+
+@pytest.mark.parametrize("tau", [1e-3, 0.05, 1.0])
+def test_large_values_of_the_teacher(pk, gen, tau):
+    """Raw logits near 10^4: as those less their maximum (exact differences), with a bound that goes by these."""
+    T, D, V, top = 60, 40, 300, 9
+    x, w, bias, idx, values = case(gen, torch.float32, T, D, V, top)
+    values = values * max(tau, 2.0**-6) + 1e4
+    there = (idx >= 0) & ~torch.isneginf(values)
+    less = values.double() - torch.where(there, values.double(), -1e30).amax(1, keepdim=True)
+    loss, lse = pk.distill(x, w, idx, values, bias=bias, temperature=tau)
+    (wl, ws), (bl, bs) = ref.distill(x, w, idx, less, bias, tau)
+    assert ref.worst(lse, ws, bs) <= 1 and ref.worst(loss, wl, bl) <= 1
+    dloss = rand(gen, T) * tau / T
+    got = pk.distill_backward(x, w, idx, values, lse, dloss, bias=bias, temperature=tau)
+    want, bound = ref.distill_backward(x, w, idx, less, lse, dloss, bias, tau)
+    for g, v, e in zip(got, want, bound):
+        assert ref.worst(g, v, e) <= 1
+
+
+@pytest.mark.parametrize("tau", [1e-3, 0.5, 2.0])
+def test_a_teachers_lowest_values(pk, gen, tau):
+    """Words masked by the type's lowest value: no share beside others, equal ones where nothing else is there."""
+    T, D, V, top = 12, 24, 200, 6
+    x, w, bias, idx, values = case(gen, torch.float32, T, D, V, top, holes=False)
+    low = torch.finfo(torch.float32).min
+    values[0:4] = low
+    values[4:8, 1:] = low
+    values[8, 0], values[8, 1:] = -low, low
+    same = values.clone()
+    same[0:4] = 0.0
+    same[4:9, 0], same[4:9, 1:] = 0.0, float("-inf")
+    a, b = (pk.distill(x, w, idx, v, bias=bias, temperature=tau) for v in (values, same))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and bool(a[0].isfinite().all())
+    g = torch.ones(T, device="cuda")
+    a, b = (pk.distill_backward(x, w, idx, v, a[1], g, bias=bias, temperature=tau) for v in (values, same))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("V", [90, 700, 20000])
 def test_words_close_together(pk, gen, dtype, V):
