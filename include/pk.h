@@ -496,7 +496,8 @@ int pk_gated_linear_backward_workspace(int dtype, const void *x, int64_t ldx, co
  * pk_quantize_rows.
  *   x [T, K] e4m3 (ldx, a multiple of 16), w [N, K] e4m3, K a multiple of 16, both 16-byte aligned; x_scale [T], w_scale [N]
  *   fp32; bias [N], residual [T, N] (ldr) and y [T, N] (ldy) in `dtype`, the first two or NULL. y may be residual itself (ldy = ldr).
- * Products are exact and sums fp32 (tensor cores; up to PK_LINEAR_FEW_T / 2 rows on the CUDA cores, without a workspace).
+ * Products are exact and sums fp32 (tensor cores; up to PK_LINEAR_FEW_T / 2 rows on the CUDA cores, without a workspace); a sum is
+ * multiplied by x_scale[t], then by w_scale[n], in fp32.
  */
 int pk_linear_q8(int dtype, const void *x, int64_t ldx, const float *x_scale, const void *w, const float *w_scale, const void *bias,
                  const void *residual, int64_t ldr, int act, int64_t T, int N, int K, void *y, int64_t ldy, void *workspace,

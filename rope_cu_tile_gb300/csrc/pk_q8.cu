@@ -4,7 +4,8 @@
 //
 // The product runs on the tensor cores at twice the 16-bit rate, with half the operands' bytes: to the kernel of pk_gemm.cuh a
 // pair of 8-bit elements is one 16-bit element of k, and only the instruction differs (kBytes). Every product of two e4m3
-// numbers is exact in fp32 and the scales stand outside the sum, so they are part of the epilogue.
+// numbers is exact in fp32 and the scales stand outside the sum, so they are part of the epilogue: the sum times s_t, then times v_n,
+// wherever it is done (s_t v_n by itself may be past either end of fp32's range where these two are not).
 #include "pk_few.cuh"
 
 namespace pk {
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(256) pk_q8_splits_kernel(const float* part, in
     const float xs = __ldcg(p.xs + r);
     load8_any<PK_F32>(p.ws, c, left, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= xs * b[j];
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * xs * b[j];
     if (p.bias) {
       load8_any<DT>(p.bias, c, left, b);
 #pragma unroll
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kFewThreads) pk_q8_few_kernel(const __grid_con
     if (t >= a.T || n >= a.N) continue;
     float v[2] = {0.0f, 0.0f};
     for (int s = 0; s < a.share; ++s) v[0] += part[g * a.share + s][e];
-    v[0] *= a.ep.xs[t] * a.ep.ws[n];
+    v[0] = v[0] * a.ep.xs[t] * a.ep.ws[n];
     if (a.ep.bias) v[0] += Ty<DT>::get(a.ep.bias, n);
     act_values<DT>(a.ep.act, v);
     if (a.ep.res) v[0] += Ty<DT>::get(a.ep.res, t * a.ep.ldres + n);

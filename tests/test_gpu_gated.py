@@ -217,6 +217,25 @@ def test_linear_q8_strided_rows(pk, gen, T):
         assert bool((wide[:, :5] == 7).all()) and bool((wide[:, 5 + N:] == 7).all())
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 256, 70), (2, 256, 70), (4, 256, 70), (5, 8192, 130), (64, 8192, 256), (700, 256, 130), (20000, 64, 256)])
+@pytest.mark.parametrize("small,large", [(1e-25, 1e-19), (1e25, 1e15), (1e-36, 1e5)])
+def test_linear_q8_scales_of_any_size(pk, gen, T, K, N, small, large):
+    """Scales whose product is past fp32's range though neither the scaled sum nor the result is, for few rows, splits of k and whole tiles; a row of zeros
+    gives zeros."""
+    xq, _ = pk.quantize_rows(rand(gen, T, K))
+    wq, _ = pk.quantize_rows(rand(gen, N, K))
+    if small * large > 1e38:  # small sums: one small number a row
+        xq, wq = (torch.zeros_like(t.float()) for t in (xq, wq))
+        xq[:, 5], wq[:, 5] = 2.0**-9, 2.0**-8
+        xq, wq = xq.to(torch.float8_e4m3fn), wq.to(torch.float8_e4m3fn)
+    xq.view(torch.uint8)[T // 2 :: 3] = 0
+    xs, ws = (1 + torch.rand(T, generator=gen, device="cuda")) * small, (1 + torch.rand(N, generator=gen, device="cuda")) * large
+    y = pk.linear_q8(xq, xs, wq, ws, out_dtype=torch.float32)
+    want, bound = ref.linear_q8(xq, xs, wq, ws, None, None, "none", torch.float32)
+    assert bool(want.any()) or T == 1
+    assert ref.worst(y, want, bound) <= 1 and not bool(y[T // 2 :: 3].any())
+
+
 @pytest.mark.parametrize("T", [2, 200])
 def test_linear_q8_undefined_rows(pk, gen, T):
     """A row that could not be scaled has no value; the others keep theirs."""
