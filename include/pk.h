@@ -510,7 +510,8 @@ int pk_linear_q8_workspace(int64_t T, int N, int K, int64_t *bytes);
  * likeliest words, the likeliest first and equal ones by their index: top_idx [T, top] int64 and top_logp [T, top]
  * (top <= PK_LOGPROBS_MAX_TOP and <= V; 0: both may be NULL). NaN is ranked above all numbers. A logit of -inf is a word
  * that cannot be: probability 0. A row of nothing else has lse and log probabilities -inf and entropy 0; one with a NaN or
- * +inf has NaN. No workspace.
+ * +inf has NaN. No workspace. How a row is shared out, and so the order of its fp32 sums, goes by dtype, T, V and top: the last
+ * bits of lse, logp and entropy may differ between calls that differ in these.
  */
 #define PK_LOGPROBS_MAX_TOP 64
 int pk_token_logprobs(int dtype, const void *logits, int64_t ld, const int64_t *labels, int64_t T, int V, int top, float *logp,

@@ -1068,7 +1068,8 @@ def token_logprobs(logits, labels, top: int = 0, status=None, stream=None):
     """(logp [T], lse [T], entropy [T], top_logp [T, top], top_idx [T, top]) of logits [T, V] and int64 labels [T]: the log
     probability of each row's label (0 for a negative label; NaN and PK_ERR_BAD_LABEL for one >= V, in `status` or last_status
     of the call's stream), the row's log-sum-exp and entropy (float32), and its `top` (at most 64) likeliest words, the
-    likeliest first and equal ones by index (int64; None, None for top 0). logits may have strided rows."""
+    likeliest first and equal ones by index (int64; None, None for top 0). logits may have strided rows. The last bits of logp, lse
+    and entropy may depend on T and top, which say how a row's sums are shared out."""
     torch = _torch()
     dev = logits.device
     code = dtype_code(logits)

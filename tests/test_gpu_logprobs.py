@@ -203,6 +203,19 @@ def test_rows_over_several_blocks(pk, gen, dtype, T, V):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", [(300, 1040), (300, 2100), (300, 4588), (160, 8192), (64, 8192), (300, 8193)])
+def test_a_block_a_row(pk, gen, dtype, T, V):
+    """Rows of blocks of 64 and of 128 threads, by how many words are asked for: each against its definition (not against each other,
+    whose sums' order differs), on the 16-byte grid and off it."""
+    wide = rand(gen, T, V + 8, std=2.5, dtype=dtype)
+    labels = torch.randint(-1, V, (T,), generator=gen, device="cuda")
+    for shift in (0, 8, 3):
+        z = wide[:, shift : shift + V]
+        for top in (0, 16, 32, 33, 64):
+            check(pk, z, labels, top)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("V", [77, 4000, 33001])
 def test_strided_rows(pk, gen, dtype, V):
     wide, out = rand(gen, 6, V + 13, std=2.0, dtype=dtype), rand(gen, 6, V + 13, dtype=dtype)
