@@ -265,18 +265,21 @@ struct StatEpi {
     if constexpr (kList) words.ask(p.lists, p.cap, row, row < M, c0 / cols);
     const int end = min(cols, N - c0);
     float m = kFloor, l = 0.0f;
-    Bias<DT, 32> b;  // of the next 32 words, on its way while these are reduced
-    if (p.bias) b.fetch(p.bias, p.bias_vec, c0, N);
+    // The bias of 32 words: with lists asked for while the 32 before are reduced, with a label just before its logits (16384 x 256
+    // over 32768 words, bf16: lists 358 us, 367 the label's way; a label 284 us, 320 the lists' way)
+    Bias<DT, 32> b;
+    if (kList && p.bias) b.fetch(p.bias, p.bias_vec, c0, N);
 #pragma unroll 1
     for (int cc = 0; cc < end; cc += 32) {
       const int c = c0 + cc;
       float v[32];
+      if (!kList && p.bias) b.fetch(p.bias, p.bias_vec, c, N);
       if (cc == 0 && !ready()) return false;
       read_acc(tacc + cc, zero, v);
       if (cc + 32 >= end) done();
       if (p.bias) {
         b.add(v);
-        if (cc + 32 < end) b.fetch(p.bias, p.bias_vec, c + 32, N);
+        if (kList && cc + 32 < end) b.fetch(p.bias, p.bias_vec, c + 32, N);
       }
       if (c + 32 > N) {
 #pragma unroll
