@@ -20,11 +20,13 @@ inline int few_share(int64_t dots, int K, int sms) {
   return share;
 }
 
-// acc[r][t] += this lane's share of W's row row(r) times x's row t, `sub` of `share` warps splitting k. Nothing where !some.
-template <int DT, int kR, int TM, class RowOf>
+// acc[r][t] += this lane's share of W's row row(r) times x's row t, `sub` of `share` warps splitting k. Nothing where !some. kX: rows of x,
+// in fp32, that are asked for together.
+template <int DT, int kX, int kR, int TM, class RowOf>
 __device__ __forceinline__ void few_dots(const void* x, int64_t ldx, int T, const void* w, int K, int vec, bool some, int sub,
                                          int share, int lane, const RowOf& row, float (&acc)[kR][TM]) {
   constexpr int kFewSteps = few_steps(DT);
+  static_assert(TM % kX == 0, "");
 #pragma unroll
   for (int r = 0; r < kR; ++r)
 #pragma unroll
@@ -69,17 +71,22 @@ __device__ __forceinline__ void few_dots(const void* x, int64_t ldx, int T, cons
 #pragma unroll
         for (int r = 0; r < kR; ++r) q[s][r].get(v[r]);
 #pragma unroll
-        for (int t = 0; t < TM; ++t) {
-          float b[8];
-          const int64_t at = min(t, T - 1) * ldx + k;
-          if (vec && k + 8 <= K)
-            load8<DT, true>(x, at, b);
-          else
-            load8_any<DT>(x, at, K - k, b);
+        for (int t0 = 0; t0 < TM; t0 += kX) {
+          float b[kX][8];
 #pragma unroll
-          for (int r = 0; r < kR; ++r)
+          for (int t = 0; t < kX; ++t) {
+            const int64_t at = min(t0 + t, T - 1) * ldx + k;
+            if (vec && k + 8 <= K)
+              load8<DT, true>(x, at, b[t]);
+            else
+              load8_any<DT>(x, at, K - k, b[t]);
+          }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(v[r][j], b[j], acc[r][t]);
+          for (int t = 0; t < kX; ++t)
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) acc[r][t0 + t] = fmaf(v[r][j], b[t][j], acc[r][t0 + t]);
         }
       }
     }

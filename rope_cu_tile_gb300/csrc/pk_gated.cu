@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kFewThreads, TM > 2 ? 1 : 4) pk_gated_few_kern
   const int n0 = (blockIdx.x * groups + group) * kCols;
   float acc[kR][TM];
   griddep_wait();
-  few_dots<DT>(a.x, a.ldx, a.T, a.w, a.K, a.vec, n0 < a.F, sub, a.share, lane,
+  few_dots<DT, 1>(a.x, a.ldx, a.T, a.w, a.K, a.vec, n0 < a.F, sub, a.share, lane,
                [&](int r) { return min(n0 + r % kCols, a.F - 1) + (r < kCols ? 0 : a.F); }, acc);
 #pragma unroll
   for (int r = 0; r < kR; ++r)

@@ -161,7 +161,10 @@ __global__ void __launch_bounds__(kFewThreads) pk_linear_few_kernel(const __grid
   const int n0 = (blockIdx.x * groups + group) * kR;
   float acc[kR][TM];
   griddep_wait();
-  few_dots<DT>(a.x, a.ldx, a.T, a.w, a.K, a.vec, n0 < a.N, sub, a.share, lane, [&](int r) { return min(n0 + r, a.N - 1); }, acc);
+  // (fp32, five to eight rows, the rows of x four at a time and one at a time, us: 8 x 515 -> 1003 5.1, 6.4; 8 x 1500 -> 4001 14.4, 17.1;
+  // 8 x 2048 -> 8192 23.2, 25.8; 8 x 1024 -> 4096 10.2, 10.1; 5 x 1024 -> 4096 10.2, 9.8. Up to four rows one at a time: 4 x 1024 -> 4096 6.4,
+  // 8.6 together. The gated kernel, whose rows of W come from two places: 8 x 1024 -> 2 x 2624 13.2, 12.2)
+  few_dots<DT, TM == 8 ? 4 : 1>(a.x, a.ldx, a.T, a.w, a.K, a.vec, n0 < a.N, sub, a.share, lane, [&](int r) { return min(n0 + r, a.N - 1); }, acc);
 #pragma unroll
   for (int r = 0; r < kR; ++r)
 #pragma unroll
