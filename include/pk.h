@@ -450,8 +450,8 @@ int pk_cross_entropy_workspace(int dtype, const void *x, int64_t ldx, const void
  *   same row stride).
  * pk_rms_norm_q8 writes the rows in 8 bits for pk_linear_q8: scale[t] = max |y| / 448 of the row (fp32), q [T, D] (ldq,
  * in bytes) = y / scale rounded to e4m3. A row of zeros has scale 0; one with a NaN, scale NaN; one with an infinity, scale
- * infinity. pk_quantize_rows does that to x itself (a weight matrix, other activations). These calls take no
- * workspace and find no errors on the device.
+ * infinity. pk_quantize_rows does that to x itself (a weight matrix, other activations; of up to PK_NORM_MAX_D columns, where
+ * pk_linear_q8 takes longer rows from elsewhere too). These calls take no workspace and find no errors on the device.
  */
 #define PK_NORM_MAX_D 16384
 int pk_rms_norm(int dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *w, float eps, int64_t T,

@@ -881,7 +881,7 @@ def rms_norm_q8(x, w, residual=None, eps: float = 1e-6, h_out=None, stream=None)
 
 def quantize_rows(x, stream=None):
     """(q [T, D] float8_e4m3fn, scale [T] float32) for x [T, D]: row t is q[t] scale[t] to 8 bits, scale the row's largest
-    magnitude / 448. For the weights of `linear_q8` and for activations that come from no norm."""
+    magnitude / 448. For the weights of `linear_q8` and for activations that come from no norm; D up to 16384."""
     torch = _torch()
     dev = x.device
     code = dtype_code(x)

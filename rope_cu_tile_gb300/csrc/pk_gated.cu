@@ -6,7 +6,8 @@
 //
 // Forward: one product whose tiles hold the same columns of both halves (pk_gemm.cuh, kPair), so that the activation and
 // the product of the two are its epilogue and neither half goes through memory unless the caller keeps them for the
-// backward. Backward: dz is made once and is an operand of both products, as in pk_linear.cu.
+// backward. Backward: dz is made once and is an operand of both products, as in pk_linear.cu, rounded to the element type as such
+// operands are: dx and dw of fp16 are then 2.9e-4 of their norm off, 2.1e-4 of it their own rounding; db sums it unrounded.
 #include "pk_dz.cuh"
 #include "pk_few.cuh"
 
@@ -37,7 +38,8 @@ __device__ __forceinline__ const void* up_half(const void* p, int F) {
 // A chunk of 32 columns: each half with its bias to `pre` where that is kept, then both again, 16 columns at a time, for y.
 // One staging tile a warp serves the three; an accumulator read twice costs less than the registers to hold both halves.
 // 16384 x 1024 -> 2 x 2624 bf16: 109 us with gelu (a plain product of that size 104; bound by its operands' way through L2 as
-// that is), 121 with both halves kept.
+// that is), 121 with both halves kept. Of 96 registers a thread 116 bytes are spilled and 340 read back, the pair's tile in 16 bits. fp32
+// 584 us (537 by six passes).
 template <int DT>
 struct GluEpi {
   using Params = GluTiles;
@@ -199,7 +201,7 @@ struct FewArgs {
 
 // Bound by the bytes of W from 10 MB on, by its launch below: one row bf16 or f16, 2 x 4096 x 4096 12.2 us (0.82 of the copy rate; 16.4
 // while both operands were unpacked first), 2 x 2624 x 1024 3.8. Up to two rows on 64 registers, for four blocks an SM: two rows 15 us, 17
-// to 18.6 without. Four rows 23 and 7.2.
+// to 18.6 without. Four rows 23 and 7.4: a step's weights are asked for, waited for and multiplied with every row in turns.
 template <int DT, int TM>
 __global__ void __launch_bounds__(kFewThreads, TM > 2 ? 1 : 4) pk_gated_few_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kR = few_r(DT, TM), kCols = kR / 2;

@@ -52,7 +52,7 @@ constexpr int kGroupM = 8;                    // tile rows walked together
 // of 16: 8e-5 over 100000 terms, where fp32 allows 1e-5 and a rounding to fp16 costs 2e-4. At most this many k steps add
 // up there before the epilogue's warps take the sum over, rounding to nearest, into the other accumulator's tensor memory:
 // 1024 terms of fp32 operands (the drift stays below 2e-6), 16384 of 16-bit ones (3e-5; a hand-over costs some 2000
-// cycles of 131000).
+// cycles of 131000), 32768 of 8-bit ones, whose steps are of 32 (2048 where their result is fp32).
 constexpr int kPhase32 = 16;
 constexpr int kPhase16 = 256;
 

@@ -755,7 +755,8 @@ __device__ __forceinline__ void slice_top(Search<kT>& sh, const Found<kT>& fd, c
     if (threadIdx.x < 32) finish<kT>(sh, n, top, emit);
     return;
   }
-  // many large ones in few threads: one maximum after another
+  // many large ones in few threads: one maximum after another, each a pass over the slice (64 likeliest of 400 x 65536 fp32, ten thousand
+  // candidates a row: 2026 us, 27 of random rows)
   uint64_t done = ~uint64_t(0);
   for (int i = 0; i < top; ++i) {
     uint64_t best = 0;

@@ -103,7 +103,8 @@ struct Group {
     }
     q = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // the weights, which every row reads again: through L1, or from their copy in shared memory
+  // the weights, which every row reads again: through L1 (kWhole), from their copy in shared memory (kSlide), or by elements through L2
+  // (kSingle, and kSlide's backward pass, which holds them from its start)
   __device__ __forceinline__ void load_shared(const void* p, int c, int D, const uint8_t* copy = nullptr, int i = 0, int t = 0) {
     if constexpr (kUnit == kWhole)
       q = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + c * Ty<DT>::kBytes);
@@ -235,7 +236,10 @@ __device__ __forceinline__ void to_e4m3(const float (&v)[N], uint32_t (&q)[N / 4
 }
 
 // Bound by bytes: 131072 x 1024 bf16 with a residual 161 us, 1.0 of the copy rate; 100000 x 1024 to 8 bits 114 us (issue slots
-// half full); rows off the 16-byte grid 100000 x 1003 bf16 178 (120 of bytes; 313 in single columns).
+// half full); quantize_rows 100000 x 1024 bf16 54 (46 of bytes), 16384 x 4096 38 (30), 4096 x 16384 fp32 73 (50). Rows off the 16-byte
+// grid 100000 x 1003 bf16 178 (120 of bytes; 313 in single columns): latency, the issue slots being 42 % full; warps wait for loads in 6.5
+// of 11.7 cycles an instruction, 24 of them an SM, and 116 bytes a thread and row spilled from 80 registers are another half
+// of the results' sectors to L2. (On the grid 52 bytes are spilled, which the copy rate hides.)
 // blocks of an SM: 85 registers a thread, 128 of fp32
 template <int DT, int kTpr>
 constexpr int kResident = kTpr > 256 ? 1 : (DT == PK_F32 ? 512 : 768) / kBlock<kTpr>;
